@@ -353,6 +353,143 @@ ssu_status_t ssu_copy_blocks(ssu_handle_t handle, const ssu_block_tensor_t *tens
  * restores the built-in choice).  All shapes copy the same bytes. */
 ssu_status_t ssu_copy_set_launch(ssu_handle_t handle, const ssu_copy_launch_t *launch);
 
+/* ---------------------------------------------------------------------------------------
+ * Prompts: the recurrence of the decode step over whole prompts, packed one after another
+ * without padding.  Prompt b holds tokens cu_tokens[b] .. cu_tokens[b + 1] - 1 of x, dt, B, C
+ * and out; for its tokens t in order, with slot s = state_batch_indices[b],
+ *
+ *     dtv = softplus(dt[t,h] + dt_bias[h]);   dA = exp(dtv * A[h])
+ *     S[p,n] = S[p,n] * dA + (dtv * x[t,h,p]) * B[t,g,n]
+ *     out[t,h,p] = bf16_rne( sum_n S[p,n] * C[t,g,n] + D[h] * x[t,h,p] )
+ *
+ * from S = state_pool[s,h] (S = 0 where fresh[b] != 0: the slot is then not read) and with
+ * state_pool[s,h] = S after the last token.  ssu_update continues such a slot token by token.
+ *
+ * cu_tokens holds batch + 1 offsets of the type shape->index_dtype, device memory, contiguous.
+ * Tokens outside every prompt are neither read nor written.  A prompt without tokens leaves its
+ * slot as it is (zeros if fresh).  A prompt is skipped and counted (ssu_get_error) if its slot
+ * is out of range or if its offsets are not 0 <= cu_tokens[b] <= cu_tokens[b + 1] <= tokens.
+ * Slots must be distinct and prompts must not overlap, as for ssu_update.
+ *
+ * shape->batch is the number of prompts; strides->x[0], out[0], dt[0], B[0] and C[0] are the
+ * strides of the token index; `tokens` (up to 2^31 - 1) is the number of token rows.
+ * `fresh` is a device array of batch bytes, or NULL (every prompt continues from its slot).
+ * `workspace` is a caller-owned device buffer, 256-byte aligned, of at least
+ * ssu_prompts_workspace_bytes bytes (which may be 0: NULL is then accepted); it must not be in
+ * use by other work until the stream has passed the call, and needs no initial contents.
+ * Enqueued on `stream`; allocates and synchronises nothing.
+ */
+ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
+                                         int64_t tokens, int64_t *bytes);
+ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
+                                const void *state_batch_indices, const void *cu_tokens,
+                                const uint8_t *fresh, const uint16_t *x, const uint16_t *dt,
+                                const float *dt_bias, const float *A, const uint16_t *B,
+                                const uint16_t *C, const float *D, uint16_t *out,
+                                const ssu_shape_t *shape, const ssu_strides_t *strides,
+                                int64_t tokens, void *workspace, int64_t workspace_bytes,
+                                ssu_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention layers of a hybrid model.  Keys and values live in pages: k_pages and v_pages are
+ * bf16 [num_pages, page_size, kv_heads, headdim]; position j of a request whose page-table row
+ * is r lies in page r[j / page_size] at row j % page_size.
+ */
+
+/* Sizes of one ssu_rotate_qk call. */
+typedef struct {
+    int64_t tokens;      /* 0 is valid and enqueues nothing */
+    int64_t q_heads;     /* >= 1 */
+    int64_t kv_heads;    /* >= 1 */
+    int64_t headdim;     /* 64, 128 or 256 */
+    int64_t rotary;      /* leading elements of a head that are rotated: a multiple of 16,
+                            0 (norm alone; the table is then not read) .. headdim */
+    int64_t num_positions; /* rows of the rotation table */
+    int64_t num_pages, page_size;
+    int32_t index_dtype; /* ssu_index_dtype_t of positions and slots */
+    int32_t interleaved; /* 0: element i turns with i + rotary / 2; 1: 2i turns with 2i + 1 */
+} ssu_rotate_shape_t;
+
+/* Element strides, outermost dimension first; the headdim strides are 1. */
+typedef struct {
+    int64_t q[2], k[2], v[2], q_out[2]; /* token, head: multiples of 8 */
+    int64_t k_pages[3], v_pages[3];     /* page, row, head: multiples of 8 */
+    int64_t table;                      /* table row: a multiple of 4 */
+    int64_t positions, slots;
+} ssu_rotate_strides_t;
+
+/*
+ * Norm and rotation of queries and keys, and their way into the cache, in one pass.  For every
+ * token t and every head of q and k, in fp32 and rounded once:
+ *
+ *     u[i] = a[i] / sqrt(mean_j a[j]^2 + eps) * weight[i]
+ *     (u[i], u[j]) <- (u[i] cos_m - u[j] sin_m, u[j] cos_m + u[i] sin_m)   m = 0 .. rotary/2 - 1
+ *
+ * with (i, j) = (m, m + rotary / 2), or (2m, 2m + 1) if interleaved, and cos_m = table[pos][m],
+ * sin_m = table[pos][rotary / 2 + m], pos = positions[t] (table fp32 [num_positions, rotary]).
+ * Queries go to q_out; keys, and v as it is, to row slots[t] % page_size of page
+ * slots[t] / page_size.  A token with slots[t] = -1 has its queries written and its key and
+ * value left out of the cache.  A token whose position lies outside the table, or whose slot is
+ * neither -1 nor inside the cache, is skipped (nothing of it is written) and counted
+ * (ssu_get_error).  Slots must be distinct.  q, k, v, q_out, k_pages, v_pages, q_weight,
+ * k_weight [headdim] fp32 and table are 16-byte aligned.  q_out may be q itself (same strides).
+ * Enqueued on `stream`; allocates and synchronises nothing.
+ */
+ssu_status_t ssu_rotate_qk(ssu_handle_t handle, const uint16_t *q, const uint16_t *k,
+                           const uint16_t *v, const float *q_weight, const float *k_weight,
+                           const float *table, const void *positions, uint16_t *q_out,
+                           uint16_t *k_pages, uint16_t *v_pages, const void *slots,
+                           const ssu_rotate_shape_t *shape, const ssu_rotate_strides_t *strides,
+                           float eps, ssu_stream_t stream);
+
+/* Sizes of one ssu_attend call. */
+typedef struct {
+    int64_t requests;    /* 0 is valid and enqueues nothing */
+    int64_t q_heads;     /* a multiple of kv_heads; query head h reads key head
+                            h / (q_heads / kv_heads) */
+    int64_t kv_heads;    /* >= 1 */
+    int64_t headdim;     /* 64, 128 or 256 */
+    int64_t num_pages;   /* valid page ids are [0, num_pages) */
+    int64_t page_size;   /* >= 1 */
+    int64_t max_pages;   /* columns of page_table */
+    int32_t index_dtype; /* ssu_index_dtype_t of page_table and lengths */
+    int32_t reserved;    /* write 0 */
+} ssu_attend_shape_t;
+
+/* Element strides, outermost dimension first; the headdim strides are 1. */
+typedef struct {
+    int64_t q[2], out[2];           /* request, head: multiples of 8 */
+    int64_t k_pages[3], v_pages[3]; /* page, row, head: multiples of 8 */
+    int64_t page_table[2];          /* request, page */
+    int64_t lengths;
+} ssu_attend_strides_t;
+
+/*
+ * Attention of one new token per request over its cached keys (the token's own key among them):
+ *
+ *     out[b,h] = bf16_rne( sum_j p_j v_j ),   p = softmax over visible j of scale * q[b,h] . k_j
+ *
+ * Positions 0 .. lengths[b] - 1 are visible; with window > 0 only those with
+ * j >= lengths[b] - window or j < sinks.  A request of length 0 gets zeros.  A request whose
+ * length is negative or above max_pages * page_size is skipped (its out rows are not touched)
+ * and counted (ssu_get_error).  A visible page whose id lies outside [0, num_pages) is left out
+ * of the sums and its request counted, once for each such page.  Scores, softmax statistics and
+ * sums are fp32; the weights p are rounded to bf16 for the product with v.
+ *
+ * q, k_pages, v_pages and out are 16-byte aligned.  `workspace` is a caller-owned device buffer,
+ * 256-byte aligned, of at least ssu_attend_workspace_bytes bytes, filled with zeros before its
+ * first use; every call leaves it so that the next can use it, and calls that share one must
+ * not overlap.  Enqueued on `stream`; allocates and synchronises nothing.
+ */
+ssu_status_t ssu_attend_workspace_bytes(ssu_handle_t handle, const ssu_attend_shape_t *shape,
+                                        int64_t *bytes);
+ssu_status_t ssu_attend(ssu_handle_t handle, const uint16_t *q, const uint16_t *k_pages,
+                        const uint16_t *v_pages, const void *page_table, const void *lengths,
+                        uint16_t *out, const ssu_attend_shape_t *shape,
+                        const ssu_attend_strides_t *strides, float scale, int64_t window,
+                        int64_t sinks, void *workspace, int64_t workspace_bytes,
+                        ssu_stream_t stream);
+
 /*
  * Allocation-free variant of ssu_update.  No counterpart exists in the paper: it serves
  * callers that cannot call cudaMalloc, such as code running under an allocator that must not

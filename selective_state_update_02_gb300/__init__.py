@@ -82,6 +82,30 @@ SSU_COPY_VEC = 1
 SSU_COPY_MAX_TENSORS = 64
 
 
+class ssu_rotate_shape_t(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("q_heads", _i64), ("kv_heads", _i64), ("headdim", _i64),
+                ("rotary", _i64), ("num_positions", _i64), ("num_pages", _i64),
+                ("page_size", _i64), ("index_dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class ssu_rotate_strides_t(ctypes.Structure):
+    _fields_ = [("q", _i64 * 2), ("k", _i64 * 2), ("v", _i64 * 2), ("q_out", _i64 * 2),
+                ("k_pages", _i64 * 3), ("v_pages", _i64 * 3), ("table", _i64),
+                ("positions", _i64), ("slots", _i64)]
+
+
+class ssu_attend_shape_t(ctypes.Structure):
+    _fields_ = [("requests", _i64), ("q_heads", _i64), ("kv_heads", _i64), ("headdim", _i64),
+                ("num_pages", _i64), ("page_size", _i64), ("max_pages", _i64),
+                ("index_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ssu_attend_strides_t(ctypes.Structure):
+    _fields_ = [("q", _i64 * 2), ("out", _i64 * 2), ("k_pages", _i64 * 3),
+                ("v_pages", _i64 * 3), ("page_table", _i64 * 2), ("lengths", _i64)]
+
+
 class SsuError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status
@@ -113,6 +137,11 @@ _EXPORTS = {
                                                       ctypes.POINTER(ssu_strides_t),
                                                       ctypes.c_int64,
                                                       ctypes.POINTER(ssu_token_strides_t), _vp]),
+    "ssu_prompts_workspace_bytes": (ctypes.c_int, [_vp, _vp, _i64, ctypes.POINTER(_i64)]),
+    "ssu_update_prompts": (ctypes.c_int, [_vp] * 15 + [_i64, _vp, _i64, _vp]),
+    "ssu_rotate_qk": (ctypes.c_int, [_vp] * 14 + [ctypes.c_float, _vp]),
+    "ssu_attend_workspace_bytes": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_i64)]),
+    "ssu_attend": (ctypes.c_int, [_vp] * 9 + [ctypes.c_float, _i64, _i64, _vp, _i64, _vp]),
     "ssu_copy_blocks": (ctypes.c_int, [_vp, ctypes.POINTER(ssu_block_tensor_t), ctypes.c_int32,
                                        _vp, _vp, ctypes.c_int64, ctypes.c_int32, _vp]),
     "ssu_copy_set_launch": (ctypes.c_int, [_vp, ctypes.POINTER(ssu_copy_launch_t)]),
@@ -442,6 +471,202 @@ def ssu_update_tokens(handle: int, state_pool, state_batch_indices, x, dt, dt_bi
                                    ctypes.byref(ts), _stream_ptr(stream)), "ssu_update_tokens")
 
 
+# ---- prompts and attention ---------------------------------------------------------------
+#
+# These calls sit in a serving loop beside the decode step and are often shorter on the device
+# than a Python call, so their marshalling fills the ABI structs from one flat list each.
+
+_INDEX_TYPE = {torch.int32: SSU_INDEX_I32, torch.int64: SSU_INDEX_I64}
+_STRIDES_WORDS = ctypes.sizeof(ssu_strides_t) // 8
+
+
+def _index_type(name: str, *tensors) -> int:
+    kind = _INDEX_TYPE.get(tensors[0].dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be int32 or int64")
+    for t in tensors[1:]:
+        if t.dtype != tensors[0].dtype:
+            raise TypeError(f"{name} must all be {tensors[0].dtype}, got {t.dtype}")
+    return kind
+
+
+def _on_one_gpu(*tensors) -> None:
+    """Every tensor lies on the same CUDA device."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("every operand must be a CUDA tensor of one device, got "
+                             + ", ".join(sorted({str(u.device) for u in tensors})))
+
+
+def _typed(dtype, ndim: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t.dtype != dtype or t.dim() != ndim:
+            raise TypeError(f"{name} must be a {ndim}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
+
+
+def _workspace(workspace) -> tuple[int | None, int]:
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous() or workspace.get_device() < 0:
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D,
+                     out):
+    """Build ``(ssu_shape_t, ssu_strides_t)`` of a prompt call (no data is touched)."""
+    if state_pool.dim() != 4 or state_pool.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("state_pool must be a 4-D float32 or bfloat16 tensor")
+    if state_batch_indices.dim() != 1 or cu_tokens.dim() != 1:
+        raise TypeError("state_batch_indices and cu_tokens must be 1-D")
+    kind = _index_type("state_batch_indices and cu_tokens", state_batch_indices, cu_tokens)
+    _typed(torch.bfloat16, 3, x=x, out=out, B=B, C=C)
+    if dt.dtype != torch.bfloat16 or dt.dim() not in (2, 3):
+        raise TypeError("dt must be a 2-D or 3-D bfloat16 tensor")
+    _expect(dt_bias, "dt_bias", torch.float32, (1, 2))
+    _expect(D, "D", torch.float32, (1, 2))
+    _expect(A, "A", torch.float32, (1, 3))
+    pool, H, P, N = state_pool.shape
+    bs, T, G = state_batch_indices.shape[0], x.shape[0], B.shape[1]
+    if x.shape[1:] != (H, P) or out.shape != x.shape:
+        raise ValueError(f"x and out must be [tokens, H, P] = {(T, H, P)}")
+    if B.shape != (T, G, N) or C.shape != B.shape:
+        raise ValueError(f"B and C must be [tokens, G, N] = {(T, G, N)}")
+    if dt.shape[:2] != (T, H) or (dt.dim() == 3 and dt.shape[2] != P):
+        raise ValueError("dt must be [tokens, H] or [tokens, H, P]")
+    if cu_tokens.shape[0] != bs + 1 or cu_tokens.stride(0) != 1:
+        raise ValueError(f"cu_tokens must be contiguous with {bs + 1} entries")
+    shape = ssu_shape_t(bs, H, P, N, G, pool, kind,
+                        SSU_STATE_BF16 if state_pool.dtype == torch.bfloat16 else SSU_STATE_F32)
+    dt_s, dims = dt.stride(), (H, P, N)
+    strides = (_i64 * _STRIDES_WORDS)(
+        *state_pool.stride(), *x.stride(), *out.stride(), *(dt_s if len(dt_s) == 3 else (*dt_s, 0)),
+        *B.stride(), *C.stride(), *_broadcast_strides(dt_bias, "dt_bias", dims, 2),
+        *_broadcast_strides(D, "D", dims, 2), *_broadcast_strides(A, "A", dims, 3),
+        state_batch_indices.stride(0))
+    return shape, strides
+
+
+def ssu_prompts_workspace_bytes(handle: int, state_pool, x, B, state_batch_indices) -> int:
+    """Device workspace bytes ``ssu_update_prompts`` needs for these operands' sizes."""
+    pool, H, P, N = state_pool.shape
+    shape = ssu_shape_t(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
+                        SSU_STATE_BF16 if state_pool.dtype == torch.bfloat16 else SSU_STATE_F32)
+    n = _i64()
+    _check(lib().ssu_prompts_workspace_bytes(handle, ctypes.byref(shape), x.shape[0],
+                                             ctypes.byref(n)), "ssu_prompts_workspace_bytes")
+    return int(n.value)
+
+
+def ssu_update_prompts(handle: int, state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias,
+                       A, B, C, D, out, workspace=None, fresh=None, stream=None) -> None:
+    """Whole prompts, packed: prompt ``b`` is rows ``cu_tokens[b]:cu_tokens[b + 1]`` of ``x``,
+    ``out`` ``[tokens, H, P]``, ``dt`` ``[tokens, H]``, ``B`` and ``C`` ``[tokens, G, N]``.  It
+    continues slot ``state_batch_indices[b]``, or starts from zero where ``fresh[b]`` (uint8 or
+    bool) is set, and leaves its last state there.  ``cu_tokens`` and ``state_batch_indices``
+    have one type; ``workspace`` is a device uint8 tensor of ``ssu_prompts_workspace_bytes``."""
+    shape, strides = describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias,
+                                      A, B, C, D, out)
+    tensors = (state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D, out)
+    _on_one_gpu(*tensors)
+    if fresh is not None:
+        if fresh.dtype not in (torch.uint8, torch.bool) or fresh.shape != (shape.batch,) or \
+                not fresh.is_contiguous() or fresh.get_device() != state_pool.get_device():
+            raise ValueError("fresh must be a contiguous uint8 or bool CUDA tensor with one entry "
+                             "per prompt")
+        fresh = fresh.data_ptr()
+    ws, nbytes = _workspace(workspace)
+    p = [t.data_ptr() for t in tensors]
+    _check(lib().ssu_update_prompts(handle, *p[:3], fresh, *p[3:], ctypes.byref(shape), strides,
+                                    x.shape[0], ws, nbytes, _stream_ptr(stream)),
+           "ssu_update_prompts")
+
+
+def ssu_rotate_qk(handle: int, q, k, v, q_weight, k_weight, table, positions, q_out, k_pages,
+                  v_pages, slots, eps: float = 1e-6, interleaved: bool = False,
+                  stream=None) -> None:
+    """RMS norm of every head of ``q`` ``[tokens, Hq, D]`` and ``k`` ``[tokens, Hk, D]``
+    (weights fp32 ``[D]``), rotation by ``table[positions[t]]`` (fp32 ``[places, rotary]``:
+    cosines, then sines), queries to ``q_out``, keys and ``v`` to row ``slots[t]`` of the pages
+    ``[pages, page_size, Hk, D]`` (-1: not stored)."""
+    _typed(torch.bfloat16, 3, q=q, k=k, v=v, q_out=q_out)
+    _typed(torch.bfloat16, 4, k_pages=k_pages, v_pages=v_pages)
+    _typed(torch.float32, 1, q_weight=q_weight, k_weight=k_weight)
+    _typed(torch.float32, 2, table=table)
+    if positions.dim() != 1 or slots.dim() != 1:
+        raise TypeError("positions and slots must be 1-D")
+    kind = _index_type("positions and slots", positions, slots)
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    if q_out.shape != q.shape or k.shape != (T, Hk, D) or v.shape != k.shape:
+        raise ValueError(f"q and q_out must be {(T, Hq, D)}, k and v {(T, Hk, D)}")
+    if k_pages.shape[2:] != (Hk, D) or v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, {Hk}, {D}]")
+    if q_weight.shape != (D,) or k_weight.shape != (D,):
+        raise ValueError(f"q_weight and k_weight must have {D} elements")
+    if positions.shape[0] != T or slots.shape[0] != T:
+        raise ValueError("positions and slots must have one entry per token")
+    tensors = (q, k, v, q_weight, k_weight, table, positions, q_out, k_pages, v_pages, slots)
+    _on_one_gpu(*tensors)
+    st = [t.stride() for t in tensors]
+    if any(s[-1] != 1 for s in (*st[:6], *st[7:10])):
+        raise ValueError("the last dimension of every operand must have stride 1")
+    shape = ssu_rotate_shape_t(T, Hq, Hk, D, table.shape[1], table.shape[0], k_pages.shape[0],
+                               k_pages.shape[1], kind, 1 if interleaved else 0)
+    strides = (_i64 * 17)(*st[0][:2], *st[1][:2], *st[2][:2], *st[7][:2], *st[8][:3], *st[9][:3],
+                          st[5][0], st[6][0], st[10][0])
+    _check(lib().ssu_rotate_qk(handle, *[t.data_ptr() for t in tensors], ctypes.byref(shape),
+                               strides, eps, _stream_ptr(stream)), "ssu_rotate_qk")
+
+
+def _attend_shape(q, k_pages, max_pages: int, kind: int) -> ssu_attend_shape_t:
+    return ssu_attend_shape_t(q.shape[0], q.shape[1], k_pages.shape[2], q.shape[2],
+                              k_pages.shape[0], k_pages.shape[1], max_pages, kind, 0)
+
+
+def ssu_attend_workspace_bytes(handle: int, q, k_pages) -> int:
+    """Device workspace bytes ``ssu_attend`` needs for these operands' sizes (fill it with zeros
+    once)."""
+    shape = _attend_shape(q, k_pages, 0, SSU_INDEX_I32)
+    n = _i64()
+    _check(lib().ssu_attend_workspace_bytes(handle, ctypes.byref(shape), ctypes.byref(n)),
+           "ssu_attend_workspace_bytes")
+    return int(n.value)
+
+
+def ssu_attend(handle: int, q, k_pages, v_pages, page_table, lengths, out, workspace=None,
+               scale: float | None = None, window: int = 0, sinks: int = 0, stream=None) -> None:
+    """One new token per request: ``q`` and ``out`` ``[requests, Hq, D]``, the cache in pages
+    ``[pages, page_size, Hk, D]`` named by ``page_table`` ``[requests, max_pages]``, of which
+    the first ``lengths[b]`` positions are visible (with ``window``: its last ``window`` and the
+    first ``sinks``).  ``scale`` defaults to ``D ** -0.5``.  ``workspace`` is a device tensor of
+    ``ssu_attend_workspace_bytes``, zero before its first use, not shared by overlapping calls."""
+    _typed(torch.bfloat16, 3, q=q, out=out)
+    _typed(torch.bfloat16, 4, k_pages=k_pages, v_pages=v_pages)
+    if page_table.dim() != 2 or lengths.dim() != 1:
+        raise TypeError("page_table must be 2-D and lengths 1-D")
+    kind = _index_type("page_table and lengths", page_table, lengths)
+    bs, _, D = q.shape
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if k_pages.shape[3] != D or v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, Hk, {D}]")
+    if page_table.shape[0] != bs or lengths.shape[0] != bs:
+        raise ValueError("page_table and lengths must have one row per request")
+    tensors = (q, k_pages, v_pages, page_table, lengths, out)
+    _on_one_gpu(*tensors)
+    st = [t.stride() for t in tensors]
+    if st[0][2] != 1 or st[1][3] != 1 or st[2][3] != 1 or st[5][2] != 1:
+        raise ValueError("the last dimension of q, out and the pages must have stride 1")
+    shape = _attend_shape(q, k_pages, page_table.shape[1], kind)
+    strides = (_i64 * 13)(*st[0][:2], *st[5][:2], *st[1][:3], *st[2][:3], *st[3], *st[4])
+    ws, nbytes = _workspace(workspace)
+    _check(lib().ssu_attend(handle, *[t.data_ptr() for t in tensors], ctypes.byref(shape),
+                            strides, D ** -0.5 if scale is None else scale, window, sinks, ws,
+                            nbytes, _stream_ptr(stream)), "ssu_attend")
+
+
 def describe_blocks(tensors) -> tuple[ctypes.Array, int]:
     """ABI descriptors for state tensors laid out as ``[num_blocks, ...]``: block k is the
     slice ``t[k]``, which must be contiguous (its bytes are copied verbatim)."""
@@ -498,6 +723,30 @@ class SelectiveStateUpdate:
                intermediate=None, stream=None):
         ssu_update_tokens(self.handle, state_pool, state_batch_indices, x, dt, dt_bias, A, B, C,
                           D, out, intermediate, stream)
+        return out
+
+    def prompts_workspace_bytes(self, state_pool, x, B, state_batch_indices) -> int:
+        return ssu_prompts_workspace_bytes(self.handle, state_pool, x, B, state_batch_indices)
+
+    def prompts(self, state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D,
+                out, workspace=None, fresh=None, stream=None):
+        ssu_update_prompts(self.handle, state_pool, state_batch_indices, cu_tokens, x, dt,
+                           dt_bias, A, B, C, D, out, workspace, fresh, stream)
+        return out
+
+    def rotate_qk(self, q, k, v, q_weight, k_weight, table, positions, q_out, k_pages, v_pages,
+                  slots, eps=1e-6, interleaved=False, stream=None):
+        ssu_rotate_qk(self.handle, q, k, v, q_weight, k_weight, table, positions, q_out, k_pages,
+                      v_pages, slots, eps, interleaved, stream)
+        return q_out
+
+    def attend_workspace_bytes(self, q, k_pages) -> int:
+        return ssu_attend_workspace_bytes(self.handle, q, k_pages)
+
+    def attend(self, q, k_pages, v_pages, page_table, lengths, out, workspace=None, scale=None,
+               window=0, sinks=0, stream=None):
+        ssu_attend(self.handle, q, k_pages, v_pages, page_table, lengths, out, workspace, scale,
+                   window, sinks, stream)
         return out
 
     def copy_blocks(self, tensors, src_idx, dst_idx, stream=None):

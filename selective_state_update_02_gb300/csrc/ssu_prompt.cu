@@ -1,0 +1,156 @@
+// Prompts: the C entry points ssu_prompts_workspace_bytes and ssu_update_prompts (validation,
+// choice of form) and the kernels' instantiations.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "ssu.h"
+#include "ssu_host.h"
+#include "ssu_prompt.cuh"
+
+using ssu_host::aligned;
+using ssu_host::DeviceGuard;
+using ssu_host::fail;
+using ssu_host::ok;
+using ssu_host::validate_impl;
+
+namespace {
+
+constexpr int kSeqSlots = 4, kSeqWarps = 4;
+
+template <int N, typename ST>
+cudaError_t launch_seq(PromptParams q, bool i64, bool pdl, cudaStream_t st) {
+    constexpr int kRows = kSeqSlots * RowGeo<N, ST>::RPI;
+    int warps = kSeqWarps;
+    while (warps > 1 && kRows * (warps / 2) >= q.p.headdim) warps >>= 1;
+    q.p.rows_per_cta = kRows * warps;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((q.p.headdim + kRows * warps - 1) / (kRows * warps)),
+                       static_cast<unsigned>(q.p.nheads),
+                       static_cast<unsigned>(q.p.batch < 65535 ? q.p.batch : 65535));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return i64 ? cudaLaunchKernelEx(&cfg, ssu_prompt_seq_kernel<kSeqSlots, N, ST, true>, q)
+               : cudaLaunchKernelEx(&cfg, ssu_prompt_seq_kernel<kSeqSlots, N, ST, false>, q);
+}
+
+cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, bool pdl,
+                       cudaStream_t st) {
+    if (dstate == 64)
+        return bf16 ? launch_seq<64, __nv_bfloat16>(q, i64, pdl, st)
+                    : launch_seq<64, float>(q, i64, pdl, st);
+    if (dstate == 128)
+        return bf16 ? launch_seq<128, __nv_bfloat16>(q, i64, pdl, st)
+                    : launch_seq<128, float>(q, i64, pdl, st);
+    return bf16 ? launch_seq<256, __nv_bfloat16>(q, i64, pdl, st)
+                : launch_seq<256, float>(q, i64, pdl, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
+                                         int64_t tokens, int64_t *bytes) {
+    if (!handle || !shape || !bytes) return fail(SSU_ERR_INVALID_ARG, "NULL argument");
+    if (shape->batch < 0 || shape->nheads < 1 || shape->headdim < 1 || shape->dstate < 1)
+        return fail(SSU_ERR_INVALID_ARG, "batch must be >= 0 and every dimension >= 1");
+    if (tokens < 0) return fail(SSU_ERR_INVALID_ARG, "tokens %lld < 0", (long long)tokens);
+    *bytes = 0;
+    return ok();
+}
+
+ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
+                                const void *state_batch_indices, const void *cu_tokens,
+                                const uint8_t *fresh, const uint16_t *x, const uint16_t *dt,
+                                const float *dt_bias, const float *A, const uint16_t *B,
+                                const uint16_t *C, const float *D, uint16_t *out,
+                                const ssu_shape_t *shape, const ssu_strides_t *strides,
+                                int64_t tokens, void *workspace, int64_t workspace_bytes,
+                                ssu_stream_t stream) {
+    if (!handle) return fail(SSU_ERR_INVALID_ARG, "NULL handle");
+    if (tokens < 0 || tokens > INT_MAX)
+        return fail(SSU_ERR_INVALID_ARG, "tokens %lld outside 0..2^31 - 1", (long long)tokens);
+    if (tokens == 0) {  // no token row is read: the operands may be empty arrays
+        static const uint16_t none[2] = {};
+        x = dt = B = C = none;
+        out = const_cast<uint16_t *>(none);
+    }
+    ssu_status_t st = validate_impl(state_pool, state_batch_indices, x, dt, dt_bias, A, B, C, D,
+                                    out, shape, strides);
+    if (st != SSU_OK || shape->batch == 0) return st;
+    const ssu_shape_t &s = *shape;
+    if (!cu_tokens) return fail(SSU_ERR_INVALID_ARG, "cu_tokens is NULL");
+    if (!aligned(cu_tokens, s.index_dtype == SSU_INDEX_I64 ? 8 : 4))
+        return fail(SSU_ERR_MISALIGNED, "cu_tokens is not aligned to its type");
+    int64_t need = 0;
+    st = ssu_prompts_workspace_bytes(handle, shape, tokens, &need);
+    if (st != SSU_OK) return st;
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(SSU_ERR_INVALID_ARG, "workspace holds %lld bytes; this shape needs %lld",
+                    (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    if (need && !aligned(workspace, 256))
+        return fail(SSU_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+
+    PromptParams q{};
+    SsuParams &p = q.p;
+    p.state = state_pool;
+    p.idx = state_batch_indices;
+    p.x = reinterpret_cast<const __nv_bfloat16 *>(x);
+    p.dt = reinterpret_cast<const __nv_bfloat16 *>(dt);
+    p.dt_bias = dt_bias;
+    p.A = A;
+    p.B = reinterpret_cast<const __nv_bfloat16 *>(B);
+    p.C = reinterpret_cast<const __nv_bfloat16 *>(C);
+    p.D = D;
+    p.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p.st_pool = strides->state[0];
+    p.st_head = strides->state[1];
+    p.st_row = strides->state[2];
+    p.x_b = strides->x[0];
+    p.x_h = strides->x[1];
+    p.out_b = strides->out[0];
+    p.out_h = strides->out[1];
+    p.dt_b = strides->dt[0];
+    p.dt_h = strides->dt[1];
+    p.B_b = strides->B[0];
+    p.B_g = strides->B[1];
+    p.C_b = strides->C[0];
+    p.C_g = strides->C[1];
+    p.bias_h = strides->dt_bias[0];
+    p.D_h = strides->D[0];
+    p.A_h = strides->A[0];
+    p.idx_s = strides->idx;
+    p.pool_size = s.pool_size;
+    p.batch = s.batch;
+    p.nheads = static_cast<int>(s.nheads);
+    p.headdim = static_cast<int>(s.headdim);
+    p.heads_per_group = static_cast<int>(s.nheads / s.ngroups);
+    p.group_magic = group_magic(static_cast<unsigned>(p.heads_per_group));
+    p.err = handle->err;
+    q.cu = cu_tokens;
+    q.fresh = fresh;
+    q.tokens = tokens;
+    const int epv = s.state_dtype == SSU_STATE_BF16 ? 8 : 4;
+    q.bc_vec = aligned(B, 2 * epv) && p.B_b % epv == 0 && p.B_g % epv == 0 &&
+               aligned(C, 2 * epv) && p.C_b % epv == 0 && p.C_g % epv == 0;
+
+    DeviceGuard guard(handle->device);
+    if (guard.err != cudaSuccess)
+        return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
+    const cudaError_t e = launch_seq(q, static_cast<int>(s.dstate), bf16, i64, handle->pdl, cs);
+    if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"
