@@ -1,5 +1,5 @@
-// Attention of one new token per request over a paged cache (ssu_attend): the C entry points and
-// the kernel.
+// Attention of one new token per request over a paged cache: the C entry points
+// ssu_attend_workspace_bytes and ssu_attend; the kernel is in ssu_attend.cuh.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -8,7 +8,7 @@
 #include <cstdint>
 
 #include "ssu.h"
-#include "ssu_device.cuh"
+#include "ssu_attend.cuh"
 #include "ssu_host.h"
 
 using ssu_host::aligned;
@@ -18,103 +18,37 @@ using ssu_host::ok;
 
 namespace {
 
-struct AttendParams {
-    const __nv_bfloat16 *q, *k, *v;
-    const void *table, *lengths;
-    __nv_bfloat16 *out;
-    long long q_b, q_h, o_b, o_h;
-    long long k_p, k_r, k_h, v_p, v_r, v_h;
-    long long t_b, t_p, len_s;
-    long long requests, num_pages, page_size, max_keys;
-    long long window, sinks;
-    int q_heads, kv_heads, share;  // share: query heads per key head
-    float scale;
-    unsigned *err;
+// Workspace: the counters, then two parts per CTA.
+struct AttendLayout {
+    long long parts, total;
 };
 
-template <bool kIdx64>
-__device__ __forceinline__ long long load_index(const void *ids, long long at) {
-    if (kIdx64) return __ldg(static_cast<const long long *>(ids) + at);
-    return static_cast<long long>(__ldg(static_cast<const int *>(ids) + at));
-}
-
-// One warp per (request, query head), one key after the other: each lane holds D / 32 elements
-// of the head.  Bound by the chain of one key after the other.
-template <int D, bool kIdx64>
-__global__ void __launch_bounds__(128) ssu_attend_kernel(AttendParams p) {
-    pdl_wait();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (h >= p.q_heads) return;
-    const int kh = h / p.share;
-    for (long long b = blockIdx.y; b < p.requests; b += gridDim.y) {
-        const long long n = load_index<kIdx64>(p.lengths, b * p.len_s);
-        if (n < 0 || n > p.max_keys) {
-            if (h == 0 && lane == 0) {
-                atomicAdd(&p.err[0], 1u);
-                atomicMin(&p.err[1], static_cast<unsigned>(b));
-            }
-            continue;
-        }
-        float q[E], o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[e] = __bfloat162float(p.q[b * p.q_b + h * p.q_h + e * 32 + lane]) * p.scale;
-            o[e] = 0.0f;
-        }
-        float m = -INFINITY, l = 0.0f;
-        for (long long j = 0; j < n; ++j) {
-            if (p.window && j < n - p.window && j >= p.sinks) continue;
-            const long long col = j / p.page_size, r = j - col * p.page_size;
-            const long long page = load_index<kIdx64>(p.table, b * p.t_b + col * p.t_p);
-            if (page < 0 || page >= p.num_pages) {
-                const long long lo = p.window && n - p.window > col * p.page_size &&
-                                             p.sinks <= col * p.page_size
-                                         ? n - p.window
-                                         : col * p.page_size;
-                if (h == 0 && lane == 0 && j == lo) {
-                    atomicAdd(&p.err[0], 1u);
-                    atomicMin(&p.err[1], static_cast<unsigned>(b));
-                }
-                continue;
-            }
-            const __nv_bfloat16 *k = p.k + page * p.k_p + r * p.k_r + kh * p.k_h + lane;
-            const __nv_bfloat16 *v = p.v + page * p.v_p + r * p.v_r + kh * p.v_h + lane;
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(k[e * 32]), s);
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            const float top = fmaxf(m, s);
-            const float keep = m == -INFINITY ? 0.0f : expf(m - top);
-            const float w = top == -INFINITY ? 0.0f : expf(s - top);
-            l = l * keep + w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(w, __bfloat162float(v[e * 32]), o[e] * keep);
-            m = top;
-        }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            p.out[b * p.o_b + h * p.o_h + e * 32 + lane] = __float2bfloat16(o[e] * inv);
-    }
+AttendLayout attend_layout(int ctas, int64_t headdim) {
+    AttendLayout w;
+    w.parts = (ctas * 4ll + 255) / 256 * 256;
+    w.total = w.parts + 2ll * ctas * (kAttendRows * headdim + 2 * kAttendRows) * 4;
+    return w;
 }
 
 template <int D>
-cudaError_t launch_attend(const AttendParams &p, bool i64, bool pdl, cudaStream_t st) {
+cudaError_t launch_attend(const AttendParams &p, ssu_handle_s &handle, bool i64,
+                          cudaStream_t st) {
+    using Geo = AttendGeo<D>;
+    auto *kernel = i64 ? ssu_attend_kernel<D, true> : ssu_attend_kernel<D, false>;
+    cudaError_t e = ssu_host::allow_smem(handle, reinterpret_cast<const void *>(kernel),
+                                         Geo::kSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.q_heads + 3) / 4),
-                       static_cast<unsigned>(p.requests < 65535 ? p.requests : 65535));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(handle.sm_count));
+    cfg.blockDim = dim3(32 * Geo::kWarps);
+    cfg.dynamicSmemBytes = Geo::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return i64 ? cudaLaunchKernelEx(&cfg, ssu_attend_kernel<D, true>, p)
-               : cudaLaunchKernelEx(&cfg, ssu_attend_kernel<D, false>, p);
+    cfg.numAttrs = handle.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 ssu_status_t validate_shape(const ssu_attend_shape_t &s) {
@@ -134,7 +68,8 @@ ssu_status_t validate_shape(const ssu_attend_shape_t &s) {
         return fail(SSU_ERR_UNSUPPORTED, "q_heads is limited to 65535");
     if (s.requests > INT_MAX / s.q_heads)
         return fail(SSU_ERR_UNSUPPORTED, "requests * q_heads exceeds 2^31");
-    if (s.max_pages > 0 && s.page_size > INT_MAX / s.max_pages)
+    if (s.num_pages > INT_MAX) return fail(SSU_ERR_UNSUPPORTED, "num_pages exceeds 2^31");
+    if (s.max_pages > 0 && s.page_size > (INT_MAX - 4096) / s.max_pages)
         return fail(SSU_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^31");
     return SSU_OK;
 }
@@ -148,7 +83,7 @@ ssu_status_t ssu_attend_workspace_bytes(ssu_handle_t handle, const ssu_attend_sh
     if (!handle || !shape || !bytes) return fail(SSU_ERR_INVALID_ARG, "NULL argument");
     const ssu_status_t st = validate_shape(*shape);
     if (st != SSU_OK) return st;
-    *bytes = 0;
+    *bytes = attend_layout(handle->sm_count, shape->headdim).total;
     return ok();
 }
 
@@ -205,22 +140,27 @@ ssu_status_t ssu_attend(ssu_handle_t handle, const uint16_t *q, const uint16_t *
     p.k_p = u.k_pages[0], p.k_r = u.k_pages[1], p.k_h = u.k_pages[2];
     p.v_p = u.v_pages[0], p.v_r = u.v_pages[1], p.v_h = u.v_pages[2];
     p.t_b = u.page_table[0], p.t_p = u.page_table[1], p.len_s = u.lengths;
-    p.requests = s.requests, p.num_pages = s.num_pages, p.page_size = s.page_size;
+    p.requests = s.requests, p.num_pages = s.num_pages;
+    p.page_size = static_cast<int>(s.page_size < INT_MAX ? s.page_size : INT_MAX);
     p.max_keys = s.max_pages * s.page_size;
     p.window = window, p.sinks = sinks;
     p.q_heads = static_cast<int>(s.q_heads), p.kv_heads = static_cast<int>(s.kv_heads);
     p.share = static_cast<int>(s.q_heads / s.kv_heads);
-    p.scale = scale;
+    p.head_tiles = (p.share + kAttendRows - 1) / kAttendRows;
+    p.scale_log2 = scale * 1.4426950408889634f;
     p.err = handle->err;
+    p.arrived = static_cast<unsigned *>(workspace);
+    p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                        attend_layout(handle->sm_count, s.headdim).parts);
 
     DeviceGuard guard(handle->device);
     if (guard.err != cudaSuccess)
         return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool i64 = s.index_dtype == SSU_INDEX_I64;
-    const cudaError_t e = s.headdim == 64    ? launch_attend<64>(p, i64, handle->pdl, cs)
-                          : s.headdim == 128 ? launch_attend<128>(p, i64, handle->pdl, cs)
-                                             : launch_attend<256>(p, i64, handle->pdl, cs);
+    const cudaError_t e = s.headdim == 64    ? launch_attend<64>(p, *handle, i64, cs)
+                          : s.headdim == 128 ? launch_attend<128>(p, *handle, i64, cs)
+                                             : launch_attend<256>(p, *handle, i64, cs);
     if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
     return ok();
 }

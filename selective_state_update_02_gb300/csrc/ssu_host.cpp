@@ -111,6 +111,20 @@ bool rows_per_warp_ok(int rows_per_warp, int64_t dstate, int32_t state_dtype) {
     return false;
 }
 
+cudaError_t allow_smem(ssu_handle_s &handle, const void *kernel, int bytes) {
+    for (const void *k : handle.big_smem)
+        if (k == kernel) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) {
+        try {
+            handle.big_smem.push_back(kernel);
+        } catch (...) {  // no memory for the note: the attribute is set again next time
+        }
+    }
+    return e;
+}
+
 }  // namespace ssu_host
 
 extern "C" {

@@ -5,8 +5,11 @@
 #include <cuda_runtime.h>
 
 #include <string>
+#include <vector>
 
 #include "ssu.h"
+
+struct ssu_handle_s;
 
 namespace ssu_host {
 
@@ -28,6 +31,10 @@ int rows_per_instruction(int64_t dstate, int32_t state_dtype);
 // Whether a kernel instantiation exists for `rows_per_warp` rows per warp: rows_per_instruction
 // x {1, 2, 4, 8}, and 16 for an fp32 state of dstate 128.
 bool rows_per_warp_ok(int rows_per_warp, int64_t dstate, int32_t state_dtype);
+
+// Allows `kernel` `bytes` of dynamic shared memory on the handle's device (the current one), once
+// per handle.
+cudaError_t allow_smem(ssu_handle_s &handle, const void *kernel, int bytes);
 
 // Restores the caller's current device on scope exit.
 struct DeviceGuard {
@@ -57,5 +64,6 @@ struct ssu_handle_s {
     ssu_launch_t override_launch{};
     bool has_copy_override = false;
     ssu_copy_launch_t copy_override{};
+    std::vector<const void *> big_smem;  // kernels allowed more than 48 KB of shared memory
     bool pdl = true;  // launch the VEC and multi-token kernels as programmatic dependents
 };
