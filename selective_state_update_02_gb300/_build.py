@@ -17,7 +17,8 @@ SOURCES = [CSRC / "ssu.cu", CSRC / "ssu_tokens.cu", CSRC / "ssu_copy.cu",
 HEADERS = [ROOT / "include" / "ssu.h", CSRC / "ssu_device.cuh", CSRC / "ssu_host.h",
            CSRC / "ssu_vec.cuh", CSRC / "ssu_stage.cuh",
            CSRC / "ssu_tokens.cuh", CSRC / "ssu_tokens_mma.cuh",
-           CSRC / "ssu_prompt.cuh", CSRC / "ssu_attend.cuh"]
+           CSRC / "ssu_prompt.cuh", CSRC / "ssu_prompt_mma.cuh",
+           CSRC / "ssu_attend.cuh"]
 OBJDIR = PKG / "_build"
 LIB = PKG / "libssu.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

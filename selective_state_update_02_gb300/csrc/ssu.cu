@@ -327,6 +327,9 @@ ssu_status_t ssu_get_error(ssu_handle_t handle, ssu_stream_t stream, uint32_t *s
     if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "ssu_get_error: %s", cudaGetErrorString(e));
     if (skipped) *skipped = host[0];
     if (first_bad) *first_bad = host[0] ? static_cast<int64_t>(host[1]) : -1;
+    if (host[2])
+        return fail(SSU_ERR_CUDA, "a kernel gave up waiting for its own copies or products; "
+                                  "the results of the calls since the last check are not valid");
     if (host[0]) return fail(SSU_ERR_INDEX_OOB, "%u request(s) named a slot outside the pool",
                              host[0]);
     return ok();

@@ -10,6 +10,7 @@
 #include "ssu.h"
 #include "ssu_host.h"
 #include "ssu_prompt.cuh"
+#include "ssu_prompt_mma.cuh"
 
 using ssu_host::aligned;
 using ssu_host::DeviceGuard;
@@ -54,6 +55,117 @@ cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, b
                 : launch_seq<256, float>(q, i64, pdl, st);
 }
 
+// ---- the chunked form ----------------------------------------------------------------
+
+// How a call is cut: chunks per stretch, the most stretches that its prompts can have, and
+// whether any prompt can have more than one.
+struct PromptPlan {
+    long long seg, stretches, columns;
+    bool first_pass;
+    long long decay, total;  // workspace: offset of the stretches' decays, bytes
+};
+
+bool mma_sizes(const ssu_shape_t &s) {
+    return (s.dstate == 64 || s.dstate == 128) && s.headdim % kSlab == 0;
+}
+
+PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
+    PromptPlan w{};
+    w.columns = s.nheads * (s.headdim / kSlab);
+    const long long slots = 2ll * sm_count;  // CTAs that run together
+    const long long chunks = tokens / kChunk + s.batch;
+    w.seg = (chunks * w.columns + slots - 1) / slots;
+    if (w.seg < 4) w.seg = 4;
+    w.stretches = tokens / (w.seg * kChunk) + s.batch;
+    w.first_pass = tokens > w.seg * kChunk;
+    if (w.first_pass) {
+        w.decay = w.stretches * w.columns * kSlab * s.dstate * 4;
+        w.total = w.decay + (w.stretches * w.columns * 4 + 255) / 256 * 256;
+    }
+    return w;
+}
+
+// x, B and C as 3-D tensors of [tokens, heads or groups, columns] in boxes of 128 tokens by 64
+// columns; false where the driver cannot describe them.
+bool encode_map(CUtensorMap *map, const void *base, int64_t columns, int64_t heads, int64_t tokens,
+                int64_t head_stride, int64_t token_stride) {
+    static const auto encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    // a dimension of one element has no stride of its own
+    const cuuint64_t strides[2] = {
+        static_cast<cuuint64_t>(heads > 1 ? head_stride * 2 : columns * 2),
+        static_cast<cuuint64_t>(tokens > 1 ? token_stride * 2 : columns * heads * 2)};
+    const cuuint32_t box[3] = {64, 1, kChunk}, steps[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                  strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Operands that the chunked form can read: 16-byte rows for the tensor maps (x, B, C) and for
+// the stores of out.
+bool mma_operands(const PromptParams &q) {
+    const SsuParams &p = q.p;
+    if (!aligned(p.x, 16) || !aligned(p.B, 16) || !aligned(p.C, 16) || !aligned(p.out, 16))
+        return false;
+    const long long strides[] = {p.x_b, p.x_h, p.B_b, p.B_g, p.C_b, p.C_g, p.out_b, p.out_h};
+    for (long long v : strides)
+        if (v % 8 != 0 || v >= (1ll << 38)) return false;
+    return true;
+}
+
+template <int N, typename ST, bool kIdx64>
+cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[3],
+                       ssu_handle_s &handle, cudaStream_t st) {
+    constexpr int kBytes = PromptSmem<N>::kTotal + 1024;
+    auto *first = ssu_prompt_mma_kernel<N, ST, kIdx64, true>;
+    auto *second = ssu_prompt_mma_kernel<N, ST, kIdx64, false>;
+    cudaError_t e =
+        ssu_host::allow_smem(handle, reinterpret_cast<const void *>(first), kBytes);
+    if (e == cudaSuccess)
+        e = ssu_host::allow_smem(handle, reinterpret_cast<const void *>(second), kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.columns));
+    cfg.blockDim = dim3(kChunk);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = handle.pdl ? 1 : 0;
+    if (w.first_pass) {
+        e = cudaLaunchKernelEx(&cfg, first, m, maps[0], maps[1], maps[2]);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, second, m, maps[0], maps[1], maps[2]);
+}
+
+cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[3],
+                       int dstate, bool bf16, bool i64, ssu_handle_s &handle, cudaStream_t st) {
+#define SSU_MMA(N_, ST_)                                              \
+    return i64 ? launch_mma<N_, ST_, true>(m, w, maps, handle, st)    \
+               : launch_mma<N_, ST_, false>(m, w, maps, handle, st)
+    if (dstate == 64) {
+        if (bf16) SSU_MMA(64, __nv_bfloat16);
+        SSU_MMA(64, float);
+    }
+    if (bf16) SSU_MMA(128, __nv_bfloat16);
+    SSU_MMA(128, float);
+#undef SSU_MMA
+}
+
 }  // namespace
 
 extern "C" {
@@ -64,7 +176,7 @@ ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t 
     if (shape->batch < 0 || shape->nheads < 1 || shape->headdim < 1 || shape->dstate < 1)
         return fail(SSU_ERR_INVALID_ARG, "batch must be >= 0 and every dimension >= 1");
     if (tokens < 0) return fail(SSU_ERR_INVALID_ARG, "tokens %lld < 0", (long long)tokens);
-    *bytes = 0;
+    *bytes = mma_sizes(*shape) ? prompt_plan(*shape, tokens, handle->sm_count).total : 0;
     return ok();
 }
 
@@ -148,7 +260,24 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
-    const cudaError_t e = launch_seq(q, static_cast<int>(s.dstate), bf16, i64, handle->pdl, cs);
+    cudaError_t e = cudaErrorNotSupported;
+    if (tokens > 0 && mma_sizes(s) && mma_operands(q)) {
+        const PromptPlan w = prompt_plan(s, tokens, handle->sm_count);
+        PromptMmaParams m{};
+        m.q = q;
+        m.seg = static_cast<int>(w.seg < INT_MAX ? w.seg : INT_MAX);
+        m.slabs = static_cast<int>(s.headdim / kSlab);
+        m.local = static_cast<float *>(workspace);
+        m.decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.decay);
+        CUtensorMap maps[3];
+        if (w.stretches * w.columns <= INT_MAX &&
+            encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b) &&
+            encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b) &&
+            encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b))
+            e = launch_mma(m, w, maps, static_cast<int>(s.dstate), bf16, i64, *handle, cs);
+    }
+    if (e == cudaErrorNotSupported)
+        e = launch_seq(q, static_cast<int>(s.dstate), bf16, i64, handle->pdl, cs);
     if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
     return ok();
 }

@@ -1,0 +1,610 @@
+// Prompts in chunked matrix form on the tcgen05 tensor cores (sm_103a), instantiated by
+// ssu_prompt.cu beside the token-by-token kernel of ssu_prompt.cuh.
+//
+// Mathematics.  Over a chunk of Q = 128 tokens with a_t = dtv_t A and s(j, i] = a_{j+1} + .. +
+// a_i, the recurrence S_t = exp(a_t) S_{t-1} + dtv_t x_t (x) B_t, y_t = S_t C_t + D x_t reads
+//
+//   y_i = sum_{j <= i} (C_i . B_j) exp(s(j, i]) dtv_j x_j  +  exp(s(0, i]) C_i S  +  D x_i
+//   S'  = exp(s(0, Q]) S  +  sum_j (exp(s(j, Q]) dtv_j x_j) (x) B_j
+//
+// that is four matrix products per chunk and head: G = C B^T [Q x Q], I = C S^T [Q x P],
+// Y = M X [Q x P] with M = G times the masked decays, and U = B^T W [N x P] with W the weighted
+// tokens.  One CTA takes one head's stretch of a prompt, chunk after chunk, its state in
+// registers (thread n holds column n of the P = 64 rows).  G, I, U and Y accumulate in TMEM
+// (256 of the SM's 512 columns, so two CTAs share an SM and one's products run under the
+// other's elementwise work); M goes back into TMEM as an A operand.
+//
+// Precision.  C, B and X are bf16 and exact.  M and the state that enters I are rounded to bf16
+// (2^-9 of a term in the mean square, as much as the bf16 readout itself carries).  W decides
+// the state that is carried on, so it enters as the sum of two bf16 parts (hi + lo leaves at
+// most 2^-17 |w|, under 2^-20 in the mean square of a sum) and the state itself stays fp32.
+// Exponents are sums over short runs that never cross a chunk: within blocks of 32 tokens
+// prefix and suffix sums, between blocks the block totals, so no exponent is a difference of
+// two large sums except inside the diagonal block, whose weights are rounded to bf16 anyway.
+// An a_t beyond +-256 (log2) is cut there: exp is then 0 (or infinite) all the same, and a cut
+// sum stays small enough to be exact.
+//
+// Stretches.  A prompt that is long for the device is cut into stretches of `seg` chunks.  A
+// first pass (kFirst) runs U alone over every stretch but a prompt's last, from a zero state;
+// the second pass starts a stretch from the prompt's own state advanced through the earlier
+// stretches' results.
+//
+// What bounds it: ~1,300 cycles of tensor pipe per chunk and head (G 512, I, Y 256 each, U 512
+// with its two parts) against 96 KB that a CTA brings in through L2.
+
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ssu_prompt.cuh"
+
+namespace {
+
+constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
+constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
+constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct PromptMmaParams {
+    PromptParams q;
+    int seg;              // chunks per stretch
+    int slabs;            // headdim / 64
+    float *local;         // [stretch][head * slabs + slab][64 p][N]
+    float *decay;         // [stretch][head * slabs + slab]: log2 of the stretch's decay
+};
+
+// ---- PTX -------------------------------------------------------------------------------
+
+__device__ __forceinline__ unsigned smem_u32(const void *p) {
+    return static_cast<unsigned>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+// Waits for the barrier's phase of `parity`; gives up (false) after a bounded number of polls.
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
+    for (int i = 0; i < (1 << 18); ++i) {
+        unsigned done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, unsigned bar, int x,
+                                         int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(unsigned bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 32 columns of the thread's TMEM lane.
+__device__ __forceinline__ void tc_load32(unsigned addr, unsigned (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_store16(unsigned addr, const unsigned (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// d (+)= a b, a and b in shared memory.
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b,
+                                       unsigned idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// d (+)= a b, a in TMEM.
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc,
+                                       bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// Shared-memory operand in rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart.
+// Read along the rows (K-major) it is [rows][64 k]; read across them (MN-major) it is
+// [64 mn][rows k], further blocks of 64 mn `block_bytes` apart.
+__device__ __forceinline__ unsigned long long operand(unsigned addr, unsigned block_bytes) {
+    return static_cast<unsigned long long>((addr >> 4) & 0x3fff) |
+           (static_cast<unsigned long long>(block_bytes >> 4) << 16) |
+           (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: bf16 operands, fp32 accumulator, M = 128.
+__host__ __device__ constexpr unsigned instruction(int n, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn_major ? 1u << 15 : 0u) |
+           (b_mn_major ? 1u << 16 : 0u) | (static_cast<unsigned>(n >> 3) << 17) |
+           (static_cast<unsigned>(kChunk >> 4) << 24);
+}
+
+// Address of 16-byte piece `piece` of row `row` of a swizzled tile.
+__device__ __forceinline__ unsigned swizzled(unsigned tile, int row, int piece) {
+    return tile + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ uint4 load_smem16(unsigned addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_smem16(unsigned addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void widen16(const uint4 &w, float (&v)[8]) {
+    const unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
+// ---- the kernel ------------------------------------------------------------------------
+
+// Shared memory: tiles first (1024-byte aligned), then the per-token values.  W's two parts take
+// C's place once G and I are done.
+template <int N>
+struct PromptSmem {
+    static constexpr int kBlocks = N / 64;  // 64-column tiles of B and C
+    static constexpr int kC = 0;            // also W hi, lo
+    static constexpr int kB = 2 * kTileBytes;
+    static constexpr int kX = kB + kBlocks * kTileBytes;
+    static constexpr int kS = kX + kTileBytes;           // state, bf16 [n][64 p]
+    static constexpr int kVec = kS + N * 128;
+    // floats: v0, prefix, dtv of the chunk's tokens (128 each), block totals (4)
+    static constexpr int kBars = kVec + (3 * kChunk + 4) * 4;
+    static constexpr int kTotal = kBars + 64;
+};
+
+// The stretch `g` of the call: its prompt and first chunk.  All threads get the answer; false
+// past the last stretch.  With `all`, every prompt is looked at and the bad ones counted.
+template <bool kIdx64>
+__device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long g, bool all,
+                                             long long *scan, long long &b, long long &index) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long before = 0;
+    if (tid == 0) scan[4] = -1;
+    for (long long b0 = 0; b0 < m.q.p.batch; b0 += kChunk) {
+        const long long bb = b0 + tid;
+        long long n = 0;
+        if (bb < m.q.p.batch) {
+            long long slot, lo, hi;
+            if (load_prompt<kIdx64>(m.q, bb, all, slot, lo, hi)) {
+                const long long per = static_cast<long long>(m.seg) * kChunk;
+                n = (hi - lo + per - 1) / per;
+                if (n == 0 && m.q.fresh && m.q.fresh[bb]) n = 1;  // only clears the slot
+            }
+        }
+        long long incl = n;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        long long base = before;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < warp) base += scan[w];
+            before += scan[w];
+        }
+        incl += base;
+        if (g >= incl - n && g < incl) {
+            scan[4] = bb;
+            scan[5] = g - (incl - n);
+        }
+        if (!all && g < before) break;
+    }
+    __syncthreads();
+    b = scan[4];
+    index = scan[5];
+    return b >= 0;
+}
+
+template <int N, typename ST, bool kIdx64, bool kFirst>
+__global__ void __launch_bounds__(128, 2)
+    ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
+                          const __grid_constant__ CUtensorMap map_x,
+                          const __grid_constant__ CUtensorMap map_b,
+                          const __grid_constant__ CUtensorMap map_c) {
+    using Smem = PromptSmem<N>;
+    constexpr int kBlocks = Smem::kBlocks;
+    extern __shared__ unsigned char raw[];
+    __shared__ long long scan[6];
+    __shared__ unsigned tmem_slot;
+    pdl_wait();
+    const SsuParams &p = m.q.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int columns = p.nheads * m.slabs;  // CTAs per stretch: heads and slabs
+    const long long g = blockIdx.x / columns;
+    const int column = static_cast<int>(blockIdx.x - g * columns);
+    const int h = column / m.slabs, slab = column - h * m.slabs;
+    long long b, index;
+    if (!find_stretch<kIdx64>(m, g, !kFirst && blockIdx.x == 0, scan, b, index)) return;
+    long long slot, begin, end;
+    load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
+    const bool fresh = m.q.fresh && m.q.fresh[b] != 0;
+    const long long from = begin + index * m.seg * kChunk;
+    long long to = from + static_cast<long long>(m.seg) * kChunk;
+    const bool last = to >= end;
+    if (last) to = end;
+    if (kFirst && last) return;  // nothing continues after a prompt's last stretch
+
+    const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char *const base_ptr = raw + (base - smem_u32(raw));
+    const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
+    const unsigned sS = base + Smem::kS, sWhi = sC, sWlo = sC + kTileBytes;
+    float *const v0 = reinterpret_cast<float *>(base_ptr + Smem::kVec);
+    float *const pre = v0 + kChunk, *const dts = pre + kChunk, *const tots = dts + kChunk;
+    const unsigned bar_full = base + Smem::kBars, bar_g = bar_full + 8, bar_y = bar_full + 16;
+
+    if (tid == 0) {
+        mbar_init(bar_full, 1);
+        mbar_init(bar_g, 1);
+        mbar_init(bar_y, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_slot)),
+                     "r"(256)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = tmem_slot;
+    // columns: G 0..127, then M 0..63 and Y 64..127 in its place; I 128..191; U 192..255
+    const unsigned tG = tmem, tY = tmem + 64, tI = tmem + 128, tU = tmem + 192;
+    const unsigned lanes = static_cast<unsigned>(warp) << 21;  // (32 warp) << 16
+
+    const int grp = group_of(h, p.group_magic);
+    const float bias = __ldg(p.dt_bias + h * p.bias_h);
+    const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+    const float D = __ldg(p.D + h * p.D_h);
+
+    // Only one thread issues copies and products.
+    const unsigned bytes = kTileBytes * (1 + kBlocks * (kFirst ? 1 : 2));
+    auto load = [&](long long tok) {
+        const int t = static_cast<int>(tok);
+        mbar_expect(bar_full, bytes);
+        tma_load(sX, &map_x, bar_full, slab * kSlab, h, t);
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+            tma_load(sB + k * kTileBytes, &map_b, bar_full, k * 64, grp, t);
+            if (!kFirst) tma_load(sC + k * kTileBytes, &map_c, bar_full, k * 64, grp, t);
+        }
+    };
+    if (tid == 0 && from < to) load(from);
+
+    // The state a stretch starts from: thread n holds S[0 .. 63][n].
+    float S[kSlab];
+    const bool own = tid < N;
+    ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
+                      static_cast<long long>(slab) * kSlab * p.st_row + tid;
+#pragma unroll
+    for (int i = 0; i < kSlab; ++i) S[i] = 0.0f;
+    if (!kFirst && own) {
+        if (!fresh) {
+#pragma unroll
+            for (int i = 0; i < kSlab; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
+        }
+        for (long long k = g - index; k < g; ++k) {
+            const float *loc = m.local + (k * columns + column) * (kSlab * N) + tid;
+            const float f = exp2f(__ldcg(m.decay + k * columns + column));
+#pragma unroll
+            for (int i = 0; i < kSlab; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
+        }
+    }
+    auto publish = [&]() {  // the state as the next chunk's bf16 operand
+        if (!kFirst && own) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                store_smem16(swizzled(sS, tid, c),
+                             make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
+                                        f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
+                                        f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
+                                        f2_to_bf2(S[8 * c + 6], S[8 * c + 7])));
+        }
+    };
+    publish();
+
+    bool alive = true;
+    float stretch_decay = 0.0f;  // log2
+    unsigned phase = 0;
+    for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
+        const int valid = static_cast<int>(to - tok < kChunk ? to - tok : kChunk);
+        // dt of the thread's token, and the decay sums around it
+        float dtv = 0.0f, a = 0.0f;
+        if (tid < valid) {
+            dtv = softplus_f32(
+                __bfloat162float(p.dt[(tok + tid) * p.dt_b + h * p.dt_h]) + bias);
+            a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
+        }
+        float up = a, down = a;  // inclusive prefix and suffix within the 32 tokens of the warp
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, up, x);
+            const float d = __shfl_down_sync(0xffffffffu, down, x);
+            if (lane >= x) up += u;
+            if (lane + x < 32) down += d;
+        }
+        float after = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 31) after = 0.0f;
+        const float v = dtv * exp2f(after);  // weight up to the end of the 32 tokens
+        v0[tid] = v;
+        pre[tid] = up;
+        dts[tid] = dtv;
+        if (lane == 31) tots[warp] = up;
+        fence_async_smem();  // S as published
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (alive) alive = mbar_wait(bar_full, phase);
+        __syncwarp();
+        if (valid < kChunk) {  // rows of the next prompt: B and X must not bring them in
+            for (int i = tid; i < (kChunk - valid) * 8 * (1 + kBlocks); i += 128) {
+                const int tile = i / ((kChunk - valid) * 8), r = i % ((kChunk - valid) * 8);
+                store_smem16(swizzled(tile == 0 ? sX : sB + (tile - 1) * kTileBytes,
+                                      valid + r / 8, r % 8),
+                             make_uint4(0, 0, 0, 0));
+            }
+            fence_async_smem();
+            __syncthreads();
+        }
+        if (!kFirst && tid == 0) {
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+                const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                mma_ss(tG, operand(sC + off, 0), operand(sB + off, 0),
+                       instruction(kChunk, false, false), k > 0);
+            }
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+                const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                mma_ss(tI, operand(sC + off, 0), operand(sS + k * 2048, 0),
+                       instruction(kSlab, false, true), k > 0);
+            }
+            tc_commit(bar_g);
+        }
+        float t4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t4[k] = tots[k];
+        float later = 0.0f, earlier = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k > warp) later += t4[k];
+            if (k < warp) earlier += t4[k];
+        }
+        const float w = v * exp2f(later);  // the token's weight in the chunk's last state
+        const float chunk_decay = (t4[0] + t4[1]) + (t4[2] + t4[3]);
+        stretch_decay += chunk_decay;
+        if (!kFirst) {
+            if (alive) alive = mbar_wait(bar_g, phase);
+            __syncwarp();
+            tc_fence_after();
+        }
+        // W = w x in two bf16 parts, the thread's token
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float x[8];
+            widen16(load_smem16(swizzled(sX, tid, c)), x);
+            unsigned hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f0 = w * x[2 * i], f1 = w * x[2 * i + 1];
+                hi[i] = f2_to_bf2(f0, f1);
+                lo[i] = f2_to_bf2(f0 - __uint_as_float(hi[i] << 16),
+                                  f1 - __uint_as_float(hi[i] & 0xffff0000u));
+            }
+            store_smem16(swizzled(sWhi, tid, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            store_smem16(swizzled(sWlo, tid, c), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+        if (!kFirst) {
+            // M = G times decays, block of 32 columns by block; the thread's row is token tid
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                unsigned mm[16];
+                if (cb <= warp) {
+                    unsigned gg[32];
+                    tc_load32(tG + lanes + 32 * cb, gg);
+                    tc_wait_ld();
+                    if (cb < warp) {
+                        float between = 0.0f;
+#pragma unroll
+                        for (int k = 1; k < 4; ++k)
+                            if (k > cb && k < warp) between += t4[k];
+                        const float f = exp2f(up + between);
+                        const float4 *vv = reinterpret_cast<const float4 *>(v0 + 32 * cb);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 q = vv[j];
+                            mm[2 * j] = f2_to_bf2(__uint_as_float(gg[4 * j]) * (f * q.x),
+                                                  __uint_as_float(gg[4 * j + 1]) * (f * q.y));
+                            mm[2 * j + 1] = f2_to_bf2(__uint_as_float(gg[4 * j + 2]) * (f * q.z),
+                                                      __uint_as_float(gg[4 * j + 3]) * (f * q.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float e[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int col = 2 * j + i;
+                                const float d = exp2f(up - pre[32 * cb + col]) *
+                                                dts[32 * cb + col] * __uint_as_float(gg[col]);
+                                e[i] = col <= lane ? d : 0.0f;
+                            }
+                            mm[j] = f2_to_bf2(e[0], e[1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) mm[j] = 0;
+                }
+                tc_store16(tG + lanes + 16 * cb, mm);
+            }
+            tc_wait_st();
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (tid == 0) {
+            if (!kFirst) {
+#pragma unroll
+                for (int k = 0; k < kChunk / 16; ++k)
+                    mma_ts(tY, tG + 8 * k, operand(sX + k * 2048, 0),
+                           instruction(kSlab, false, true), k > 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * kChunk / 16; ++k) {
+                const int kk = k % (kChunk / 16);
+                mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
+                       operand((k < kChunk / 16 ? sWhi : sWlo) + kk * 2048, 0),
+                       instruction(kSlab, true, true), k > 0);
+            }
+            tc_commit(bar_y);
+        }
+        if (alive) alive = mbar_wait(bar_y, phase);
+        __syncwarp();
+        tc_fence_after();
+        if (!kFirst) {
+            const float fi = exp2f(up + earlier);
+            __nv_bfloat16 *const dst = p.out + (tok + tid) * p.out_b + h * p.out_h + slab * kSlab;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                unsigned ii[32], yy[32];
+                tc_load32(tI + lanes + 32 * half, ii);
+                tc_load32(tY + lanes + 32 * half, yy);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float x[8], y[8];
+                    widen16(load_smem16(swizzled(sX, tid, 4 * half + c)), x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[i] = fmaf(D, x[i], fmaf(fi, __uint_as_float(ii[8 * c + i]),
+                                                  __uint_as_float(yy[8 * c + i])));
+                    if (tid < valid)
+                        *reinterpret_cast<uint4 *>(dst + 32 * half + 8 * c) =
+                            make_uint4(f2_to_bf2(y[0], y[1]), f2_to_bf2(y[2], y[3]),
+                                       f2_to_bf2(y[4], y[5]), f2_to_bf2(y[6], y[7]));
+                }
+            }
+        }
+        const float f = exp2f(chunk_decay);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            unsigned uu[32];
+            tc_load32(tU + lanes + 32 * half, uu);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                S[32 * half + i] = fmaf(S[32 * half + i], f, __uint_as_float(uu[i]));
+        }
+        publish();
+        // every thread is done with X and the accumulators: the next chunk may come in
+        __syncthreads();
+        if (tid == 0 && tok + kChunk < to) load(tok + kChunk);
+    }
+
+    if (own) {
+        if (kFirst) {
+            float *loc = m.local + (g * columns + column) * (kSlab * N) + tid;
+#pragma unroll
+            for (int i = 0; i < kSlab; ++i) __stcg(loc + i * N, S[i]);
+            if (tid == 0) __stcg(m.decay + g * columns + column, stretch_decay);
+        } else if (last) {
+#pragma unroll
+            for (int i = 0; i < kSlab; ++i) {
+                if constexpr (sizeof(ST) == 4)
+                    state[i * p.st_row] = S[i];
+                else
+                    state[i * p.st_row] = __float2bfloat16(S[i]);
+            }
+        }
+    }
+    if (!alive) atomicOr(&p.err[2], 1u);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256)
+                     : "memory");
+    }
+}
+
+}  // namespace
