@@ -137,7 +137,7 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.columns));
-    cfg.blockDim = dim3(kChunk);
+    cfg.blockDim = dim3(kPromptThreads);
     cfg.dynamicSmemBytes = kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -16,8 +16,9 @@
 //
 // Precision.  C, B and X are bf16 and exact.  M and the state that enters I are rounded to bf16
 // (2^-9 of a term in the mean square, as much as the bf16 readout itself carries).  W decides
-// the state that is carried on, so it enters as the sum of two bf16 parts (hi + lo leaves at
-// most 2^-17 |w|, under 2^-20 in the mean square of a sum) and the state itself stays fp32.
+// the state that is carried on, so it enters as the sum of three bf16 parts (24 bits: all of an
+// fp32 value; two parts measured 1.1e-6 of the state in the 2-norm, against 1e-7) where the state
+// is kept in fp32, of two where it is rounded to bf16 in the end, and runs in fp32 either way.
 // Exponents are sums over short runs that never cross a chunk: within blocks of 32 tokens
 // prefix and suffix sums, between blocks the block totals, so no exponent is a difference of
 // two large sums except inside the diagonal block, whose weights are rounded to bf16 anyway.
@@ -29,8 +30,8 @@
 // the second pass starts a stretch from the prompt's own state advanced through the earlier
 // stretches' results.
 //
-// What bounds it: ~1,300 cycles of tensor pipe per chunk and head (G 512, I, Y 256 each, U 512
-// with its two parts) against 96 KB that a CTA brings in through L2.
+// What bounds it: ~1,800 cycles of tensor pipe per chunk and head (G 512, I, Y 256 each, U 768
+// with its three parts) against 96 KB that a CTA brings in through L2.
 
 #pragma once
 
@@ -46,6 +47,8 @@ namespace {
 
 constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
+constexpr int kPromptThreads = 256;
+constexpr int kHalf = kSlab / 2;  // a thread's share of its row: the two warpgroups halve it
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -208,19 +211,27 @@ __device__ __forceinline__ void widen16(const uint4 &w, float (&v)[8]) {
     }
 }
 
+// 2^x by the hardware's approximation (2 ulp), results below 2^-126 as 0: for weights that are
+// rounded to bf16 next.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---- the kernel ------------------------------------------------------------------------
 
-// Shared memory: tiles first (1024-byte aligned), then the per-token values.  W's two parts take
-// C's place once G and I are done.
+// Shared memory: tiles first (1024-byte aligned), then the per-token values.  W's three parts take
+// the places of C and S once G and I are done.
 template <int N>
 struct PromptSmem {
     static constexpr int kBlocks = N / 64;  // 64-column tiles of B and C
-    static constexpr int kC = 0;            // also W hi, lo
+    static constexpr int kC = 0;            // also W's first two parts
     static constexpr int kB = 2 * kTileBytes;
     static constexpr int kX = kB + kBlocks * kTileBytes;
-    static constexpr int kS = kX + kTileBytes;           // state, bf16 [n][64 p]
-    static constexpr int kVec = kS + N * 128;
-    // floats: v0, prefix, dtv of the chunk's tokens (128 each), block totals (4)
+    static constexpr int kS = kX + kTileBytes;  // state, bf16 [n][64 p]; also W's third part
+    static constexpr int kVec = kS + kTileBytes;
+    // floats of the chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4)
     static constexpr int kBars = kVec + (3 * kChunk + 4) * 4;
     static constexpr int kTotal = kBars + 64;
 };
@@ -232,8 +243,9 @@ __device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long
                                              long long *scan, long long &b, long long &index) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long before = 0;
-    if (tid == 0) scan[4] = -1;
-    for (long long b0 = 0; b0 < m.q.p.batch; b0 += kChunk) {
+    constexpr int kWarps = kPromptThreads / 32;
+    if (tid == 0) scan[kWarps] = -1;
+    for (long long b0 = 0; b0 < m.q.p.batch; b0 += kPromptThreads) {
         const long long bb = b0 + tid;
         long long n = 0;
         if (bb < m.q.p.batch) {
@@ -255,33 +267,34 @@ __device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long
         __syncthreads();
         long long base = before;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp) base += scan[w];
             before += scan[w];
         }
         incl += base;
         if (g >= incl - n && g < incl) {
-            scan[4] = bb;
-            scan[5] = g - (incl - n);
+            scan[kWarps] = bb;
+            scan[kWarps + 1] = g - (incl - n);
         }
         if (!all && g < before) break;
     }
     __syncthreads();
-    b = scan[4];
-    index = scan[5];
+    b = scan[kWarps];
+    index = scan[kWarps + 1];
     return b >= 0;
 }
 
 template <int N, typename ST, bool kIdx64, bool kFirst>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(kPromptThreads, 2)
     ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
                           const __grid_constant__ CUtensorMap map_x,
                           const __grid_constant__ CUtensorMap map_b,
                           const __grid_constant__ CUtensorMap map_c) {
     using Smem = PromptSmem<N>;
     constexpr int kBlocks = Smem::kBlocks;
+    constexpr int kParts = sizeof(ST) == 4 ? 3 : 2;  // bf16 parts of W
     extern __shared__ unsigned char raw[];
-    __shared__ long long scan[6];
+    __shared__ long long scan[kPromptThreads / 32 + 2];
     __shared__ unsigned tmem_slot;
     pdl_wait();
     const SsuParams &p = m.q.p;
@@ -304,13 +317,16 @@ __global__ void __launch_bounds__(128, 2)
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char *const base_ptr = raw + (base - smem_u32(raw));
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
-    const unsigned sS = base + Smem::kS, sWhi = sC, sWlo = sC + kTileBytes;
+    const unsigned sS = base + Smem::kS;
     float *const v0 = reinterpret_cast<float *>(base_ptr + Smem::kVec);
-    float *const pre = v0 + kChunk, *const dts = pre + kChunk, *const tots = dts + kChunk;
-    const unsigned bar_full = base + Smem::kBars, bar_g = bar_full + 8, bar_y = bar_full + 16;
+    float2 *const pre = reinterpret_cast<float2 *>(v0 + kChunk);
+    float *const tots = v0 + 3 * kChunk;
+    const unsigned bar_full = base + Smem::kBars, bar_x = bar_full + 8;
+    const unsigned bar_g = bar_full + 16, bar_y = bar_full + 24;
 
     if (tid == 0) {
         mbar_init(bar_full, 1);
+        mbar_init(bar_x, 1);
         mbar_init(bar_g, 1);
         mbar_init(bar_y, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -326,9 +342,12 @@ __global__ void __launch_bounds__(128, 2)
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = tmem_slot;
-    // columns: G 0..127, then M 0..63 and Y 64..127 in its place; I 128..191; U 192..255
-    const unsigned tG = tmem, tY = tmem + 64, tI = tmem + 128, tU = tmem + 192;
-    const unsigned lanes = static_cast<unsigned>(warp) << 21;  // (32 warp) << 16
+    // columns: G 0..127, then Y 0..63 and U 64..127 in its place; M 128..191; I 192..255
+    const unsigned tG = tmem, tY = tmem, tU = tmem + 64, tM = tmem + 128, tI = tmem + 192;
+    // A thread's row (token of the chunk, TMEM lane, column n of the state) is the same in both
+    // warpgroups; `part` says which.
+    const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
+    const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
 
     const int grp = group_of(h, p.group_magic);
     const float bias = __ldg(p.dt_bias + h * p.bias_h);
@@ -336,43 +355,42 @@ __global__ void __launch_bounds__(128, 2)
     const float D = __ldg(p.D + h * p.D_h);
 
     // Only one thread issues copies and products.
-    const unsigned bytes = kTileBytes * (1 + kBlocks * (kFirst ? 1 : 2));
-    auto load = [&](long long tok) {
+    auto load_bc = [&](long long tok) {
         const int t = static_cast<int>(tok);
-        mbar_expect(bar_full, bytes);
-        tma_load(sX, &map_x, bar_full, slab * kSlab, h, t);
+        mbar_expect(bar_full, kTileBytes * kBlocks * (kFirst ? 1 : 2));
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) {
             tma_load(sB + k * kTileBytes, &map_b, bar_full, k * 64, grp, t);
             if (!kFirst) tma_load(sC + k * kTileBytes, &map_c, bar_full, k * 64, grp, t);
         }
     };
-    if (tid == 0 && from < to) load(from);
+    if (tid == 0 && from < to) load_bc(from);
 
-    // The state a stretch starts from: thread n holds S[0 .. 63][n].
-    float S[kSlab];
-    const bool own = tid < N;
+    // The state a stretch starts from: the thread holds S[32 part .. 32 part + 31][row].
+    float S[kHalf];
+    const bool own = row < N;
     ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                      static_cast<long long>(slab) * kSlab * p.st_row + tid;
+                      static_cast<long long>(slab * kSlab + kHalf * part) * p.st_row + row;
 #pragma unroll
-    for (int i = 0; i < kSlab; ++i) S[i] = 0.0f;
+    for (int i = 0; i < kHalf; ++i) S[i] = 0.0f;
     if (!kFirst && own) {
         if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < kSlab; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
+            for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
         }
         for (long long k = g - index; k < g; ++k) {
-            const float *loc = m.local + (k * columns + column) * (kSlab * N) + tid;
+            const float *loc =
+                m.local + ((k * columns + column) * kSlab + kHalf * part) * N + row;
             const float f = exp2f(__ldcg(m.decay + k * columns + column));
 #pragma unroll
-            for (int i = 0; i < kSlab; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
+            for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
         }
     }
     auto publish = [&]() {  // the state as the next chunk's bf16 operand
         if (!kFirst && own) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                store_smem16(swizzled(sS, tid, c),
+            for (int c = 0; c < 4; ++c)
+                store_smem16(swizzled(sS, row, 4 * part + c),
                              make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
                                         f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
                                         f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
@@ -381,44 +399,51 @@ __global__ void __launch_bounds__(128, 2)
     };
     publish();
 
+    const __nv_bfloat16 *const dt_col = p.dt + h * p.dt_h;
+    float dt_next = 0.0f;
+    if (part == 0 && from + row < to) dt_next = __bfloat162float(dt_col[(from + row) * p.dt_b]);
     bool alive = true;
     float stretch_decay = 0.0f;  // log2
     unsigned phase = 0;
     for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
         const int valid = static_cast<int>(to - tok < kChunk ? to - tok : kChunk);
-        // dt of the thread's token, and the decay sums around it
-        float dtv = 0.0f, a = 0.0f;
-        if (tid < valid) {
-            dtv = softplus_f32(
-                __bfloat162float(p.dt[(tok + tid) * p.dt_b + h * p.dt_h]) + bias);
-            a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
-        }
-        float up = a, down = a;  // inclusive prefix and suffix within the 32 tokens of the warp
+        if (part == 0) {
+            // dt of the thread's token, and the decay sums around it
+            float dtv = 0.0f, a = 0.0f;
+            if (row < valid) {
+                dtv = softplus_f32(dt_next + bias);
+                a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
+            }
+            if (tok + kChunk + row < to)
+                dt_next = __bfloat162float(dt_col[(tok + kChunk + row) * p.dt_b]);
+            float up = a, down = a;  // inclusive prefix and suffix within the warp's 32 tokens
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, up, x);
-            const float d = __shfl_down_sync(0xffffffffu, down, x);
-            if (lane >= x) up += u;
-            if (lane + x < 32) down += d;
+            for (int x = 1; x < 32; x <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, x);
+                const float d = __shfl_down_sync(0xffffffffu, down, x);
+                if (lane >= x) up += u;
+                if (lane + x < 32) down += d;
+            }
+            float after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 31) after = 0.0f;
+            v0[row] = dtv * exp2f(after);  // weight up to the end of the 32 tokens
+            pre[row] = make_float2(up, dtv);
+            if (lane == 31) tots[quarter] = up;
         }
-        float after = __shfl_down_sync(0xffffffffu, down, 1);
-        if (lane == 31) after = 0.0f;
-        const float v = dtv * exp2f(after);  // weight up to the end of the 32 tokens
-        v0[tid] = v;
-        pre[tid] = up;
-        dts[tid] = dtv;
-        if (lane == 31) tots[warp] = up;
-        fence_async_smem();  // S as published
+        fence_async_smem();  // S as published, and the readout staged in X, are behind us
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
+        if (tid == 0) {
+            mbar_expect(bar_x, kTileBytes);
+            tma_load(sX, &map_x, bar_x, slab * kSlab, h, static_cast<int>(tok));
+        }
         if (alive) alive = mbar_wait(bar_full, phase);
         __syncwarp();
-        if (valid < kChunk) {  // rows of the next prompt: B and X must not bring them in
-            for (int i = tid; i < (kChunk - valid) * 8 * (1 + kBlocks); i += 128) {
+        if (valid < kChunk) {  // rows of the next prompt: B must not bring them in
+            for (int i = tid; i < (kChunk - valid) * 8 * kBlocks; i += kPromptThreads) {
                 const int tile = i / ((kChunk - valid) * 8), r = i % ((kChunk - valid) * 8);
-                store_smem16(swizzled(tile == 0 ? sX : sB + (tile - 1) * kTileBytes,
-                                      valid + r / 8, r % 8),
+                store_smem16(swizzled(sB + tile * kTileBytes, valid + r / 8, r % 8),
                              make_uint4(0, 0, 0, 0));
             }
             fence_async_smem();
@@ -445,47 +470,65 @@ __global__ void __launch_bounds__(128, 2)
         float later = 0.0f, earlier = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (k > warp) later += t4[k];
-            if (k < warp) earlier += t4[k];
+            if (k > quarter) later += t4[k];
+            if (k < quarter) earlier += t4[k];
         }
-        const float w = v * exp2f(later);  // the token's weight in the chunk's last state
+        const float up = pre[row].x;
+        const float w = v0[row] * exp2f(later);  // the token's weight in the chunk's last state
         const float chunk_decay = (t4[0] + t4[1]) + (t4[2] + t4[3]);
         stretch_decay += chunk_decay;
+        if (alive) alive = mbar_wait(bar_x, phase);
+        __syncwarp();
+        uint4 xr[4];  // the thread's half of its token's x; zeros past the prompt's end
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            xr[c] = row < valid ? load_smem16(swizzled(sX, row, 4 * part + c))
+                                : make_uint4(0, 0, 0, 0);
+        if (row >= valid) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) store_smem16(swizzled(sX, row, 4 * part + c), xr[c]);
+        }
         if (!kFirst) {
             if (alive) alive = mbar_wait(bar_g, phase);
             __syncwarp();
             tc_fence_after();
         }
-        // W = w x in two bf16 parts, the thread's token
+        // W = w x in bf16 parts
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
             float x[8];
-            widen16(load_smem16(swizzled(sX, tid, c)), x);
-            unsigned hi[4], lo[4];
+            widen16(xr[c], x);
+            unsigned bits[kParts][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float f0 = w * x[2 * i], f1 = w * x[2 * i + 1];
-                hi[i] = f2_to_bf2(f0, f1);
-                lo[i] = f2_to_bf2(f0 - __uint_as_float(hi[i] << 16),
-                                  f1 - __uint_as_float(hi[i] & 0xffff0000u));
+                float f0 = w * x[2 * i], f1 = w * x[2 * i + 1];
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    bits[k][i] = f2_to_bf2(f0, f1);
+                    f0 -= __uint_as_float(bits[k][i] << 16);
+                    f1 -= __uint_as_float(bits[k][i] & 0xffff0000u);
+                }
             }
-            store_smem16(swizzled(sWhi, tid, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            store_smem16(swizzled(sWlo, tid, c), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+            for (int k = 0; k < kParts; ++k)
+                store_smem16(swizzled(k < 2 ? sC + k * kTileBytes : sS, row, 4 * part + c),
+                             make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
         }
         if (!kFirst) {
-            // M = G times decays, block of 32 columns by block; the thread's row is token tid
+            // M = G times decays, two blocks of 32 columns per warpgroup
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
+            for (int half = 0; half < 2; ++half) {
+                const int cb = 2 * part + half;
                 unsigned mm[16];
-                if (cb <= warp) {
+                if (cb <= quarter) {
                     unsigned gg[32];
                     tc_load32(tG + lanes + 32 * cb, gg);
                     tc_wait_ld();
-                    if (cb < warp) {
+                    if (cb < quarter) {
                         float between = 0.0f;
 #pragma unroll
                         for (int k = 1; k < 4; ++k)
-                            if (k > cb && k < warp) between += t4[k];
+                            if (k > cb && k < quarter) between += t4[k];
                         const float f = exp2f(up + between);
                         const float4 *vv = reinterpret_cast<const float4 *>(v0 + 32 * cb);
 #pragma unroll
@@ -497,24 +540,22 @@ __global__ void __launch_bounds__(128, 2)
                                                       __uint_as_float(gg[4 * j + 3]) * (f * q.w));
                         }
                     } else {
+                        const float4 *pp = reinterpret_cast<const float4 *>(pre + 32 * cb);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            float e[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int col = 2 * j + i;
-                                const float d = exp2f(up - pre[32 * cb + col]) *
-                                                dts[32 * cb + col] * __uint_as_float(gg[col]);
-                                e[i] = col <= lane ? d : 0.0f;
-                            }
-                            mm[j] = f2_to_bf2(e[0], e[1]);
+                            const float4 q = pp[j];  // (prefix, dtv) of columns 2 j and 2 j + 1
+                            const float e0 = exp2_ftz(up - q.x) * (q.y * __uint_as_float(gg[2 * j]));
+                            const float e1 =
+                                exp2_ftz(up - q.z) * (q.w * __uint_as_float(gg[2 * j + 1]));
+                            mm[j] = f2_to_bf2(2 * j <= lane ? e0 : 0.0f,
+                                              2 * j + 1 <= lane ? e1 : 0.0f);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) mm[j] = 0;
                 }
-                tc_store16(tG + lanes + 16 * cb, mm);
+                tc_store16(tM + lanes + 16 * cb, mm);
             }
             tc_wait_st();
         }
@@ -526,70 +567,83 @@ __global__ void __launch_bounds__(128, 2)
             if (!kFirst) {
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; ++k)
-                    mma_ts(tY, tG + 8 * k, operand(sX + k * 2048, 0),
+                    mma_ts(tY, tM + 8 * k, operand(sX + k * 2048, 0),
                            instruction(kSlab, false, true), k > 0);
             }
 #pragma unroll
-            for (int k = 0; k < 2 * kChunk / 16; ++k) {
-                const int kk = k % (kChunk / 16);
+            for (int k = 0; k < kParts * kChunk / 16; ++k) {
+                const int which = k / (kChunk / 16), kk = k % (kChunk / 16);
                 mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
-                       operand((k < kChunk / 16 ? sWhi : sWlo) + kk * 2048, 0),
+                       operand((which < 2 ? sC + which * kTileBytes : sS) + kk * 2048, 0),
                        instruction(kSlab, true, true), k > 0);
             }
             tc_commit(bar_y);
         }
+        float y[kHalf];  // the readout's other two terms, while the products run
+        if (!kFirst) {
+            const float fi = exp2f(up + earlier);
+            unsigned ii[32];
+            tc_load32(tI + lanes + kHalf * part, ii);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float x[8];
+                widen16(xr[c], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[8 * c + i] = fmaf(fi, __uint_as_float(ii[8 * c + i]), D * x[i]);
+            }
+        }
         if (alive) alive = mbar_wait(bar_y, phase);
         __syncwarp();
         tc_fence_after();
+        // B and C of this chunk are used up: the next may come
+        if (tid == 0 && tok + kChunk < to) load_bc(tok + kChunk);
         if (!kFirst) {
-            const float fi = exp2f(up + earlier);
-            __nv_bfloat16 *const dst = p.out + (tok + tid) * p.out_b + h * p.out_h + slab * kSlab;
+            // y of the thread's half row, staged in X's place so that rows leave in whole lines
+            unsigned yy[32];
+            tc_load32(tY + lanes + kHalf * part, yy);
+            tc_wait_ld();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                unsigned ii[32], yy[32];
-                tc_load32(tI + lanes + 32 * half, ii);
-                tc_load32(tY + lanes + 32 * half, yy);
-                tc_wait_ld();
+            for (int i = 0; i < kHalf; ++i) y[i] += __uint_as_float(yy[i]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[8], y[8];
-                    widen16(load_smem16(swizzled(sX, tid, 4 * half + c)), x);
+            for (int c = 0; c < 4; ++c)
+                store_smem16(swizzled(sX, row, 4 * part + c),
+                             make_uint4(f2_to_bf2(y[8 * c], y[8 * c + 1]),
+                                        f2_to_bf2(y[8 * c + 2], y[8 * c + 3]),
+                                        f2_to_bf2(y[8 * c + 4], y[8 * c + 5]),
+                                        f2_to_bf2(y[8 * c + 6], y[8 * c + 7])));
+            __syncwarp();
+            __nv_bfloat16 *const dst = p.out + h * p.out_h + slab * kSlab + kHalf * part +
+                                       (lane & 3) * 8;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = fmaf(D, x[i], fmaf(fi, __uint_as_float(ii[8 * c + i]),
-                                                  __uint_as_float(yy[8 * c + i])));
-                    if (tid < valid)
-                        *reinterpret_cast<uint4 *>(dst + 32 * half + 8 * c) =
-                            make_uint4(f2_to_bf2(y[0], y[1]), f2_to_bf2(y[2], y[3]),
-                                       f2_to_bf2(y[4], y[5]), f2_to_bf2(y[6], y[7]));
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int r = 32 * quarter + 8 * i + (lane >> 2);
+                const uint4 v = load_smem16(swizzled(sX, r, 4 * part + (lane & 3)));
+                if (r < valid)
+                    *reinterpret_cast<uint4 *>(dst + (tok + r) * p.out_b) = v;
             }
         }
         const float f = exp2f(chunk_decay);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        {
             unsigned uu[32];
-            tc_load32(tU + lanes + 32 * half, uu);
+            tc_load32(tU + lanes + kHalf * part, uu);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                S[32 * half + i] = fmaf(S[32 * half + i], f, __uint_as_float(uu[i]));
+            for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __uint_as_float(uu[i]));
         }
         publish();
-        // every thread is done with X and the accumulators: the next chunk may come in
-        __syncthreads();
-        if (tid == 0 && tok + kChunk < to) load(tok + kChunk);
     }
 
     if (own) {
         if (kFirst) {
-            float *loc = m.local + (g * columns + column) * (kSlab * N) + tid;
+            float *loc = m.local + ((g * columns + column) * kSlab + kHalf * part) * N + row;
 #pragma unroll
-            for (int i = 0; i < kSlab; ++i) __stcg(loc + i * N, S[i]);
+            for (int i = 0; i < kHalf; ++i) __stcg(loc + i * N, S[i]);
             if (tid == 0) __stcg(m.decay + g * columns + column, stretch_decay);
         } else if (last) {
 #pragma unroll
-            for (int i = 0; i < kSlab; ++i) {
+            for (int i = 0; i < kHalf; ++i) {
                 if constexpr (sizeof(ST) == 4)
                     state[i * p.st_row] = S[i];
                 else
