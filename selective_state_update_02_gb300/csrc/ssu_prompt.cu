@@ -267,6 +267,7 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         m.q = q;
         m.seg = static_cast<int>(w.seg < INT_MAX ? w.seg : INT_MAX);
         m.slabs = static_cast<int>(s.headdim / kSlab);
+        m.out32 = aligned(out, 32) && p.out_b % 16 == 0 && p.out_h % 16 == 0;
         m.local = static_cast<float *>(workspace);
         m.decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.decay);
         CUtensorMap maps[3];

@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
-constexpr int kPromptThreads = 256;
+constexpr int kPromptThreads = 256 + 32;  // two warpgroups for the elementwise work, one warp to issue
 constexpr int kHalf = kSlab / 2;  // a thread's share of its row: the two warpgroups halve it
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,6 +56,7 @@ struct PromptMmaParams {
     PromptParams q;
     int seg;              // chunks per stretch
     int slabs;            // headdim / 64
+    int out32;            // out's rows are 32-byte aligned
     float *local;         // [stretch][head * slabs + slab][64 p][N]
     float *decay;         // [stretch][head * slabs + slab]: log2 of the stretch's decay
 };
@@ -68,6 +69,10 @@ __device__ __forceinline__ unsigned smem_u32(const void *p) {
 
 __device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(unsigned bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
@@ -146,6 +151,19 @@ __device__ __forceinline__ void tc_store16(unsigned addr, const unsigned (&r)[16
         : "memory");
 }
 
+__device__ __forceinline__ void tc_store32(unsigned addr, const unsigned (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 // d (+)= a b, a and b in shared memory.
 __device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b,
                                        unsigned idesc, bool add) {
@@ -211,6 +229,15 @@ __device__ __forceinline__ void widen16(const uint4 &w, float (&v)[8]) {
     }
 }
 
+// 32 bytes, one whole sector, by one thread.
+__device__ __forceinline__ void store_sector(void *dst, unsigned a, unsigned b, unsigned c,
+                                             unsigned d, unsigned e, unsigned f, unsigned g,
+                                             unsigned h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
+                 "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
 // 2^x by the hardware's approximation (2 ulp), results below 2^-126 as 0: for weights that are
 // rounded to bf16 next.
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -231,8 +258,10 @@ struct PromptSmem {
     static constexpr int kX = kB + kBlocks * kTileBytes;
     static constexpr int kS = kX + kTileBytes;  // state, bf16 [n][64 p]; also W's third part
     static constexpr int kVec = kS + kTileBytes;
-    // floats of the chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4)
-    static constexpr int kBars = kVec + (3 * kChunk + 4) * 4;
+    // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4); two of
+    // them, for this chunk and the next
+    static constexpr int kVecFloats = 3 * kChunk + 4;
+    static constexpr int kBars = kVec + 2 * kVecFloats * 4;
     static constexpr int kTotal = kBars + 64;
 };
 
@@ -266,7 +295,6 @@ __device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
         long long base = before;
-#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) base += scan[w];
             before += scan[w];
@@ -284,6 +312,40 @@ __device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long
     return b >= 0;
 }
 
+// Decay sums of one chunk, by the four warps of one warpgroup (one token per thread, `row`): the
+// token's weight up to the end of its 32 tokens, its prefix within them, dtv, the blocks' totals.
+__device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, float bias, float A2,
+                                             int row, int lane) {
+    float dtv = 0.0f, a = 0.0f;
+    if (live) {
+        dtv = softplus_f32(dt + bias);
+        a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
+    }
+    float up = a, down = a;  // inclusive prefix and suffix
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, up, x);
+        const float d = __shfl_down_sync(0xffffffffu, down, x);
+        if (lane >= x) up += u;
+        if (lane + x < 32) down += d;
+    }
+    float after = __shfl_down_sync(0xffffffffu, down, 1);
+    if (lane == 31) after = 0.0f;
+    vec[row] = dtv * exp2f(after);
+    reinterpret_cast<float2 *>(vec + kChunk)[row] = make_float2(up, dtv);
+    if (lane == 31) vec[3 * kChunk + row / 32] = up;
+}
+
+// Roles.  Warp 8 issues: one of its threads starts the copies and the products, as their inputs
+// become ready.  Warps 0 .. 7 do the elementwise work; a thread's row (token of the chunk, TMEM
+// lane, column n of the state) is the same in both warpgroups, which halve each row's columns.
+// Per chunk, with the barrier that each hand-over uses:
+//
+//   issue:    [full, done] G, I -> [w] U -> next B, C -> [m] Y -> next X
+//   compute:  [x] W's parts in registers -> [g] W into C and S -> w; I scaled, D x added; M -> m;
+//             the next chunk's decays; [u] S advanced and published; [y] readout out -> done
+//
+// so U runs under M, and the copies under everything that does not need them.
 template <int N, typename ST, bool kIdx64, bool kFirst>
 __global__ void __launch_bounds__(kPromptThreads, 2)
     ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
@@ -293,6 +355,7 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
     using Smem = PromptSmem<N>;
     constexpr int kBlocks = Smem::kBlocks;
     constexpr int kParts = sizeof(ST) == 4 ? 3 : 2;  // bf16 parts of W
+    constexpr int kCompute = 256;
     extern __shared__ unsigned char raw[];
     __shared__ long long scan[kPromptThreads / 32 + 2];
     __shared__ unsigned tmem_slot;
@@ -307,7 +370,6 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
     if (!find_stretch<kIdx64>(m, g, !kFirst && blockIdx.x == 0, scan, b, index)) return;
     long long slot, begin, end;
     load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
-    const bool fresh = m.q.fresh && m.q.fresh[b] != 0;
     const long long from = begin + index * m.seg * kChunk;
     long long to = from + static_cast<long long>(m.seg) * kChunk;
     const bool last = to >= end;
@@ -315,23 +377,19 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
     if (kFirst && last) return;  // nothing continues after a prompt's last stretch
 
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
-    unsigned char *const base_ptr = raw + (base - smem_u32(raw));
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
     const unsigned sS = base + Smem::kS;
-    float *const v0 = reinterpret_cast<float *>(base_ptr + Smem::kVec);
-    float2 *const pre = reinterpret_cast<float2 *>(v0 + kChunk);
-    float *const tots = v0 + 3 * kChunk;
-    const unsigned bar_full = base + Smem::kBars, bar_x = bar_full + 8;
-    const unsigned bar_g = bar_full + 16, bar_y = bar_full + 24;
+    float *const vecs = reinterpret_cast<float *>(raw + (base - smem_u32(raw)) + Smem::kVec);
+    const unsigned bar_full = base + Smem::kBars, bar_x = bar_full + 8, bar_g = bar_full + 16,
+                   bar_u = bar_full + 24, bar_y = bar_full + 32, bar_w = bar_full + 40,
+                   bar_m = bar_full + 48, bar_done = bar_full + 56;
 
     if (tid == 0) {
-        mbar_init(bar_full, 1);
-        mbar_init(bar_x, 1);
-        mbar_init(bar_g, 1);
-        mbar_init(bar_y, 1);
+        for (int i = 0; i < 5; ++i) mbar_init(bar_full + 8 * i, 1);
+        for (int i = 5; i < 8; ++i) mbar_init(bar_full + 8 * i, kCompute);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_slot)),
                      "r"(256)
@@ -342,319 +400,350 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = tmem_slot;
-    // columns: G 0..127, then Y 0..63 and U 64..127 in its place; M 128..191; I 192..255
-    const unsigned tG = tmem, tY = tmem, tU = tmem + 64, tM = tmem + 128, tI = tmem + 192;
-    // A thread's row (token of the chunk, TMEM lane, column n of the state) is the same in both
-    // warpgroups; `part` says which.
-    const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
-    const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
-
-    const int grp = group_of(h, p.group_magic);
-    const float bias = __ldg(p.dt_bias + h * p.bias_h);
-    const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
-    const float D = __ldg(p.D + h * p.D_h);
-
-    // Only one thread issues copies and products.
-    auto load_bc = [&](long long tok) {
-        const int t = static_cast<int>(tok);
-        mbar_expect(bar_full, kTileBytes * kBlocks * (kFirst ? 1 : 2));
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-            tma_load(sB + k * kTileBytes, &map_b, bar_full, k * 64, grp, t);
-            if (!kFirst) tma_load(sC + k * kTileBytes, &map_c, bar_full, k * 64, grp, t);
-        }
-    };
-    if (tid == 0 && from < to) load_bc(from);
-
-    // The state a stretch starts from: the thread holds S[32 part .. 32 part + 31][row].
-    float S[kHalf];
-    const bool own = row < N;
-    ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                      static_cast<long long>(slab * kSlab + kHalf * part) * p.st_row + row;
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i) S[i] = 0.0f;
-    if (!kFirst && own) {
-        if (!fresh) {
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
-        }
-        for (long long k = g - index; k < g; ++k) {
-            const float *loc =
-                m.local + ((k * columns + column) * kSlab + kHalf * part) * N + row;
-            const float f = exp2f(__ldcg(m.decay + k * columns + column));
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
-        }
-    }
-    auto publish = [&]() {  // the state as the next chunk's bf16 operand
-        if (!kFirst && own) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                store_smem16(swizzled(sS, row, 4 * part + c),
-                             make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
-                                        f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
-                                        f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
-                                        f2_to_bf2(S[8 * c + 6], S[8 * c + 7])));
-        }
-    };
-    publish();
-
-    const __nv_bfloat16 *const dt_col = p.dt + h * p.dt_h;
-    float dt_next = 0.0f;
-    if (part == 0 && from + row < to) dt_next = __bfloat162float(dt_col[(from + row) * p.dt_b]);
+    // columns: G 0..127, U 128..191, I and then Y 192..255.  M takes G's place piece by piece: its
+    // tokens 0..63 (bf16 pairs) columns 0..31, 64..127 columns 64..95, each written by the
+    // warpgroup that has read the columns of G there.
+    const unsigned tG = tmem, tU = tmem + 128, tY = tmem + 192;
     bool alive = true;
-    float stretch_decay = 0.0f;  // log2
-    unsigned phase = 0;
-    for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
-        const int valid = static_cast<int>(to - tok < kChunk ? to - tok : kChunk);
-        if (part == 0) {
-            // dt of the thread's token, and the decay sums around it
-            float dtv = 0.0f, a = 0.0f;
-            if (row < valid) {
-                dtv = softplus_f32(dt_next + bias);
-                a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
-            }
-            if (tok + kChunk + row < to)
-                dt_next = __bfloat162float(dt_col[(tok + kChunk + row) * p.dt_b]);
-            float up = a, down = a;  // inclusive prefix and suffix within the warp's 32 tokens
+
+    if (warp == 8) {
+        if (lane == 0) {
+            const int grp = group_of(h, p.group_magic);
+            auto load_bc = [&](long long tok) {
+                const int t = static_cast<int>(tok);
+                mbar_expect(bar_full, kTileBytes * kBlocks * (kFirst ? 1 : 2));
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, up, x);
-                const float d = __shfl_down_sync(0xffffffffu, down, x);
-                if (lane >= x) up += u;
-                if (lane + x < 32) down += d;
-            }
-            float after = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 31) after = 0.0f;
-            v0[row] = dtv * exp2f(after);  // weight up to the end of the 32 tokens
-            pre[row] = make_float2(up, dtv);
-            if (lane == 31) tots[quarter] = up;
-        }
-        fence_async_smem();  // S as published, and the readout staged in X, are behind us
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (tid == 0) {
-            mbar_expect(bar_x, kTileBytes);
-            tma_load(sX, &map_x, bar_x, slab * kSlab, h, static_cast<int>(tok));
-        }
-        if (alive) alive = mbar_wait(bar_full, phase);
-        __syncwarp();
-        if (valid < kChunk) {  // rows of the next prompt: B must not bring them in
-            for (int i = tid; i < (kChunk - valid) * 8 * kBlocks; i += kPromptThreads) {
-                const int tile = i / ((kChunk - valid) * 8), r = i % ((kChunk - valid) * 8);
-                store_smem16(swizzled(sB + tile * kTileBytes, valid + r / 8, r % 8),
-                             make_uint4(0, 0, 0, 0));
-            }
-            fence_async_smem();
-            __syncthreads();
-        }
-        if (!kFirst && tid == 0) {
-#pragma unroll
-            for (int k = 0; k < N / 16; ++k) {
-                const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                mma_ss(tG, operand(sC + off, 0), operand(sB + off, 0),
-                       instruction(kChunk, false, false), k > 0);
-            }
-#pragma unroll
-            for (int k = 0; k < N / 16; ++k) {
-                const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                mma_ss(tI, operand(sC + off, 0), operand(sS + k * 2048, 0),
-                       instruction(kSlab, false, true), k > 0);
-            }
-            tc_commit(bar_g);
-        }
-        float t4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) t4[k] = tots[k];
-        float later = 0.0f, earlier = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k > quarter) later += t4[k];
-            if (k < quarter) earlier += t4[k];
-        }
-        const float up = pre[row].x;
-        const float w = v0[row] * exp2f(later);  // the token's weight in the chunk's last state
-        const float chunk_decay = (t4[0] + t4[1]) + (t4[2] + t4[3]);
-        stretch_decay += chunk_decay;
-        if (alive) alive = mbar_wait(bar_x, phase);
-        __syncwarp();
-        uint4 xr[4];  // the thread's half of its token's x; zeros past the prompt's end
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            xr[c] = row < valid ? load_smem16(swizzled(sX, row, 4 * part + c))
-                                : make_uint4(0, 0, 0, 0);
-        if (row >= valid) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) store_smem16(swizzled(sX, row, 4 * part + c), xr[c]);
-        }
-        if (!kFirst) {
-            if (alive) alive = mbar_wait(bar_g, phase);
-            __syncwarp();
-            tc_fence_after();
-        }
-        // W = w x in bf16 parts
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float x[8];
-            widen16(xr[c], x);
-            unsigned bits[kParts][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f0 = w * x[2 * i], f1 = w * x[2 * i + 1];
-#pragma unroll
-                for (int k = 0; k < kParts; ++k) {
-                    bits[k][i] = f2_to_bf2(f0, f1);
-                    f0 -= __uint_as_float(bits[k][i] << 16);
-                    f1 -= __uint_as_float(bits[k][i] & 0xffff0000u);
+                for (int k = 0; k < kBlocks; ++k) {
+                    tma_load(sB + k * kTileBytes, &map_b, bar_full, k * 64, grp, t);
+                    if (!kFirst) tma_load(sC + k * kTileBytes, &map_c, bar_full, k * 64, grp, t);
                 }
+            };
+            auto load_x = [&](long long tok) {
+                mbar_expect(bar_x, kTileBytes);
+                tma_load(sX, &map_x, bar_x, slab * kSlab, h, static_cast<int>(tok));
+            };
+            if (from < to) {
+                load_bc(from);
+                load_x(from);
             }
+            unsigned phase = 0;
+            for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
+                const bool more = tok + kChunk < to;
+                if (!kFirst) {
+                    if (alive) alive = mbar_wait(bar_full, phase);
+                    if (alive) alive = mbar_wait(bar_done, phase);  // S and TMEM: see below
+                    tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kParts; ++k)
-                store_smem16(swizzled(k < 2 ? sC + k * kTileBytes : sS, row, 4 * part + c),
-                             make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
-        }
-        if (!kFirst) {
-            // M = G times decays, two blocks of 32 columns per warpgroup
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int cb = 2 * part + half;
-                unsigned mm[16];
-                if (cb <= quarter) {
-                    unsigned gg[32];
-                    tc_load32(tG + lanes + 32 * cb, gg);
-                    tc_wait_ld();
-                    if (cb < quarter) {
-                        float between = 0.0f;
-#pragma unroll
-                        for (int k = 1; k < 4; ++k)
-                            if (k > cb && k < quarter) between += t4[k];
-                        const float f = exp2f(up + between);
-                        const float4 *vv = reinterpret_cast<const float4 *>(v0 + 32 * cb);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 q = vv[j];
-                            mm[2 * j] = f2_to_bf2(__uint_as_float(gg[4 * j]) * (f * q.x),
-                                                  __uint_as_float(gg[4 * j + 1]) * (f * q.y));
-                            mm[2 * j + 1] = f2_to_bf2(__uint_as_float(gg[4 * j + 2]) * (f * q.z),
-                                                      __uint_as_float(gg[4 * j + 3]) * (f * q.w));
-                        }
-                    } else {
-                        const float4 *pp = reinterpret_cast<const float4 *>(pre + 32 * cb);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float4 q = pp[j];  // (prefix, dtv) of columns 2 j and 2 j + 1
-                            const float e0 = exp2_ftz(up - q.x) * (q.y * __uint_as_float(gg[2 * j]));
-                            const float e1 =
-                                exp2_ftz(up - q.z) * (q.w * __uint_as_float(gg[2 * j + 1]));
-                            mm[j] = f2_to_bf2(2 * j <= lane ? e0 : 0.0f,
-                                              2 * j + 1 <= lane ? e1 : 0.0f);
-                        }
+                    for (int k = 0; k < N / 16; ++k) {
+                        const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                        mma_ss(tG, operand(sC + off, 0), operand(sB + off, 0),
+                               instruction(kChunk, false, false), k > 0);
                     }
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) mm[j] = 0;
+                    for (int k = 0; k < N / 16; ++k) {
+                        const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                        mma_ss(tY, operand(sC + off, 0), operand(sS + k * 2048, 0),
+                               instruction(kSlab, false, true), k > 0);
+                    }
+                    tc_commit(bar_g);
                 }
-                tc_store16(tM + lanes + 16 * cb, mm);
-            }
-            tc_wait_st();
-        }
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (tid == 0) {
-            if (!kFirst) {
+                if (alive) alive = mbar_wait(bar_w, phase);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kParts * kChunk / 16; ++k) {
+                    const int which = k / (kChunk / 16), kk = k % (kChunk / 16);
+                    mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
+                           operand((which < 2 ? sC + which * kTileBytes : sS) + kk * 2048, 0),
+                           instruction(kSlab, true, true), k > 0);
+                }
+                tc_commit(bar_u);
+                if (kFirst) {  // U alone reads the tiles (x went through registers)
+                    if (more) load_x(tok + kChunk);
+                    if (alive) alive = mbar_wait(bar_u, phase);
+                    if (more) load_bc(tok + kChunk);
+                    continue;
+                }
+                if (alive) alive = mbar_wait(bar_m, phase);
+                tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kChunk / 16; ++k)
-                    mma_ts(tY, tM + 8 * k, operand(sX + k * 2048, 0),
-                           instruction(kSlab, false, true), k > 0);
+                    mma_ts(tY, tG + (k < 4 ? 8 * k : 32 + 8 * k), operand(sX + k * 2048, 0),
+                           instruction(kSlab, false, true), true);
+                tc_commit(bar_y);
+                if (alive) alive = mbar_wait(bar_u, phase);
+                if (more) load_bc(tok + kChunk);
+                if (alive) alive = mbar_wait(bar_y, phase);
+                if (more) load_x(tok + kChunk);
             }
-#pragma unroll
-            for (int k = 0; k < kParts * kChunk / 16; ++k) {
-                const int which = k / (kChunk / 16), kk = k % (kChunk / 16);
-                mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
-                       operand((which < 2 ? sC + which * kTileBytes : sS) + kk * 2048, 0),
-                       instruction(kSlab, true, true), k > 0);
-            }
-            tc_commit(bar_y);
         }
-        float y[kHalf];  // the readout's other two terms, while the products run
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
+        const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
+        const bool fresh = m.q.fresh && m.q.fresh[b] != 0;
+        const float bias = __ldg(p.dt_bias + h * p.bias_h);
+        const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+        const float D = __ldg(p.D + h * p.D_h);
+        const __nv_bfloat16 *const dt_col = p.dt + h * p.dt_h;
+        // The second warpgroup has less of M and works the decays out, a chunk ahead.
+        float dt_next = 0.0f;
+        if (part == 1) {
+            float dt = 0.0f;
+            if (from + row < to) dt = __bfloat162float(dt_col[(from + row) * p.dt_b]);
+            if (from + kChunk + row < to)
+                dt_next = __bfloat162float(dt_col[(from + kChunk + row) * p.dt_b]);
+            chunk_decays(vecs, from + row < to, dt, bias, A2, row, lane);
+        }
+
+        // The state a stretch starts from: the thread holds S[32 part .. 32 part + 31][row].
+        float S[kHalf];
+        const bool own = row < N;
+        ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
+                          static_cast<long long>(slab * kSlab + kHalf * part) * p.st_row + row;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) S[i] = 0.0f;
+        if (!kFirst && own) {
+            if (!fresh) {
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
+            }
+            for (long long k = g - index; k < g; ++k) {
+                const float *loc =
+                    m.local + ((k * columns + column) * kSlab + kHalf * part) * N + row;
+                const float f = exp2f(__ldcg(m.decay + k * columns + column));
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
+            }
+        }
+        // The state as the next chunk's bf16 operand; then the issuing warp may use it and TMEM.
+        auto publish = [&]() {
+            if (own) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    store_smem16(swizzled(sS, row, 4 * part + c),
+                                 make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
+                                            f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
+                                            f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
+                                            f2_to_bf2(S[8 * c + 6], S[8 * c + 7])));
+            }
+            fence_async_smem();
+        };
         if (!kFirst) {
-            const float fi = exp2f(up + earlier);
-            unsigned ii[32];
-            tc_load32(tI + lanes + kHalf * part, ii);
-            tc_wait_ld();
+            publish();
+            mbar_arrive(bar_done);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");  // the decays
+
+        float stretch_decay = 0.0f;  // log2
+        unsigned phase = 0;
+        for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
+            const int valid = static_cast<int>(to - tok < kChunk ? to - tok : kChunk);
+            float *const v0 = vecs + phase * Smem::kVecFloats;
+            const float2 *const pre = reinterpret_cast<const float2 *>(v0 + kChunk);
+            const float4 t4 = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+            const float t[4] = {t4.x, t4.y, t4.z, t4.w};
+            float later = 0.0f, earlier = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k > quarter) later += t[k];
+                if (k < quarter) earlier += t[k];
+            }
+            const float up = pre[row].x;
+            const float w = v0[row] * exp2f(later);  // the token's weight in the chunk's last state
+            const float chunk_decay = (t[0] + t[1]) + (t[2] + t[3]);
+            stretch_decay += chunk_decay;
+            if (alive) alive = mbar_wait(bar_x, phase);
+            uint4 xr[4];  // the thread's half of its token's x; zeros past the prompt's end
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                xr[c] = row < valid ? load_smem16(swizzled(sX, row, 4 * part + c))
+                                    : make_uint4(0, 0, 0, 0);
+            // C and S are W's to take once G and I are done
+            if (alive) alive = mbar_wait(kFirst ? bar_full : bar_g, phase);
+            __syncwarp();
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x[8];
                 widen16(xr[c], x);
+                unsigned bits[kParts][4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[8 * c + i] = fmaf(fi, __uint_as_float(ii[8 * c + i]), D * x[i]);
+                for (int i = 0; i < 4; ++i) {
+                    float2 f = __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) {
+                        bits[k][i] = f2_to_bf2(f.x, f.y);
+                        f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k][i] << 16),
+                                                      -__uint_as_float(bits[k][i] & 0xffff0000u)));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kParts; ++k)
+                    store_smem16(swizzled(k < 2 ? sC + k * kTileBytes : sS, row, 4 * part + c),
+                                 make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
             }
-        }
-        if (alive) alive = mbar_wait(bar_y, phase);
-        __syncwarp();
-        tc_fence_after();
-        // B and C of this chunk are used up: the next may come
-        if (tid == 0 && tok + kChunk < to) load_bc(tok + kChunk);
-        if (!kFirst) {
-            // y of the thread's half row, staged in X's place so that rows leave in whole lines
+            if (row >= valid) {  // tokens of the next prompt: X and B must not bring them in
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    store_smem16(swizzled(sX, row, 4 * part + c), make_uint4(0, 0, 0, 0));
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k)
+                        store_smem16(swizzled(sB + k * kTileBytes, row, 4 * part + c),
+                                     make_uint4(0, 0, 0, 0));
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bar_w);
+            if (!kFirst) {
+                // The state's share of the readout and D x, where Y will add to them
+                const float fi = exp2f(up + earlier);
+                unsigned ii[32];
+                tc_load32(tY + lanes + kHalf * part, ii);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float x[8];
+                    widen16(xr[c], x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = __ffma2_rn(
+                            make_float2(fi, fi),
+                            make_float2(__uint_as_float(ii[8 * c + 2 * i]),
+                                        __uint_as_float(ii[8 * c + 2 * i + 1])),
+                            __fmul2_rn(make_float2(D, D), make_float2(x[2 * i], x[2 * i + 1])));
+                        ii[8 * c + 2 * i] = __float_as_uint(y.x);
+                        ii[8 * c + 2 * i + 1] = __float_as_uint(y.y);
+                    }
+                }
+                tc_store32(tY + lanes + kHalf * part, ii);
+                // M = G times decays, two blocks of 32 columns per warpgroup
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int cb = 2 * part + half;
+                    unsigned mm[16];
+                    if (cb <= quarter) {
+                        unsigned gg[32];
+                        tc_load32(tG + lanes + 32 * cb, gg);
+                        tc_wait_ld();
+                        if (cb < quarter) {
+                            float between = 0.0f;
+#pragma unroll
+                            for (int k = 1; k < 4; ++k)
+                                if (k > cb && k < quarter) between += t[k];
+                            const float f = exp2f(up + between);
+                            const float4 *vv = reinterpret_cast<const float4 *>(v0 + 32 * cb);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 q = vv[j];
+                                const float2 lo = __fmul2_rn(
+                                    make_float2(__uint_as_float(gg[4 * j]),
+                                                __uint_as_float(gg[4 * j + 1])),
+                                    __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
+                                const float2 hi = __fmul2_rn(
+                                    make_float2(__uint_as_float(gg[4 * j + 2]),
+                                                __uint_as_float(gg[4 * j + 3])),
+                                    __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
+                                mm[2 * j] = f2_to_bf2(lo.x, lo.y);
+                                mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
+                            }
+                        } else {
+                            const float4 *pp = reinterpret_cast<const float4 *>(pre + 32 * cb);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float4 q = pp[j];  // (prefix, dtv) of columns 2j, 2j + 1
+                                const float e0 = exp2_ftz(up - q.x) *
+                                                 (q.y * __uint_as_float(gg[2 * j]));
+                                const float e1 = exp2_ftz(up - q.z) *
+                                                 (q.w * __uint_as_float(gg[2 * j + 1]));
+                                mm[j] = f2_to_bf2(2 * j <= lane ? e0 : 0.0f,
+                                                  2 * j + 1 <= lane ? e1 : 0.0f);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) mm[j] = 0;
+                    }
+                    tc_store16(tG + lanes + 64 * part + 16 * half, mm);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar_m);
+            }
+            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
+                const float dt = dt_next;
+                if (tok + 2 * kChunk + row < to)
+                    dt_next = __bfloat162float(dt_col[(tok + 2 * kChunk + row) * p.dt_b]);
+                chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
+                             bias, A2, row, lane);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
+            const float f = exp2f(chunk_decay);
+            if (alive) alive = mbar_wait(bar_u, phase);
+            __syncwarp();
+            tc_fence_after();
+            {
+                unsigned uu[32];
+                tc_load32(tU + lanes + kHalf * part, uu);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < kHalf; i += 2) {
+                    const float2 s = __ffma2_rn(
+                        make_float2(S[i], S[i + 1]), make_float2(f, f),
+                        make_float2(__uint_as_float(uu[i]), __uint_as_float(uu[i + 1])));
+                    S[i] = s.x;
+                    S[i + 1] = s.y;
+                }
+            }
+            if (kFirst) continue;
+            publish();
+            if (alive) alive = mbar_wait(bar_y, phase);
+            __syncwarp();
+            tc_fence_after();
             unsigned yy[32];
             tc_load32(tY + lanes + kHalf * part, yy);
             tc_wait_ld();
+            tc_fence_before();
+            mbar_arrive(bar_done);
+            if (row < valid) {
+                unsigned o[16];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) y[i] += __uint_as_float(yy[i]);
+                for (int i = 0; i < 16; ++i)
+                    o[i] = f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+                __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
+                                           slab * kSlab + kHalf * part;
+                if (m.out32) {
+                    store_sector(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+                    store_sector(dst + 16, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
+                } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                store_smem16(swizzled(sX, row, 4 * part + c),
-                             make_uint4(f2_to_bf2(y[8 * c], y[8 * c + 1]),
-                                        f2_to_bf2(y[8 * c + 2], y[8 * c + 3]),
-                                        f2_to_bf2(y[8 * c + 4], y[8 * c + 5]),
-                                        f2_to_bf2(y[8 * c + 6], y[8 * c + 7])));
-            __syncwarp();
-            __nv_bfloat16 *const dst = p.out + h * p.out_h + slab * kSlab + kHalf * part +
-                                       (lane & 3) * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 32 * quarter + 8 * i + (lane >> 2);
-                const uint4 v = load_smem16(swizzled(sX, r, 4 * part + (lane & 3)));
-                if (r < valid)
-                    *reinterpret_cast<uint4 *>(dst + (tok + r) * p.out_b) = v;
+                    for (int c = 0; c < 4; ++c)
+                        reinterpret_cast<uint4 *>(dst)[c] =
+                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
             }
         }
-        const float f = exp2f(chunk_decay);
-        {
-            unsigned uu[32];
-            tc_load32(tU + lanes + kHalf * part, uu);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __uint_as_float(uu[i]));
-        }
-        publish();
-    }
 
-    if (own) {
-        if (kFirst) {
-            float *loc = m.local + ((g * columns + column) * kSlab + kHalf * part) * N + row;
+        if (own) {
+            if (kFirst) {
+                float *loc = m.local + ((g * columns + column) * kSlab + kHalf * part) * N + row;
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) __stcg(loc + i * N, S[i]);
-            if (tid == 0) __stcg(m.decay + g * columns + column, stretch_decay);
-        } else if (last) {
+                for (int i = 0; i < kHalf; ++i) __stcg(loc + i * N, S[i]);
+                if (tid == 0) __stcg(m.decay + g * columns + column, stretch_decay);
+            } else if (last) {
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) {
-                if constexpr (sizeof(ST) == 4)
-                    state[i * p.st_row] = S[i];
-                else
-                    state[i * p.st_row] = __float2bfloat16(S[i]);
+                for (int i = 0; i < kHalf; ++i) {
+                    if constexpr (sizeof(ST) == 4)
+                        state[i * p.st_row] = S[i];
+                    else
+                        state[i * p.st_row] = __float2bfloat16(S[i]);
+                }
             }
         }
     }
     if (!alive) atomicOr(&p.err[2], 1u);
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 8) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256)
                      : "memory");
