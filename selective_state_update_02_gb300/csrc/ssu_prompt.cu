@@ -60,7 +60,7 @@ cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, b
 // How a call is cut: chunks per stretch, the most stretches that its prompts can have, and
 // whether any prompt can have more than one.
 struct PromptPlan {
-    long long seg, stretches, columns;
+    long long seg, stretches, columns, ctas;  // ctas: per stretch
     bool first_pass;
     long long decay, total;  // workspace: offset of the stretches' decays, bytes
 };
@@ -72,9 +72,9 @@ bool mma_sizes(const ssu_shape_t &s) {
 PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     PromptPlan w{};
     w.columns = s.nheads * (s.headdim / kSlab);
-    const long long slots = 2ll * sm_count;  // CTAs that run together
+    w.ctas = s.ngroups * ((w.columns / s.ngroups + 1) / 2);
     const long long chunks = tokens / kChunk + s.batch;
-    w.seg = (chunks * w.columns + slots - 1) / slots;
+    w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;  // one CTA per SM
     if (w.seg < 4) w.seg = 4;
     w.stretches = tokens / (w.seg * kChunk) + s.batch;
     w.first_pass = tokens > w.seg * kChunk;
@@ -125,7 +125,7 @@ bool mma_operands(const PromptParams &q) {
 }
 
 template <int N, typename ST, bool kIdx64>
-cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[3],
+cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[4],
                        ssu_handle_s &handle, cudaStream_t st) {
     constexpr int kBytes = PromptSmem<N>::kTotal + 1024;
     auto *first = ssu_prompt_mma_kernel<N, ST, kIdx64, true>;
@@ -136,7 +136,7 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
         e = ssu_host::allow_smem(handle, reinterpret_cast<const void *>(second), kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.columns));
+    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.ctas));
     cfg.blockDim = dim3(kPromptThreads);
     cfg.dynamicSmemBytes = kBytes;
     cfg.stream = st;
@@ -146,13 +146,13 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
     cfg.attrs = attr;
     cfg.numAttrs = handle.pdl ? 1 : 0;
     if (w.first_pass) {
-        e = cudaLaunchKernelEx(&cfg, first, m, maps[0], maps[1], maps[2]);
+        e = cudaLaunchKernelEx(&cfg, first, m, maps[0], maps[1], maps[2], maps[3]);
         if (e != cudaSuccess) return e;
     }
-    return cudaLaunchKernelEx(&cfg, second, m, maps[0], maps[1], maps[2]);
+    return cudaLaunchKernelEx(&cfg, second, m, maps[0], maps[1], maps[2], maps[3]);
 }
 
-cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[3],
+cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[4],
                        int dstate, bool bf16, bool i64, ssu_handle_s &handle, cudaStream_t st) {
 #define SSU_MMA(N_, ST_)                                              \
     return i64 ? launch_mma<N_, ST_, true>(m, w, maps, handle, st)    \
@@ -267,14 +267,14 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         m.q = q;
         m.seg = static_cast<int>(w.seg < INT_MAX ? w.seg : INT_MAX);
         m.slabs = static_cast<int>(s.headdim / kSlab);
-        m.out32 = aligned(out, 32) && p.out_b % 16 == 0 && p.out_h % 16 == 0;
         m.local = static_cast<float *>(workspace);
         m.decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.decay);
-        CUtensorMap maps[3];
-        if (w.stretches * w.columns <= INT_MAX &&
+        CUtensorMap maps[4];
+        if (w.stretches * w.ctas <= INT_MAX &&
             encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b) &&
             encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b) &&
-            encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b))
+            encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b) &&
+            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b))
             e = launch_mma(m, w, maps, static_cast<int>(s.dstate), bf16, i64, *handle, cs);
     }
     if (e == cudaErrorNotSupported)

@@ -8,7 +8,7 @@
 //   S'  = exp(s(0, Q]) S  +  sum_j (exp(s(j, Q]) dtv_j x_j) (x) B_j
 //
 // that is four matrix products per chunk and head: G = C B^T [Q x Q], I = C S^T [Q x P],
-// Y = M X [Q x P] with M = G times the masked decays, and U = B^T W [N x P] with W the weighted
+// Y = M X [Q x P] with M = G times the masked decays plus D on the diagonal, and U = B^T W [N x P] with W the weighted
 // tokens.  One CTA takes one head's stretch of a prompt, chunk after chunk, its state in
 // registers (thread n holds column n of the P = 64 rows).  G, I, U and Y accumulate in TMEM
 // (256 of the SM's 512 columns, so two CTAs share an SM and one's products run under the
@@ -47,8 +47,10 @@ namespace {
 
 constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
-constexpr int kPromptThreads = 256 + 32;  // two warpgroups for the elementwise work, one warp to issue
-constexpr int kHalf = kSlab / 2;  // a thread's share of its row: the two warpgroups halve it
+constexpr int kPair = 2;         // columns (a head's 64-row slab) per CTA, of one group
+constexpr int kCompute = kPair * 256;              // threads of the elementwise work
+constexpr int kPromptThreads = kCompute + 64;      // one warp to issue, one to store
+constexpr int kHalf = kSlab / 2;  // a thread's share of its row: two warpgroups halve it
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -56,7 +58,6 @@ struct PromptMmaParams {
     PromptParams q;
     int seg;              // chunks per stretch
     int slabs;            // headdim / 64
-    int out32;            // out's rows are 32-byte aligned
     float *local;         // [stretch][head * slabs + slab][64 p][N]
     float *decay;         // [stretch][head * slabs + slab]: log2 of the stretch's decay
 };
@@ -105,6 +106,14 @@ __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, u
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, unsigned src, int x, int y,
+                                          int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     map),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -126,17 +135,14 @@ __device__ __forceinline__ void tc_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 32 columns of the thread's TMEM lane.
-__device__ __forceinline__ void tc_load32(unsigned addr, unsigned (&r)[32]) {
+// 16 columns of the thread's TMEM lane.
+__device__ __forceinline__ void tc_load16(unsigned addr, unsigned (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[14]), "=r"(r[15])
         : "r"(addr)
         : "memory");
 }
@@ -151,16 +157,10 @@ __device__ __forceinline__ void tc_store16(unsigned addr, const unsigned (&r)[16
         : "memory");
 }
 
-__device__ __forceinline__ void tc_store32(unsigned addr, const unsigned (&r)[32]) {
+__device__ __forceinline__ void tc_store8(unsigned addr, const unsigned (&r)[8]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31, %32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 
@@ -229,15 +229,6 @@ __device__ __forceinline__ void widen16(const uint4 &w, float (&v)[8]) {
     }
 }
 
-// 32 bytes, one whole sector, by one thread.
-__device__ __forceinline__ void store_sector(void *dst, unsigned a, unsigned b, unsigned c,
-                                             unsigned d, unsigned e, unsigned f, unsigned g,
-                                             unsigned h) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
-                 "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
-
 // 2^x by the hardware's approximation (2 ulp), results below 2^-126 as 0: for weights that are
 // rounded to bf16 next.
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -248,21 +239,23 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 
 // ---- the kernel ------------------------------------------------------------------------
 
-// Shared memory: tiles first (1024-byte aligned), then the per-token values.  W's three parts take
-// the places of C and S once G and I are done.
+// Shared memory: tiles first (1024-byte aligned), then the per-token values.  x, S and W hold one
+// tile per column, side by side, as the two blocks of an operand 128 wide.
 template <int N>
 struct PromptSmem {
     static constexpr int kBlocks = N / 64;  // 64-column tiles of B and C
-    static constexpr int kC = 0;            // also W's first two parts
-    static constexpr int kB = 2 * kTileBytes;
+    static constexpr int kC = 0;
+    static constexpr int kB = kC + kBlocks * kTileBytes;
     static constexpr int kX = kB + kBlocks * kTileBytes;
-    static constexpr int kS = kX + kTileBytes;  // state, bf16 [n][64 p]; also W's third part
-    static constexpr int kVec = kS + kTileBytes;
-    // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4); two of
-    // them, for this chunk and the next
+    static constexpr int kS = kX + kPair * kTileBytes;    // state, bf16 [n][64 p]
+    static constexpr int kW = kS + kPair * N * 128;       // W's first part, second part,
+    static constexpr int kW3 = kW + 2 * kPair * kTileBytes;  // third part, tokens 64 .. 127
+    static constexpr int kVec = kW3 + kPair * kTileBytes / 2;
+    // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4); for this
+    // chunk and the next, for each column
     static constexpr int kVecFloats = 3 * kChunk + 4;
-    static constexpr int kBars = kVec + 2 * kVecFloats * 4;
-    static constexpr int kTotal = kBars + 64;
+    static constexpr int kBars = kVec + 2 * kPair * kVecFloats * 4;
+    static constexpr int kTotal = kBars + 128;
 };
 
 // The stretch `g` of the call: its prompt and first chunk.  All threads get the answer; false
@@ -336,176 +329,239 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
     if (lane == 31) vec[3 * kChunk + row / 32] = up;
 }
 
-// Roles.  Warp 8 issues: one of its threads starts the copies and the products, as their inputs
-// become ready.  Warps 0 .. 7 do the elementwise work; a thread's row (token of the chunk, TMEM
-// lane, column n of the state) is the same in both warpgroups, which halve each row's columns.
-// Per chunk, with the barrier that each hand-over uses:
+// Roles.  One thread starts the loads and the products as their inputs become ready, another the
+// stores.  Sixteen warps do the elementwise work, eight per column; a thread's row (token of the
+// chunk, TMEM lane, column n of the state) is the same in a column's two warpgroups, which halve
+// each row.  Per chunk, with the barrier that each hand-over uses:
 //
-//   issue:    [full, done] G, I -> [w] U -> next B, C -> [m] Y -> next X
-//   compute:  [x] W's parts in registers -> [g] W into C and S -> w; I scaled, D x added; M -> m;
-//             the next chunk's decays; [u] S advanced and published; [y] readout out -> done
+//   issue:    [c, done] I -> [b] G -> [w] U -> [g] next C -> [m] Y -> [u] next B -> [y] next X
+//   compute:  the next chunk's decays; [x, st] W -> w; [i] I scaled; [g] M -> m;
+//             [u] S advanced and published; [y] readout into W's place -> done
+//   store:    [done] readout out -> st
 //
-// so U runs under M, and the copies under everything that does not need them.
+// so U runs under M, and the copies under everything that does not need them.  (Readouts stored
+// by the threads themselves, a half row each, kept the shared-memory pipe busy for thousands of
+// cycles per chunk: 32 lines per instruction.)
 template <int N, typename ST, bool kIdx64, bool kFirst>
-__global__ void __launch_bounds__(kPromptThreads, 2)
+__global__ void __launch_bounds__(kPromptThreads, 1)
     ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
                           const __grid_constant__ CUtensorMap map_x,
                           const __grid_constant__ CUtensorMap map_b,
-                          const __grid_constant__ CUtensorMap map_c) {
+                          const __grid_constant__ CUtensorMap map_c,
+                          const __grid_constant__ CUtensorMap map_out) {
     using Smem = PromptSmem<N>;
     constexpr int kBlocks = Smem::kBlocks;
     constexpr int kParts = sizeof(ST) == 4 ? 3 : 2;  // bf16 parts of W
-    constexpr int kCompute = 256;
     extern __shared__ unsigned char raw[];
     __shared__ long long scan[kPromptThreads / 32 + 2];
     __shared__ unsigned tmem_slot;
     pdl_wait();
     const SsuParams &p = m.q.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int columns = p.nheads * m.slabs;  // CTAs per stretch: heads and slabs
-    const long long g = blockIdx.x / columns;
-    const int column = static_cast<int>(blockIdx.x - g * columns);
-    const int h = column / m.slabs, slab = column - h * m.slabs;
+    // Column c is head c / slabs, slab c % slabs; a group's columns go to CTAs in pairs, an odd
+    // last one alone (its CTA then works on it twice and keeps one result).
+    const int per_group = p.heads_per_group * m.slabs, pairs = (per_group + 1) / 2;
+    const int ctas = p.nheads / p.heads_per_group * pairs;  // per stretch
+    const long long g = blockIdx.x / ctas;
+    const int cta = static_cast<int>(blockIdx.x - g * ctas), grp = cta / pairs;
+    const int first_column = grp * per_group + 2 * (cta - grp * pairs);
+    const bool paired = 2 * (cta - grp * pairs) + 1 < per_group;
+    const int columns = p.nheads * m.slabs;
     long long b, index;
     if (!find_stretch<kIdx64>(m, g, !kFirst && blockIdx.x == 0, scan, b, index)) return;
     long long slot, begin, end;
     load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
-    const long long from = begin + index * m.seg * kChunk;
-    long long to = from + static_cast<long long>(m.seg) * kChunk;
-    const bool last = to >= end;
-    if (last) to = end;
+    const int from = static_cast<int>(begin + index * m.seg * kChunk);  // tokens fit 31 bits
+    const bool last = end - from <= static_cast<long long>(m.seg) * kChunk;
+    const int to = last ? static_cast<int>(end) : from + m.seg * kChunk;
     if (kFirst && last) return;  // nothing continues after a prompt's last stretch
 
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
-    const unsigned sS = base + Smem::kS;
-    float *const vecs = reinterpret_cast<float *>(raw + (base - smem_u32(raw)) + Smem::kVec);
-    const unsigned bar_full = base + Smem::kBars, bar_x = bar_full + 8, bar_g = bar_full + 16,
-                   bar_u = bar_full + 24, bar_y = bar_full + 32, bar_w = bar_full + 40,
-                   bar_m = bar_full + 48, bar_done = bar_full + 56;
-
+    const unsigned sS = base + Smem::kS, sW = base + Smem::kW, sW3 = base + Smem::kW3;
+    const unsigned bars = base + Smem::kBars;
+    const unsigned bar_b = bars, bar_c = bars + 8, bar_x = bars + 16, bar_g = bars + 24,
+                   bar_i = bars + 32, bar_u = bars + 40, bar_y = bars + 48, bar_w = bars + 56,
+                   bar_m = bars + 64, bar_done = bars + 72, bar_st = bars + 80;
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(bar_full + 8 * i, 1);
-        for (int i = 5; i < 8; ++i) mbar_init(bar_full + 8 * i, kCompute);
+        for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 7; i < 10; ++i) mbar_init(bars + 8 * i, kCompute);
+        mbar_init(bar_st, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    constexpr int kIssuer = kCompute / 32;  // the issuing warp
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_slot)),
-                     "r"(256)
+                     "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const unsigned tmem = tmem_slot;
-    // columns: G 0..127, U 128..191, I and then Y 192..255.  M takes G's place piece by piece: its
-    // tokens 0..63 (bf16 pairs) columns 0..31, 64..127 columns 64..95, each written by the
-    // warpgroup that has read the columns of G there.
-    const unsigned tG = tmem, tU = tmem + 128, tY = tmem + 192;
+    // TMEM columns: G (both columns'), M, I and then Y, U (each one after the other)
+    const unsigned tG = tmem_slot, tM = tG + 128, tY = tG + 256, tU = tG + 384;
     bool alive = true;
 
-    if (warp == 8) {
+    if (warp == kIssuer) {
         if (lane == 0) {
-            const int grp = group_of(h, p.group_magic);
-            auto load_bc = [&](long long tok) {
-                const int t = static_cast<int>(tok);
-                mbar_expect(bar_full, kTileBytes * kBlocks * (kFirst ? 1 : 2));
+            auto load_b = [&](int tok) {
+                mbar_expect(bar_b, kTileBytes * kBlocks);
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
-                    tma_load(sB + k * kTileBytes, &map_b, bar_full, k * 64, grp, t);
-                    if (!kFirst) tma_load(sC + k * kTileBytes, &map_c, bar_full, k * 64, grp, t);
+                for (int k = 0; k < kBlocks; ++k)
+                    tma_load(sB + k * kTileBytes, &map_b, bar_b, k * 64, grp,
+                             tok);
+            };
+            auto load_c = [&](int tok) {
+                mbar_expect(bar_c, kTileBytes * kBlocks);
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k)
+                    tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp,
+                             tok);
+            };
+            auto load_x = [&](int tok) {
+                mbar_expect(bar_x, kPair * kTileBytes);
+#pragma unroll
+                for (int k = 0; k < kPair; ++k) {
+                    const int c = first_column + (paired ? k : 0);
+                    tma_load(sX + k * kTileBytes, &map_x, bar_x, c % m.slabs * kSlab, c / m.slabs,
+                             tok);
                 }
             };
-            auto load_x = [&](long long tok) {
-                mbar_expect(bar_x, kTileBytes);
-                tma_load(sX, &map_x, bar_x, slab * kSlab, h, static_cast<int>(tok));
-            };
             if (from < to) {
-                load_bc(from);
                 load_x(from);
+                load_b(from);
+                if (!kFirst) load_c(from);
             }
             unsigned phase = 0;
-            for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
+            for (int tok = from; tok < to; tok += kChunk, phase ^= 1) {
                 const bool more = tok + kChunk < to;
                 if (!kFirst) {
-                    if (alive) alive = mbar_wait(bar_full, phase);
-                    if (alive) alive = mbar_wait(bar_done, phase);  // S and TMEM: see below
+                    if (alive) alive = mbar_wait(bar_c, phase);
+                    if (alive) alive = mbar_wait(bar_done, phase);  // S published, Y read
                     tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < N / 16; ++k) {
+                        const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                        mma_ss(tY, operand(sC + off, 0), operand(sS + k * 2048, N * 128),
+                               instruction(kPair * kSlab, false, true), k > 0);
+                    }
+                    tc_commit(bar_i);
+                    // G's readers of the chunk before were done before its M was
+                    if (alive) alive = mbar_wait(bar_b, phase);
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k) {
                         const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
                         mma_ss(tG, operand(sC + off, 0), operand(sB + off, 0),
                                instruction(kChunk, false, false), k > 0);
                     }
-#pragma unroll
-                    for (int k = 0; k < N / 16; ++k) {
-                        const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                        mma_ss(tY, operand(sC + off, 0), operand(sS + k * 2048, 0),
-                               instruction(kSlab, false, true), k > 0);
-                    }
                     tc_commit(bar_g);
+                } else if (alive) {
+                    alive = mbar_wait(bar_b, phase);
                 }
                 if (alive) alive = mbar_wait(bar_w, phase);
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kParts * kChunk / 16; ++k) {
-                    const int which = k / (kChunk / 16), kk = k % (kChunk / 16);
+                for (int k = 0; k < (kParts == 3 ? 20 : 16); ++k) {
+                    const int part = k / 8, kk = k % 8 + (part == 2 ? 4 : 0);
+                    const unsigned w = part < 2 ? sW + part * kPair * kTileBytes + kk * 2048
+                                                : sW3 + (kk - 4) * 2048;
                     mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
-                           operand((which < 2 ? sC + which * kTileBytes : sS) + kk * 2048, 0),
-                           instruction(kSlab, true, true), k > 0);
+                           operand(w, part < 2 ? kTileBytes : kTileBytes / 2),
+                           instruction(kPair * kSlab, true, true), k > 0);
                 }
                 tc_commit(bar_u);
                 if (kFirst) {  // U alone reads the tiles (x went through registers)
                     if (more) load_x(tok + kChunk);
                     if (alive) alive = mbar_wait(bar_u, phase);
-                    if (more) load_bc(tok + kChunk);
+                    if (more) load_b(tok + kChunk);
                     continue;
                 }
+                if (alive) alive = mbar_wait(bar_g, phase);
+                if (more) load_c(tok + kChunk);
                 if (alive) alive = mbar_wait(bar_m, phase);
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k)
-                    mma_ts(tY, tG + (k < 4 ? 8 * k : 32 + 8 * k), operand(sX + k * 2048, 0),
-                           instruction(kSlab, false, true), true);
+                for (int c = 0; c < kPair; ++c)
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k)
+                        mma_ts(tY + c * kSlab, tM + c * 64 + 8 * k,
+                               operand(sX + c * kTileBytes + k * 2048, 0),
+                               instruction(kSlab, false, true), true);
                 tc_commit(bar_y);
                 if (alive) alive = mbar_wait(bar_u, phase);
-                if (more) load_bc(tok + kChunk);
+                if (more) load_b(tok + kChunk);
                 if (alive) alive = mbar_wait(bar_y, phase);
                 if (more) load_x(tok + kChunk);
             }
         }
         __syncwarp();
+    } else if (warp == kIssuer + 1) {
+        // Whole chunks go out as tiles; the compute threads store a prompt's last, shorter one.
+        if (!kFirst && lane == 0) {
+            if (alive) alive = mbar_wait(bar_done, 0);  // the start's
+            unsigned phase = 1;
+            for (int tok = from; tok + kChunk <= to; tok += kChunk, phase ^= 1) {
+                if (alive) alive = mbar_wait(bar_done, phase);
+#pragma unroll
+                for (int k = 0; k < kPair; ++k) {
+                    const int c = first_column + k;
+                    if (k == 0 || paired)
+                        tma_store(&map_out, sW + k * kTileBytes, c % m.slabs * kSlab, c / m.slabs,
+                                  tok);
+                }
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(bar_st);
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
     } else {
-        const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
+        const int which = warp >> 3, part = (warp >> 2) & 1, quarter = warp & 3;
+        const int row = 32 * quarter + lane;
+        const bool keeps = which == 0 || paired;
+        const int column = first_column + (paired ? which : 0);
+        const int h = column / m.slabs, slab = column - h * m.slabs;
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
-        const bool fresh = m.q.fresh && m.q.fresh[b] != 0;
+        const unsigned myX = sX + which * kTileBytes, myS = sS + which * N * 128;
+        const unsigned myY = tY + which * kSlab + kHalf * part + lanes;
+        const unsigned myU = tU + which * kSlab + kHalf * part + lanes;
+        float *const vecs =
+            reinterpret_cast<float *>(raw + (base - smem_u32(raw)) + Smem::kVec) +
+            which * 2 * Smem::kVecFloats;
+        auto column_sync = [&]() {
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "n"(kCompute / kPair) : "memory");
+        };
         const float bias = __ldg(p.dt_bias + h * p.bias_h);
         const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
         const float D = __ldg(p.D + h * p.D_h);
-        const __nv_bfloat16 *const dt_col = p.dt + h * p.dt_h;
-        // The second warpgroup has less of M and works the decays out, a chunk ahead.
-        float dt_next = 0.0f;
+        // The second warpgroup has less of M and works the decays out, a chunk ahead.  dt waits as
+        // raw bits: a conversion right behind its load would wait for it.
+        const unsigned short *const dt_col =
+            reinterpret_cast<const unsigned short *>(p.dt) + h * p.dt_h;
+        unsigned dt_next = 0;
         if (part == 1) {
-            float dt = 0.0f;
-            if (from + row < to) dt = __bfloat162float(dt_col[(from + row) * p.dt_b]);
-            if (from + kChunk + row < to)
-                dt_next = __bfloat162float(dt_col[(from + kChunk + row) * p.dt_b]);
-            chunk_decays(vecs, from + row < to, dt, bias, A2, row, lane);
+            unsigned dt = 0;
+            if (from + row < to) dt = dt_col[(from + row) * p.dt_b];
+            if (from + kChunk + row < to) dt_next = dt_col[(from + kChunk + row) * p.dt_b];
+            chunk_decays(vecs, from + row < to, __uint_as_float(dt << 16), bias, A2, row, lane);
         }
 
         // The state a stretch starts from: the thread holds S[32 part .. 32 part + 31][row].
         float S[kHalf];
         const bool own = row < N;
-        ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                          static_cast<long long>(slab * kSlab + kHalf * part) * p.st_row + row;
+        auto state_at = [&](int i) {
+            return static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
+                   static_cast<long long>(slab * kSlab + kHalf * part + i) * p.st_row + row;
+        };
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) S[i] = 0.0f;
         if (!kFirst && own) {
-            if (!fresh) {
+            if (!(m.q.fresh && m.q.fresh[b] != 0)) {
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(state[i * p.st_row]);
+                for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(*state_at(i));
             }
             for (long long k = g - index; k < g; ++k) {
                 const float *loc =
@@ -515,12 +571,11 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
                 for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
             }
         }
-        // The state as the next chunk's bf16 operand; then the issuing warp may use it and TMEM.
-        auto publish = [&]() {
+        auto publish = [&]() {  // the state as the next chunk's bf16 operand
             if (own) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    store_smem16(swizzled(sS, row, 4 * part + c),
+                    store_smem16(swizzled(myS, row, 4 * part + c),
                                  make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
                                             f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
                                             f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
@@ -532,44 +587,40 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
             publish();
             mbar_arrive(bar_done);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");  // the decays
+        column_sync();  // the decays
 
         float stretch_decay = 0.0f;  // log2
         unsigned phase = 0;
-        for (long long tok = from; tok < to; tok += kChunk, phase ^= 1) {
-            const int valid = static_cast<int>(to - tok < kChunk ? to - tok : kChunk);
+        for (int tok = from; tok < to; tok += kChunk, phase ^= 1) {
+            const int valid = to - tok < kChunk ? to - tok : kChunk;
             float *const v0 = vecs + phase * Smem::kVecFloats;
             const float2 *const pre = reinterpret_cast<const float2 *>(v0 + kChunk);
-            const float4 t4 = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
-            const float t[4] = {t4.x, t4.y, t4.z, t4.w};
-            float later = 0.0f, earlier = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k > quarter) later += t[k];
-                if (k < quarter) earlier += t[k];
+            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
+                const float dt = __uint_as_float(dt_next << 16);
+                if (tok + 2 * kChunk + row < to)
+                    dt_next = dt_col[(tok + 2 * kChunk + row) * p.dt_b];
+                chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
+                             bias, A2, row, lane);
             }
-            const float up = pre[row].x;
-            const float w = v0[row] * exp2f(later);  // the token's weight in the chunk's last state
-            const float chunk_decay = (t[0] + t[1]) + (t[2] + t[3]);
-            stretch_decay += chunk_decay;
+            // the token's weight in the chunk's last state: from its own 32 tokens' end onwards
+            float w = v0[row];
+            {
+                const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+                w *= exp2f((quarter < 1 ? t.y : 0.0f) + (quarter < 2 ? t.z : 0.0f) +
+                           (quarter < 3 ? t.w : 0.0f));
+            }
             if (alive) alive = mbar_wait(bar_x, phase);
-            uint4 xr[4];  // the thread's half of its token's x; zeros past the prompt's end
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                xr[c] = row < valid ? load_smem16(swizzled(sX, row, 4 * part + c))
-                                    : make_uint4(0, 0, 0, 0);
-            // C and S are W's to take once G and I are done
-            if (alive) alive = mbar_wait(kFirst ? bar_full : bar_g, phase);
-            __syncwarp();
-            tc_fence_after();
+            // W's place is free: its readout has left (the chunk before was a whole one)
+            if (!kFirst && tok > from && alive) alive = mbar_wait(bar_st, phase ^ 1);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x[8];
-                widen16(xr[c], x);
+                widen16(load_smem16(swizzled(myX, row, 4 * part + c)), x);
                 unsigned bits[kParts][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float2 f = __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
+                    if (row >= valid) f = make_float2(0.0f, 0.0f);  // the next prompt's x
 #pragma unroll
                     for (int k = 0; k < kParts; ++k) {
                         bits[k][i] = f2_to_bf2(f.x, f.y);
@@ -578,164 +629,192 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kParts; ++k)
-                    store_smem16(swizzled(k < 2 ? sC + k * kTileBytes : sS, row, 4 * part + c),
-                                 make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
+                for (int k = 0; k < 2; ++k)
+                    store_smem16(
+                        swizzled(sW + (k * kPair + which) * kTileBytes, row, 4 * part + c),
+                        make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
+                if constexpr (kParts == 3)
+                    if (row >= 64)
+                        store_smem16(
+                            swizzled(sW3 + which * (kTileBytes / 2), row - 64, 4 * part + c),
+                            make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
             }
-            if (row >= valid) {  // tokens of the next prompt: X and B must not bring them in
+            if (valid < kChunk) {  // tokens of the next prompt: X and B must not bring them in
+                if (alive) alive = mbar_wait(bar_b, phase);
+                if (row >= valid) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    store_smem16(swizzled(sX, row, 4 * part + c), make_uint4(0, 0, 0, 0));
+                    for (int c = 0; c < 4; ++c) {
+                        store_smem16(swizzled(myX, row, 4 * part + c), make_uint4(0, 0, 0, 0));
+                        if (which == 0)
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k)
-                        store_smem16(swizzled(sB + k * kTileBytes, row, 4 * part + c),
-                                     make_uint4(0, 0, 0, 0));
+                            for (int k = 0; k < kBlocks; ++k)
+                                store_smem16(swizzled(sB + k * kTileBytes, row, 4 * part + c),
+                                             make_uint4(0, 0, 0, 0));
+                    }
                 }
             }
             fence_async_smem();
             mbar_arrive(bar_w);
             if (!kFirst) {
-                // The state's share of the readout and D x, where Y will add to them
-                const float fi = exp2f(up + earlier);
-                unsigned ii[32];
-                tc_load32(tY + lanes + kHalf * part, ii);
-                tc_wait_ld();
+                // The state's share of the readout, where Y will add to it
+                const float up = pre[row].x;
+                const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+                const float fi = exp2f(up + ((quarter > 0 ? t.x : 0.0f) +
+                                             (quarter > 1 ? t.y : 0.0f) +
+                                             (quarter > 2 ? t.z : 0.0f)));
+                if (alive) alive = mbar_wait(bar_i, phase);
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[8];
-                    widen16(xr[c], x);
+                for (int piece = 0; piece < 2; ++piece) {
+                    unsigned ii[16];
+                    tc_load16(myY + 16 * piece, ii);
+                    tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = __ffma2_rn(
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = __fmul2_rn(
                             make_float2(fi, fi),
-                            make_float2(__uint_as_float(ii[8 * c + 2 * i]),
-                                        __uint_as_float(ii[8 * c + 2 * i + 1])),
-                            __fmul2_rn(make_float2(D, D), make_float2(x[2 * i], x[2 * i + 1])));
-                        ii[8 * c + 2 * i] = __float_as_uint(y.x);
-                        ii[8 * c + 2 * i + 1] = __float_as_uint(y.y);
+                            make_float2(__uint_as_float(ii[i]), __uint_as_float(ii[i + 1])));
+                        ii[i] = __float_as_uint(y.x);
+                        ii[i + 1] = __float_as_uint(y.y);
                     }
+                    tc_store16(myY + 16 * piece, ii);
                 }
-                tc_store32(tY + lanes + kHalf * part, ii);
                 // M = G times decays, two blocks of 32 columns per warpgroup
+                if (alive) alive = mbar_wait(bar_g, phase);
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int cb = 2 * part + half;
-                    unsigned mm[16];
-                    if (cb <= quarter) {
-                        unsigned gg[32];
-                        tc_load32(tG + lanes + 32 * cb, gg);
-                        tc_wait_ld();
-                        if (cb < quarter) {
-                            float between = 0.0f;
+                    float f = 0.0f;
+                    if (cb < quarter)  // the blocks between the columns' and the row's
+                        f = exp2f(up + ((cb < 1 && quarter > 1 ? t.y : 0.0f) +
+                                        (cb < 2 && quarter > 2 ? t.z : 0.0f)));
 #pragma unroll
-                            for (int k = 1; k < 4; ++k)
-                                if (k > cb && k < quarter) between += t[k];
-                            const float f = exp2f(up + between);
-                            const float4 *vv = reinterpret_cast<const float4 *>(v0 + 32 * cb);
+                    for (int piece = 0; piece < 2; ++piece) {
+                        const int col = 32 * cb + 16 * piece;
+                        unsigned mm[8];
+                        if (cb <= quarter) {
+                            unsigned gg[16];
+                            tc_load16(tG + lanes + col, gg);
+                            tc_wait_ld();
+                            if (cb < quarter) {
+                                const float4 *vv = reinterpret_cast<const float4 *>(v0 + col);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 q = vv[j];
-                                const float2 lo = __fmul2_rn(
-                                    make_float2(__uint_as_float(gg[4 * j]),
-                                                __uint_as_float(gg[4 * j + 1])),
-                                    __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
-                                const float2 hi = __fmul2_rn(
-                                    make_float2(__uint_as_float(gg[4 * j + 2]),
-                                                __uint_as_float(gg[4 * j + 3])),
-                                    __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
-                                mm[2 * j] = f2_to_bf2(lo.x, lo.y);
-                                mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
+                                for (int j = 0; j < 4; ++j) {
+                                    const float4 q = vv[j];
+                                    const float2 lo = __fmul2_rn(
+                                        make_float2(__uint_as_float(gg[4 * j]),
+                                                    __uint_as_float(gg[4 * j + 1])),
+                                        __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
+                                    const float2 hi = __fmul2_rn(
+                                        make_float2(__uint_as_float(gg[4 * j + 2]),
+                                                    __uint_as_float(gg[4 * j + 3])),
+                                        __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
+                                    mm[2 * j] = f2_to_bf2(lo.x, lo.y);
+                                    mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
+                                }
+                            } else {
+                                const float4 *pp = reinterpret_cast<const float4 *>(pre + col);
+                                const int edge = lane - 16 * piece;  // the last column kept
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float4 q = pp[j];  // (prefix, dtv) of two columns
+                                    const float e0 = exp2_ftz(up - q.x) *
+                                                     (q.y * __uint_as_float(gg[2 * j]));
+                                    const float e1 = exp2_ftz(up - q.z) *
+                                                     (q.w * __uint_as_float(gg[2 * j + 1]));
+                                    // on the diagonal, D x of the token itself
+                                    mm[j] = f2_to_bf2(2 * j < edge    ? e0
+                                                      : 2 * j == edge ? e0 + D
+                                                                      : 0.0f,
+                                                      2 * j + 1 < edge    ? e1
+                                                      : 2 * j + 1 == edge ? e1 + D
+                                                                          : 0.0f);
+                                }
                             }
                         } else {
-                            const float4 *pp = reinterpret_cast<const float4 *>(pre + 32 * cb);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float4 q = pp[j];  // (prefix, dtv) of columns 2j, 2j + 1
-                                const float e0 = exp2_ftz(up - q.x) *
-                                                 (q.y * __uint_as_float(gg[2 * j]));
-                                const float e1 = exp2_ftz(up - q.z) *
-                                                 (q.w * __uint_as_float(gg[2 * j + 1]));
-                                mm[j] = f2_to_bf2(2 * j <= lane ? e0 : 0.0f,
-                                                  2 * j + 1 <= lane ? e1 : 0.0f);
-                            }
+                            for (int j = 0; j < 8; ++j) mm[j] = 0;
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) mm[j] = 0;
+                        tc_store8(tM + which * 64 + lanes + col / 2, mm);
                     }
-                    tc_store16(tG + lanes + 64 * part + 16 * half, mm);
                 }
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar_m);
             }
-            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
-                const float dt = dt_next;
-                if (tok + 2 * kChunk + row < to)
-                    dt_next = __bfloat162float(dt_col[(tok + 2 * kChunk + row) * p.dt_b]);
-                chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
-                             bias, A2, row, lane);
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
-            const float f = exp2f(chunk_decay);
+            const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+            const float chunk_decay = (t.x + t.y) + (t.z + t.w), f = exp2f(chunk_decay);
+            stretch_decay += chunk_decay;
+            column_sync();  // the next decays
             if (alive) alive = mbar_wait(bar_u, phase);
             __syncwarp();
             tc_fence_after();
-            {
-                unsigned uu[32];
-                tc_load32(tU + lanes + kHalf * part, uu);
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece) {
+                unsigned uu[16];
+                tc_load16(myU + 16 * piece, uu);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < kHalf; i += 2) {
-                    const float2 s = __ffma2_rn(
-                        make_float2(S[i], S[i + 1]), make_float2(f, f),
+                for (int i = 0; i < 16; i += 2) {
+                    float *const s = S + 16 * piece + i;
+                    const float2 v = __ffma2_rn(
+                        make_float2(s[0], s[1]), make_float2(f, f),
                         make_float2(__uint_as_float(uu[i]), __uint_as_float(uu[i + 1])));
-                    S[i] = s.x;
-                    S[i + 1] = s.y;
+                    s[0] = v.x;
+                    s[1] = v.y;
                 }
             }
+            tc_fence_before();
             if (kFirst) continue;
             publish();
             if (alive) alive = mbar_wait(bar_y, phase);
             __syncwarp();
             tc_fence_after();
-            unsigned yy[32];
-            tc_load32(tY + lanes + kHalf * part, yy);
-            tc_wait_ld();
-            tc_fence_before();
-            mbar_arrive(bar_done);
-            if (row < valid) {
-                unsigned o[16];
+            unsigned o[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[i] = f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+            for (int piece = 0; piece < 2; ++piece) {
+                unsigned yy[16];
+                tc_load16(myY + 16 * piece, yy);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[8 * piece + i] =
+                        f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+            }
+            if (valid == kChunk) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    store_smem16(swizzled(sW + which * kTileBytes, row, 4 * part + c),
+                                 make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+                fence_async_smem();
+            } else if (row < valid && keeps) {
                 __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
                                            slab * kSlab + kHalf * part;
-                if (m.out32) {
-                    store_sector(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
-                    store_sector(dst + 16, o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]);
-                } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        reinterpret_cast<uint4 *>(dst)[c] =
-                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                }
+                for (int c = 0; c < 4; ++c)
+                    reinterpret_cast<uint4 *>(dst)[c] =
+                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
+            tc_fence_before();
+            mbar_arrive(bar_done);
         }
 
-        if (own) {
+        if (own && keeps) {
             if (kFirst) {
                 float *loc = m.local + ((g * columns + column) * kSlab + kHalf * part) * N + row;
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) __stcg(loc + i * N, S[i]);
-                if (tid == 0) __stcg(m.decay + g * columns + column, stretch_decay);
+                if (part == 0 && row == 0) __stcg(m.decay + g * columns + column, stretch_decay);
             } else if (last) {
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) {
                     if constexpr (sizeof(ST) == 4)
-                        state[i * p.st_row] = S[i];
+                        *state_at(i) = S[i];
                     else
-                        state[i * p.st_row] = __float2bfloat16(S[i]);
+                        *state_at(i) = __float2bfloat16(S[i]);
                 }
             }
         }
@@ -743,9 +822,9 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
     if (!alive) atomicOr(&p.err[2], 1u);
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kIssuer) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tG), "r"(512)
                      : "memory");
     }
 }
