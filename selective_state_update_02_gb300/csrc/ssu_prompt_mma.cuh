@@ -106,6 +106,12 @@ __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, u
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, unsigned src, int x, int y,
                                           int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -240,16 +246,18 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 // ---- the kernel ------------------------------------------------------------------------
 
 // Shared memory: tiles first (1024-byte aligned), then the per-token values.  x, S and W hold one
-// tile per column, side by side, as the two blocks of an operand 128 wide.
+// tile per column, side by side, as the two blocks of an operand 128 wide.  B has two places (the
+// next chunk's G is formed before this one's U is done); W's second part takes S's place, which
+// I has read by then, and gives it back when U is done; readouts leave from x's place.
 template <int N>
 struct PromptSmem {
     static constexpr int kBlocks = N / 64;  // 64-column tiles of B and C
     static constexpr int kC = 0;
     static constexpr int kB = kC + kBlocks * kTileBytes;
-    static constexpr int kX = kB + kBlocks * kTileBytes;
-    static constexpr int kS = kX + kPair * kTileBytes;    // state, bf16 [n][64 p]
-    static constexpr int kW = kS + kPair * N * 128;       // W's first part, second part,
-    static constexpr int kW3 = kW + 2 * kPair * kTileBytes;  // third part, tokens 64 .. 127
+    static constexpr int kX = kB + 2 * kBlocks * kTileBytes;
+    static constexpr int kW1 = kX + kPair * kTileBytes;
+    static constexpr int kW2 = kW1 + kPair * kTileBytes;  // also S: bf16 [n][64 p]
+    static constexpr int kW3 = kW2 + kPair * kTileBytes;  // tokens 64 .. 127
     static constexpr int kVec = kW3 + kPair * kTileBytes / 2;
     // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4); for this
     // chunk and the next, for each column
@@ -334,14 +342,14 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
 // chunk, TMEM lane, column n of the state) is the same in a column's two warpgroups, which halve
 // each row.  Per chunk, with the barrier that each hand-over uses:
 //
-//   issue:    [c, done] I -> [b] G -> [w] U -> [g] next C -> [m] Y -> [u] next B -> [y] next X
-//   compute:  the next chunk's decays; [x, st] W -> w; [i] I scaled; [g] M -> m;
-//             [u] S advanced and published; [y] readout into W's place -> done
-//   store:    [done] readout out -> st
+//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [b, c] next G -> g; [w] U -> u
+//   compute:  [g] M, [i] I scaled -> m; [x] W -> w; the next chunk's decays; [y] readout into x's
+//             place -> r; [u] S advanced and published -> done
+//   store:    [r] readout out, then next x
 //
-// so U runs under M, and the copies under everything that does not need them.  (Readouts stored
-// by the threads themselves, a half row each, kept the shared-memory pipe busy for thousands of
-// cycles per chunk: 32 lines per instruction.)
+// so Y runs under W, U under the readout and the decays, I and the loads under M.  (Readouts
+// stored by the threads themselves, a half row each, kept the shared-memory pipe busy for
+// thousands of cycles per chunk: 32 lines per instruction.)
 template <int N, typename ST, bool kIdx64, bool kFirst>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
@@ -378,15 +386,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
-    const unsigned sS = base + Smem::kS, sW = base + Smem::kW, sW3 = base + Smem::kW3;
+    const unsigned sW1 = base + Smem::kW1, sW2 = base + Smem::kW2, sW3 = base + Smem::kW3;
+    const unsigned sS = sW2;
     const unsigned bars = base + Smem::kBars;
     const unsigned bar_b = bars, bar_c = bars + 8, bar_x = bars + 16, bar_g = bars + 24,
                    bar_i = bars + 32, bar_u = bars + 40, bar_y = bars + 48, bar_w = bars + 56,
-                   bar_m = bars + 64, bar_done = bars + 72, bar_st = bars + 80;
+                   bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80;
     if (tid == 0) {
         for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
-        for (int i = 7; i < 10; ++i) mbar_init(bars + 8 * i, kCompute);
-        mbar_init(bar_st, 1);
+        for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = kCompute / 32;  // the issuing warp
@@ -404,42 +412,64 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const unsigned tG = tmem_slot, tM = tG + 128, tY = tG + 256, tU = tG + 384;
     bool alive = true;
 
+    constexpr int kBBytes = kBlocks * kTileBytes;  // one place of B
+    auto load_x = [&](int tok) {
+        mbar_expect(bar_x, kPair * kTileBytes);
+#pragma unroll
+        for (int k = 0; k < kPair; ++k) {
+            const int c = first_column + (paired ? k : 0);
+            tma_load(sX + k * kTileBytes, &map_x, bar_x, c % m.slabs * kSlab, c / m.slabs, tok);
+        }
+    };
     if (warp == kIssuer) {
         if (lane == 0) {
-            auto load_b = [&](int tok) {
-                mbar_expect(bar_b, kTileBytes * kBlocks);
+            auto load_b = [&](int tok, unsigned place) {
+                mbar_expect(bar_b, kBBytes);
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k)
-                    tma_load(sB + k * kTileBytes, &map_b, bar_b, k * 64, grp,
-                             tok);
+                    tma_load(sB + place * kBBytes + k * kTileBytes, &map_b, bar_b, k * 64, grp, tok);
             };
             auto load_c = [&](int tok) {
-                mbar_expect(bar_c, kTileBytes * kBlocks);
+                mbar_expect(bar_c, kBBytes);
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k)
-                    tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp,
-                             tok);
+                    tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp, tok);
             };
-            auto load_x = [&](int tok) {
-                mbar_expect(bar_x, kPair * kTileBytes);
+            auto product_g = [&](unsigned place) {
 #pragma unroll
-                for (int k = 0; k < kPair; ++k) {
-                    const int c = first_column + (paired ? k : 0);
-                    tma_load(sX + k * kTileBytes, &map_x, bar_x, c % m.slabs * kSlab, c / m.slabs,
-                             tok);
+                for (int k = 0; k < N / 16; ++k) {
+                    const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
+                    mma_ss(tG, operand(sC + off, 0), operand(sB + place * kBBytes + off, 0),
+                           instruction(kChunk, false, false), k > 0);
                 }
+                tc_commit(bar_g);
             };
             if (from < to) {
-                load_x(from);
-                load_b(from);
+                load_b(from, 0);
                 if (!kFirst) load_c(from);
+                load_x(from);
+                if (!kFirst) {
+                    alive = mbar_wait(bar_b, 0);
+                    if (alive) alive = mbar_wait(bar_c, 0);
+                    product_g(0);
+                }
             }
             unsigned phase = 0;
             for (int tok = from; tok < to; tok += kChunk, phase ^= 1) {
                 const bool more = tok + kChunk < to;
+                // the next B takes the place that the chunk before this one's U has left
+                if (kFirst && alive) alive = mbar_wait(bar_b, phase);
+                if (more) load_b(tok + kChunk, phase ^ 1);
                 if (!kFirst) {
-                    if (alive) alive = mbar_wait(bar_c, phase);
-                    if (alive) alive = mbar_wait(bar_done, phase);  // S published, Y read
+                    if (tok + 2 * kChunk < to) {  // from HBM into L2 long before it is waited for
+#pragma unroll
+                        for (int k = 0; k < kPair; ++k) {
+                            const int c = first_column + (paired ? k : 0);
+                            tma_prefetch(&map_x, c % m.slabs * kSlab, c / m.slabs,
+                                         tok + 2 * kChunk);
+                        }
+                    }
+                    if (alive) alive = mbar_wait(bar_done, phase);  // S published, Y and U read
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k) {
@@ -448,72 +478,60 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                instruction(kPair * kSlab, false, true), k > 0);
                     }
                     tc_commit(bar_i);
-                    // G's readers of the chunk before were done before its M was
-                    if (alive) alive = mbar_wait(bar_b, phase);
+                    if (alive) alive = mbar_wait(bar_i, phase);
+                    if (more) load_c(tok + kChunk);
+                    if (alive) alive = mbar_wait(bar_m, phase);
+                    if (alive) alive = mbar_wait(bar_x, phase);
+                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < N / 16; ++k) {
-                        const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                        mma_ss(tG, operand(sC + off, 0), operand(sB + off, 0),
-                               instruction(kChunk, false, false), k > 0);
+                    for (int c = 0; c < kPair; ++c)
+#pragma unroll
+                        for (int k = 0; k < kChunk / 16; ++k)
+                            mma_ts(tY + c * kSlab, tM + c * 64 + 8 * k,
+                                   operand(sX + c * kTileBytes + k * 2048, 0),
+                                   instruction(kSlab, false, true), true);
+                    tc_commit(bar_y);
+                    if (more) {  // every reader of G has passed m
+                        if (alive) alive = mbar_wait(bar_b, phase ^ 1);
+                        if (alive) alive = mbar_wait(bar_c, phase ^ 1);
+                        product_g(phase ^ 1);
                     }
-                    tc_commit(bar_g);
-                } else if (alive) {
-                    alive = mbar_wait(bar_b, phase);
                 }
                 if (alive) alive = mbar_wait(bar_w, phase);
                 tc_fence_after();
+                const unsigned b_now = sB + phase * kBBytes;
 #pragma unroll
                 for (int k = 0; k < (kParts == 3 ? 20 : 16); ++k) {
                     const int part = k / 8, kk = k % 8 + (part == 2 ? 4 : 0);
-                    const unsigned w = part < 2 ? sW + part * kPair * kTileBytes + kk * 2048
-                                                : sW3 + (kk - 4) * 2048;
-                    mma_ss(tU, operand(sB + kk * 2048, N == 128 ? kTileBytes : 0),
+                    const unsigned w = part == 0   ? sW1 + kk * 2048
+                                       : part == 1 ? sW2 + kk * 2048
+                                                   : sW3 + (kk - 4) * 2048;
+                    mma_ss(tU, operand(b_now + kk * 2048, N == 128 ? kTileBytes : 0),
                            operand(w, part < 2 ? kTileBytes : kTileBytes / 2),
                            instruction(kPair * kSlab, true, true), k > 0);
                 }
                 tc_commit(bar_u);
-                if (kFirst) {  // U alone reads the tiles (x went through registers)
-                    if (more) load_x(tok + kChunk);
-                    if (alive) alive = mbar_wait(bar_u, phase);
-                    if (more) load_b(tok + kChunk);
-                    continue;
-                }
-                if (alive) alive = mbar_wait(bar_g, phase);
-                if (more) load_c(tok + kChunk);
-                if (alive) alive = mbar_wait(bar_m, phase);
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < kPair; ++c)
-#pragma unroll
-                    for (int k = 0; k < kChunk / 16; ++k)
-                        mma_ts(tY + c * kSlab, tM + c * 64 + 8 * k,
-                               operand(sX + c * kTileBytes + k * 2048, 0),
-                               instruction(kSlab, false, true), true);
-                tc_commit(bar_y);
+                if (kFirst && more) load_x(tok + kChunk);  // x is in registers, or past them
                 if (alive) alive = mbar_wait(bar_u, phase);
-                if (more) load_b(tok + kChunk);
-                if (alive) alive = mbar_wait(bar_y, phase);
-                if (more) load_x(tok + kChunk);
             }
         }
         __syncwarp();
     } else if (warp == kIssuer + 1) {
         // Whole chunks go out as tiles; the compute threads store a prompt's last, shorter one.
         if (!kFirst && lane == 0) {
-            if (alive) alive = mbar_wait(bar_done, 0);  // the start's
-            unsigned phase = 1;
+            unsigned phase = 0;
             for (int tok = from; tok + kChunk <= to; tok += kChunk, phase ^= 1) {
-                if (alive) alive = mbar_wait(bar_done, phase);
+                if (alive) alive = mbar_wait(bar_r, phase);
 #pragma unroll
                 for (int k = 0; k < kPair; ++k) {
                     const int c = first_column + k;
                     if (k == 0 || paired)
-                        tma_store(&map_out, sW + k * kTileBytes, c % m.slabs * kSlab, c / m.slabs,
+                        tma_store(&map_out, sX + k * kTileBytes, c % m.slabs * kSlab, c / m.slabs,
                                   tok);
                 }
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                mbar_arrive(bar_st);
+                if (tok + kChunk < to) load_x(tok + kChunk);
             }
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
@@ -595,51 +613,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int valid = to - tok < kChunk ? to - tok : kChunk;
             float *const v0 = vecs + phase * Smem::kVecFloats;
             const float2 *const pre = reinterpret_cast<const float2 *>(v0 + kChunk);
-            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
-                const float dt = __uint_as_float(dt_next << 16);
-                if (tok + 2 * kChunk + row < to)
-                    dt_next = dt_col[(tok + 2 * kChunk + row) * p.dt_b];
-                chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
-                             bias, A2, row, lane);
-            }
-            // the token's weight in the chunk's last state: from its own 32 tokens' end onwards
-            float w = v0[row];
-            {
-                const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
-                w *= exp2f((quarter < 1 ? t.y : 0.0f) + (quarter < 2 ? t.z : 0.0f) +
-                           (quarter < 3 ? t.w : 0.0f));
-            }
-            if (alive) alive = mbar_wait(bar_x, phase);
-            // W's place is free: its readout has left (the chunk before was a whole one)
-            if (!kFirst && tok > from && alive) alive = mbar_wait(bar_st, phase ^ 1);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float x[8];
-                widen16(load_smem16(swizzled(myX, row, 4 * part + c)), x);
-                unsigned bits[kParts][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float2 f = __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
-                    if (row >= valid) f = make_float2(0.0f, 0.0f);  // the next prompt's x
-#pragma unroll
-                    for (int k = 0; k < kParts; ++k) {
-                        bits[k][i] = f2_to_bf2(f.x, f.y);
-                        f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k][i] << 16),
-                                                      -__uint_as_float(bits[k][i] & 0xffff0000u)));
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    store_smem16(
-                        swizzled(sW + (k * kPair + which) * kTileBytes, row, 4 * part + c),
-                        make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
-                if constexpr (kParts == 3)
-                    if (row >= 64)
-                        store_smem16(
-                            swizzled(sW3 + which * (kTileBytes / 2), row - 64, 4 * part + c),
-                            make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
-            }
             if (valid < kChunk) {  // tokens of the next prompt: X and B must not bring them in
+                if (alive) alive = mbar_wait(bar_x, phase);
                 if (alive) alive = mbar_wait(bar_b, phase);
                 if (row >= valid) {
 #pragma unroll
@@ -648,38 +623,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         if (which == 0)
 #pragma unroll
                             for (int k = 0; k < kBlocks; ++k)
-                                store_smem16(swizzled(sB + k * kTileBytes, row, 4 * part + c),
+                                store_smem16(swizzled(sB + phase * kBBytes + k * kTileBytes, row,
+                                                      4 * part + c),
                                              make_uint4(0, 0, 0, 0));
                     }
                 }
+                fence_async_smem();
             }
-            fence_async_smem();
-            mbar_arrive(bar_w);
             if (!kFirst) {
-                // The state's share of the readout, where Y will add to it
                 const float up = pre[row].x;
                 const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
-                const float fi = exp2f(up + ((quarter > 0 ? t.x : 0.0f) +
-                                             (quarter > 1 ? t.y : 0.0f) +
-                                             (quarter > 2 ? t.z : 0.0f)));
-                if (alive) alive = mbar_wait(bar_i, phase);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int piece = 0; piece < 2; ++piece) {
-                    unsigned ii[16];
-                    tc_load16(myY + 16 * piece, ii);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 y = __fmul2_rn(
-                            make_float2(fi, fi),
-                            make_float2(__uint_as_float(ii[i]), __uint_as_float(ii[i + 1])));
-                        ii[i] = __float_as_uint(y.x);
-                        ii[i + 1] = __float_as_uint(y.y);
-                    }
-                    tc_store16(myY + 16 * piece, ii);
-                }
                 // M = G times decays, two blocks of 32 columns per warpgroup
                 if (alive) alive = mbar_wait(bar_g, phase);
                 __syncwarp();
@@ -741,14 +694,110 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         tc_store8(tM + which * 64 + lanes + col / 2, mm);
                     }
                 }
+                // The state's share of the readout, where Y will add to it
+                const float fi = exp2f(up + ((quarter > 0 ? t.x : 0.0f) +
+                                             (quarter > 1 ? t.y : 0.0f) +
+                                             (quarter > 2 ? t.z : 0.0f)));
+                if (alive) alive = mbar_wait(bar_i, phase);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll
+                for (int piece = 0; piece < 2; ++piece) {
+                    unsigned ii[16];
+                    tc_load16(myY + 16 * piece, ii);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = __fmul2_rn(
+                            make_float2(fi, fi),
+                            make_float2(__uint_as_float(ii[i]), __uint_as_float(ii[i + 1])));
+                        ii[i] = __float_as_uint(y.x);
+                        ii[i + 1] = __float_as_uint(y.y);
+                    }
+                    tc_store16(myY + 16 * piece, ii);
+                }
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar_m);
             }
+            {
+                // the token's weight in the chunk's last state: from its own 32 tokens' end onwards
+                const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+                const float w = v0[row] * exp2f((quarter < 1 ? t.y : 0.0f) +
+                                                (quarter < 2 ? t.z : 0.0f) +
+                                                (quarter < 3 ? t.w : 0.0f));
+                if (alive) alive = mbar_wait(bar_x, phase);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float x[8];
+                    widen16(load_smem16(swizzled(myX, row, 4 * part + c)), x);
+                    unsigned bits[kParts][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float2 f = __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k) {
+                            bits[k][i] = f2_to_bf2(f.x, f.y);
+                            f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k][i] << 16),
+                                                          -__uint_as_float(bits[k][i] & 0xffff0000u)));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        store_smem16(
+                            swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, 4 * part + c),
+                            make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
+                    if constexpr (kParts == 3)
+                        if (row >= 64)
+                            store_smem16(
+                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, 4 * part + c),
+                                make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bar_w);
             const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
             const float chunk_decay = (t.x + t.y) + (t.z + t.w), f = exp2f(chunk_decay);
             stretch_decay += chunk_decay;
-            column_sync();  // the next decays
+            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
+                const float dt = __uint_as_float(dt_next << 16);
+                if (tok + 2 * kChunk + row < to)
+                    dt_next = dt_col[(tok + 2 * kChunk + row) * p.dt_b];
+                chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
+                             bias, A2, row, lane);
+            }
+            column_sync();
+            if (!kFirst) {
+                if (alive) alive = mbar_wait(bar_y, phase);
+                __syncwarp();
+                tc_fence_after();
+                unsigned o[16];
+#pragma unroll
+                for (int piece = 0; piece < 2; ++piece) {
+                    unsigned yy[16];
+                    tc_load16(myY + 16 * piece, yy);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[8 * piece + i] =
+                            f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+                }
+                if (valid == kChunk) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        store_smem16(swizzled(myX, row, 4 * part + c),
+                                     make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+                    fence_async_smem();
+                    mbar_arrive(bar_r);
+                } else if (row < valid && keeps) {
+                    __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
+                                               slab * kSlab + kHalf * part;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        reinterpret_cast<uint4 *>(dst)[c] =
+                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
+            }
             if (alive) alive = mbar_wait(bar_u, phase);
             __syncwarp();
             tc_fence_after();
@@ -768,38 +817,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
             tc_fence_before();
-            if (kFirst) continue;
-            publish();
-            if (alive) alive = mbar_wait(bar_y, phase);
-            __syncwarp();
-            tc_fence_after();
-            unsigned o[16];
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-                unsigned yy[16];
-                tc_load16(myY + 16 * piece, yy);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[8 * piece + i] =
-                        f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+            if (!kFirst) {
+                publish();
+                mbar_arrive(bar_done);
             }
-            if (valid == kChunk) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    store_smem16(swizzled(sW + which * kTileBytes, row, 4 * part + c),
-                                 make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
-                fence_async_smem();
-            } else if (row < valid && keeps) {
-                __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
-                                           slab * kSlab + kHalf * part;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    reinterpret_cast<uint4 *>(dst)[c] =
-                        make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            }
-            tc_fence_before();
-            mbar_arrive(bar_done);
         }
 
         if (own && keeps) {
