@@ -48,9 +48,10 @@ namespace {
 constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
 constexpr int kPair = 2;         // columns (a head's 64-row slab) per CTA, of one group
-constexpr int kCompute = kPair * 256;              // threads of the elementwise work
+constexpr int kSplit = 1;        // warpgroups per column
+constexpr int kCompute = kPair * kSplit * 128;     // threads of the elementwise work
 constexpr int kPromptThreads = kCompute + 64;      // one warp to issue, one to store
-constexpr int kHalf = kSlab / 2;  // a thread's share of its row: two warpgroups halve it
+constexpr int kShare = kSlab / kSplit;  // a thread's share of its row
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -74,6 +75,13 @@ __device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
 
 __device__ __forceinline__ void mbar_arrive(unsigned bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// One arrival for the whole warp: the barrier counts warps (an arrival of every thread would be
+// 32 updates of one word, one after the other).
+__device__ __forceinline__ void warp_arrive(unsigned bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
@@ -259,9 +267,10 @@ struct PromptSmem {
     static constexpr int kW2 = kW1 + kPair * kTileBytes;  // also S: bf16 [n][64 p]
     static constexpr int kW3 = kW2 + kPair * kTileBytes;  // tokens 64 .. 127
     static constexpr int kVec = kW3 + kPair * kTileBytes / 2;
-    // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4); for this
-    // chunk and the next, for each column
-    static constexpr int kVecFloats = 3 * kChunk + 4;
+    // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4), the
+    // head's dt_bias, A log2 e and D (4); for this chunk and the next, for each column
+    static constexpr int kConst = 3 * kChunk + 4;
+    static constexpr int kVecFloats = kConst + 4;
     static constexpr int kBars = kVec + 2 * kPair * kVecFloats * 4;
     static constexpr int kTotal = kBars + 128;
 };
@@ -342,7 +351,7 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
 // chunk, TMEM lane, column n of the state) is the same in a column's two warpgroups, which halve
 // each row.  Per chunk, with the barrier that each hand-over uses:
 //
-//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [b, c] next G -> g; [w] U -> u
+//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [w] U -> u; [b, c] next G -> g
 //   compute:  [g] M, [i] I scaled -> m; [x] W -> w; the next chunk's decays; [y] readout into x's
 //             place -> r; [u] S advanced and published -> done
 //   store:    [r] readout out, then next x
@@ -394,7 +403,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                    bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80;
     if (tid == 0) {
         for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
-        for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute);
+        for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = kCompute / 32;  // the issuing warp
@@ -435,11 +444,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (int k = 0; k < kBlocks; ++k)
                     tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp, tok);
             };
+            // Shared-memory address of a tile, from an opaque copy of the base: the operands' many
+            // descriptors are worked out where they are used instead of held in registers.
+            auto tile = [&](int offset) {
+                unsigned at = base;
+                asm volatile("" : "+r"(at));
+                return at + offset;
+            };
             auto product_g = [&](unsigned place) {
+                const unsigned c = tile(Smem::kC), b = tile(Smem::kB) + place * kBBytes;
 #pragma unroll
                 for (int k = 0; k < N / 16; ++k) {
                     const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                    mma_ss(tG, operand(sC + off, 0), operand(sB + place * kBBytes + off, 0),
+                    mma_ss(tG, operand(c + off, 0), operand(b + off, 0),
                            instruction(kChunk, false, false), k > 0);
                 }
                 tc_commit(bar_g);
@@ -471,10 +488,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     if (alive) alive = mbar_wait(bar_done, phase);  // S published, Y and U read
                     tc_fence_after();
+                    const unsigned c_now = tile(Smem::kC), s_now = tile(Smem::kW2);
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k) {
                         const unsigned off = (k / 4) * kTileBytes + (k % 4) * 32;
-                        mma_ss(tY, operand(sC + off, 0), operand(sS + k * 2048, N * 128),
+                        mma_ss(tY, operand(c_now + off, 0), operand(s_now + k * 2048, N * 128),
                                instruction(kPair * kSlab, false, true), k > 0);
                     }
                     tc_commit(bar_i);
@@ -483,34 +501,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (alive) alive = mbar_wait(bar_m, phase);
                     if (alive) alive = mbar_wait(bar_x, phase);
                     tc_fence_after();
+                    const unsigned x_now = tile(Smem::kX);
 #pragma unroll
                     for (int c = 0; c < kPair; ++c)
 #pragma unroll
                         for (int k = 0; k < kChunk / 16; ++k)
                             mma_ts(tY + c * kSlab, tM + c * 64 + 8 * k,
-                                   operand(sX + c * kTileBytes + k * 2048, 0),
+                                   operand(x_now + c * kTileBytes + k * 2048, 0),
                                    instruction(kSlab, false, true), true);
                     tc_commit(bar_y);
-                    if (more) {  // every reader of G has passed m
-                        if (alive) alive = mbar_wait(bar_b, phase ^ 1);
-                        if (alive) alive = mbar_wait(bar_c, phase ^ 1);
-                        product_g(phase ^ 1);
-                    }
                 }
                 if (alive) alive = mbar_wait(bar_w, phase);
                 tc_fence_after();
-                const unsigned b_now = sB + phase * kBBytes;
+                const unsigned b_now = tile(Smem::kB) + phase * kBBytes;
+                const unsigned w1 = tile(Smem::kW1), w2 = tile(Smem::kW2), w3 = tile(Smem::kW3);
 #pragma unroll
                 for (int k = 0; k < (kParts == 3 ? 20 : 16); ++k) {
                     const int part = k / 8, kk = k % 8 + (part == 2 ? 4 : 0);
-                    const unsigned w = part == 0   ? sW1 + kk * 2048
-                                       : part == 1 ? sW2 + kk * 2048
-                                                   : sW3 + (kk - 4) * 2048;
+                    const unsigned w = part == 0   ? w1 + kk * 2048
+                                       : part == 1 ? w2 + kk * 2048
+                                                   : w3 + (kk - 4) * 2048;
                     mma_ss(tU, operand(b_now + kk * 2048, N == 128 ? kTileBytes : 0),
                            operand(w, part < 2 ? kTileBytes : kTileBytes / 2),
                            instruction(kPair * kSlab, true, true), k > 0);
                 }
                 tc_commit(bar_u);
+                if (!kFirst && more) {  // every reader of G has passed m
+                    if (alive) alive = mbar_wait(bar_b, phase ^ 1);
+                    if (alive) alive = mbar_wait(bar_c, phase ^ 1);
+                    product_g(phase ^ 1);
+                }
                 if (kFirst && more) load_x(tok + kChunk);  // x is in registers, or past them
                 if (alive) alive = mbar_wait(bar_u, phase);
             }
@@ -537,63 +557,76 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
     } else {
-        const int which = warp >> 3, part = (warp >> 2) & 1, quarter = warp & 3;
+        const int which = warp / (4 * kSplit), part = (warp >> 2) % kSplit, quarter = warp & 3;
         const int row = 32 * quarter + lane;
-        const bool keeps = which == 0 || paired;
-        const int column = first_column + (paired ? which : 0);
-        const int h = column / m.slabs, slab = column - h * m.slabs;
+        // The thread's place in the call, worked out again where it is needed rather than held in
+        // registers through the loop (the opaque copy keeps the compiler from holding it).
+        auto place = [&](int &column, int &h, int &slab) {
+            unsigned block = blockIdx.x;
+            asm volatile("" : "+r"(block));
+            const int c = static_cast<int>(block % ctas), grp = c / pairs;
+            const int first = grp * per_group + 2 * (c - grp * pairs);
+            const bool paired = 2 * (c - grp * pairs) + 1 < per_group;
+            column = first + (paired ? which : 0);
+            h = column / m.slabs, slab = column - h * m.slabs;
+            return which == 0 || paired;  // whether this thread's results are kept
+        };
+        int column, h, slab;
+        place(column, h, slab);
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
         const unsigned myX = sX + which * kTileBytes, myS = sS + which * N * 128;
-        const unsigned myY = tY + which * kSlab + kHalf * part + lanes;
-        const unsigned myU = tU + which * kSlab + kHalf * part + lanes;
+        const unsigned myY = tY + which * kSlab + kShare * part + lanes;
+        const unsigned myU = tU + which * kSlab + kShare * part + lanes;
         float *const vecs =
             reinterpret_cast<float *>(raw + (base - smem_u32(raw)) + Smem::kVec) +
             which * 2 * Smem::kVecFloats;
         auto column_sync = [&]() {
             asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "n"(kCompute / kPair) : "memory");
         };
-        const float bias = __ldg(p.dt_bias + h * p.bias_h);
-        const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
-        const float D = __ldg(p.D + h * p.D_h);
+        float *const head = vecs + Smem::kConst;
+        if (part == kSplit - 1 && row == 0) head[2] = __ldg(p.D + h * p.D_h);
         // The second warpgroup has less of M and works the decays out, a chunk ahead.  dt waits as
         // raw bits: a conversion right behind its load would wait for it.
         const unsigned short *const dt_col =
             reinterpret_cast<const unsigned short *>(p.dt) + h * p.dt_h;
         unsigned dt_next = 0;
-        if (part == 1) {
+        if (part == kSplit - 1) {
             unsigned dt = 0;
             if (from + row < to) dt = dt_col[(from + row) * p.dt_b];
             if (from + kChunk + row < to) dt_next = dt_col[(from + kChunk + row) * p.dt_b];
+            const float bias = __ldg(p.dt_bias + h * p.bias_h);
+            const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+            if (row == 0) head[0] = bias, head[1] = A2;
             chunk_decays(vecs, from + row < to, __uint_as_float(dt << 16), bias, A2, row, lane);
         }
 
-        // The state a stretch starts from: the thread holds S[32 part .. 32 part + 31][row].
-        float S[kHalf];
+        // The state a stretch starts from: the thread holds S[kShare part ..][row].
+        float S[kShare];
         const bool own = row < N;
         auto state_at = [&](int i) {
             return static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                   static_cast<long long>(slab * kSlab + kHalf * part + i) * p.st_row + row;
+                   static_cast<long long>(slab * kSlab + kShare * part + i) * p.st_row + row;
         };
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) S[i] = 0.0f;
+        for (int i = 0; i < kShare; ++i) S[i] = 0.0f;
         if (!kFirst && own) {
             if (!(m.q.fresh && m.q.fresh[b] != 0)) {
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) S[i] = static_cast<float>(*state_at(i));
+                for (int i = 0; i < kShare; ++i) S[i] = static_cast<float>(*state_at(i));
             }
             for (long long k = g - index; k < g; ++k) {
                 const float *loc =
-                    m.local + ((k * columns + column) * kSlab + kHalf * part) * N + row;
+                    m.local + ((k * columns + column) * kSlab + kShare * part) * N + row;
                 const float f = exp2f(__ldcg(m.decay + k * columns + column));
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
+                for (int i = 0; i < kShare; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
             }
         }
         auto publish = [&]() {  // the state as the next chunk's bf16 operand
             if (own) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    store_smem16(swizzled(myS, row, 4 * part + c),
+                for (int c = 0; c < kShare / 8; ++c)
+                    store_smem16(swizzled(myS, row, kShare / 8 * part + c),
                                  make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
                                             f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
                                             f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
@@ -603,7 +636,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         if (!kFirst) {
             publish();
-            mbar_arrive(bar_done);
+            warp_arrive(bar_done, lane);
         }
         column_sync();  // the decays
 
@@ -618,13 +651,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (alive) alive = mbar_wait(bar_b, phase);
                 if (row >= valid) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        store_smem16(swizzled(myX, row, 4 * part + c), make_uint4(0, 0, 0, 0));
+                    for (int c = 0; c < kShare / 8; ++c) {
+                        store_smem16(swizzled(myX, row, kShare / 8 * part + c), make_uint4(0, 0, 0, 0));
                         if (which == 0)
 #pragma unroll
                             for (int k = 0; k < kBlocks; ++k)
                                 store_smem16(swizzled(sB + phase * kBBytes + k * kTileBytes, row,
-                                                      4 * part + c),
+                                                      kShare / 8 * part + c),
                                              make_uint4(0, 0, 0, 0));
                     }
                 }
@@ -633,66 +666,73 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!kFirst) {
                 const float up = pre[row].x;
                 const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
+                const float D = head[2];
                 // M = G times decays, two blocks of 32 columns per warpgroup
                 if (alive) alive = mbar_wait(bar_g, phase);
                 __syncwarp();
                 tc_fence_after();
+                // (rolled loops: unrolled, with the cases of every block side by side, the code is
+                // larger than the instruction cache and M took twice as long)
+                const unsigned myM = tM + which * 64 + lanes;
+                const int block0 = 4 / kSplit * part, blocks = 4 / kSplit;
+                const int full = quarter < block0 ? 0 : min(quarter - block0, blocks);
+#pragma unroll 1
+                for (int k = 0; k < 2 * full; ++k) {  // columns before the row's 32 tokens
+                    const int col = 32 * block0 + 16 * k, cb = col / 32;
+                    unsigned gg[16], mm[8];
+                    tc_load16(tG + lanes + col, gg);
+                    // the blocks between the columns' and the row's
+                    const float f = exp2f(up + ((cb < 1 && quarter > 1 ? t.y : 0.0f) +
+                                                (cb < 2 && quarter > 2 ? t.z : 0.0f)));
+                    const float4 *vv = reinterpret_cast<const float4 *>(v0 + col);
+                    tc_wait_ld();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int cb = 2 * part + half;
-                    float f = 0.0f;
-                    if (cb < quarter)  // the blocks between the columns' and the row's
-                        f = exp2f(up + ((cb < 1 && quarter > 1 ? t.y : 0.0f) +
-                                        (cb < 2 && quarter > 2 ? t.z : 0.0f)));
-#pragma unroll
-                    for (int piece = 0; piece < 2; ++piece) {
-                        const int col = 32 * cb + 16 * piece;
-                        unsigned mm[8];
-                        if (cb <= quarter) {
-                            unsigned gg[16];
-                            tc_load16(tG + lanes + col, gg);
-                            tc_wait_ld();
-                            if (cb < quarter) {
-                                const float4 *vv = reinterpret_cast<const float4 *>(v0 + col);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float4 q = vv[j];
-                                    const float2 lo = __fmul2_rn(
-                                        make_float2(__uint_as_float(gg[4 * j]),
-                                                    __uint_as_float(gg[4 * j + 1])),
-                                        __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
-                                    const float2 hi = __fmul2_rn(
-                                        make_float2(__uint_as_float(gg[4 * j + 2]),
-                                                    __uint_as_float(gg[4 * j + 3])),
-                                        __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
-                                    mm[2 * j] = f2_to_bf2(lo.x, lo.y);
-                                    mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
-                                }
-                            } else {
-                                const float4 *pp = reinterpret_cast<const float4 *>(pre + col);
-                                const int edge = lane - 16 * piece;  // the last column kept
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const float4 q = pp[j];  // (prefix, dtv) of two columns
-                                    const float e0 = exp2_ftz(up - q.x) *
-                                                     (q.y * __uint_as_float(gg[2 * j]));
-                                    const float e1 = exp2_ftz(up - q.z) *
-                                                     (q.w * __uint_as_float(gg[2 * j + 1]));
-                                    // on the diagonal, D x of the token itself
-                                    mm[j] = f2_to_bf2(2 * j < edge    ? e0
-                                                      : 2 * j == edge ? e0 + D
-                                                                      : 0.0f,
-                                                      2 * j + 1 < edge    ? e1
-                                                      : 2 * j + 1 == edge ? e1 + D
-                                                                          : 0.0f);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) mm[j] = 0;
-                        }
-                        tc_store8(tM + which * 64 + lanes + col / 2, mm);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 q = vv[j];
+                        const float2 lo = __fmul2_rn(
+                            make_float2(__uint_as_float(gg[4 * j]),
+                                        __uint_as_float(gg[4 * j + 1])),
+                            __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
+                        const float2 hi = __fmul2_rn(
+                            make_float2(__uint_as_float(gg[4 * j + 2]),
+                                        __uint_as_float(gg[4 * j + 3])),
+                            __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
+                        mm[2 * j] = f2_to_bf2(lo.x, lo.y);
+                        mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
                     }
+                    tc_store8(myM + col / 2, mm);
+                }
+                if (quarter >= block0 && quarter < block0 + blocks) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {  // the row's own 32 tokens
+                        const int col = 32 * quarter + 16 * k;
+                        unsigned gg[16], mm[8];
+                        tc_load16(tG + lanes + col, gg);
+                        const float4 *pp = reinterpret_cast<const float4 *>(pre + col);
+                        const int edge = lane - 16 * k;  // the last column kept
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 q = pp[j];  // (prefix, dtv) of two columns
+                            const float e0 =
+                                exp2_ftz(up - q.x) * (q.y * __uint_as_float(gg[2 * j]));
+                            const float e1 =
+                                exp2_ftz(up - q.z) * (q.w * __uint_as_float(gg[2 * j + 1]));
+                            // on the diagonal, D x of the token itself
+                            mm[j] = f2_to_bf2(2 * j < edge    ? e0
+                                              : 2 * j == edge ? e0 + D
+                                                              : 0.0f,
+                                              2 * j + 1 < edge    ? e1
+                                              : 2 * j + 1 == edge ? e1 + D
+                                                                  : 0.0f);
+                        }
+                        tc_store8(myM + col / 2, mm);
+                    }
+                }
+#pragma unroll 1
+                for (int cb = max(quarter + 1, block0); cb < block0 + blocks; ++cb) {
+                    const unsigned zero[16] = {};
+                    tc_store16(myM + 16 * cb, zero);
                 }
                 // The state's share of the readout, where Y will add to it
                 const float fi = exp2f(up + ((quarter > 0 ? t.x : 0.0f) +
@@ -701,24 +741,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (alive) alive = mbar_wait(bar_i, phase);
                 __syncwarp();
                 tc_fence_after();
-#pragma unroll
-                for (int piece = 0; piece < 2; ++piece) {
-                    unsigned ii[16];
-                    tc_load16(myY + 16 * piece, ii);
+#pragma unroll 1
+                for (int half = 0; half < kShare / 32; ++half) {
+                    unsigned ii[2][16];
+                    tc_load16(myY + 32 * half, ii[0]);
+                    tc_load16(myY + 32 * half + 16, ii[1]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 y = __fmul2_rn(
-                            make_float2(fi, fi),
-                            make_float2(__uint_as_float(ii[i]), __uint_as_float(ii[i + 1])));
-                        ii[i] = __float_as_uint(y.x);
-                        ii[i + 1] = __float_as_uint(y.y);
+                    for (int piece = 0; piece < 2; ++piece) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 y =
+                                __fmul2_rn(make_float2(fi, fi),
+                                           make_float2(__uint_as_float(ii[piece][i]),
+                                                       __uint_as_float(ii[piece][i + 1])));
+                            ii[piece][i] = __float_as_uint(y.x);
+                            ii[piece][i + 1] = __float_as_uint(y.y);
+                        }
+                        tc_store16(myY + 32 * half + 16 * piece, ii[piece]);
                     }
-                    tc_store16(myY + 16 * piece, ii);
                 }
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar_m);
+                warp_arrive(bar_m, lane);
             }
             {
                 // the token's weight in the chunk's last state: from its own 32 tokens' end onwards
@@ -727,10 +772,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                                 (quarter < 2 ? t.z : 0.0f) +
                                                 (quarter < 3 ? t.w : 0.0f));
                 if (alive) alive = mbar_wait(bar_x, phase);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+#pragma unroll 2
+                for (int c = 0; c < kShare / 8; ++c) {
                     float x[8];
-                    widen16(load_smem16(swizzled(myX, row, 4 * part + c)), x);
+                    widen16(load_smem16(swizzled(myX, row, kShare / 8 * part + c)), x);
                     unsigned bits[kParts][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -745,73 +790,79 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         store_smem16(
-                            swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, 4 * part + c),
+                            swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, kShare / 8 * part + c),
                             make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
                     if constexpr (kParts == 3)
                         if (row >= 64)
                             store_smem16(
-                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, 4 * part + c),
+                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, kShare / 8 * part + c),
                                 make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
                 }
             }
             fence_async_smem();
-            mbar_arrive(bar_w);
+            warp_arrive(bar_w, lane);
             const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
             const float chunk_decay = (t.x + t.y) + (t.z + t.w), f = exp2f(chunk_decay);
-            stretch_decay += chunk_decay;
-            if (part == 1 && tok + kChunk < to) {  // the next chunk's decays
+            if (kFirst) stretch_decay += chunk_decay;
+            if (part == kSplit - 1 && tok + kChunk < to) {  // the next chunk's decays
                 const float dt = __uint_as_float(dt_next << 16);
                 if (tok + 2 * kChunk + row < to)
                     dt_next = dt_col[(tok + 2 * kChunk + row) * p.dt_b];
                 chunk_decays(vecs + (phase ^ 1) * Smem::kVecFloats, tok + kChunk + row < to, dt,
-                             bias, A2, row, lane);
+                             head[0], head[1], row, lane);
             }
             column_sync();
             if (!kFirst) {
                 if (alive) alive = mbar_wait(bar_y, phase);
                 __syncwarp();
                 tc_fence_after();
-                unsigned o[16];
 #pragma unroll
-                for (int piece = 0; piece < 2; ++piece) {
-                    unsigned yy[16];
-                    tc_load16(myY + 16 * piece, yy);
+                for (int half = 0; half < kShare / 32; ++half) {
+                    unsigned yy[2][16], o[16];
+                    tc_load16(myY + 32 * half, yy[0]);
+                    tc_load16(myY + 32 * half + 16, yy[1]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[8 * piece + i] =
-                            f2_to_bf2(__uint_as_float(yy[2 * i]), __uint_as_float(yy[2 * i + 1]));
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = f2_to_bf2(__uint_as_float(yy[i / 8][2 * i % 16]),
+                                         __uint_as_float(yy[i / 8][2 * i % 16 + 1]));
+                    int column, h, slab;
+                    if (valid == kChunk) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            store_smem16(swizzled(myX, row, kShare / 8 * part + 4 * half + c),
+                                         make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2],
+                                                    o[4 * c + 3]));
+                    } else if (place(column, h, slab) && row < valid) {
+                        __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
+                                                   slab * kSlab + kShare * part + 32 * half;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            reinterpret_cast<uint4 *>(dst)[c] = make_uint4(
+                                o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    }
                 }
                 if (valid == kChunk) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        store_smem16(swizzled(myX, row, 4 * part + c),
-                                     make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
                     fence_async_smem();
-                    mbar_arrive(bar_r);
-                } else if (row < valid && keeps) {
-                    __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
-                                               slab * kSlab + kHalf * part;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        reinterpret_cast<uint4 *>(dst)[c] =
-                            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    warp_arrive(bar_r, lane);
                 }
             }
             if (alive) alive = mbar_wait(bar_u, phase);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-                unsigned uu[16];
-                tc_load16(myU + 16 * piece, uu);
+            for (int half = 0; half < kShare / 32; ++half) {
+                unsigned uu[2][16];
+                tc_load16(myU + 32 * half, uu[0]);
+                tc_load16(myU + 32 * half + 16, uu[1]);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float *const s = S + 16 * piece + i;
-                    const float2 v = __ffma2_rn(
-                        make_float2(s[0], s[1]), make_float2(f, f),
-                        make_float2(__uint_as_float(uu[i]), __uint_as_float(uu[i + 1])));
+                for (int i = 0; i < 32; i += 2) {
+                    float *const s = S + 32 * half + i;
+                    const float2 v =
+                        __ffma2_rn(make_float2(s[0], s[1]), make_float2(f, f),
+                                   make_float2(__uint_as_float(uu[i / 16][i % 16]),
+                                               __uint_as_float(uu[i / 16][i % 16 + 1])));
                     s[0] = v.x;
                     s[1] = v.y;
                 }
@@ -819,19 +870,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tc_fence_before();
             if (!kFirst) {
                 publish();
-                mbar_arrive(bar_done);
+                warp_arrive(bar_done, lane);
             }
         }
 
+        int column_, h_, slab_;
+        const bool keeps = place(column_, h_, slab_);
+        column = column_, h = h_, slab = slab_;
         if (own && keeps) {
             if (kFirst) {
-                float *loc = m.local + ((g * columns + column) * kSlab + kHalf * part) * N + row;
+                float *loc = m.local + ((g * columns + column) * kSlab + kShare * part) * N + row;
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) __stcg(loc + i * N, S[i]);
+                for (int i = 0; i < kShare; ++i) __stcg(loc + i * N, S[i]);
                 if (part == 0 && row == 0) __stcg(m.decay + g * columns + column, stretch_decay);
             } else if (last) {
+                slot = load_slot<kIdx64>(p, scan[kPromptThreads / 32]);
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) {
+                for (int i = 0; i < kShare; ++i) {
                     if constexpr (sizeof(ST) == 4)
                         *state_at(i) = S[i];
                     else
