@@ -16,6 +16,7 @@ Strided views are accepted as they are; nothing is copied.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 import torch
@@ -474,88 +475,109 @@ def ssu_update_tokens(handle: int, state_pool, state_batch_indices, x, dt, dt_bi
 # ---- prompts and attention ---------------------------------------------------------------
 #
 # These calls sit in a serving loop beside the decode step and are often shorter on the device
-# than a Python call, so their marshalling fills the ABI structs from one flat list each.
+# than their marshalling, so it is written out: one look at every tensor, the ABI's structs packed
+# as bytes (a struct of N words costs 0.3 us this way, 1.6 us as a ctypes array), and messages only
+# where a check has failed.
 
+_BF16, _F32 = torch.bfloat16, torch.float32
 _INDEX_TYPE = {torch.int32: SSU_INDEX_I32, torch.int64: SSU_INDEX_I64}
-_STRIDES_WORDS = ctypes.sizeof(ssu_strides_t) // 8
+_STATE_TYPE = {_F32: SSU_STATE_F32, _BF16: SSU_STATE_BF16}
+_SHAPE = struct.Struct("6q2i")            # ssu_shape_t
+_STRIDES = struct.Struct("27q")           # ssu_strides_t
+_ROTATE_SHAPE = struct.Struct("8q2i")     # ssu_rotate_shape_t
+_ROTATE_STRIDES = struct.Struct("17q")    # ssu_rotate_strides_t
+_ATTEND_SHAPE = struct.Struct("7q2i")     # ssu_attend_shape_t
+_ATTEND_STRIDES = struct.Struct("13q")    # ssu_attend_strides_t
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else \
+    lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
-def _index_type(name: str, *tensors) -> int:
-    kind = _INDEX_TYPE.get(tensors[0].dtype)
-    if kind is None:
-        raise TypeError(f"{name} must be int32 or int64")
-    for t in tensors[1:]:
-        if t.dtype != tensors[0].dtype:
-            raise TypeError(f"{name} must all be {tensors[0].dtype}, got {t.dtype}")
-    return kind
+def _refuse_types(**wanted) -> None:
+    """Raises for the first tensor that is not of its wanted (dtype, dims)."""
+    for name, (t, dtypes, dims) in wanted.items():
+        if t.dtype not in dtypes or t.dim() not in dims:
+            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))} with "
+                            f"{' or '.join(map(str, dims))} dims, got {t.dtype} with {t.dim()}")
+    raise TypeError("operand types do not fit together")
 
 
-def _on_one_gpu(*tensors) -> None:
-    """Every tensor lies on the same CUDA device."""
+def _device_of(tensors) -> int:
+    """The CUDA device on which every tensor lies."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev or dev < 0:
             raise ValueError("every operand must be a CUDA tensor of one device, got "
                              + ", ".join(sorted({str(u.device) for u in tensors})))
+    return dev
 
 
-def _typed(dtype, ndim: int, **tensors) -> None:
-    for name, t in tensors.items():
-        if t.dtype != dtype or t.dim() != ndim:
-            raise TypeError(f"{name} must be a {ndim}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
-
-
-def _workspace(workspace) -> tuple[int | None, int]:
+def _workspace(workspace, dev: int) -> tuple[int | None, int]:
     if workspace is None:
         return None, 0
-    if not workspace.is_contiguous() or workspace.get_device() < 0:
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor of the operands' device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def _stream_on(dev: int, stream) -> int:
+    if stream is None:
+        return _raw_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _head_strides(t, name: str, dims: tuple[int, ...]) -> tuple[int, ...]:
+    """Strides of a per-head operand in its expanded form (missing dimensions: 0)."""
+    if t.shape != dims[:t.dim()]:
+        raise ValueError(f"{name} must have the shape {dims} or {dims[:1]}, got {tuple(t.shape)}")
+    st = t.stride()
+    return st if len(st) == len(dims) else (*st, *(0,) * (len(dims) - len(st)))
 
 
 def describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D,
-                     out):
-    """Build ``(ssu_shape_t, ssu_strides_t)`` of a prompt call (no data is touched)."""
-    if state_pool.dim() != 4 or state_pool.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("state_pool must be a 4-D float32 or bfloat16 tensor")
-    if state_batch_indices.dim() != 1 or cu_tokens.dim() != 1:
-        raise TypeError("state_batch_indices and cu_tokens must be 1-D")
-    kind = _index_type("state_batch_indices and cu_tokens", state_batch_indices, cu_tokens)
-    _typed(torch.bfloat16, 3, x=x, out=out, B=B, C=C)
-    if dt.dtype != torch.bfloat16 or dt.dim() not in (2, 3):
-        raise TypeError("dt must be a 2-D or 3-D bfloat16 tensor")
-    _expect(dt_bias, "dt_bias", torch.float32, (1, 2))
-    _expect(D, "D", torch.float32, (1, 2))
-    _expect(A, "A", torch.float32, (1, 3))
+                     out) -> tuple[bytes, bytes]:
+    """The ``ssu_shape_t`` and ``ssu_strides_t`` of a prompt call, as bytes (no data is touched)."""
+    kind, state = _INDEX_TYPE.get(cu_tokens.dtype), _STATE_TYPE.get(state_pool.dtype)
+    sp, sx, so, sd = state_pool.stride(), x.stride(), out.stride(), dt.stride()
+    sb, sc, si = B.stride(), C.stride(), state_batch_indices.stride()
+    if not (x.dtype is dt.dtype is B.dtype is C.dtype is out.dtype is _BF16
+            and dt_bias.dtype is A.dtype is D.dtype is _F32 and kind is not None
+            and state_batch_indices.dtype is cu_tokens.dtype and state is not None
+            and len(sp) == 4 and len(sx) == len(so) == len(sb) == len(sc) == 3
+            and len(sd) in (2, 3) and len(si) == cu_tokens.dim() == 1
+            and dt_bias.dim() in (1, 2) and D.dim() in (1, 2) and A.dim() in (1, 3)):
+        ints = (torch.int32, torch.int64)
+        _refuse_types(state_pool=(state_pool, (_F32, _BF16), (4,)), x=(x, (_BF16,), (3,)),
+                      dt=(dt, (_BF16,), (2, 3)), B=(B, (_BF16,), (3,)), C=(C, (_BF16,), (3,)),
+                      out=(out, (_BF16,), (3,)), dt_bias=(dt_bias, (_F32,), (1, 2)),
+                      A=(A, (_F32,), (1, 3)), D=(D, (_F32,), (1, 2)),
+                      cu_tokens=(cu_tokens, ints, (1,)),
+                      state_batch_indices=(state_batch_indices, (cu_tokens.dtype,), (1,)))
     pool, H, P, N = state_pool.shape
-    bs, T, G = state_batch_indices.shape[0], x.shape[0], B.shape[1]
-    if x.shape[1:] != (H, P) or out.shape != x.shape:
+    T, G, _ = B.shape
+    bs, = state_batch_indices.shape
+    if x.shape != (T, H, P) or out.shape != x.shape:
         raise ValueError(f"x and out must be [tokens, H, P] = {(T, H, P)}")
     if B.shape != (T, G, N) or C.shape != B.shape:
         raise ValueError(f"B and C must be [tokens, G, N] = {(T, G, N)}")
-    if dt.shape[:2] != (T, H) or (dt.dim() == 3 and dt.shape[2] != P):
-        raise ValueError("dt must be [tokens, H] or [tokens, H, P]")
+    if dt.shape != (T, H, P)[:len(sd)]:
+        raise ValueError(f"dt must be {(T, H)} or {(T, H, P)}")
     if cu_tokens.shape[0] != bs + 1 or cu_tokens.stride(0) != 1:
         raise ValueError(f"cu_tokens must be contiguous with {bs + 1} entries")
-    shape = ssu_shape_t(bs, H, P, N, G, pool, kind,
-                        SSU_STATE_BF16 if state_pool.dtype == torch.bfloat16 else SSU_STATE_F32)
-    dt_s, dims = dt.stride(), (H, P, N)
-    strides = (_i64 * _STRIDES_WORDS)(
-        *state_pool.stride(), *x.stride(), *out.stride(), *(dt_s if len(dt_s) == 3 else (*dt_s, 0)),
-        *B.stride(), *C.stride(), *_broadcast_strides(dt_bias, "dt_bias", dims, 2),
-        *_broadcast_strides(D, "D", dims, 2), *_broadcast_strides(A, "A", dims, 3),
-        state_batch_indices.stride(0))
-    return shape, strides
+    return (_SHAPE.pack(bs, H, P, N, G, pool, kind, state),
+            _STRIDES.pack(*sp, *sx, *so, *(sd if len(sd) == 3 else (*sd, 0)), *sb, *sc,
+                          *_head_strides(dt_bias, "dt_bias", (H, P)),
+                          *_head_strides(D, "D", (H, P)), *_head_strides(A, "A", (H, P, N)), *si))
 
 
 def ssu_prompts_workspace_bytes(handle: int, state_pool, x, B, state_batch_indices) -> int:
     """Device workspace bytes ``ssu_update_prompts`` needs for these operands' sizes."""
     pool, H, P, N = state_pool.shape
-    shape = ssu_shape_t(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
-                        SSU_STATE_BF16 if state_pool.dtype == torch.bfloat16 else SSU_STATE_F32)
+    shape = _SHAPE.pack(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
+                        _STATE_TYPE.get(state_pool.dtype, SSU_STATE_F32))
     n = _i64()
-    _check(lib().ssu_prompts_workspace_bytes(handle, ctypes.byref(shape), x.shape[0],
-                                             ctypes.byref(n)), "ssu_prompts_workspace_bytes")
+    _check(lib().ssu_prompts_workspace_bytes(handle, shape, x.shape[0], ctypes.byref(n)),
+           "ssu_prompts_workspace_bytes")
     return int(n.value)
 
 
@@ -569,18 +591,20 @@ def ssu_update_prompts(handle: int, state_pool, state_batch_indices, cu_tokens, 
     shape, strides = describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias,
                                       A, B, C, D, out)
     tensors = (state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D, out)
-    _on_one_gpu(*tensors)
+    dev = _device_of(tensors)
     if fresh is not None:
-        if fresh.dtype not in (torch.uint8, torch.bool) or fresh.shape != (shape.batch,) or \
-                not fresh.is_contiguous() or fresh.get_device() != state_pool.get_device():
+        if fresh.dtype not in (torch.uint8, torch.bool) or \
+                fresh.shape != state_batch_indices.shape or not fresh.is_contiguous() or \
+                fresh.get_device() != dev:
             raise ValueError("fresh must be a contiguous uint8 or bool CUDA tensor with one entry "
                              "per prompt")
         fresh = fresh.data_ptr()
-    ws, nbytes = _workspace(workspace)
+    ws, nbytes = _workspace(workspace, dev)
     p = [t.data_ptr() for t in tensors]
-    _check(lib().ssu_update_prompts(handle, *p[:3], fresh, *p[3:], ctypes.byref(shape), strides,
-                                    x.shape[0], ws, nbytes, _stream_ptr(stream)),
-           "ssu_update_prompts")
+    st = lib().ssu_update_prompts(handle, p[0], p[1], p[2], fresh, *p[3:], shape, strides,
+                                  x.shape[0], ws, nbytes, _stream_on(dev, stream))
+    if st:
+        _check(st, "ssu_update_prompts")
 
 
 def ssu_rotate_qk(handle: int, q, k, v, q_weight, k_weight, table, positions, q_out, k_pages,
@@ -590,47 +614,53 @@ def ssu_rotate_qk(handle: int, q, k, v, q_weight, k_weight, table, positions, q_
     (weights fp32 ``[D]``), rotation by ``table[positions[t]]`` (fp32 ``[places, rotary]``:
     cosines, then sines), queries to ``q_out``, keys and ``v`` to row ``slots[t]`` of the pages
     ``[pages, page_size, Hk, D]`` (-1: not stored)."""
-    _typed(torch.bfloat16, 3, q=q, k=k, v=v, q_out=q_out)
-    _typed(torch.bfloat16, 4, k_pages=k_pages, v_pages=v_pages)
-    _typed(torch.float32, 1, q_weight=q_weight, k_weight=k_weight)
-    _typed(torch.float32, 2, table=table)
-    if positions.dim() != 1 or slots.dim() != 1:
-        raise TypeError("positions and slots must be 1-D")
-    kind = _index_type("positions and slots", positions, slots)
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), q_out.stride()
+    kp, vp, st = k_pages.stride(), v_pages.stride(), table.stride()
+    kind = _INDEX_TYPE.get(slots.dtype)
+    if not (q.dtype is k.dtype is v.dtype is q_out.dtype is k_pages.dtype is v_pages.dtype is _BF16
+            and q_weight.dtype is k_weight.dtype is table.dtype is _F32 and kind is not None
+            and positions.dtype is slots.dtype and len(sq) == len(sk) == len(sv) == len(so) == 3
+            and len(kp) == len(vp) == 4 and len(st) == 2):
+        ints = (torch.int32, torch.int64)
+        _refuse_types(q=(q, (_BF16,), (3,)), k=(k, (_BF16,), (3,)), v=(v, (_BF16,), (3,)),
+                      q_out=(q_out, (_BF16,), (3,)), k_pages=(k_pages, (_BF16,), (4,)),
+                      v_pages=(v_pages, (_BF16,), (4,)), q_weight=(q_weight, (_F32,), (1,)),
+                      k_weight=(k_weight, (_F32,), (1,)), table=(table, (_F32,), (2,)),
+                      slots=(slots, ints, (1,)), positions=(positions, (slots.dtype,), (1,)))
     T, Hq, D = q.shape
     Hk = k.shape[1]
     if q_out.shape != q.shape or k.shape != (T, Hk, D) or v.shape != k.shape:
         raise ValueError(f"q and q_out must be {(T, Hq, D)}, k and v {(T, Hk, D)}")
-    if k_pages.shape[2:] != (Hk, D) or v_pages.shape != k_pages.shape:
+    pages, page = k_pages.shape[:2]
+    if k_pages.shape != (pages, page, Hk, D) or v_pages.shape != k_pages.shape:
         raise ValueError(f"k_pages and v_pages must be [pages, page_size, {Hk}, {D}]")
-    if q_weight.shape != (D,) or k_weight.shape != (D,):
-        raise ValueError(f"q_weight and k_weight must have {D} elements")
-    if positions.shape[0] != T or slots.shape[0] != T:
+    if q_weight.shape != (D,) or k_weight.shape != (D,) or q_weight.stride() != (1,) or \
+            k_weight.stride() != (1,):
+        raise ValueError(f"q_weight and k_weight must be contiguous with {D} elements")
+    if positions.shape != (T,) or slots.shape != (T,):
         raise ValueError("positions and slots must have one entry per token")
-    tensors = (q, k, v, q_weight, k_weight, table, positions, q_out, k_pages, v_pages, slots)
-    _on_one_gpu(*tensors)
-    st = [t.stride() for t in tensors]
-    if any(s[-1] != 1 for s in (*st[:6], *st[7:10])):
+    if not (sq[2] == sk[2] == sv[2] == so[2] == kp[3] == vp[3] == st[1] == 1):
         raise ValueError("the last dimension of every operand must have stride 1")
-    shape = ssu_rotate_shape_t(T, Hq, Hk, D, table.shape[1], table.shape[0], k_pages.shape[0],
-                               k_pages.shape[1], kind, 1 if interleaved else 0)
-    strides = (_i64 * 17)(*st[0][:2], *st[1][:2], *st[2][:2], *st[7][:2], *st[8][:3], *st[9][:3],
-                          st[5][0], st[6][0], st[10][0])
-    _check(lib().ssu_rotate_qk(handle, *[t.data_ptr() for t in tensors], ctypes.byref(shape),
-                               strides, eps, _stream_ptr(stream)), "ssu_rotate_qk")
-
-
-def _attend_shape(q, k_pages, max_pages: int, kind: int) -> ssu_attend_shape_t:
-    return ssu_attend_shape_t(q.shape[0], q.shape[1], k_pages.shape[2], q.shape[2],
-                              k_pages.shape[0], k_pages.shape[1], max_pages, kind, 0)
+    tensors = (q, k, v, q_weight, k_weight, table, positions, q_out, k_pages, v_pages, slots)
+    dev = _device_of(tensors)
+    places, rotary = table.shape
+    status = lib().ssu_rotate_qk(
+        handle, *[t.data_ptr() for t in tensors],
+        _ROTATE_SHAPE.pack(T, Hq, Hk, D, rotary, places, pages, page, kind, bool(interleaved)),
+        _ROTATE_STRIDES.pack(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1], kp[0], kp[1],
+                             kp[2], vp[0], vp[1], vp[2], st[0], *positions.stride(),
+                             *slots.stride()), eps, _stream_on(dev, stream))
+    if status:
+        _check(status, "ssu_rotate_qk")
 
 
 def ssu_attend_workspace_bytes(handle: int, q, k_pages) -> int:
     """Device workspace bytes ``ssu_attend`` needs for these operands' sizes (fill it with zeros
     once)."""
-    shape = _attend_shape(q, k_pages, 0, SSU_INDEX_I32)
     n = _i64()
-    _check(lib().ssu_attend_workspace_bytes(handle, ctypes.byref(shape), ctypes.byref(n)),
+    shape = _ATTEND_SHAPE.pack(*q.shape[:2], k_pages.shape[2], q.shape[2], *k_pages.shape[:2], 0,
+                               SSU_INDEX_I32, 0)
+    _check(lib().ssu_attend_workspace_bytes(handle, shape, ctypes.byref(n)),
            "ssu_attend_workspace_bytes")
     return int(n.value)
 
@@ -642,29 +672,38 @@ def ssu_attend(handle: int, q, k_pages, v_pages, page_table, lengths, out, works
     the first ``lengths[b]`` positions are visible (with ``window``: its last ``window`` and the
     first ``sinks``).  ``scale`` defaults to ``D ** -0.5``.  ``workspace`` is a device tensor of
     ``ssu_attend_workspace_bytes``, zero before its first use, not shared by overlapping calls."""
-    _typed(torch.bfloat16, 3, q=q, out=out)
-    _typed(torch.bfloat16, 4, k_pages=k_pages, v_pages=v_pages)
-    if page_table.dim() != 2 or lengths.dim() != 1:
-        raise TypeError("page_table must be 2-D and lengths 1-D")
-    kind = _index_type("page_table and lengths", page_table, lengths)
-    bs, _, D = q.shape
+    sq, so, kp, vp = q.stride(), out.stride(), k_pages.stride(), v_pages.stride()
+    st, sl = page_table.stride(), lengths.stride()
+    kind = _INDEX_TYPE.get(lengths.dtype)
+    if not (q.dtype is k_pages.dtype is v_pages.dtype is out.dtype is _BF16 and kind is not None
+            and page_table.dtype is lengths.dtype and len(sq) == len(so) == 3
+            and len(kp) == len(vp) == 4 and len(st) == 2 and len(sl) == 1):
+        _refuse_types(q=(q, (_BF16,), (3,)), out=(out, (_BF16,), (3,)),
+                      k_pages=(k_pages, (_BF16,), (4,)), v_pages=(v_pages, (_BF16,), (4,)),
+                      lengths=(lengths, (torch.int32, torch.int64), (1,)),
+                      page_table=(page_table, (lengths.dtype,), (2,)))
+    bs, Hq, D = q.shape
+    pages, page, Hk, _ = k_pages.shape
+    most = page_table.shape[1]
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if k_pages.shape[3] != D or v_pages.shape != k_pages.shape:
         raise ValueError(f"k_pages and v_pages must be [pages, page_size, Hk, {D}]")
     if page_table.shape[0] != bs or lengths.shape[0] != bs:
         raise ValueError("page_table and lengths must have one row per request")
-    tensors = (q, k_pages, v_pages, page_table, lengths, out)
-    _on_one_gpu(*tensors)
-    st = [t.stride() for t in tensors]
-    if st[0][2] != 1 or st[1][3] != 1 or st[2][3] != 1 or st[5][2] != 1:
+    if not (sq[2] == so[2] == kp[3] == vp[3] == 1):
         raise ValueError("the last dimension of q, out and the pages must have stride 1")
-    shape = _attend_shape(q, k_pages, page_table.shape[1], kind)
-    strides = (_i64 * 13)(*st[0][:2], *st[5][:2], *st[1][:3], *st[2][:3], *st[3], *st[4])
-    ws, nbytes = _workspace(workspace)
-    _check(lib().ssu_attend(handle, *[t.data_ptr() for t in tensors], ctypes.byref(shape),
-                            strides, D ** -0.5 if scale is None else scale, window, sinks, ws,
-                            nbytes, _stream_ptr(stream)), "ssu_attend")
+    tensors = (q, k_pages, v_pages, page_table, lengths, out)
+    dev = _device_of(tensors)
+    ws, nbytes = _workspace(workspace, dev)
+    status = lib().ssu_attend(
+        handle, *[t.data_ptr() for t in tensors],
+        _ATTEND_SHAPE.pack(bs, Hq, Hk, D, pages, page, most, kind, 0),
+        _ATTEND_STRIDES.pack(sq[0], sq[1], so[0], so[1], kp[0], kp[1], kp[2], vp[0], vp[1], vp[2],
+                             *st, *sl), D ** -0.5 if scale is None else scale, window, sinks, ws,
+        nbytes, _stream_on(dev, stream))
+    if status:
+        _check(status, "ssu_attend")
 
 
 def describe_blocks(tensors) -> tuple[ctypes.Array, int]:
