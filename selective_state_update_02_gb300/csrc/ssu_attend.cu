@@ -147,6 +147,15 @@ ssu_status_t ssu_attend(ssu_handle_t handle, const uint16_t *q, const uint16_t *
     p.q_heads = static_cast<int>(s.q_heads), p.kv_heads = static_cast<int>(s.kv_heads);
     p.share = static_cast<int>(s.q_heads / s.kv_heads);
     p.head_tiles = (p.share + kAttendRows - 1) / kAttendRows;
+    // The last vector of the caches, in 16-byte vectors from their start (in double: a stride may
+    // be any number of an array with one page).
+    const double last_k = static_cast<double>(s.num_pages) * u.k_pages[0] +
+                          static_cast<double>(s.page_size) * u.k_pages[1] +
+                          static_cast<double>(s.kv_heads) * u.k_pages[2];
+    const double last_v = static_cast<double>(s.num_pages) * u.v_pages[0] +
+                          static_cast<double>(s.page_size) * u.v_pages[1] +
+                          static_cast<double>(s.kv_heads) * u.v_pages[2];
+    p.wide = last_k / 8 > 4e9 || last_v / 8 > 4e9;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.err = handle->err;
     p.arrived = static_cast<unsigned *>(workspace);

@@ -278,6 +278,18 @@ def test_long_cache_past_32_bit_offsets(op):
     check(d["out"], ref)
 
 
+def test_extents_past_32_bits_of_vectors(op):
+    """Strides that put a cache's extent past 2^32 16-byte vectors (a single page, so no such
+    memory is there)."""
+    d = make([60, 13], Hq=4, Hk=2, D=64, page=64, seed=16)
+    d["page_table"][1] = d["page_table"][0]
+    for k in ("k_pages", "v_pages"):
+        one = d[k][int(d["page_table"][0, 0])].clone()
+        d[k] = one.as_strided((1, 64, 2, 64), (2 ** 37, 128, 64, 1))
+    d["page_table"][:] = 0
+    run_and_check(op, d)
+
+
 def test_no_requests(op):
     d = make([], seed=14)
     d["page_table"] = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
