@@ -57,12 +57,11 @@ cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, b
 
 // ---- the chunked form ----------------------------------------------------------------
 
-// How a call is cut: chunks per stretch, the most stretches that its prompts can have, and
-// whether any prompt can have more than one.
+// How a call is cut: chunks per stretch, the most stretches that gives, the most of them that are
+// not their prompt's last (those have a first pass), and the workspace.
 struct PromptPlan {
-    long long seg, stretches, columns, ctas;  // ctas: per stretch
-    bool first_pass;
-    long long decay, total;  // workspace: offset of the stretches' decays, bytes
+    long long seg, stretches, earlier, columns, ctas;  // ctas: per stretch
+    long long decay, total;  // offset of the stretches' decays, bytes
 };
 
 bool mma_sizes(const ssu_shape_t &s) {
@@ -73,12 +72,24 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     PromptPlan w{};
     w.columns = s.nheads * (s.headdim / kSlab);
     w.ctas = s.ngroups * ((w.columns / s.ngroups + 1) / 2);
+    // One CTA per SM: as many chunks per stretch as spread the call's over them.  Where the prompts
+    // alone come to more than half the SMs, a prompt of up to twice the mean length stays whole, as
+    // what a cut would gain it costs in the first pass (6 prompts of 5 to 10 chunks, 16 CTAs each:
+    // CUT_US cut in two, WHOLE_US whole; 24 of 1 to 25, 8 CTAs each: RAG5_US in stretches of 5,
+    // RAG6_US of 6; one of 16 chunks, 8 CTAs: ONE1_US in stretches of 1, ONE4_US of 4).
     const long long chunks = tokens / kChunk + s.batch;
-    w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;  // one CTA per SM
-    if (w.seg < 4) w.seg = 4;
+    w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;
+    if (2 * s.batch * w.ctas > sm_count) {
+        const long long whole = 2 * (tokens / kChunk) / s.batch;
+        if (w.seg < whole) w.seg = whole;
+    }
+    if (s.batch == 1) w.seg = (tokens / kChunk * w.ctas + sm_count - 1) / sm_count;
+    if (w.seg < 1) w.seg = 1;
+    if (w.seg > 1 << 23) w.seg = 1 << 23;  // token offsets stay below 2^31
     w.stretches = tokens / (w.seg * kChunk) + s.batch;
-    w.first_pass = tokens > w.seg * kChunk;
-    if (w.first_pass) {
+    w.earlier = tokens / (w.seg * kChunk);
+    if (tokens <= w.seg * kChunk) w.earlier = 0;
+    if (w.earlier) {
         w.decay = w.stretches * w.columns * kSlab * s.dstate * 4;
         w.total = w.decay + (w.stretches * w.columns * 4 + 255) / 256 * 256;
     }
@@ -136,7 +147,6 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
         e = ssu_host::allow_smem(handle, reinterpret_cast<const void *>(second), kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.ctas));
     cfg.blockDim = dim3(kPromptThreads);
     cfg.dynamicSmemBytes = kBytes;
     cfg.stream = st;
@@ -145,10 +155,12 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = handle.pdl ? 1 : 0;
-    if (w.first_pass) {
+    if (w.earlier) {
+        cfg.gridDim = dim3(static_cast<unsigned>(w.earlier * w.ctas));
         e = cudaLaunchKernelEx(&cfg, first, m, maps[0], maps[1], maps[2], maps[3]);
         if (e != cudaSuccess) return e;
     }
+    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.ctas));
     return cudaLaunchKernelEx(&cfg, second, m, maps[0], maps[1], maps[2], maps[3]);
 }
 
@@ -265,7 +277,8 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         const PromptPlan w = prompt_plan(s, tokens, handle->sm_count);
         PromptMmaParams m{};
         m.q = q;
-        m.seg = static_cast<int>(w.seg < INT_MAX ? w.seg : INT_MAX);
+        m.seg = static_cast<int>(w.seg);
+        m.after_first = w.earlier > 0 && handle->pdl;
         m.slabs = static_cast<int>(s.headdim / kSlab);
         m.local = static_cast<float *>(workspace);
         m.decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.decay);

@@ -25,10 +25,9 @@
 // An a_t beyond +-256 (log2) is cut there: exp is then 0 (or infinite) all the same, and a cut
 // sum stays small enough to be exact.
 //
-// Stretches.  A prompt that is long for the device is cut into stretches of `seg` chunks.  A
-// first pass (kFirst) runs U alone over every stretch but a prompt's last, from a zero state;
-// the second pass starts a stretch from the prompt's own state advanced through the earlier
-// stretches' results.
+// Stretches.  A prompt that is long for the device is cut into stretches.  A first pass (kFirst) runs
+// U alone over every stretch but a prompt's last, the first from the prompt's state and the others
+// from zero; the second pass starts a stretch from the results of those before it.
 //
 // What bounds it: ~1,800 cycles of tensor pipe per chunk and head (G 512, I, Y 256 each, U 768
 // with its three parts) against 96 KB that a CTA brings in through L2.
@@ -59,6 +58,7 @@ struct PromptMmaParams {
     PromptParams q;
     int seg;              // chunks per stretch
     int slabs;            // headdim / 64
+    int after_first;      // a first pass was launched before the second
     float *local;         // [stretch][head * slabs + slab][64 p][N]
     float *decay;         // [stretch][head * slabs + slab]: log2 of the stretch's decay
 };
@@ -275,27 +275,34 @@ struct PromptSmem {
     static constexpr int kTotal = kBars + 128;
 };
 
-// The stretch `g` of the call: its prompt and first chunk.  All threads get the answer; false
-// past the last stretch.  With `all`, every prompt is looked at and the bad ones counted.
-template <bool kIdx64>
-__device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long g, bool all,
-                                             long long *scan, long long &b, long long &index) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long before = 0;
+// Where a CTA works.
+struct Stretch {
+    long long b;       // prompt; -1: past the last stretch
+    long long g;       // the stretch's number in the call
+    int index, count;  // of the prompt's stretches
+};
+
+// The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's last;
+// all threads get the answer.  With `all`, every prompt is looked at and the bad ones counted.
+template <bool kIdx64, bool kFirst>
+__device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long long at, bool all,
+                                                long long *scan) {
     constexpr int kWarps = kPromptThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long per = static_cast<long long>(m.seg) * kChunk;
+    long long before = 0;  // stretches of the prompts before: all << 32 | those not the last
     if (tid == 0) scan[kWarps] = -1;
-    for (long long b0 = 0; b0 < m.q.p.batch; b0 += kPromptThreads) {
-        const long long bb = b0 + tid;
-        long long n = 0;
-        if (bb < m.q.p.batch) {
-            long long slot, lo, hi;
-            if (load_prompt<kIdx64>(m.q, bb, all, slot, lo, hi)) {
-                const long long per = static_cast<long long>(m.seg) * kChunk;
-                n = (hi - lo + per - 1) / per;
-                if (n == 0 && m.q.fresh && m.q.fresh[bb]) n = 1;  // only clears the slot
-            }
+    auto pick = [](long long v) { return kFirst ? v & 0xffffffffll : v >> 32; };
+#pragma unroll 1
+    for (long long b0 = 0; b0 < m.q.p.batch && (all || at >= pick(before)); b0 += kPromptThreads) {
+        const long long b = b0 + tid;
+        long long n = 0, slot, lo, hi;
+        if (b < m.q.p.batch && load_prompt<kIdx64>(m.q, b, all, slot, lo, hi)) {
+            n = (hi - lo + per - 1) / per;
+            if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
         }
-        long long incl = n;
+        const long long mine = n << 32 | (n > 1 ? n - 1 : 0);
+        long long incl = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
             const long long o = __shfl_up_sync(0xffffffffu, incl, x);
@@ -304,22 +311,22 @@ __device__ __forceinline__ bool find_stretch(const PromptMmaParams &m, long long
         __syncthreads();
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
-        long long base = before;
+        long long start = before + incl - mine;
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) base += scan[w];
+            if (w < warp) start += scan[w];
             before += scan[w];
         }
-        incl += base;
-        if (g >= incl - n && g < incl) {
-            scan[kWarps] = bb;
-            scan[kWarps + 1] = g - (incl - n);
+        const long long index = at - pick(start);
+        if (index >= 0 && index < pick(mine)) {
+            scan[kWarps] = b;
+            scan[kWarps + 1] = (start >> 32) + index;
+            scan[kWarps + 2] = index << 32 | n;
         }
-        if (!all && g < before) break;
     }
     __syncthreads();
-    b = scan[kWarps];
-    index = scan[kWarps + 1];
-    return b >= 0;
+    return Stretch{scan[kWarps], scan[kWarps + 1], static_cast<int>(scan[kWarps + 2] >> 32),
+                   static_cast<int>(scan[kWarps + 2])};
 }
 
 // Decay sums of one chunk, by the four warps of one warpgroup (one token per thread, `row`): the
@@ -370,28 +377,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     constexpr int kBlocks = Smem::kBlocks;
     constexpr int kParts = sizeof(ST) == 4 ? 3 : 2;  // bf16 parts of W
     extern __shared__ unsigned char raw[];
-    __shared__ long long scan[kPromptThreads / 32 + 2];
+    __shared__ long long scan[kPromptThreads / 32 + 3];
     __shared__ unsigned tmem_slot;
-    pdl_wait();
+    // A second pass behind a first is let in when the first has begun, so what came before the first
+    // is complete; it waits for the first before it reads its results, and before it ends.
+    if (kFirst || !m.after_first) pdl_wait();
+    if (kFirst) pdl_trigger();
     const SsuParams &p = m.q.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // Column c is head c / slabs, slab c % slabs; a group's columns go to CTAs in pairs, an odd
     // last one alone (its CTA then works on it twice and keeps one result).
     const int per_group = p.heads_per_group * m.slabs, pairs = (per_group + 1) / 2;
     const int ctas = p.nheads / p.heads_per_group * pairs;  // per stretch
-    const long long g = blockIdx.x / ctas;
-    const int cta = static_cast<int>(blockIdx.x - g * ctas), grp = cta / pairs;
+    const long long nth = blockIdx.x / ctas;
+    const int cta = static_cast<int>(blockIdx.x - nth * ctas), grp = cta / pairs;
     const int first_column = grp * per_group + 2 * (cta - grp * pairs);
     const bool paired = 2 * (cta - grp * pairs) + 1 < per_group;
     const int columns = p.nheads * m.slabs;
-    long long b, index;
-    if (!find_stretch<kIdx64>(m, g, !kFirst && blockIdx.x == 0, scan, b, index)) return;
+    const Stretch my =
+        find_stretch<kIdx64, kFirst>(m, nth, !kFirst && blockIdx.x == 0, scan);
+    if (my.b < 0) {
+        if (!kFirst && m.after_first) pdl_wait();
+        return;
+    }
+    const long long b = my.b, g = my.g;
     long long slot, begin, end;
     load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
-    const int from = static_cast<int>(begin + index * m.seg * kChunk);  // tokens fit 31 bits
-    const bool last = end - from <= static_cast<long long>(m.seg) * kChunk;
+    const int from = static_cast<int>(begin) + my.index * m.seg * kChunk;  // tokens fit 31 bits
+    const bool last = my.index == my.count - 1;
     const int to = last ? static_cast<int>(end) : from + m.seg * kChunk;
-    if (kFirst && last) return;  // nothing continues after a prompt's last stretch
 
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
@@ -609,17 +623,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
 #pragma unroll
         for (int i = 0; i < kShare; ++i) S[i] = 0.0f;
-        if (!kFirst && own) {
-            if (!(m.q.fresh && m.q.fresh[b] != 0)) {
+        // A prompt's state before a stretch: its slot's (or zeros) before the first, which a first
+        // pass also puts by where the last stretch would have its result, as the last stretch of the
+        // second pass overwrites the slot while the first may not have begun; what the first pass
+        // leaves of the stretches before any other.
+        auto kept = [&](long long k) {
+            return m.local + ((k * columns + column) * kSlab + kShare * part) * N + row;
+        };
+        const long long g0 = g - my.index;  // the prompt's first stretch
+        if (!kFirst && my.count > 1 && m.after_first) pdl_wait();
+        if (own && my.index == 0) {
+            if (!kFirst && my.count > 1) {
+#pragma unroll
+                for (int i = 0; i < kShare; ++i) S[i] = __ldcg(kept(g0 + my.count - 1) + i * N);
+            } else if (!(m.q.fresh && m.q.fresh[b] != 0)) {
 #pragma unroll
                 for (int i = 0; i < kShare; ++i) S[i] = static_cast<float>(*state_at(i));
             }
-            for (long long k = g - index; k < g; ++k) {
-                const float *loc =
-                    m.local + ((k * columns + column) * kSlab + kShare * part) * N + row;
-                const float f = exp2f(__ldcg(m.decay + k * columns + column));
+            int column_, h_, slab_;
+            if (kFirst && place(column_, h_, slab_)) {
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) S[i] = fmaf(S[i], f, __ldcg(loc + i * N));
+                for (int i = 0; i < kShare; ++i) __stcg(kept(g0 + my.count - 1) + i * N, S[i]);
+            }
+        }
+        if (!kFirst && own) {
+            for (long long k = g0; k < g; ++k) {
+                const float f = k == g0 ? 0.0f : exp2f(__ldcg(m.decay + k * columns + column));
+#pragma unroll
+                for (int i = 0; i < kShare; ++i)
+                    S[i] = k == g0 ? __ldcg(kept(k) + i * N) : fmaf(S[i], f, __ldcg(kept(k) + i * N));
             }
         }
         auto publish = [&]() {  // the state as the next chunk's bf16 operand
@@ -896,6 +928,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
     }
     if (!alive) atomicOr(&p.err[2], 1u);
+    if (!kFirst && m.after_first) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == kIssuer) {
