@@ -8,11 +8,13 @@
 //   S'  = exp(s(0, Q]) S  +  sum_j (exp(s(j, Q]) dtv_j x_j) (x) B_j
 //
 // that is four matrix products per chunk and head: G = C B^T [Q x Q], I = C S^T [Q x P],
-// Y = M X [Q x P] with M = G times the masked decays plus D on the diagonal, and U = B^T W [N x P] with W the weighted
-// tokens.  One CTA takes one head's stretch of a prompt, chunk after chunk, its state in
-// registers (thread n holds column n of the P = 64 rows).  G, I, U and Y accumulate in TMEM
-// (256 of the SM's 512 columns, so two CTAs share an SM and one's products run under the
-// other's elementwise work); M goes back into TMEM as an A operand.
+// Y = M X [Q x P] with M = G times the masked decays plus D on the diagonal, and U = B^T W [N x P]
+// with W the weighted tokens.  A column is 64 rows of one head's state; a CTA takes two columns of
+// one group through a prompt's stretch, chunk after chunk, so that G and every read of B and C are
+// shared, and I and U of both are one product 128 wide (an MMA of N = 128 takes 63 cycles where two
+// of N = 64 take 96: those read the first operand from shared memory twice).  The states stay in
+// registers (thread n holds column n of the 64 rows).  G, I, Y and U accumulate in TMEM (all 512
+// columns with M, which goes back there as Y's first operand), so a CTA has its SM to itself.
 //
 // Precision.  C, B and X are bf16 and exact.  M and the state that enters I are rounded to bf16
 // (2^-9 of a term in the mean square, as much as the bf16 readout itself carries).  W decides
@@ -25,12 +27,17 @@
 // An a_t beyond +-256 (log2) is cut there: exp is then 0 (or infinite) all the same, and a cut
 // sum stays small enough to be exact.
 //
-// Stretches.  A prompt that is long for the device is cut into stretches.  A first pass (kFirst) runs
-// U alone over every stretch but a prompt's last, the first from the prompt's state and the others
-// from zero; the second pass starts a stretch from the results of those before it.
+// Stretches.  A prompt that is long for the device is cut into stretches.  A first pass (kFirst)
+// runs U alone over every stretch but a prompt's last, the first from the prompt's state and the
+// others from zero; the second pass starts a stretch from the results of those before it.
 //
-// What bounds it: ~1,800 cycles of tensor pipe per chunk and head (G 512, I, Y 256 each, U 768
-// with its three parts) against 96 KB that a CTA brings in through L2.
+// What bounds it: the chain of a chunk's steps.  Of some 8,000 cycles per pair of columns and chunk
+// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 265 us, 2.2 TB/s, 0.2 of
+// the tensor pipe) M takes 2,000, W 1,900, Y and U 2,400 with the decays and the readout under
+// them, I 500 and the state 650; the tensor pipe is busy for 3,000 of them, issue slots for a third.
+// Products that run under M or the readout slow their TMEM loads by more than they hide: M a chunk
+// ahead measured 298 us, W before M 306, sixteen warps 279 to 300, one column per CTA and two CTAs
+// per SM 360.
 
 #pragma once
 
@@ -47,10 +54,8 @@ namespace {
 constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
 constexpr int kPair = 2;         // columns (a head's 64-row slab) per CTA, of one group
-constexpr int kSplit = 1;        // warpgroups per column
-constexpr int kCompute = kPair * kSplit * 128;     // threads of the elementwise work
-constexpr int kPromptThreads = kCompute + 64;      // one warp to issue, one to store
-constexpr int kShare = kSlab / kSplit;  // a thread's share of its row
+constexpr int kCompute = kPair * kChunk;       // threads of the elementwise work: a row each
+constexpr int kPromptThreads = kCompute + 64;  // one warp to issue, one to store
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -89,9 +94,10 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
                  : "memory");
 }
 
-// Waits for the barrier's phase of `parity`; gives up (false) after a bounded number of polls.
+// Waits for the barrier's phase of `parity`; gives up (false) after a second.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
-    for (int i = 0; i < (1 << 18); ++i) {
+    unsigned long long start = 0;
+    while (true) {
         unsigned done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -101,8 +107,11 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
             : "r"(bar), "r"(parity)
             : "memory");
         if (done) return true;
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+        if (!start) start = now;
+        if (now - start > 1000000000ull) return false;
     }
-    return false;
 }
 
 __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, unsigned bar, int x,
@@ -354,18 +363,17 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
 }
 
 // Roles.  One thread starts the loads and the products as their inputs become ready, another the
-// stores.  Sixteen warps do the elementwise work, eight per column; a thread's row (token of the
-// chunk, TMEM lane, column n of the state) is the same in a column's two warpgroups, which halve
-// each row.  Per chunk, with the barrier that each hand-over uses:
+// stores.  Eight warps do the elementwise work, four per column, a thread per row (token of the
+// chunk, TMEM lane, column n of the state).  Per chunk, with the barrier that each hand-over uses:
 //
 //   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [w] U -> u; [b, c] next G -> g
 //   compute:  [g] M, [i] I scaled -> m; [x] W -> w; the next chunk's decays; [y] readout into x's
 //             place -> r; [u] S advanced and published -> done
 //   store:    [r] readout out, then next x
 //
-// so Y runs under W, U under the readout and the decays, I and the loads under M.  (Readouts
-// stored by the threads themselves, a half row each, kept the shared-memory pipe busy for
-// thousands of cycles per chunk: 32 lines per instruction.)
+// so Y runs under W, U under the decays and the readout, I and the loads under M.  (Readouts
+// stored by the threads themselves kept the shared-memory pipe busy for thousands of cycles per
+// chunk: 32 lines per instruction.)
 template <int N, typename ST, bool kIdx64, bool kFirst>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
@@ -571,26 +579,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
     } else {
-        const int which = warp / (4 * kSplit), part = (warp >> 2) % kSplit, quarter = warp & 3;
+        const int which = warp >> 2, quarter = warp & 3;
         const int row = 32 * quarter + lane;
         // The thread's place in the call, worked out again where it is needed rather than held in
         // registers through the loop (the opaque copy keeps the compiler from holding it).
-        auto place = [&](int &column, int &h, int &slab) {
+        struct Place {
+            int column, h, slab;
+            bool keeps;  // whether the thread's results are kept
+        };
+        auto place = [&]() {
             unsigned block = blockIdx.x;
             asm volatile("" : "+r"(block));
-            const int c = static_cast<int>(block % ctas), grp = c / pairs;
-            const int first = grp * per_group + 2 * (c - grp * pairs);
-            const bool paired = 2 * (c - grp * pairs) + 1 < per_group;
-            column = first + (paired ? which : 0);
-            h = column / m.slabs, slab = column - h * m.slabs;
-            return which == 0 || paired;  // whether this thread's results are kept
+            const int c = static_cast<int>(block % ctas), of_group = 2 * (c % pairs);
+            const bool paired = of_group + 1 < per_group;
+            Place at;
+            at.column = c / pairs * per_group + of_group + (paired ? which : 0);
+            at.h = at.column / m.slabs, at.slab = at.column - at.h * m.slabs;
+            at.keeps = which == 0 || paired;
+            return at;
         };
-        int column, h, slab;
-        place(column, h, slab);
+        const Place here = place();
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
         const unsigned myX = sX + which * kTileBytes, myS = sS + which * N * 128;
-        const unsigned myY = tY + which * kSlab + kShare * part + lanes;
-        const unsigned myU = tU + which * kSlab + kShare * part + lanes;
+        const unsigned myY = tY + which * kSlab + lanes;
+        const unsigned myU = tU + which * kSlab + lanes;
         float *const vecs =
             reinterpret_cast<float *>(raw + (base - smem_u32(raw)) + Smem::kVec) +
             which * 2 * Smem::kVecFloats;
@@ -598,67 +610,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "n"(kCompute / kPair) : "memory");
         };
         float *const head = vecs + Smem::kConst;
-        if (part == kSplit - 1 && row == 0) head[2] = __ldg(p.D + h * p.D_h);
-        // The second warpgroup has less of M and works the decays out, a chunk ahead.  dt waits as
-        // raw bits: a conversion right behind its load would wait for it.
+        if (row == 0) head[2] = __ldg(p.D + here.h * p.D_h);
+        // The decays are worked out a chunk ahead.  dt waits as raw bits: a conversion right behind its
+        // load would wait for it.
         const unsigned short *const dt_col =
-            reinterpret_cast<const unsigned short *>(p.dt) + h * p.dt_h;
+            reinterpret_cast<const unsigned short *>(p.dt) + here.h * p.dt_h;
         unsigned dt_next = 0;
-        if (part == kSplit - 1) {
+        {
             unsigned dt = 0;
             if (from + row < to) dt = dt_col[(from + row) * p.dt_b];
             if (from + kChunk + row < to) dt_next = dt_col[(from + kChunk + row) * p.dt_b];
-            const float bias = __ldg(p.dt_bias + h * p.bias_h);
-            const float A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+            const float bias = __ldg(p.dt_bias + here.h * p.bias_h);
+            const float A2 = __ldg(p.A + here.h * p.A_h) * kLog2e;
             if (row == 0) head[0] = bias, head[1] = A2;
             chunk_decays(vecs, from + row < to, __uint_as_float(dt << 16), bias, A2, row, lane);
         }
 
-        // The state a stretch starts from: the thread holds S[kShare part ..][row].
-        float S[kShare];
+        // The state a stretch starts from: the thread holds S[0 ..][row].
+        float S[kSlab];
         const bool own = row < N;
-        auto state_at = [&](int i) {
-            return static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                   static_cast<long long>(slab * kSlab + kShare * part + i) * p.st_row + row;
+        auto state_at = [&](const Place &at, int i) {
+            return static_cast<ST *>(p.state) + slot * p.st_pool + at.h * p.st_head +
+                   static_cast<long long>(at.slab * kSlab + i) * p.st_row + row;
         };
 #pragma unroll
-        for (int i = 0; i < kShare; ++i) S[i] = 0.0f;
+        for (int i = 0; i < kSlab; ++i) S[i] = 0.0f;
         // A prompt's state before a stretch: its slot's (or zeros) before the first, which a first
         // pass also puts by where the last stretch would have its result, as the last stretch of the
         // second pass overwrites the slot while the first may not have begun; what the first pass
         // leaves of the stretches before any other.
         auto kept = [&](long long k) {
-            return m.local + ((k * columns + column) * kSlab + kShare * part) * N + row;
+            return m.local + (k * columns + here.column) * (kSlab * N) + row;
         };
         const long long g0 = g - my.index;  // the prompt's first stretch
         if (!kFirst && my.count > 1 && m.after_first) pdl_wait();
         if (own && my.index == 0) {
             if (!kFirst && my.count > 1) {
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) S[i] = __ldcg(kept(g0 + my.count - 1) + i * N);
+                for (int i = 0; i < kSlab; ++i) S[i] = __ldcg(kept(g0 + my.count - 1) + i * N);
             } else if (!(m.q.fresh && m.q.fresh[b] != 0)) {
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) S[i] = static_cast<float>(*state_at(i));
+                for (int i = 0; i < kSlab; ++i) S[i] = static_cast<float>(*state_at(here, i));
             }
-            int column_, h_, slab_;
-            if (kFirst && place(column_, h_, slab_)) {
+            if (kFirst && here.keeps) {
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) __stcg(kept(g0 + my.count - 1) + i * N, S[i]);
+                for (int i = 0; i < kSlab; ++i) __stcg(kept(g0 + my.count - 1) + i * N, S[i]);
             }
         }
         if (!kFirst && own) {
             for (long long k = g0; k < g; ++k) {
-                const float f = k == g0 ? 0.0f : exp2f(__ldcg(m.decay + k * columns + column));
+                const float f = k == g0 ? 0.0f : exp2f(__ldcg(m.decay + k * columns + here.column));
 #pragma unroll
-                for (int i = 0; i < kShare; ++i)
+                for (int i = 0; i < kSlab; ++i)
                     S[i] = k == g0 ? __ldcg(kept(k) + i * N) : fmaf(S[i], f, __ldcg(kept(k) + i * N));
             }
         }
         auto publish = [&]() {  // the state as the next chunk's bf16 operand
             if (own) {
 #pragma unroll
-                for (int c = 0; c < kShare / 8; ++c)
-                    store_smem16(swizzled(myS, row, kShare / 8 * part + c),
+                for (int c = 0; c < 8; ++c)
+                    store_smem16(swizzled(myS, row, c),
                                  make_uint4(f2_to_bf2(S[8 * c], S[8 * c + 1]),
                                             f2_to_bf2(S[8 * c + 2], S[8 * c + 3]),
                                             f2_to_bf2(S[8 * c + 4], S[8 * c + 5]),
@@ -683,13 +694,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (alive) alive = mbar_wait(bar_b, phase);
                 if (row >= valid) {
 #pragma unroll
-                    for (int c = 0; c < kShare / 8; ++c) {
-                        store_smem16(swizzled(myX, row, kShare / 8 * part + c), make_uint4(0, 0, 0, 0));
+                    for (int c = 0; c < 8; ++c) {
+                        store_smem16(swizzled(myX, row, c), make_uint4(0, 0, 0, 0));
                         if (which == 0)
 #pragma unroll
                             for (int k = 0; k < kBlocks; ++k)
                                 store_smem16(swizzled(sB + phase * kBBytes + k * kTileBytes, row,
-                                                      kShare / 8 * part + c),
+                                                      c),
                                              make_uint4(0, 0, 0, 0));
                     }
                 }
@@ -706,16 +717,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // (rolled loops: unrolled, with the cases of every block side by side, the code is
                 // larger than the instruction cache and M took twice as long)
                 const unsigned myM = tM + which * 64 + lanes;
-                const int block0 = 4 / kSplit * part, blocks = 4 / kSplit;
-                const int full = quarter < block0 ? 0 : min(quarter - block0, blocks);
 #pragma unroll 1
-                for (int k = 0; k < 2 * full; ++k) {  // columns before the row's 32 tokens
-                    const int col = 32 * block0 + 16 * k, cb = col / 32;
+                for (int col = 0; col < 32 * quarter; col += 16) {  // before the row's 32 tokens
                     unsigned gg[16], mm[8];
                     tc_load16(tG + lanes + col, gg);
                     // the blocks between the columns' and the row's
-                    const float f = exp2f(up + ((cb < 1 && quarter > 1 ? t.y : 0.0f) +
-                                                (cb < 2 && quarter > 2 ? t.z : 0.0f)));
+                    const float f = exp2f(up + ((col < 32 && quarter > 1 ? t.y : 0.0f) +
+                                                (col < 64 && quarter > 2 ? t.z : 0.0f)));
                     const float4 *vv = reinterpret_cast<const float4 *>(v0 + col);
                     tc_wait_ld();
 #pragma unroll
@@ -734,35 +742,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     tc_store8(myM + col / 2, mm);
                 }
-                if (quarter >= block0 && quarter < block0 + blocks) {
 #pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {  // the row's own 32 tokens
-                        const int col = 32 * quarter + 16 * k;
-                        unsigned gg[16], mm[8];
-                        tc_load16(tG + lanes + col, gg);
-                        const float4 *pp = reinterpret_cast<const float4 *>(pre + col);
-                        const int edge = lane - 16 * k;  // the last column kept
-                        tc_wait_ld();
+                for (int k = 0; k < 2; ++k) {  // the row's own 32 tokens
+                    const int col = 32 * quarter + 16 * k;
+                    unsigned gg[16], mm[8];
+                    tc_load16(tG + lanes + col, gg);
+                    const float4 *pp = reinterpret_cast<const float4 *>(pre + col);
+                    const int edge = lane - 16 * k;  // the last column kept
+                    tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 q = pp[j];  // (prefix, dtv) of two columns
-                            const float e0 =
-                                exp2_ftz(up - q.x) * (q.y * __uint_as_float(gg[2 * j]));
-                            const float e1 =
-                                exp2_ftz(up - q.z) * (q.w * __uint_as_float(gg[2 * j + 1]));
-                            // on the diagonal, D x of the token itself
-                            mm[j] = f2_to_bf2(2 * j < edge    ? e0
-                                              : 2 * j == edge ? e0 + D
-                                                              : 0.0f,
-                                              2 * j + 1 < edge    ? e1
-                                              : 2 * j + 1 == edge ? e1 + D
-                                                                  : 0.0f);
-                        }
-                        tc_store8(myM + col / 2, mm);
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 q = pp[j];  // (prefix, dtv) of two columns
+                        const float e0 =
+                            exp2_ftz(up - q.x) * (q.y * __uint_as_float(gg[2 * j]));
+                        const float e1 =
+                            exp2_ftz(up - q.z) * (q.w * __uint_as_float(gg[2 * j + 1]));
+                        // on the diagonal, D x of the token itself
+                        mm[j] = f2_to_bf2(2 * j < edge    ? e0
+                                          : 2 * j == edge ? e0 + D
+                                                          : 0.0f,
+                                          2 * j + 1 < edge    ? e1
+                                          : 2 * j + 1 == edge ? e1 + D
+                                                              : 0.0f);
                     }
+                    tc_store8(myM + col / 2, mm);
                 }
 #pragma unroll 1
-                for (int cb = max(quarter + 1, block0); cb < block0 + blocks; ++cb) {
+                for (int cb = quarter + 1; cb < 4; ++cb) {
                     const unsigned zero[16] = {};
                     tc_store16(myM + 16 * cb, zero);
                 }
@@ -774,7 +780,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
-                for (int half = 0; half < kShare / 32; ++half) {
+                for (int half = 0; half < 2; ++half) {
                     unsigned ii[2][16];
                     tc_load16(myY + 32 * half, ii[0]);
                     tc_load16(myY + 32 * half + 16, ii[1]);
@@ -805,9 +811,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                                 (quarter < 3 ? t.w : 0.0f));
                 if (alive) alive = mbar_wait(bar_x, phase);
 #pragma unroll 2
-                for (int c = 0; c < kShare / 8; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     float x[8];
-                    widen16(load_smem16(swizzled(myX, row, kShare / 8 * part + c)), x);
+                    widen16(load_smem16(swizzled(myX, row, c)), x);
                     unsigned bits[kParts][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -822,12 +828,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         store_smem16(
-                            swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, kShare / 8 * part + c),
+                            swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, c),
                             make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
                     if constexpr (kParts == 3)
                         if (row >= 64)
                             store_smem16(
-                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, kShare / 8 * part + c),
+                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, c),
                                 make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
                 }
             }
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const float4 t = *reinterpret_cast<const float4 *>(v0 + 3 * kChunk);
             const float chunk_decay = (t.x + t.y) + (t.z + t.w), f = exp2f(chunk_decay);
             if (kFirst) stretch_decay += chunk_decay;
-            if (part == kSplit - 1 && tok + kChunk < to) {  // the next chunk's decays
+            if (tok + kChunk < to) {  // the next chunk's decays
                 const float dt = __uint_as_float(dt_next << 16);
                 if (tok + 2 * kChunk + row < to)
                     dt_next = dt_col[(tok + 2 * kChunk + row) * p.dt_b];
@@ -849,7 +855,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int half = 0; half < kShare / 32; ++half) {
+                for (int half = 0; half < 2; ++half) {
                     unsigned yy[2][16], o[16];
                     tc_load16(myY + 32 * half, yy[0]);
                     tc_load16(myY + 32 * half + 16, yy[1]);
@@ -858,16 +864,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     for (int i = 0; i < 16; ++i)
                         o[i] = f2_to_bf2(__uint_as_float(yy[i / 8][2 * i % 16]),
                                          __uint_as_float(yy[i / 8][2 * i % 16 + 1]));
-                    int column, h, slab;
                     if (valid == kChunk) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            store_smem16(swizzled(myX, row, kShare / 8 * part + 4 * half + c),
+                            store_smem16(swizzled(myX, row, 4 * half + c),
                                          make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2],
                                                     o[4 * c + 3]));
-                    } else if (place(column, h, slab) && row < valid) {
-                        __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b + h * p.out_h +
-                                                   slab * kSlab + kShare * part + 32 * half;
+                    } else if (const Place at = place(); at.keeps && row < valid) {
+                        __nv_bfloat16 *const dst = p.out + (tok + row) * p.out_b +
+                                                   at.h * p.out_h + at.slab * kSlab + 32 * half;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             reinterpret_cast<uint4 *>(dst)[c] = make_uint4(
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int half = 0; half < kShare / 32; ++half) {
+            for (int half = 0; half < 2; ++half) {
                 unsigned uu[2][16];
                 tc_load16(myU + 32 * half, uu[0]);
                 tc_load16(myU + 32 * half + 16, uu[1]);
@@ -906,23 +911,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
         }
 
-        int column_, h_, slab_;
-        const bool keeps = place(column_, h_, slab_);
-        column = column_, h = h_, slab = slab_;
-        if (own && keeps) {
+        const Place at = place();
+        if (own && at.keeps) {
             if (kFirst) {
-                float *loc = m.local + ((g * columns + column) * kSlab + kShare * part) * N + row;
+                float *loc = m.local + (g * columns + at.column) * (kSlab * N) + row;
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) __stcg(loc + i * N, S[i]);
-                if (part == 0 && row == 0) __stcg(m.decay + g * columns + column, stretch_decay);
+                for (int i = 0; i < kSlab; ++i) __stcg(loc + i * N, S[i]);
+                if (row == 0) __stcg(m.decay + g * columns + at.column, stretch_decay);
             } else if (last) {
                 slot = load_slot<kIdx64>(p, scan[kPromptThreads / 32]);
 #pragma unroll
-                for (int i = 0; i < kShare; ++i) {
+                for (int i = 0; i < kSlab; ++i) {
                     if constexpr (sizeof(ST) == 4)
-                        *state_at(i) = S[i];
+                        *state_at(at, i) = S[i];
                     else
-                        *state_at(i) = __float2bfloat16(S[i]);
+                        *state_at(at, i) = __float2bfloat16(S[i]);
                 }
             }
         }
