@@ -76,7 +76,7 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     // alone come to more than half the SMs, a prompt of up to twice the mean length stays whole, as
     // what a cut would gain it costs in the first pass (6 prompts of 5 to 10 chunks, 16 CTAs each:
     // 57 us cut in two, 44.7 whole; 24 of 1 to 25, 8 CTAs each: 54.5 us in stretches of 3,
-    // 49.0 of 5, 62.3 of 8; one of 16 chunks, 8 CTAs: 28.7 in stretches of 1, 38.4 of 5).
+    // 49.8 of 5, 62.3 of 8; one of 16 chunks, 8 CTAs: 29.2 in stretches of 1, 38.4 of 5).
     const long long chunks = tokens / kChunk + s.batch;
     w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;
     if (2 * s.batch * w.ctas > sm_count) {

@@ -19,8 +19,9 @@
 // Precision.  C, B and X are bf16 and exact.  M and the state that enters I are rounded to bf16
 // (2^-9 of a term in the mean square, as much as the bf16 readout itself carries).  W decides
 // the state that is carried on, so it enters as the sum of three bf16 parts (24 bits: all of an
-// fp32 value; two parts measured 1.1e-6 of the state in the 2-norm, against 1e-7) where the state
-// is kept in fp32, of two where it is rounded to bf16 in the end, and runs in fp32 either way.
+// fp32 value; with two a head's state is up to 3e-6 off in the 2-norm, with three below 4.4e-7)
+// where the state is kept in fp32, of two where it is rounded to bf16 in the end, and runs in fp32
+// either way.
 // Exponents are sums over short runs that never cross a chunk: within blocks of 32 tokens
 // prefix and suffix sums, between blocks the block totals, so no exponent is a difference of
 // two large sums except inside the diagonal block, whose weights are rounded to bf16 anyway.
@@ -31,13 +32,13 @@
 // runs U alone over every stretch but a prompt's last, the first from the prompt's state and the
 // others from zero; the second pass starts a stretch from the results of those before it.
 //
-// What bounds it: the chain of a chunk's steps.  Of some 8,000 cycles per pair of columns and chunk
-// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 265 us, 2.2 TB/s, 0.2 of
-// the tensor pipe) M takes 2,000, W 1,900, Y and U 2,400 with the decays and the readout under
-// them, I 500 and the state 650; the tensor pipe is busy for 3,000 of them, issue slots for a third.
+// What bounds it: the chain of a chunk's steps.  Of some 8,300 cycles per pair of columns and chunk
+// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 277 us, 2.1 TB/s, 0.2 of
+// the tensor pipe) M takes 2,000, W 2,000, Y and U 2,600 with the decays and the readout under
+// them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a third.
 // Products that run under M or the readout slow their TMEM loads by more than they hide: M a chunk
-// ahead measured 298 us, W before M 306, sixteen warps 279 to 300, one column per CTA and two CTAs
-// per SM 360.
+// ahead measured 1.11 of the time, W before M 1.14, sixteen warps 1.04 to 1.12, one column per CTA
+// and two CTAs per SM 1.34.
 
 #pragma once
 
@@ -265,7 +266,10 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 // Shared memory: tiles first (1024-byte aligned), then the per-token values.  x, S and W hold one
 // tile per column, side by side, as the two blocks of an operand 128 wide.  B has two places (the
 // next chunk's G is formed before this one's U is done); W's second part takes S's place, which
-// I has read by then, and gives it back when U is done; readouts leave from x's place.
+// I has read by then, and gives it back when U is done; readouts leave from x's place.  W's third
+// part has half a tile per column for tokens 64 .. 127; for tokens 0 .. 63, where dstate is 128 and
+// no room is left, it takes the upper columns of C's place, which the next C gets once those
+// products (U's first) are done.
 template <int N>
 struct PromptSmem {
     static constexpr int kBlocks = N / 64;  // 64-column tiles of B and C
@@ -275,7 +279,8 @@ struct PromptSmem {
     static constexpr int kW1 = kX + kPair * kTileBytes;
     static constexpr int kW2 = kW1 + kPair * kTileBytes;  // also S: bf16 [n][64 p]
     static constexpr int kW3 = kW2 + kPair * kTileBytes;  // tokens 64 .. 127
-    static constexpr int kVec = kW3 + kPair * kTileBytes / 2;
+    static constexpr int kW3First = N == 128 ? kC + kTileBytes : kW3 + kTileBytes;  // 0 .. 63
+    static constexpr int kVec = kW3 + (N == 128 ? 1 : 2) * kTileBytes;
     // floats of a chunk's tokens: v0 (128), pairs (prefix, dtv) (256), block totals (4), the
     // head's dt_bias, A log2 e and D (4); for this chunk and the next, for each column
     static constexpr int kConst = 3 * kChunk + 4;
@@ -291,8 +296,8 @@ struct Stretch {
     int index, count;  // of the prompt's stretches
 };
 
-// The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's last;
-// all threads get the answer.  With `all`, every prompt is looked at and the bad ones counted.
+// The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's
+// last; all threads get the answer.  With `all`, every prompt is looked at and the bad ones counted.
 template <bool kIdx64, bool kFirst>
 __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long long at, bool all,
                                                 long long *scan) {
@@ -366,7 +371,8 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
 // stores.  Eight warps do the elementwise work, four per column, a thread per row (token of the
 // chunk, TMEM lane, column n of the state).  Per chunk, with the barrier that each hand-over uses:
 //
-//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [w] U -> u; [b, c] next G -> g
+//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [w] U -> 3, u; [3] rest of C;
+//             [b, c] next G -> g
 //   compute:  [g] M, [i] I scaled -> m; [x] W -> w; the next chunk's decays; [y] readout into x's
 //             place -> r; [u] S advanced and published -> done
 //   store:    [r] readout out, then next x
@@ -417,15 +423,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
-    const unsigned sW1 = base + Smem::kW1, sW2 = base + Smem::kW2, sW3 = base + Smem::kW3;
+    const unsigned sW1 = base + Smem::kW1, sW2 = base + Smem::kW2;
     const unsigned sS = sW2;
     const unsigned bars = base + Smem::kBars;
     const unsigned bar_b = bars, bar_c = bars + 8, bar_x = bars + 16, bar_g = bars + 24,
                    bar_i = bars + 32, bar_u = bars + 40, bar_y = bars + 48, bar_w = bars + 56,
-                   bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80;
+                   bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80, bar_3 = bars + 88;
     if (tid == 0) {
         for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
         for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute / 32);
+        mbar_init(bar_3, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = kCompute / 32;  // the issuing warp
@@ -460,12 +467,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (int k = 0; k < kBlocks; ++k)
                     tma_load(sB + place * kBBytes + k * kTileBytes, &map_b, bar_b, k * 64, grp, tok);
             };
-            auto load_c = [&](int tok) {
-                mbar_expect(bar_c, kBBytes);
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k)
-                    tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp, tok);
+            auto load_c = [&](int tok, int k) {
+                if (k == 0) mbar_expect(bar_c, kBBytes);
+                tma_load(sC + k * kTileBytes, &map_c, bar_c, k * 64, grp, tok);
             };
+            constexpr bool kShared = kParts == 3 && N == 128;  // W3 and C's upper columns
             // Shared-memory address of a tile, from an opaque copy of the base: the operands' many
             // descriptors are worked out where they are used instead of held in registers.
             auto tile = [&](int offset) {
@@ -485,7 +491,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             };
             if (from < to) {
                 load_b(from, 0);
-                if (!kFirst) load_c(from);
+                if (!kFirst)
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k) load_c(from, k);
                 load_x(from);
                 if (!kFirst) {
                     alive = mbar_wait(bar_b, 0);
@@ -519,7 +527,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     tc_commit(bar_i);
                     if (alive) alive = mbar_wait(bar_i, phase);
-                    if (more) load_c(tok + kChunk);
+                    if (more)
+#pragma unroll
+                        for (int k = 0; k < (kShared ? 1 : kBlocks); ++k) load_c(tok + kChunk, k);
                     if (alive) alive = mbar_wait(bar_m, phase);
                     if (alive) alive = mbar_wait(bar_x, phase);
                     tc_fence_after();
@@ -536,17 +546,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (alive) alive = mbar_wait(bar_w, phase);
                 tc_fence_after();
                 const unsigned b_now = tile(Smem::kB) + phase * kBBytes;
-                const unsigned w1 = tile(Smem::kW1), w2 = tile(Smem::kW2), w3 = tile(Smem::kW3);
-#pragma unroll
-                for (int k = 0; k < (kParts == 3 ? 20 : 16); ++k) {
-                    const int part = k / 8, kk = k % 8 + (part == 2 ? 4 : 0);
-                    const unsigned w = part == 0   ? w1 + kk * 2048
-                                       : part == 1 ? w2 + kk * 2048
-                                                   : w3 + (kk - 4) * 2048;
+                const unsigned w1 = tile(Smem::kW1), w2 = tile(Smem::kW2), w3 = tile(Smem::kW3),
+                               w3_first = tile(Smem::kW3First);
+                auto product_u = [&](unsigned w, int kk, unsigned block, bool more_of_it) {
                     mma_ss(tU, operand(b_now + kk * 2048, N == 128 ? kTileBytes : 0),
-                           operand(w, part < 2 ? kTileBytes : kTileBytes / 2),
-                           instruction(kPair * kSlab, true, true), k > 0);
+                           operand(w, block), instruction(kPair * kSlab, true, true), more_of_it);
+                };
+                if constexpr (kParts == 3) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        product_u(w3_first + k * 2048, k, kTileBytes / 2, k > 0);
+                    if (kShared && !kFirst) tc_commit(bar_3);
+#pragma unroll
+                    for (int k = 4; k < 8; ++k)
+                        product_u(w3 + (k - 4) * 2048, k, kTileBytes / 2, true);
                 }
+                if (kShared && !kFirst) {  // (under the products just given)
+                    if (alive) alive = mbar_wait(bar_3, phase);
+                    if (more) load_c(tok + kChunk, 1);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k)  // the small parts first: sums lose less
+                    product_u((k < 8 ? w2 : w1) + k % 8 * 2048, k % 8, kTileBytes,
+                              kParts == 3 || k > 0);
                 tc_commit(bar_u);
                 if (!kFirst && more) {  // every reader of G has passed m
                     if (alive) alive = mbar_wait(bar_b, phase ^ 1);
@@ -601,6 +623,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const Place here = place();
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;  // (32 quarter) << 16
         const unsigned myX = sX + which * kTileBytes, myS = sS + which * N * 128;
+        const unsigned myW3 = base + (row < 64 ? Smem::kW3First : Smem::kW3) +
+                              which * (kTileBytes / 2);
         const unsigned myY = tY + which * kSlab + lanes;
         const unsigned myU = tU + which * kSlab + lanes;
         float *const vecs =
@@ -611,8 +635,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         float *const head = vecs + Smem::kConst;
         if (row == 0) head[2] = __ldg(p.D + here.h * p.D_h);
-        // The decays are worked out a chunk ahead.  dt waits as raw bits: a conversion right behind its
-        // load would wait for it.
+        // The decays are worked out a chunk ahead.  dt waits as raw bits: a conversion right behind
+        // its load would wait for it.
         const unsigned short *const dt_col =
             reinterpret_cast<const unsigned short *>(p.dt) + here.h * p.dt_h;
         unsigned dt_next = 0;
@@ -831,10 +855,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                             swizzled((k == 0 ? sW1 : sW2) + which * kTileBytes, row, c),
                             make_uint4(bits[k][0], bits[k][1], bits[k][2], bits[k][3]));
                     if constexpr (kParts == 3)
-                        if (row >= 64)
-                            store_smem16(
-                                swizzled(sW3 + which * (kTileBytes / 2), row - 64, c),
-                                make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
+                        store_smem16(swizzled(myW3, row & 63, c),
+                                     make_uint4(bits[2][0], bits[2][1], bits[2][2], bits[2][3]));
                 }
             }
             fence_async_smem();
@@ -930,7 +952,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
         }
     }
-    if (!alive) atomicOr(&p.err[2], 1u);
+    if (!alive) {  // what is in flight lands long before this is over
+        atomicOr(&p.err[2], 1u);
+        __nanosleep(1000000);
+    }
     if (!kFirst && m.after_first) pdl_wait();
     tc_fence_before();
     __syncthreads();
