@@ -201,7 +201,9 @@ ssu_status_t ssu_update_from_host(ssu_handle_t handle, void *state_pool,
  * Synchronise `stream`, then read and clear the handle's device counters.
  * *skipped receives the number of requests skipped since the last read (may be NULL);
  * *first_bad receives the smallest skipped request index b, or -1 (may be NULL).
- * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_OK otherwise.
+ * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_ERR_CUDA when a prompt kernel gave up a wait
+ * for its own copies or products (after a second; its results are then not valid), SSU_OK
+ * otherwise.
  */
 ssu_status_t ssu_get_error(ssu_handle_t handle, ssu_stream_t stream, uint32_t *skipped,
                            int64_t *first_bad);
@@ -371,6 +373,13 @@ ssu_status_t ssu_copy_set_launch(ssu_handle_t handle, const ssu_copy_launch_t *l
  * is out of range or if its offsets are not 0 <= cu_tokens[b] <= cu_tokens[b + 1] <= tokens.
  * Slots must be distinct and prompts must not overlap, as for ssu_update.
  *
+ * Two forms.  Where headdim is a multiple of 64, dstate 64 or 128, and x, B, C and out are 16-byte
+ * aligned with strides that are multiples of 8, chunks of 128 tokens run as matrix products: states
+ * in fp32, while the readout's weights and the state it reads are rounded to bf16 once per chunk
+ * (about 2^-9 of the readout in the mean square, as much as its own rounding).  Any other call runs
+ * token by token in fp32.  An infinity or NaN in x, B, C or dt of a token may then spread to the
+ * readouts of its prompt's earlier tokens in the same chunk (never to other prompts).
+ *
  * shape->batch is the number of prompts; strides->x[0], out[0], dt[0], B[0] and C[0] are the
  * strides of the token index; `tokens` (up to 2^31 - 1) is the number of token rows.
  * `fresh` is a device array of batch bytes, or NULL (every prompt continues from its slot).
@@ -431,7 +440,7 @@ typedef struct {
  * slots[t] / page_size.  A token with slots[t] = -1 has its queries written and its key and
  * value left out of the cache.  A token whose position lies outside the table, or whose slot is
  * neither -1 nor inside the cache, is skipped (nothing of it is written) and counted
- * (ssu_get_error).  Slots must be distinct.  q, k, v, q_out, k_pages, v_pages, q_weight,
+ * (ssu_get_error).  Slots must be distinct.  Head strides are at most 2^31 - 1.  q, k, v, q_out, k_pages, v_pages, q_weight,
  * k_weight [headdim] fp32 and table are 16-byte aligned.  q_out may be q itself (same strides).
  * Enqueued on `stream`; allocates and synchronises nothing.
  */
