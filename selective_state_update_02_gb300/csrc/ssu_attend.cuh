@@ -619,12 +619,17 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
         return count ? (count + Geo::kTile - 1) / Geo::kTile + kUnitCost : 0;
     };
     long long total = 0;
+    bool empty = false;  // a request without places, which this CTA sees to in the end
 #pragma unroll 1
-    for (long long b = tid; b < p.requests; b += kThreads) total += places_of(b);
+    for (long long b = tid; b < p.requests; b += kThreads) {
+        const long long n = places_of(b);
+        total += n;
+        empty |= n == 0 && static_cast<unsigned>(b) % gridDim.x == blockIdx.x;
+    }
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
     if (lane == 0) scan[warp] = total;
-    __syncthreads();
+    const bool any_empty = __syncthreads_or(empty);
     total = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) total += scan[w];
@@ -771,7 +776,7 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
     }
 
     // Requests without visible keys: zeros; invalid lengths: counted.
-    for (long long b = blockIdx.x; b < p.requests; b += gridDim.x) {
+    for (long long b = blockIdx.x; any_empty && b < p.requests; b += gridDim.x) {
         bool good;
         if (visible_of<kIdx64>(p, b, good).count) continue;
         if (!good) {
