@@ -19,9 +19,9 @@
 // output; units cut by a stretch's end leave their part in the workspace and the last CTA to
 // arrive joins the parts, in their order, so results do not depend on timing.
 //
-// Inside a CTA every warp takes its 16 or 32 of a tile's keys into its own ring of stages with cp.async (rows
-// 16 bytes apart in banks, so ldmatrix has no conflicts), ahead of their use across unit borders,
-// and keeps its own m, l, o: no barrier until a unit ends.  (A bulk copy per row and lane instead
+// Inside a CTA every warp takes its 16 or 32 of a tile's keys into its own ring of stages with
+// cp.async (rows 16 bytes apart in banks, so ldmatrix has no conflicts), ahead of their use across
+// unit borders, and keeps its own m, l, o: no barrier until a unit ends.  (A bulk copy per row and lane instead
 // was 20 % slower: its operands are a warp's, so 32 rows are 32 turns.)
 
 #pragma once
@@ -164,8 +164,8 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const unsigned (&a)[4], 
 }
 
 // Where the lane's key of a step lies (where a step has 16 keys, lanes 16 .. 31 repeat lanes 0 ..
-// 15).  The page id is kept as it was loaded, a step ahead of its use: a look at it right behind the
-// load would wait for it.
+// 15).  The page id is kept as it was loaded, a step ahead of its use: a look at it right behind
+// the load would wait for it.
 template <bool kIdx64>
 struct KeyPlace {
     using Id = typename std::conditional<kIdx64, long long, int>::type;
@@ -500,11 +500,12 @@ __device__ __forceinline__ void write_part(const AttendParams &p, int unit, int 
     }
 }
 
-// Joins the parts of a unit and writes its rows: the parts come into shared memory (the ring is free
-// by now), as many at a time as fit, all their copies together; (m, l) become each row's weights
-// (a running maximum from part to part was a chain of 200 cycles for each), and every thread sums the pairs that it owns over the parts.  The order is fixed.  The loops stay
-// rolled: this code runs once per CTA, after a stream that has pushed it out of every cache, and
-// unrolled its fetch alone took longer than the join (14 us for 38 parts).
+// Joins the parts of a unit and writes its rows: the parts come into shared memory (the ring is
+// free by now), as many at a time as fit, all their copies together; (m, l) become each row's
+// weights (a running maximum from part to part was a chain of 200 cycles for each), and every
+// thread sums the pairs that it owns over the parts.  The order is fixed.  The loops stay rolled:
+// this code runs once per CTA, after a stream that has pushed it out of every cache, and unrolled
+// its fetch alone took longer than the join (14 us for 38 parts).
 template <int D>
 __device__ __forceinline__ void join_parts(const AttendParams &p, const Partial &u, int first,
                                            int last, float2 *room, float2 *stat, int warp,
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
     using Geo = AttendGeo<D>;
     constexpr int W = Geo::kWarps, kThreads = 32 * W, S = Geo::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long scan[W];
+    __shared__ longlong2 scan[W];
     __shared__ long long found[2];
     __shared__ unsigned joins[2];
     pdl_wait();
@@ -610,57 +611,71 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
     const unsigned ring = smem_addr(smem) + warp * (S * Geo::kStageBytes);
 
     // The line's length for one unit of each request, then this CTA's stretch and the request that
-    // holds its first place.
+    // holds its first place.  A scan of the first kThreads requests gives both at once; the sums
+    // of 32 threads' places fit 32 bits (a request has at most 2^31 / kTile).
     const int units = p.kv_heads * p.head_tiles;
-    auto places_of = [&](long long b) -> long long {
+    auto places_of = [&](long long b) -> unsigned {
         if (b >= p.requests) return 0;
         bool good;
         const int count = visible_of<kIdx64>(p, b, good).count;
         return count ? (count + Geo::kTile - 1) / Geo::kTile + kUnitCost : 0;
     };
-    long long total = 0;
-    bool empty = false;  // a request without places, which this CTA sees to in the end
+    auto warp_scan = [&](unsigned n) {  // inclusive
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const unsigned o = __shfl_up_sync(0xffffffffu, n, x);
+            if (lane >= x) n += o;
+        }
+        return n;
+    };
+    const unsigned n0 = places_of(tid), incl0 = warp_scan(n0);
+    bool empty = n0 == 0 && tid % gridDim.x == blockIdx.x;  // a request this CTA sees to in the end
+    long long rest = 0;
 #pragma unroll 1
-    for (long long b = tid; b < p.requests; b += kThreads) {
-        const long long n = places_of(b);
-        total += n;
-        empty |= n == 0 && static_cast<unsigned>(b) % gridDim.x == blockIdx.x;
+    for (long long b0 = kThreads; b0 < p.requests; b0 += kThreads) {
+        const unsigned n = places_of(b0 + tid);
+        rest += n;
+        empty |= n == 0 && static_cast<unsigned>(b0 + tid) % gridDim.x == blockIdx.x;
     }
+    if (p.requests > kThreads) {
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-    if (lane == 0) scan[warp] = total;
+        for (int x = 16; x >= 1; x >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, x);
+    }
+    if (lane == 31) scan[warp] = longlong2{incl0, rest};
     const bool any_empty = __syncthreads_or(empty);
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) total += scan[w];
+    long long to = incl0, before = 0, total = 0;  // places up to and with request tid; of the first
+#pragma unroll                                    // kThreads; of all
+    for (int w = 0; w < W; ++w) {
+        const longlong2 v = scan[w];
+        if (w < warp) to += v.x;
+        before += v.x;
+        total += v.x + v.y;
+    }
     const long long all = total * units;
     const long long each = (all + gridDim.x - 1) / gridDim.x;
     const long long begin = blockIdx.x * each;
     const long long end = begin + each < all ? begin + each : all;
     if (begin < end) {
-        long long before = 0;
-#pragma unroll 1
-        for (long long b0 = 0; begin >= before * units; b0 += kThreads) {
-            const long long n = places_of(b0 + tid);
-            long long incl = n;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, incl, x);
-                if (lane >= x) incl += o;
-            }
-            __syncthreads();
-            if (lane == 31) scan[warp] = incl;
-            __syncthreads();
-            long long to = before + incl;  // places of one unit up to and with request b0 + tid
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (w < warp) to += scan[w];
-                before += scan[w];
-            }
+        auto look = [&](long long b, unsigned n, long long to) {
             if (n > 0 && begin >= (to - n) * units && begin < to * units) {
-                found[0] = b0 + tid;
+                found[0] = b;
                 found[1] = (to - n) * units;
             }
+        };
+        look(tid, n0, to);
+#pragma unroll 1
+        for (long long b0 = kThreads; begin >= before * units; b0 += kThreads) {
+            const unsigned n = places_of(b0 + tid), incl = warp_scan(n);
+            __syncthreads();
+            if (lane == 31) scan[warp].x = incl;
+            __syncthreads();
+            to = before + incl;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) to += scan[w].x;
+                before += scan[w].x;
+            }
+            look(b0 + tid, n, to);
         }
         __syncthreads();
 
@@ -677,9 +692,9 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
             advance<D, kIdx64>(p, at);
         }
 
-        // `ahead` is the place of the next step to start, `next` the lane's key of it, and `live` says
-        // of each of the `flying` steps in flight which of its keys exist.  The first S - 1 turns
-        // only fill the ring.
+        // `ahead` is the place of the next step to start, `next` the lane's key of it, and `live`
+        // says of each of the `flying` steps in flight which of its keys exist.  The first S - 1
+        // turns only fill the ring.
         Cursor ahead = at;
         int fill = 0, use = 0;  // stages: of the next step to start, of the next to compute
         int flying = 0, turn = 1 - S;
@@ -770,8 +785,8 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
                                   static_cast<int>(partial[slot].begin / each),
                                   static_cast<int>((partial[slot].begin + partial[slot].tiles - 1) /
                                                    each),
-                                  reinterpret_cast<float2 *>(smem), reinterpret_cast<float2 *>(stat), warp,
-                                  lane);
+                                  reinterpret_cast<float2 *>(smem),
+                                  reinterpret_cast<float2 *>(stat), warp, lane);
         }
     }
 
