@@ -202,7 +202,7 @@ ssu_status_t ssu_update_from_host(ssu_handle_t handle, void *state_pool,
  * *skipped receives the number of requests skipped since the last read (may be NULL);
  * *first_bad receives the smallest skipped request index b, or -1 (may be NULL).
  * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_ERR_CUDA when a prompt kernel gave up a wait
- * for its own copies or products (after a second; its results are then not valid), SSU_OK
+ * for its own copies or products (after ten seconds; its results are then not valid), SSU_OK
  * otherwise.
  */
 ssu_status_t ssu_get_error(ssu_handle_t handle, ssu_stream_t stream, uint32_t *skipped,

@@ -61,7 +61,8 @@ cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, b
 // not their prompt's last (those have a first pass), and the workspace.
 struct PromptPlan {
     long long seg, stretches, earlier, columns, ctas;  // ctas: per stretch
-    long long decay, total;  // offset of the stretches' decays, bytes
+    long long decay, hand, turn, total;  // offsets of PromptMmaParams' arrays; bytes
+    bool line;               // the second pass runs along the line
 };
 
 bool mma_sizes(const ssu_shape_t &s) {
@@ -79,7 +80,15 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     // 49.8 of 5, 62.3 of 8; one of 16 chunks, 8 CTAs: 29.2 in stretches of 1, 38.4 of 5).
     const long long chunks = tokens / kChunk + s.batch;
     w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;
-    if (2 * s.batch * w.ctas > sm_count) {
+    // Where the prompts alone are more than the SMs, whole ones take the time of `rounds` of them
+    // and the line (ssu_prompt_mma.cuh) that of their share, and some 4 chunks more for the parts
+    // that it adds.  16 heads, line / whole, us: 24 prompts of 4 chunks 52 / 50 (saves 3.3 chunks),
+    // 60 of 4 98 / 96 (3.8), 24 of 8 74 / 84 (6.3), 20 of 8 64 / 83 (8), 24 of 16 117 / 149 (12);
+    // lengths that differ by factors move these by 10 % either way.
+    const long long units = s.batch * w.ctas, rounds = (units + sm_count - 1) / sm_count;
+    const double mean = 0.5 + static_cast<double>(tokens) / kChunk / s.batch;
+    w.line = rounds > 1 && mean * (rounds - static_cast<double>(units) / sm_count) > 4.5;
+    if (!w.line && 2 * units > sm_count) {
         const long long whole = 2 * (tokens / kChunk) / s.batch;
         if (w.seg < whole) w.seg = whole;
     }
@@ -92,6 +101,11 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     if (w.earlier) {
         w.decay = w.stretches * w.columns * kSlab * s.dstate * 4;
         w.total = w.decay + (w.stretches * w.columns * 4 + 255) / 256 * 256;
+    }
+    if (w.line) {
+        w.hand = w.total;
+        w.turn = w.hand + static_cast<long long>(sm_count) * kPair * kSlab * s.dstate * 4;
+        w.total = w.turn + (4ll * (sm_count + 1) + 255) / 256 * 256;
     }
     return w;
 }
@@ -139,8 +153,9 @@ template <int N, typename ST, bool kIdx64>
 cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUtensorMap (&maps)[4],
                        ssu_handle_s &handle, cudaStream_t st) {
     constexpr int kBytes = PromptSmem<N>::kTotal + 1024;
-    auto *first = ssu_prompt_mma_kernel<N, ST, kIdx64, true>;
-    auto *second = ssu_prompt_mma_kernel<N, ST, kIdx64, false>;
+    auto *first = ssu_prompt_mma_kernel<N, ST, kIdx64, Pass::kFirst>;
+    auto *second = w.line ? ssu_prompt_mma_kernel<N, ST, kIdx64, Pass::kLine>
+                          : ssu_prompt_mma_kernel<N, ST, kIdx64, Pass::kSecond>;
     cudaError_t e =
         ssu_host::allow_smem(handle, reinterpret_cast<const void *>(first), kBytes);
     if (e == cudaSuccess)
@@ -155,12 +170,17 @@ cudaError_t launch_mma(const PromptMmaParams &m, const PromptPlan &w, const CUte
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = handle.pdl ? 1 : 0;
+    if (w.line) {
+        e = cudaMemsetAsync(m.turn, 0, 4 * (handle.sm_count + 1), st);
+        if (e != cudaSuccess) return e;
+    }
     if (w.earlier) {
         cfg.gridDim = dim3(static_cast<unsigned>(w.earlier * w.ctas));
         e = cudaLaunchKernelEx(&cfg, first, m, maps[0], maps[1], maps[2], maps[3]);
         if (e != cudaSuccess) return e;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(w.stretches * w.ctas));
+    cfg.gridDim = dim3(w.line ? static_cast<unsigned>(handle.sm_count)
+                              : static_cast<unsigned>(w.stretches * w.ctas));
     return cudaLaunchKernelEx(&cfg, second, m, maps[0], maps[1], maps[2], maps[3]);
 }
 
@@ -281,9 +301,12 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         m.after_first = w.earlier > 0 && handle->pdl;
         m.slabs = static_cast<int>(s.headdim / kSlab);
         m.local = static_cast<float *>(workspace);
-        m.decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.decay);
+        char *const room = static_cast<char *>(workspace);
+        m.decay = reinterpret_cast<float *>(room + w.decay);
+        m.hand = reinterpret_cast<float *>(room + w.hand);
+        m.turn = reinterpret_cast<unsigned *>(room + w.turn);
         CUtensorMap maps[4];
-        if (w.stretches * w.ctas <= INT_MAX &&
+        if (w.earlier * w.ctas <= INT_MAX &&
             encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b) &&
             encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b) &&
             encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b) &&

@@ -30,15 +30,17 @@
 //
 // Stretches.  A prompt that is long for the device is cut into stretches.  A first pass (kFirst)
 // runs U alone over every stretch but a prompt's last, the first from the prompt's state and the
-// others from zero; the second pass starts a stretch from the results of those before it.
+// others from zero; the second pass starts a stretch from the results of those before it.  Where
+// there are more stretches than SMs, CTAs share their chunks along a line (below).
 //
 // What bounds it: the chain of a chunk's steps.  Of some 8,300 cycles per pair of columns and chunk
-// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 277 us, 2.1 TB/s, 0.2 of
+// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 250 us, 2.3 TB/s, 0.2 of
 // the tensor pipe) M takes 2,000, W 2,000, Y and U 2,600 with the decays and the readout under
 // them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a third.
 // Products that run under M or the readout slow their TMEM loads by more than they hide: M a chunk
 // ahead measured 1.11 of the time, W before M 1.14, sixteen warps 1.04 to 1.12, one column per CTA
-// and two CTAs per SM 1.34.
+// and two CTAs per SM 1.34.  A stretch costs 5 us on top (first loads and decays, the state in and
+// out).
 
 #pragma once
 
@@ -65,6 +67,8 @@ struct PromptMmaParams {
     int seg;              // chunks per stretch
     int slabs;            // headdim / 64
     int after_first;      // a first pass was launched before the second
+    float *hand;          // [CTA of the line][column of the pair][64 p][N]: states handed on
+    unsigned *turn;       // CTAs of the line begun; then per CTA whether its state is handed on
     float *local;         // [stretch][head * slabs + slab][64 p][N]
     float *decay;         // [stretch][head * slabs + slab]: log2 of the stretch's decay
 };
@@ -95,7 +99,10 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes) {
                  : "memory");
 }
 
-// Waits for the barrier's phase of `parity`; gives up (false) after a second.
+// A wait gives up after this many ns: longer than any call's CTA waits for another's state.
+constexpr unsigned long long kGiveUp = 10000000000;
+
+// Waits for the barrier's phase of `parity`; false where it gave up.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
     unsigned long long start = 0;
     while (true) {
@@ -111,7 +118,7 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
         unsigned long long now;
         asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
         if (!start) start = now;
-        if (now - start > 1000000000ull) return false;
+        if (now - start > kGiveUp) return false;
     }
 }
 
@@ -289,6 +296,12 @@ struct PromptSmem {
     static constexpr int kTotal = kBars + 128;
 };
 
+// A copy of v that the compiler takes for another value.
+__device__ __forceinline__ unsigned opaque(unsigned v) {
+    asm volatile("" : "+r"(v));
+    return v;
+}
+
 // Where a CTA works.
 struct Stretch {
     long long b;       // prompt; -1: past the last stretch
@@ -343,6 +356,147 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
                    static_cast<int>(scan[kWarps + 2])};
 }
 
+// The passes: over every stretch but a prompt's last, for the states alone; over every stretch,
+// one or (along the line) several parts of them per CTA.
+enum class Pass { kFirst, kSecond, kLine };
+
+// What a CTA is working on: chunks c0 .. c1 - 1 of a stretch (c1 < 0: to its end), for the `cta`-th
+// pair of columns.
+struct Part {
+    long long b, g;    // as in Stretch
+    int index, count;
+    int cta, c0, c1;
+    int more;          // 0: no part
+    int turn;          // the CTA's place among those of the line
+    // where the part's stretch begins in the line, and the CTA's share of the line
+    long long at, begin, end;
+    int chunks;        // of the stretch
+};
+
+// Chunks and stretches of prompt b (of chunks `per`), packed as chunks << 32 | stretches.
+template <bool kIdx64>
+__device__ __forceinline__ unsigned long long prompt_extent(const PromptMmaParams &m, long long b,
+                                                            bool counts) {
+    long long slot, lo, hi;
+    if (b >= m.q.p.batch || !load_prompt<kIdx64>(m.q, b, counts, slot, lo, hi)) return 0;
+    const unsigned chunks = static_cast<unsigned>((hi - lo + kChunk - 1) / kChunk);
+    unsigned n = (chunks + m.seg - 1) / m.seg;
+    if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
+    return static_cast<unsigned long long>(chunks) << 32 | n;
+}
+
+__device__ __forceinline__ int stretch_chunks(const PromptMmaParams &m, unsigned long long extent,
+                                              int index) {
+    const int n = static_cast<int>(extent), chunks = static_cast<int>(extent >> 32);
+    return index == n - 1 ? chunks - index * m.seg : m.seg;
+}
+
+// The line: every stretch `ctas` times (once per pair of columns), two places per chunk and one
+// for what a part costs before its first chunk and after its last; cut evenly, wherever that
+// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 250 us, whole
+// stretches in two rounds 277).  A CTA goes through its share backwards: a stretch cut by its end
+// first, whose state goes to the next CTA, and the one that the CTA before began last, when that one
+// has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those alone
+// that run already.
+__device__ __forceinline__ void set_chunks(Part &w) {
+    w.c0 = w.begin > w.at ? static_cast<int>((w.begin - w.at + 1) / 2) : 0;
+    w.c1 = static_cast<int>(min((w.end - w.at + 1) / 2, 1ll << 30));
+    if (w.c1 >= w.chunks) w.c1 = -1;
+}
+
+// The part before, in the line, that has something to do (one thread).
+template <bool kIdx64>
+__device__ __forceinline__ void step_back(const PromptMmaParams &m, Part &w, int ctas) {
+    do {
+        w.more = w.at > w.begin;
+        if (!w.more) return;
+        if (--w.cta < 0) {
+            w.cta = ctas - 1;
+            --w.g;
+            unsigned long long extent;
+            if (--w.index < 0) {
+                do
+                    extent = prompt_extent<kIdx64>(m, --w.b, false);
+                while (static_cast<unsigned>(extent) == 0);
+                w.count = static_cast<int>(extent);
+                w.index = w.count - 1;
+            } else {
+                extent = prompt_extent<kIdx64>(m, w.b, false);
+            }
+            w.chunks = stretch_chunks(m, extent, w.index);
+        }
+        w.at -= 2 * w.chunks + 1;
+        set_chunks(w);
+    } while (w.chunks && (w.c1 < 0 ? w.chunks : w.c1) <= w.c0);
+}
+
+// The last part of the CTA's share; all threads call it.
+template <bool kIdx64>
+__device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Part &w,
+                                          long long *scan) {
+    constexpr int kWarps = kPromptThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto places = [&](unsigned long long v) {
+        return (2 * static_cast<long long>(v >> 32) + static_cast<unsigned>(v)) * ctas;
+    };
+    if (tid == 0) {
+        w.more = 0;
+        w.turn = static_cast<int>(atomicAdd(m.turn, 1u));
+    }
+    unsigned long long all = 0;
+#pragma unroll 1
+    for (long long b = tid; b < m.q.p.batch; b += kPromptThreads)
+        all += prompt_extent<kIdx64>(m, b, blockIdx.x == 0);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+    if (lane == 0) scan[warp] = static_cast<long long>(all);
+    __syncthreads();
+    all = 0;
+#pragma unroll 1
+    for (int k = 0; k < kWarps; ++k) all += static_cast<unsigned long long>(scan[k]);
+    const long long total = places(all);
+    // at least two places, so that every share has some chunk's first
+    const long long each = max((total + gridDim.x - 1) / gridDim.x, 2ll);
+    const long long begin = w.turn * each, end = min(begin + each, total);
+    if (begin >= end) return;
+    unsigned long long before = 0;
+#pragma unroll 1
+    for (long long b0 = 0; end > places(before); b0 += kPromptThreads) {
+        const unsigned long long mine = prompt_extent<kIdx64>(m, b0 + tid, false);
+        unsigned long long incl = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = static_cast<long long>(incl);
+        __syncthreads();
+        unsigned long long start = before + incl - mine;
+#pragma unroll 1
+        for (int k = 0; k < kWarps; ++k) {
+            if (k < warp) start += static_cast<unsigned long long>(scan[k]);
+            before += static_cast<unsigned long long>(scan[k]);
+        }
+        if (end > places(start) && end <= places(start + mine)) {
+            const long long stretch = (2ll * m.seg + 1) * ctas;  // places of a whole one
+            long long o = end - 1 - places(start);
+            w.b = b0 + tid;
+            w.count = static_cast<int>(mine);
+            w.index = static_cast<int>(min(o / stretch, w.count - 1ll));
+            w.g = static_cast<unsigned>(start) + w.index;
+            w.chunks = stretch_chunks(m, mine, w.index);
+            o -= w.index * stretch;
+            w.cta = static_cast<int>(o / (2 * w.chunks + 1));
+            w.at = end - 1 - (o - static_cast<long long>(w.cta) * (2 * w.chunks + 1));
+            w.begin = begin, w.end = end;
+            w.more = 1;
+            set_chunks(w);
+            if (w.chunks && (w.c1 < 0 ? w.chunks : w.c1) <= w.c0) step_back<kIdx64>(m, w, ctas);
+        }
+    }
+}
+
 // Decay sums of one chunk, by the four warps of one warpgroup (one token per thread, `row`): the
 // token's weight up to the end of its 32 tokens, its prefix within them, dtv, the blocks' totals.
 __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, float bias, float A2,
@@ -367,6 +521,52 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
     if (lane == 31) vec[3 * kChunk + row / 32] = up;
 }
 
+// Waits until the CTA whose flag it is has handed its state on; false where it gave up.
+__device__ __forceinline__ bool handed_on(const unsigned *flag, int lane) {
+    bool done = true;
+    if (lane == 0) {
+        unsigned long long start, now;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(start));
+        while (true) {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+            if (v) break;
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+            done = now - start < kGiveUp;
+            if (!done) break;
+            __nanosleep(200);
+        }
+    }
+    return __shfl_sync(0xffffffffu, done, 0);
+}
+
+// The CTA's place in the call, of which threads hold as little as they can: a group's columns (one
+// is 64 rows of a head: column c is head c / slabs, slab c % slabs) go to CTAs in pairs, an odd last
+// one alone (its CTA works on it twice and keeps one result).
+__device__ __forceinline__ int columns_per_group(const PromptMmaParams &m) {
+    return static_cast<int>(opaque(m.q.p.heads_per_group)) * m.slabs;
+}
+
+__device__ __forceinline__ int ctas_per_stretch(const PromptMmaParams &m) {
+    return m.q.p.nheads / m.q.p.heads_per_group * ((columns_per_group(m) + 1) / 2);
+}
+
+__device__ __forceinline__ unsigned tiles_at(const unsigned char *raw) {
+    return (opaque(smem_u32(raw)) + 1023u) & ~1023u;
+}
+
+constexpr int kIssuer = kCompute / 32;  // the issuing warp; the next one stores
+constexpr int kBars = 12;
+
+__device__ __forceinline__ void init_barriers(unsigned bars) {
+    for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
+    for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute / 32);
+    mbar_init(bars + 88, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// One part, by all threads; false in those whose wait gave up.
+//
 // Roles.  One thread starts the loads and the products as their inputs become ready, another the
 // stores.  Eight warps do the elementwise work, four per column, a thread per row (token of the
 // chunk, TMEM lane, column n of the state).  Per chunk, with the barrier that each hand-over uses:
@@ -380,48 +580,19 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
 // so Y runs under W, U under the decays and the readout, I and the loads under M.  (Readouts
 // stored by the threads themselves kept the shared-memory pipe busy for thousands of cycles per
 // chunk: 32 lines per instruction.)
-template <int N, typename ST, bool kIdx64, bool kFirst>
-__global__ void __launch_bounds__(kPromptThreads, 1)
-    ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
-                          const __grid_constant__ CUtensorMap map_x,
-                          const __grid_constant__ CUtensorMap map_b,
-                          const __grid_constant__ CUtensorMap map_c,
-                          const __grid_constant__ CUtensorMap map_out) {
+template <int N, typename ST, bool kIdx64, Pass kPass>
+__device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtensorMap &map_x,
+                                         const CUtensorMap &map_b, const CUtensorMap &map_c,
+                                         const CUtensorMap &map_out, const Part &part, Part &next,
+                                         unsigned char *raw, unsigned tmem) {
+    constexpr bool kFirst = kPass == Pass::kFirst, line = kPass == Pass::kLine;
     using Smem = PromptSmem<N>;
     constexpr int kBlocks = Smem::kBlocks;
     constexpr int kParts = sizeof(ST) == 4 ? 3 : 2;  // bf16 parts of W
-    extern __shared__ unsigned char raw[];
-    __shared__ long long scan[kPromptThreads / 32 + 3];
-    __shared__ unsigned tmem_slot;
-    // A second pass behind a first is let in when the first has begun, so what came before the first
-    // is complete; it waits for the first before it reads its results, and before it ends.
-    if (kFirst || !m.after_first) pdl_wait();
-    if (kFirst) pdl_trigger();
     const SsuParams &p = m.q.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // Column c is head c / slabs, slab c % slabs; a group's columns go to CTAs in pairs, an odd
-    // last one alone (its CTA then works on it twice and keeps one result).
-    const int per_group = p.heads_per_group * m.slabs, pairs = (per_group + 1) / 2;
-    const int ctas = p.nheads / p.heads_per_group * pairs;  // per stretch
-    const long long nth = blockIdx.x / ctas;
-    const int cta = static_cast<int>(blockIdx.x - nth * ctas), grp = cta / pairs;
-    const int first_column = grp * per_group + 2 * (cta - grp * pairs);
-    const bool paired = 2 * (cta - grp * pairs) + 1 < per_group;
-    const int columns = p.nheads * m.slabs;
-    const Stretch my =
-        find_stretch<kIdx64, kFirst>(m, nth, !kFirst && blockIdx.x == 0, scan);
-    if (my.b < 0) {
-        if (!kFirst && m.after_first) pdl_wait();
-        return;
-    }
-    const long long b = my.b, g = my.g;
-    long long slot, begin, end;
-    load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
-    const int from = static_cast<int>(begin) + my.index * m.seg * kChunk;  // tokens fit 31 bits
-    const bool last = my.index == my.count - 1;
-    const int to = last ? static_cast<int>(end) : from + m.seg * kChunk;
-
-    const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
+    bool alive = true;
+    const int tid = opaque(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const unsigned base = tiles_at(raw);
     const unsigned sC = base + Smem::kC, sB = base + Smem::kB, sX = base + Smem::kX;
     const unsigned sW1 = base + Smem::kW1, sW2 = base + Smem::kW2;
     const unsigned sS = sW2;
@@ -429,26 +600,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const unsigned bar_b = bars, bar_c = bars + 8, bar_x = bars + 16, bar_g = bars + 24,
                    bar_i = bars + 32, bar_u = bars + 40, bar_y = bars + 48, bar_w = bars + 56,
                    bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80, bar_3 = bars + 88;
-    if (tid == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
-        for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute / 32);
-        mbar_init(bar_3, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    constexpr int kIssuer = kCompute / 32;  // the issuing warp
-    if (warp == kIssuer) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&tmem_slot)),
-                     "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     // TMEM columns: G (both columns'), M, I and then Y, U (each one after the other)
-    const unsigned tG = tmem_slot, tM = tG + 128, tY = tG + 256, tU = tG + 384;
-    bool alive = true;
+    const unsigned tG = opaque(tmem), tM = tG + 128, tY = tG + 256, tU = tG + 384;
+    const int per_group = columns_per_group(m), pairs = (per_group + 1) / 2;
+    const int columns = p.nheads * m.slabs;
+    const int grp = part.cta / pairs;
+    const int first_column = grp * per_group + 2 * (part.cta - grp * pairs);
+    const bool paired = 2 * (part.cta - grp * pairs) + 1 < per_group;
+    const long long b = part.b, g = part.g;
+    long long slot, begin, end;
+    load_prompt<kIdx64>(m.q, b, false, slot, begin, end);
+    // tokens fit 31 bits
+    const int start = static_cast<int>(begin) + part.index * m.seg * kChunk;
+    const int from = start + part.c0 * kChunk;
+    const bool last = part.index == part.count - 1 && part.c1 < 0;
+    const int to = part.c1 >= 0 ? start + part.c1 * kChunk
+                   : last       ? static_cast<int>(end)
+                                : start + m.seg * kChunk;
 
     constexpr int kBBytes = kBlocks * kTileBytes;  // one place of B
     auto load_x = [&](int tok) {
@@ -499,6 +667,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     alive = mbar_wait(bar_b, 0);
                     if (alive) alive = mbar_wait(bar_c, 0);
                     product_g(0);
+                }
+            }
+            if constexpr (line) {  // the part to come, whose first tiles are then in L2
+                next = part;
+                step_back<kIdx64>(m, next, ctas_per_stretch(m));
+                if (next.more) {
+                    long long slot_, first, end_;
+                    load_prompt<kIdx64>(m.q, next.b, false, slot_, first, end_);
+                    const int at = static_cast<int>(first) +
+                                   (next.index * m.seg + next.c0) * kChunk;
+                    const int group = next.cta / pairs;
+                    const int c = group * per_group + 2 * (next.cta - group * pairs);
+                    for (int k = 0; k < kBlocks && at < end_; ++k) {
+                        tma_prefetch(&map_b, k * 64, group, at);
+                        tma_prefetch(&map_c, k * 64, group, at);
+                    }
+                    for (int k = 0; k < kPair && at < end_; ++k)
+                        tma_prefetch(&map_x, min(c + k, columns - 1) % m.slabs * kSlab,
+                                     min(c + k, columns - 1) / m.slabs, at);
                 }
             }
             unsigned phase = 0;
@@ -597,22 +784,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 if (tok + kChunk < to) load_x(tok + kChunk);
             }
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!line) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
         __syncwarp();
     } else {
         const int which = warp >> 2, quarter = warp & 3;
         const int row = 32 * quarter + lane;
         // The thread's place in the call, worked out again where it is needed rather than held in
-        // registers through the loop (the opaque copy keeps the compiler from holding it).
+        // registers through the loop.
         struct Place {
             int column, h, slab;
             bool keeps;  // whether the thread's results are kept
         };
         auto place = [&]() {
-            unsigned block = blockIdx.x;
-            asm volatile("" : "+r"(block));
-            const int c = static_cast<int>(block % ctas), of_group = 2 * (c % pairs);
+            const int c = opaque(part.cta), per_group = columns_per_group(m);
+            const int pairs = (per_group + 1) / 2, of_group = 2 * (c % pairs);
             const bool paired = of_group + 1 < per_group;
             Place at;
             at.column = c / pairs * per_group + of_group + (paired ? which : 0);
@@ -666,22 +852,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         auto kept = [&](long long k) {
             return m.local + (k * columns + here.column) * (kSlab * N) + row;
         };
-        const long long g0 = g - my.index;  // the prompt's first stretch
-        if (!kFirst && my.count > 1 && m.after_first) pdl_wait();
-        if (own && my.index == 0) {
-            if (!kFirst && my.count > 1) {
+        const int index = part.index, count = part.count;
+        const long long g0 = g - index;  // the prompt's first stretch
+        if (!kFirst && count > 1 && m.after_first) pdl_wait();
+        if (line && part.c0 > 0) {
+            if (alive) alive = handed_on(m.turn + part.turn, lane);
+            if (own) {
+                const float *const hand =
+                    m.hand + ((part.turn - 1ll) * kPair + which) * (kSlab * N) + row;
 #pragma unroll
-                for (int i = 0; i < kSlab; ++i) S[i] = __ldcg(kept(g0 + my.count - 1) + i * N);
+                for (int i = 0; i < kSlab; ++i) S[i] = __ldcg(hand + i * N);
+            }
+        } else if (own && index == 0) {
+            if (!kFirst && count > 1) {
+#pragma unroll
+                for (int i = 0; i < kSlab; ++i) S[i] = __ldcg(kept(g0 + count - 1) + i * N);
             } else if (!(m.q.fresh && m.q.fresh[b] != 0)) {
 #pragma unroll
                 for (int i = 0; i < kSlab; ++i) S[i] = static_cast<float>(*state_at(here, i));
             }
             if (kFirst && here.keeps) {
 #pragma unroll
-                for (int i = 0; i < kSlab; ++i) __stcg(kept(g0 + my.count - 1) + i * N, S[i]);
+                for (int i = 0; i < kSlab; ++i) __stcg(kept(g0 + count - 1) + i * N, S[i]);
             }
         }
-        if (!kFirst && own) {
+        if (!kFirst && own && part.c0 == 0) {
             for (long long k = g0; k < g; ++k) {
                 const float f = k == g0 ? 0.0f : exp2f(__ldcg(m.decay + k * columns + here.column));
 #pragma unroll
@@ -941,7 +1136,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (int i = 0; i < kSlab; ++i) __stcg(loc + i * N, S[i]);
                 if (row == 0) __stcg(m.decay + g * columns + at.column, stretch_decay);
             } else if (last) {
-                slot = load_slot<kIdx64>(p, scan[kPromptThreads / 32]);
+                slot = load_slot<kIdx64>(p, part.b);
 #pragma unroll
                 for (int i = 0; i < kSlab; ++i) {
                     if constexpr (sizeof(ST) == 4)
@@ -951,17 +1146,101 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
         }
+        if (line && part.c1 >= 0) {
+            if (own) {
+                float *const hand =
+                    m.hand + (part.turn * static_cast<long long>(kPair) + which) * (kSlab * N) + row;
+#pragma unroll
+                for (int i = 0; i < kSlab; ++i) __stcg(hand + i * N, S[i]);
+            }
+            __threadfence();
+            asm volatile("bar.sync %0, %1;" ::"n"(1 + kPair), "n"(kCompute) : "memory");
+            if (tid == 0) {
+                __threadfence();
+                atomicExch(m.turn + 1 + part.turn, 1u);
+            }
+        }
     }
+    return alive;
+}
+
+template <int N, typename ST, bool kIdx64, Pass kPass>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    ssu_prompt_mma_kernel(const __grid_constant__ PromptMmaParams m,
+                          const __grid_constant__ CUtensorMap map_x,
+                          const __grid_constant__ CUtensorMap map_b,
+                          const __grid_constant__ CUtensorMap map_c,
+                          const __grid_constant__ CUtensorMap map_out) {
+    constexpr bool kFirst = kPass == Pass::kFirst;
+    extern __shared__ unsigned char raw[];
+    __shared__ long long scan[kPromptThreads / 32 + 3];
+    __shared__ Part part, next;
+    __shared__ unsigned tmem_slot;
+    // A second pass behind a first is let in when the first has begun, so what came before the
+    // first is complete; it waits for the first before it reads its results, and before it ends.
+    if (kFirst || !m.after_first) pdl_wait();
+    if (kFirst) pdl_trigger();
+    const int tid = threadIdx.x;
+    const int ctas = ctas_per_stretch(m);
+    if constexpr (kPass == Pass::kLine) {
+        find_line<kIdx64>(m, ctas, part, scan);
+    } else {
+        const long long nth = blockIdx.x / ctas;
+        const Stretch my =
+            find_stretch<kIdx64, kFirst>(m, nth, !kFirst && blockIdx.x == 0, scan);
+        if (tid == 0) {
+            part.b = my.b, part.g = my.g, part.index = my.index, part.count = my.count;
+            part.cta = static_cast<int>(blockIdx.x - nth * ctas);
+            part.c0 = 0, part.c1 = -1;
+            part.more = my.b >= 0;
+        }
+    }
+    __syncthreads();
+    if (!part.more) {
+        if (!kFirst && m.after_first) pdl_wait();
+        return;
+    }
+    const unsigned bars = tiles_at(raw) + PromptSmem<N>::kBars;
+    if (tid == 0) init_barriers(bars);
+    if (tid / 32 == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    bool alive;
+    while (true) {
+        alive = run_part<N, ST, kIdx64, kPass>(m, map_x, map_b, map_c, map_out, part, next, raw,
+                                               tmem_slot);
+        tc_fence_before();
+        if (__syncthreads_or(!alive) || kPass != Pass::kLine) break;
+        if (tid == 0) {  // fresh barriers for the part before
+            for (int i = 0; i < kBars; ++i)
+                asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bars + 8 * i)
+                             : "memory");
+            init_barriers(bars);
+            part = next;
+        }
+        __syncthreads();
+        tc_fence_after();
+        if (!part.more) break;
+    }
+    if (kPass == Pass::kLine && tid == 32 * (kIssuer + 1))
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!alive) {  // what is in flight lands long before this is over
-        atomicOr(&p.err[2], 1u);
+        atomicOr(&m.q.p.err[2], 1u);
         __nanosleep(1000000);
     }
     if (!kFirst && m.after_first) pdl_wait();
-    tc_fence_before();
     __syncthreads();
-    if (warp == kIssuer) {
+    if (tid / 32 == kIssuer) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tG), "r"(512)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot),
+                     "r"(512)
                      : "memory");
     }
 }

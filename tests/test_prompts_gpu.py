@@ -380,6 +380,27 @@ def test_on_a_side_stream_and_in_a_graph(op):
     check(d, out.cpu(), g["pool"].cpu(), ref)
 
 
+@pytest.mark.parametrize("H,P,N,state,idx", [(8, 64, 128, torch.float32, torch.int32),
+                                             (4, 128, 64, torch.bfloat16, torch.int64)])
+def test_more_prompts_than_the_device_holds(op, H, P, N, state, idx):
+    """Enough prompts (four pairs of columns each) that CTAs share the chunks of all of them and
+    hand states on in the middle of a prompt; among them empty ones, one bad, one long."""
+    lens = [500 + (97 * i) % 301 for i in range(39)]
+    lens[5] = lens[6] = lens[38] = 0
+    lens[7], lens[20], lens[21] = 1, 3100, 128
+    d = make(lens, H=H, P=P, N=N, state=state, idx=idx, seed=29)
+    d["fresh"][5], d["fresh"][6] = True, False
+    d["slots"][11] = len(lens) + 50
+    ref = reference(d, skip=(11,))
+    out, pool = call(op, d)
+    assert op.get_error() == (1, 11)
+    check(d, out, pool, ref)
+    again = call(op, d)
+    assert op.get_error() == (1, 11)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16))
+    assert torch.equal(pool.view(torch.int16), again[1].view(torch.int16))
+
+
 @pytest.mark.parametrize("N", [64, 128])
 @pytest.mark.parametrize("slow", [False, True])
 def test_an_fp32_state_is_carried_in_fp32(op, N, slow):
