@@ -21,8 +21,8 @@
 //
 // Inside a CTA every warp takes its 16 or 32 of a tile's keys into its own ring of stages with
 // cp.async (rows 16 bytes apart in banks, so ldmatrix has no conflicts), ahead of their use across
-// unit borders, and keeps its own m, l, o: no barrier until a unit ends.  (A bulk copy per row and lane instead
-// was 20 % slower: its operands are a warp's, so 32 rows are 32 turns.)
+// unit borders, and keeps its own m, l, o: no barrier until a unit ends.  (A bulk copy per row and
+// lane instead was 20 % slower: its operands are a warp's, so 32 rows are 32 turns.)
 
 #pragma once
 
@@ -425,7 +425,8 @@ __device__ __forceinline__ void merge_warps(Sums<D> &s, float *merge, float *sta
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
                 float2 &at = buf[(warp * (D / 8) + n) * 32 + lane];
-                at = make_float2(fmaf(s.o[n][2 * h], own, at.x), fmaf(s.o[n][2 * h + 1], own, at.y));
+                at = make_float2(fmaf(s.o[n][2 * h], own, at.x),
+                                 fmaf(s.o[n][2 * h + 1], own, at.y));
             }
         }
         __syncthreads();
@@ -539,8 +540,8 @@ __device__ __forceinline__ void join_parts(const AttendParams &p, const Partial 
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         {
-            // 2 W threads per row: its largest m, then weights exp2(m - m*) in m's place; the sum of
-            // l and m* itself go where the first part's l was
+            // 2 W threads per row: its largest m, then weights exp2(m - m*) in m's place; m* and
+            // the sum of l go to `stat`
             const int row = tid / (2 * W), j = tid % (2 * W);
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
@@ -643,8 +644,9 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
     }
     if (lane == 31) scan[warp] = longlong2{incl0, rest};
     const bool any_empty = __syncthreads_or(empty);
-    long long to = incl0, before = 0, total = 0;  // places up to and with request tid; of the first
-#pragma unroll                                    // kThreads; of all
+    // places up to and with request tid; of the first kThreads; of all
+    long long to = incl0, before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < W; ++w) {
         const longlong2 v = scan[w];
         if (w < warp) to += v.x;

@@ -36,7 +36,8 @@
 // What bounds it: the chain of a chunk's steps.  Of some 8,300 cycles per pair of columns and chunk
 // (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 250 us, 2.3 TB/s, 0.2 of
 // the tensor pipe) M takes 2,000, W 2,000, Y and U 2,600 with the decays and the readout under
-// them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a third.
+// them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a
+// third.
 // Products that run under M or the readout slow their TMEM loads by more than they hide: M a chunk
 // ahead measured 1.11 of the time, W before M 1.14, sixteen warps 1.04 to 1.12, one column per CTA
 // and two CTAs per SM 1.34.  A stretch costs 5 us on top (first loads and decays, the state in and
@@ -310,7 +311,8 @@ struct Stretch {
 };
 
 // The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's
-// last; all threads get the answer.  With `all`, every prompt is looked at and the bad ones counted.
+// last; all threads get the answer.  With `all`, every prompt is looked at and the bad ones
+// counted.
 template <bool kIdx64, bool kFirst>
 __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long long at, bool all,
                                                 long long *scan) {
@@ -395,9 +397,9 @@ __device__ __forceinline__ int stretch_chunks(const PromptMmaParams &m, unsigned
 // for what a part costs before its first chunk and after its last; cut evenly, wherever that
 // falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 250 us, whole
 // stretches in two rounds 277).  A CTA goes through its share backwards: a stretch cut by its end
-// first, whose state goes to the next CTA, and the one that the CTA before began last, when that one
-// has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those alone
-// that run already.
+// first, whose state goes to the next CTA, and the one that the CTA before began last, when that
+// one has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those
+// alone that run already.
 __device__ __forceinline__ void set_chunks(Part &w) {
     w.c0 = w.begin > w.at ? static_cast<int>((w.begin - w.at + 1) / 2) : 0;
     w.c1 = static_cast<int>(min((w.end - w.at + 1) / 2, 1ll << 30));
@@ -541,8 +543,8 @@ __device__ __forceinline__ bool handed_on(const unsigned *flag, int lane) {
 }
 
 // The CTA's place in the call, of which threads hold as little as they can: a group's columns (one
-// is 64 rows of a head: column c is head c / slabs, slab c % slabs) go to CTAs in pairs, an odd last
-// one alone (its CTA works on it twice and keeps one result).
+// is 64 rows of a head: column c is head c / slabs, slab c % slabs) go to CTAs in pairs, an odd
+// last one alone (its CTA works on it twice and keeps one result).
 __device__ __forceinline__ int columns_per_group(const PromptMmaParams &m) {
     return static_cast<int>(opaque(m.q.p.heads_per_group)) * m.slabs;
 }
@@ -633,7 +635,8 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
                 mbar_expect(bar_b, kBBytes);
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k)
-                    tma_load(sB + place * kBBytes + k * kTileBytes, &map_b, bar_b, k * 64, grp, tok);
+                    tma_load(sB + place * kBBytes + k * kTileBytes, &map_b, bar_b, k * 64, grp,
+                             tok);
             };
             auto load_c = [&](int tok, int k) {
                 if (k == 0) mbar_expect(bar_c, kBBytes);
@@ -846,7 +849,7 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
 #pragma unroll
         for (int i = 0; i < kSlab; ++i) S[i] = 0.0f;
         // A prompt's state before a stretch: its slot's (or zeros) before the first, which a first
-        // pass also puts by where the last stretch would have its result, as the last stretch of the
+        // pass also puts by where the last stretch would have its result, as the last one of the
         // second pass overwrites the slot while the first may not have begun; what the first pass
         // leaves of the stretches before any other.
         auto kept = [&](long long k) {
@@ -881,7 +884,8 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
                 const float f = k == g0 ? 0.0f : exp2f(__ldcg(m.decay + k * columns + here.column));
 #pragma unroll
                 for (int i = 0; i < kSlab; ++i)
-                    S[i] = k == g0 ? __ldcg(kept(k) + i * N) : fmaf(S[i], f, __ldcg(kept(k) + i * N));
+                    S[i] = k == g0 ? __ldcg(kept(k) + i * N)
+                                   : fmaf(S[i], f, __ldcg(kept(k) + i * N));
             }
         }
         auto publish = [&]() {  // the state as the next chunk's bf16 operand
@@ -1036,12 +1040,14 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
                     unsigned bits[kParts][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float2 f = __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
+                        float2 f =
+                            __fmul2_rn(make_float2(w, w), make_float2(x[2 * i], x[2 * i + 1]));
 #pragma unroll
                         for (int k = 0; k < kParts; ++k) {
                             bits[k][i] = f2_to_bf2(f.x, f.y);
-                            f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k][i] << 16),
-                                                          -__uint_as_float(bits[k][i] & 0xffff0000u)));
+                            f = __fadd2_rn(
+                                f, make_float2(-__uint_as_float(bits[k][i] << 16),
+                                               -__uint_as_float(bits[k][i] & 0xffff0000u)));
                         }
                     }
 #pragma unroll
@@ -1149,7 +1155,7 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
         if (line && part.c1 >= 0) {
             if (own) {
                 float *const hand =
-                    m.hand + (part.turn * static_cast<long long>(kPair) + which) * (kSlab * N) + row;
+                    m.hand + (part.turn * 1ll * kPair + which) * (kSlab * N) + row;
 #pragma unroll
                 for (int i = 0; i < kSlab; ++i) __stcg(hand + i * N, S[i]);
             }

@@ -100,7 +100,8 @@ __device__ __forceinline__ void load_turn(Turn &a, const float *weight, const fl
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             a.own[i] = make_float2(w[2 * i] * c[2 * i], w[2 * i + 1] * c[2 * i + 1]);
-            a.other[i] = make_float2(sign * p[2 * i] * s[2 * i], sign * p[2 * i + 1] * s[2 * i + 1]);
+            a.other[i] =
+                make_float2(sign * p[2 * i] * s[2 * i], sign * p[2 * i + 1] * s[2 * i + 1]);
         }
     }
 }
@@ -142,7 +143,8 @@ constexpr int kRotateWarps = 4, kRotateUnroll = 4;
 // A warp takes kRotateUnroll * 32 / LPH neighbouring heads of one token (queries, then keys, then
 // values): all their loads go out together, and the table row is read once for them.
 template <int LPH, bool kInterleaved, bool kIdx64>
-__global__ void __launch_bounds__(32 * kRotateWarps, 32 / kRotateWarps) ssu_rotate_kernel(RotateParams p) {
+__global__ void __launch_bounds__(32 * kRotateWarps, 32 / kRotateWarps)
+    ssu_rotate_kernel(RotateParams p) {
     pdl_wait();
     pdl_trigger();
     constexpr int HPW = 32 / LPH, U = kRotateUnroll;  // heads per warp instruction
@@ -297,7 +299,8 @@ extern "C" ssu_status_t ssu_rotate_qk(ssu_handle_t handle, const uint16_t *q, co
     }
     if (u.table < 0 || u.positions < 0 || u.slots < 0)
         return fail(SSU_ERR_INVALID_ARG, "negative stride");
-    if (s.rotary && u.table % 4) return fail(SSU_ERR_MISALIGNED, "the table stride is not a multiple of 4");
+    if (s.rotary && u.table % 4)
+        return fail(SSU_ERR_MISALIGNED, "the table stride is not a multiple of 4");
     if (!q || !k || !v || !q_weight || !k_weight || !positions || !q_out || !slots ||
         (s.rotary && s.num_positions && !table) || (s.num_pages && (!k_pages || !v_pages)))
         return fail(SSU_ERR_INVALID_ARG, "a data pointer is NULL");
