@@ -16,7 +16,7 @@ Strided views are accepted as they are; nothing is copied.
 from __future__ import annotations
 
 import ctypes
-import struct
+import importlib
 from pathlib import Path
 
 import torch
@@ -474,110 +474,43 @@ def ssu_update_tokens(handle: int, state_pool, state_batch_indices, x, dt, dt_bi
 
 # ---- prompts and attention ---------------------------------------------------------------
 #
-# These calls sit in a serving loop beside the decode step and are often shorter on the device
-# than their marshalling, so it is written out: one look at every tensor, the ABI's structs packed
-# as bytes (a struct of N words costs 0.3 us this way, 1.6 us as a ctypes array), and messages only
-# where a check has failed.
+# These calls are often shorter on the device than their marshalling from Python would be, so
+# _marshal.so (csrc/ssu_marshal.cpp) looks at the tensors, checks them and calls the C entry points.
 
-_BF16, _F32 = torch.bfloat16, torch.float32
-_INDEX_TYPE = {torch.int32: SSU_INDEX_I32, torch.int64: SSU_INDEX_I64}
-_STATE_TYPE = {_F32: SSU_STATE_F32, _BF16: SSU_STATE_BF16}
-_SHAPE = struct.Struct("6q2i")            # ssu_shape_t
-_STRIDES = struct.Struct("27q")           # ssu_strides_t
-_ROTATE_SHAPE = struct.Struct("8q2i")     # ssu_rotate_shape_t
-_ROTATE_STRIDES = struct.Struct("17q")    # ssu_rotate_strides_t
-_ATTEND_SHAPE = struct.Struct("7q2i")     # ssu_attend_shape_t
-_ATTEND_STRIDES = struct.Struct("13q")    # ssu_attend_strides_t
+_STATE_TYPE = {torch.float32: SSU_STATE_F32, torch.bfloat16: SSU_STATE_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else \
     lambda device: torch.cuda.current_stream(device).cuda_stream
+_bound = None
 
 
-def _refuse_types(**wanted) -> None:
-    """Raises for the first tensor that is not of its wanted (dtype, dims)."""
-    for name, (t, dtypes, dims) in wanted.items():
-        if t.dtype not in dtypes or t.dim() not in dims:
-            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))} with "
-                            f"{' or '.join(map(str, dims))} dims, got {t.dtype} with {t.dim()}")
-    raise TypeError("operand types do not fit together")
+def _calls():
+    """The marshalling module, bound to the library's entry points.  Raises if it has not been
+    built."""
+    global _bound
+    if _bound is None:
+        module = importlib.import_module(f"{__name__}._marshal")
+        module.bind(*(ctypes.cast(getattr(lib(), name), _vp).value
+                      for name in ("ssu_update_prompts", "ssu_rotate_qk", "ssu_attend")))
+        _bound = module
+    return _bound
 
 
-def _device_of(tensors) -> int:
-    """The CUDA device on which every tensor lies."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError("every operand must be a CUDA tensor of one device, got "
-                             + ", ".join(sorted({str(u.device) for u in tensors})))
-    return dev
-
-
-def _workspace(workspace, dev: int) -> tuple[int | None, int]:
-    if workspace is None:
-        return None, 0
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor of the operands' device")
-    return workspace.data_ptr(), workspace.nbytes
-
-
-def _stream_on(dev: int, stream) -> int:
+def _stream_on(t, stream) -> int:
     if stream is None:
-        return _raw_stream(dev)
+        device = t.get_device()
+        return _raw_stream(device) if device >= 0 else 0
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _head_strides(t, name: str, dims: tuple[int, ...]) -> tuple[int, ...]:
-    """Strides of a per-head operand in its expanded form (missing dimensions: 0)."""
-    if t.shape != dims[:t.dim()]:
-        raise ValueError(f"{name} must have the shape {dims} or {dims[:1]}, got {tuple(t.shape)}")
-    st = t.stride()
-    return st if len(st) == len(dims) else (*st, *(0,) * (len(dims) - len(st)))
-
-
-def describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D,
-                     out) -> tuple[bytes, bytes]:
-    """The ``ssu_shape_t`` and ``ssu_strides_t`` of a prompt call, as bytes (no data is touched)."""
-    kind, state = _INDEX_TYPE.get(cu_tokens.dtype), _STATE_TYPE.get(state_pool.dtype)
-    sp, sx, so, sd = state_pool.stride(), x.stride(), out.stride(), dt.stride()
-    sb, sc, si = B.stride(), C.stride(), state_batch_indices.stride()
-    if not (x.dtype is dt.dtype is B.dtype is C.dtype is out.dtype is _BF16
-            and dt_bias.dtype is A.dtype is D.dtype is _F32 and kind is not None
-            and state_batch_indices.dtype is cu_tokens.dtype and state is not None
-            and len(sp) == 4 and len(sx) == len(so) == len(sb) == len(sc) == 3
-            and len(sd) in (2, 3) and len(si) == cu_tokens.dim() == 1
-            and dt_bias.dim() in (1, 2) and D.dim() in (1, 2) and A.dim() in (1, 3)):
-        ints = (torch.int32, torch.int64)
-        _refuse_types(state_pool=(state_pool, (_F32, _BF16), (4,)), x=(x, (_BF16,), (3,)),
-                      dt=(dt, (_BF16,), (2, 3)), B=(B, (_BF16,), (3,)), C=(C, (_BF16,), (3,)),
-                      out=(out, (_BF16,), (3,)), dt_bias=(dt_bias, (_F32,), (1, 2)),
-                      A=(A, (_F32,), (1, 3)), D=(D, (_F32,), (1, 2)),
-                      cu_tokens=(cu_tokens, ints, (1,)),
-                      state_batch_indices=(state_batch_indices, (cu_tokens.dtype,), (1,)))
-    pool, H, P, N = state_pool.shape
-    T, G, _ = B.shape
-    bs, = state_batch_indices.shape
-    if x.shape != (T, H, P) or out.shape != x.shape:
-        raise ValueError(f"x and out must be [tokens, H, P] = {(T, H, P)}")
-    if B.shape != (T, G, N) or C.shape != B.shape:
-        raise ValueError(f"B and C must be [tokens, G, N] = {(T, G, N)}")
-    if dt.shape != (T, H, P)[:len(sd)]:
-        raise ValueError(f"dt must be {(T, H)} or {(T, H, P)}")
-    if cu_tokens.shape[0] != bs + 1 or cu_tokens.stride(0) != 1:
-        raise ValueError(f"cu_tokens must be contiguous with {bs + 1} entries")
-    return (_SHAPE.pack(bs, H, P, N, G, pool, kind, state),
-            _STRIDES.pack(*sp, *sx, *so, *(sd if len(sd) == 3 else (*sd, 0)), *sb, *sc,
-                          *_head_strides(dt_bias, "dt_bias", (H, P)),
-                          *_head_strides(D, "D", (H, P)), *_head_strides(A, "A", (H, P, N)), *si))
 
 
 def ssu_prompts_workspace_bytes(handle: int, state_pool, x, B, state_batch_indices) -> int:
     """Device workspace bytes ``ssu_update_prompts`` needs for these operands' sizes."""
     pool, H, P, N = state_pool.shape
-    shape = _SHAPE.pack(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
+    shape = ssu_shape_t(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
                         _STATE_TYPE.get(state_pool.dtype, SSU_STATE_F32))
     n = _i64()
-    _check(lib().ssu_prompts_workspace_bytes(handle, shape, x.shape[0], ctypes.byref(n)),
-           "ssu_prompts_workspace_bytes")
+    _check(lib().ssu_prompts_workspace_bytes(handle, ctypes.byref(shape), x.shape[0],
+                                             ctypes.byref(n)), "ssu_prompts_workspace_bytes")
     return int(n.value)
 
 
@@ -588,21 +521,9 @@ def ssu_update_prompts(handle: int, state_pool, state_batch_indices, cu_tokens, 
     continues slot ``state_batch_indices[b]``, or starts from zero where ``fresh[b]`` (uint8 or
     bool) is set, and leaves its last state there.  ``cu_tokens`` and ``state_batch_indices``
     have one type; ``workspace`` is a device uint8 tensor of ``ssu_prompts_workspace_bytes``."""
-    shape, strides = describe_prompts(state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias,
-                                      A, B, C, D, out)
-    tensors = (state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D, out)
-    dev = _device_of(tensors)
-    if fresh is not None:
-        if fresh.dtype not in (torch.uint8, torch.bool) or \
-                fresh.shape != state_batch_indices.shape or not fresh.is_contiguous() or \
-                fresh.get_device() != dev:
-            raise ValueError("fresh must be a contiguous uint8 or bool CUDA tensor with one entry "
-                             "per prompt")
-        fresh = fresh.data_ptr()
-    ws, nbytes = _workspace(workspace, dev)
-    p = [t.data_ptr() for t in tensors]
-    st = lib().ssu_update_prompts(handle, p[0], p[1], p[2], fresh, *p[3:], shape, strides,
-                                  x.shape[0], ws, nbytes, _stream_on(dev, stream))
+    st = _calls().update_prompts(handle, state_pool, state_batch_indices, cu_tokens, x, dt,
+                                 dt_bias, A, B, C, D, out, workspace, fresh,
+                                 _stream_on(x, stream))
     if st:
         _check(st, "ssu_update_prompts")
 
@@ -614,53 +535,19 @@ def ssu_rotate_qk(handle: int, q, k, v, q_weight, k_weight, table, positions, q_
     (weights fp32 ``[D]``), rotation by ``table[positions[t]]`` (fp32 ``[places, rotary]``:
     cosines, then sines), queries to ``q_out``, keys and ``v`` to row ``slots[t]`` of the pages
     ``[pages, page_size, Hk, D]`` (-1: not stored)."""
-    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), q_out.stride()
-    kp, vp, st = k_pages.stride(), v_pages.stride(), table.stride()
-    kind = _INDEX_TYPE.get(slots.dtype)
-    if not (q.dtype is k.dtype is v.dtype is q_out.dtype is k_pages.dtype is v_pages.dtype is _BF16
-            and q_weight.dtype is k_weight.dtype is table.dtype is _F32 and kind is not None
-            and positions.dtype is slots.dtype and len(sq) == len(sk) == len(sv) == len(so) == 3
-            and len(kp) == len(vp) == 4 and len(st) == 2):
-        ints = (torch.int32, torch.int64)
-        _refuse_types(q=(q, (_BF16,), (3,)), k=(k, (_BF16,), (3,)), v=(v, (_BF16,), (3,)),
-                      q_out=(q_out, (_BF16,), (3,)), k_pages=(k_pages, (_BF16,), (4,)),
-                      v_pages=(v_pages, (_BF16,), (4,)), q_weight=(q_weight, (_F32,), (1,)),
-                      k_weight=(k_weight, (_F32,), (1,)), table=(table, (_F32,), (2,)),
-                      slots=(slots, ints, (1,)), positions=(positions, (slots.dtype,), (1,)))
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if q_out.shape != q.shape or k.shape != (T, Hk, D) or v.shape != k.shape:
-        raise ValueError(f"q and q_out must be {(T, Hq, D)}, k and v {(T, Hk, D)}")
-    pages, page = k_pages.shape[:2]
-    if k_pages.shape != (pages, page, Hk, D) or v_pages.shape != k_pages.shape:
-        raise ValueError(f"k_pages and v_pages must be [pages, page_size, {Hk}, {D}]")
-    if q_weight.shape != (D,) or k_weight.shape != (D,) or q_weight.stride() != (1,) or \
-            k_weight.stride() != (1,):
-        raise ValueError(f"q_weight and k_weight must be contiguous with {D} elements")
-    if positions.shape != (T,) or slots.shape != (T,):
-        raise ValueError("positions and slots must have one entry per token")
-    if not (sq[2] == sk[2] == sv[2] == so[2] == kp[3] == vp[3] == st[1] == 1):
-        raise ValueError("the last dimension of every operand must have stride 1")
-    tensors = (q, k, v, q_weight, k_weight, table, positions, q_out, k_pages, v_pages, slots)
-    dev = _device_of(tensors)
-    places, rotary = table.shape
-    status = lib().ssu_rotate_qk(
-        handle, *[t.data_ptr() for t in tensors],
-        _ROTATE_SHAPE.pack(T, Hq, Hk, D, rotary, places, pages, page, kind, bool(interleaved)),
-        _ROTATE_STRIDES.pack(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1], kp[0], kp[1],
-                             kp[2], vp[0], vp[1], vp[2], st[0], *positions.stride(),
-                             *slots.stride()), eps, _stream_on(dev, stream))
-    if status:
-        _check(status, "ssu_rotate_qk")
+    st = _calls().rotate_qk(handle, q, k, v, q_weight, k_weight, table, positions, q_out, k_pages,
+                            v_pages, slots, eps, interleaved, _stream_on(q, stream))
+    if st:
+        _check(st, "ssu_rotate_qk")
 
 
 def ssu_attend_workspace_bytes(handle: int, q, k_pages) -> int:
     """Device workspace bytes ``ssu_attend`` needs for these operands' sizes (fill it with zeros
     once)."""
     n = _i64()
-    shape = _ATTEND_SHAPE.pack(*q.shape[:2], k_pages.shape[2], q.shape[2], *k_pages.shape[:2], 0,
+    shape = ssu_attend_shape_t(*q.shape[:2], k_pages.shape[2], q.shape[2], *k_pages.shape[:2], 0,
                                SSU_INDEX_I32, 0)
-    _check(lib().ssu_attend_workspace_bytes(handle, shape, ctypes.byref(n)),
+    _check(lib().ssu_attend_workspace_bytes(handle, ctypes.byref(shape), ctypes.byref(n)),
            "ssu_attend_workspace_bytes")
     return int(n.value)
 
@@ -672,38 +559,10 @@ def ssu_attend(handle: int, q, k_pages, v_pages, page_table, lengths, out, works
     the first ``lengths[b]`` positions are visible (with ``window``: its last ``window`` and the
     first ``sinks``).  ``scale`` defaults to ``D ** -0.5``.  ``workspace`` is a device tensor of
     ``ssu_attend_workspace_bytes``, zero before its first use, not shared by overlapping calls."""
-    sq, so, kp, vp = q.stride(), out.stride(), k_pages.stride(), v_pages.stride()
-    st, sl = page_table.stride(), lengths.stride()
-    kind = _INDEX_TYPE.get(lengths.dtype)
-    if not (q.dtype is k_pages.dtype is v_pages.dtype is out.dtype is _BF16 and kind is not None
-            and page_table.dtype is lengths.dtype and len(sq) == len(so) == 3
-            and len(kp) == len(vp) == 4 and len(st) == 2 and len(sl) == 1):
-        _refuse_types(q=(q, (_BF16,), (3,)), out=(out, (_BF16,), (3,)),
-                      k_pages=(k_pages, (_BF16,), (4,)), v_pages=(v_pages, (_BF16,), (4,)),
-                      lengths=(lengths, (torch.int32, torch.int64), (1,)),
-                      page_table=(page_table, (lengths.dtype,), (2,)))
-    bs, Hq, D = q.shape
-    pages, page, Hk, _ = k_pages.shape
-    most = page_table.shape[1]
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    if k_pages.shape[3] != D or v_pages.shape != k_pages.shape:
-        raise ValueError(f"k_pages and v_pages must be [pages, page_size, Hk, {D}]")
-    if page_table.shape[0] != bs or lengths.shape[0] != bs:
-        raise ValueError("page_table and lengths must have one row per request")
-    if not (sq[2] == so[2] == kp[3] == vp[3] == 1):
-        raise ValueError("the last dimension of q, out and the pages must have stride 1")
-    tensors = (q, k_pages, v_pages, page_table, lengths, out)
-    dev = _device_of(tensors)
-    ws, nbytes = _workspace(workspace, dev)
-    status = lib().ssu_attend(
-        handle, *[t.data_ptr() for t in tensors],
-        _ATTEND_SHAPE.pack(bs, Hq, Hk, D, pages, page, most, kind, 0),
-        _ATTEND_STRIDES.pack(sq[0], sq[1], so[0], so[1], kp[0], kp[1], kp[2], vp[0], vp[1], vp[2],
-                             *st, *sl), D ** -0.5 if scale is None else scale, window, sinks, ws,
-        nbytes, _stream_on(dev, stream))
-    if status:
-        _check(status, "ssu_attend")
+    st = _calls().attend(handle, q, k_pages, v_pages, page_table, lengths, out, workspace, scale,
+                         window, sinks, _stream_on(q, stream))
+    if st:
+        _check(st, "ssu_attend")
 
 
 def describe_blocks(tensors) -> tuple[ctypes.Array, int]:
