@@ -318,7 +318,7 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
                                                 long long *scan) {
     constexpr int kWarps = kPromptThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long per = static_cast<long long>(m.seg) * kChunk;
+    const unsigned per = static_cast<unsigned>(m.seg) * kChunk;  // at most 2^30
     long long before = 0;  // stretches of the prompts before: all << 32 | those not the last
     if (tid == 0) scan[kWarps] = -1;
     auto pick = [](long long v) { return kFirst ? v & 0xffffffffll : v >> 32; };
@@ -327,7 +327,7 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
         const long long b = b0 + tid;
         long long n = 0, slot, lo, hi;
         if (b < m.q.p.batch && load_prompt<kIdx64>(m.q, b, all, slot, lo, hi)) {
-            n = (hi - lo + per - 1) / per;
+            n = (static_cast<unsigned>(hi - lo) + per - 1) / per;  // tokens fit 31 bits
             if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
         }
         const long long mine = n << 32 | (n > 1 ? n - 1 : 0);
@@ -341,7 +341,7 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
         long long start = before + incl - mine;
-#pragma unroll 1
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) start += scan[w];
             before += scan[w];
