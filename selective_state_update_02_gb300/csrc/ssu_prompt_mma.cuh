@@ -1159,12 +1159,11 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
 #pragma unroll
                 for (int i = 0; i < kSlab; ++i) __stcg(hand + i * N, S[i]);
             }
-            __threadfence();
             asm volatile("bar.sync %0, %1;" ::"n"(1 + kPair), "n"(kCompute) : "memory");
-            if (tid == 0) {
-                __threadfence();
-                atomicExch(m.turn + 1 + part.turn, 1u);
-            }
+            if (tid == 0)
+                asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(m.turn + 1 + part.turn),
+                             "r"(1u)
+                             : "memory");
         }
     }
     return alive;
