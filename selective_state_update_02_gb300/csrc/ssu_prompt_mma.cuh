@@ -941,29 +941,33 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
                 // larger than the instruction cache and M took twice as long)
                 const unsigned myM = tM + which * 64 + lanes;
 #pragma unroll 1
-                for (int col = 0; col < 32 * quarter; col += 16) {  // before the row's 32 tokens
-                    unsigned gg[16], mm[8];
-                    tc_load16(tG + lanes + col, gg);
+                for (int col = 0; col < 32 * quarter; col += 32) {  // before the row's 32 tokens
+                    unsigned gg[2][16], mm[2][8];
+                    tc_load16(tG + lanes + col, gg[0]);
+                    tc_load16(tG + lanes + col + 16, gg[1]);
                     // the blocks between the columns' and the row's
                     const float f = exp2f(up + ((col < 32 && quarter > 1 ? t.y : 0.0f) +
                                                 (col < 64 && quarter > 2 ? t.z : 0.0f)));
                     const float4 *vv = reinterpret_cast<const float4 *>(v0 + col);
                     tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 q = vv[j];
-                        const float2 lo = __fmul2_rn(
-                            make_float2(__uint_as_float(gg[4 * j]),
-                                        __uint_as_float(gg[4 * j + 1])),
-                            __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
-                        const float2 hi = __fmul2_rn(
-                            make_float2(__uint_as_float(gg[4 * j + 2]),
-                                        __uint_as_float(gg[4 * j + 3])),
-                            __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
-                        mm[2 * j] = f2_to_bf2(lo.x, lo.y);
-                        mm[2 * j + 1] = f2_to_bf2(hi.x, hi.y);
+                    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 q = vv[4 * k + j];
+                            const float2 lo = __fmul2_rn(
+                                make_float2(__uint_as_float(gg[k][4 * j]),
+                                            __uint_as_float(gg[k][4 * j + 1])),
+                                __fmul2_rn(make_float2(f, f), make_float2(q.x, q.y)));
+                            const float2 hi = __fmul2_rn(
+                                make_float2(__uint_as_float(gg[k][4 * j + 2]),
+                                            __uint_as_float(gg[k][4 * j + 3])),
+                                __fmul2_rn(make_float2(f, f), make_float2(q.z, q.w)));
+                            mm[k][2 * j] = f2_to_bf2(lo.x, lo.y);
+                            mm[k][2 * j + 1] = f2_to_bf2(hi.x, hi.y);
+                        }
+                        tc_store8(myM + col / 2 + 8 * k, mm[k]);
                     }
-                    tc_store8(myM + col / 2, mm);
                 }
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {  // the row's own 32 tokens
