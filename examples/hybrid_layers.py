@@ -119,6 +119,7 @@ def _norm(t):
 
 
 def main():
+    torch.manual_seed(0)
     lens = [37, 300, 5, 129]
     pair = HybridPair(conversations=6, max_tokens=512)
     who = torch.tensor([4, 0, 5, 2], dtype=torch.int32, device="cuda")
