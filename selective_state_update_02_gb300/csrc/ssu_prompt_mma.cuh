@@ -34,7 +34,7 @@
 // there are more stretches than SMs, CTAs share their chunks along a line (below).
 //
 // What bounds it: the chain of a chunk's steps.  Of some 8,300 cycles per pair of columns and chunk
-// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 250 us, 2.3 TB/s, 0.2 of
+// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 262 us, 2.2 TB/s, 0.3 of
 // the tensor pipe) M takes 2,000, W 2,000, Y and U 2,600 with the decays and the readout under
 // them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a
 // third.
@@ -59,7 +59,7 @@ constexpr int kChunk = 128;      // tokens per chunk: the MMA's M
 constexpr int kSlab = 64;        // state rows per CTA: the MMA's N
 constexpr int kPair = 2;         // columns (a head's 64-row slab) per CTA, of one group
 constexpr int kCompute = kPair * kChunk;       // threads of the elementwise work: a row each
-constexpr int kPromptThreads = kCompute + 64;  // one warp to issue, one to store
+constexpr int kPromptThreads = kCompute + 96;  // one warp to issue, two to look x over and store
 constexpr int kTileBytes = kChunk * 128;  // a 64-column bf16 tile of 128 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -294,7 +294,11 @@ struct PromptSmem {
     static constexpr int kConst = 3 * kChunk + 4;
     static constexpr int kVecFloats = kConst + 4;
     static constexpr int kBars = kVec + 2 * kPair * kVecFloats * 4;
-    static constexpr int kTotal = kBars + 128;
+    // per column, for this chunk and the next: whether x holds infinities or NaN, and from which
+    // token of the chunk on each state row is lost to them
+    static constexpr int kLost = kBars + 128;
+    static constexpr int kLostInts = 4 + kSlab;
+    static constexpr int kTotal = kLost + 2 * kPair * kLostInts * 4;
 };
 
 // A copy of v that the compiler takes for another value.
@@ -395,8 +399,8 @@ __device__ __forceinline__ int stretch_chunks(const PromptMmaParams &m, unsigned
 
 // The line: every stretch `ctas` times (once per pair of columns), two places per chunk and one
 // for what a part costs before its first chunk and after its last; cut evenly, wherever that
-// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 250 us, whole
-// stretches in two rounds 277).  A CTA goes through its share backwards: a stretch cut by its end
+// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 262 us, whole
+// stretches in two rounds 290).  A CTA goes through its share backwards: a stretch cut by its end
 // first, whose state goes to the next CTA, and the one that the CTA before began last, when that
 // one has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those
 // alone that run already.
@@ -558,13 +562,67 @@ __device__ __forceinline__ unsigned tiles_at(const unsigned char *raw) {
 }
 
 constexpr int kIssuer = kCompute / 32;  // the issuing warp; the next one stores
-constexpr int kBars = 12;
+constexpr int kBars = 13;
 
 __device__ __forceinline__ void init_barriers(unsigned bars) {
     for (int i = 0; i < 7; ++i) mbar_init(bars + 8 * i, 1);
     for (int i = 7; i < 11; ++i) mbar_init(bars + 8 * i, kCompute / 32);
     mbar_init(bars + 88, 1);
+    mbar_init(bars + 96, kPair);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ int *lost_of(unsigned char *raw, unsigned phase) {
+    using Smem = PromptSmem<N>;
+    return reinterpret_cast<int *>(raw + (tiles_at(raw) - smem_u32(raw)) + Smem::kLost) +
+           phase * (kPair * Smem::kLostInts);
+}
+
+__device__ __forceinline__ unsigned load_smem2(unsigned at) {
+    unsigned short u;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+    return u;
+}
+
+__device__ __forceinline__ void store_smem2(unsigned at, unsigned v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<unsigned short>(v))
+                 : "memory");
+}
+
+// Whether `valid` tokens' rows of a tile of x hold infinities or NaN (one warp, under M).
+__device__ __forceinline__ bool look_over(unsigned x, int valid, int lane) {
+    constexpr int kLoads = kTileBytes / 512;  // 4 rows each
+    __nv_bfloat162 sum[4] = {};
+    const __nv_bfloat162 zero{};
+#pragma unroll 16
+    for (int k = 0; k < kLoads; ++k) {
+        const uint4 v = load_smem16(x + k * 512 + lane * 16);
+        if (4 * k + lane / 8 >= valid) continue;  // no token of this prompt
+        sum[0] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.x), zero, sum[0]);
+        sum[1] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.y), zero, sum[1]);
+        sum[2] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.z), zero, sum[2]);
+        sum[3] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.w), zero, sum[3]);
+    }
+    sum[0] = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+    return __any_sync(0xffffffffu,
+                      (reinterpret_cast<const unsigned &>(sum[0]) & 0x7fff7fffu) != 0);
+}
+
+// Takes them out; `lost` says from which token on a state row is lost to them.
+__device__ __forceinline__ void take_out(unsigned x, int *lost, int valid, int lane) {
+    for (int p = lane; p < kSlab; p += 32) lost[4 + p] = kChunk;
+    __syncwarp();
+#pragma unroll 1
+    for (int row = lane; row < valid; row += 32)
+#pragma unroll 1
+        for (int p = 0; p < kSlab; ++p) {
+            const unsigned at = swizzled(x, row, p / 8) + 2 * (p % 8);
+            if ((load_smem2(at) & 0x7f80) != 0x7f80) continue;
+            store_smem2(at, 0);
+            atomicMin(lost + 4 + p, row);
+        }
+    fence_async_smem();
 }
 
 // One part, by all threads; false in those whose wait gave up.
@@ -573,11 +631,11 @@ __device__ __forceinline__ void init_barriers(unsigned bars) {
 // stores.  Eight warps do the elementwise work, four per column, a thread per row (token of the
 // chunk, TMEM lane, column n of the state).  Per chunk, with the barrier that each hand-over uses:
 //
-//   issue:    next B; [done] I -> i; [i] next C; [m, x] Y -> y; [w] U -> 3, u; [3] rest of C;
+//   issue:    next B; [done] I -> i; [i] next C; [m, v] Y -> y; [w] U -> 3, u; [3] rest of C;
 //             [b, c] next G -> g
 //   compute:  [g] M, [i] I scaled -> m; [x] W -> w; the next chunk's decays; [y] readout into x's
 //             place -> r; [u] S advanced and published -> done
-//   store:    [r] readout out, then next x
+//   store:    (two warps, a column each) [x] x looked over -> v; one: [r] readout out, then next x
 //
 // so Y runs under W, U under the decays and the readout, I and the loads under M.  (Readouts
 // stored by the threads themselves kept the shared-memory pipe busy for thousands of cycles per
@@ -601,7 +659,8 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
     const unsigned bars = base + Smem::kBars;
     const unsigned bar_b = bars, bar_c = bars + 8, bar_x = bars + 16, bar_g = bars + 24,
                    bar_i = bars + 32, bar_u = bars + 40, bar_y = bars + 48, bar_w = bars + 56,
-                   bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80, bar_3 = bars + 88;
+                   bar_m = bars + 64, bar_done = bars + 72, bar_r = bars + 80, bar_3 = bars + 88,
+                   bar_v = bars + 96;
     // TMEM columns: G (both columns'), M, I and then Y, U (each one after the other)
     const unsigned tG = opaque(tmem), tM = tG + 128, tY = tG + 256, tU = tG + 384;
     const int per_group = columns_per_group(m), pairs = (per_group + 1) / 2;
@@ -721,7 +780,7 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
 #pragma unroll
                         for (int k = 0; k < (kShared ? 1 : kBlocks); ++k) load_c(tok + kChunk, k);
                     if (alive) alive = mbar_wait(bar_m, phase);
-                    if (alive) alive = mbar_wait(bar_x, phase);
+                    if (alive) alive = mbar_wait(bar_v, phase);
                     tc_fence_after();
                     const unsigned x_now = tile(Smem::kX);
 #pragma unroll
@@ -770,24 +829,49 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
             }
         }
         __syncwarp();
-    } else if (warp == kIssuer + 1) {
-        // Whole chunks go out as tiles; the compute threads store a prompt's last, shorter one.
-        if (!kFirst && lane == 0) {
+    } else if (warp > kIssuer) {
+        // Looks x over before Y reads it; then whole chunks go out as tiles (the compute threads
+        // store a prompt's last, shorter one).
+        if (!kFirst) {
             unsigned phase = 0;
-            for (int tok = from; tok + kChunk <= to; tok += kChunk, phase ^= 1) {
-                if (alive) alive = mbar_wait(bar_r, phase);
-#pragma unroll
-                for (int k = 0; k < kPair; ++k) {
-                    const int c = first_column + k;
-                    if (k == 0 || paired)
-                        tma_store(&map_out, sX + k * kTileBytes, c % m.slabs * kSlab, c / m.slabs,
-                                  tok);
+            for (int tok = from; tok < to; tok += kChunk, phase ^= 1) {
+                const int valid = to - tok < kChunk ? to - tok : kChunk;
+                if (alive) alive = mbar_wait(bar_x, phase);
+                // In the product with M a token's x meets the weights of all rows, zeros before the
+                // token, and zero times an infinity or NaN is NaN: those are taken out of x
+                // once W has been made of it, and the readouts that they spoil are spoilt by
+                // hand.  (5 % of the largest call, as Y waits for it: one warp for both columns
+                // 8 %, the compute threads each their row 8 %.)
+                const int column = warp - kIssuer - 1;
+                const unsigned tile = sX + column * kTileBytes;
+                int *const lost = lost_of<N>(raw, phase) + column * Smem::kLostInts;
+                const bool any = look_over(tile, valid, lane);
+                if (lane == 0) lost[0] = any;
+                if (any) {
+                    if (alive) alive = mbar_wait(bar_w, phase);
+                    take_out(tile, lost, valid, lane);
                 }
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                if (tok + kChunk < to) load_x(tok + kChunk);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_v);
+                    if (column == 0 && valid == kChunk) {
+                        if (alive) alive = mbar_wait(bar_r, phase);
+#pragma unroll
+                        for (int k = 0; k < kPair; ++k) {
+                            const int c = first_column + k;
+                            if (k == 0 || paired)
+                                tma_store(&map_out, sX + k * kTileBytes, c % m.slabs * kSlab,
+                                          c / m.slabs, tok);
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        if (tok + kChunk < to) load_x(tok + kChunk);
+                    }
+                }
+                __syncwarp();
             }
-            if (!line) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!line && warp == kIssuer + 1 && lane == 0)
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -1104,6 +1188,19 @@ __device__ __forceinline__ bool run_part(const PromptMmaParams &m, const CUtenso
                         for (int c = 0; c < 4; ++c)
                             reinterpret_cast<uint4 *>(dst)[c] = make_uint4(
                                 o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    }
+                }
+                const int *const lost = lost_of<N>(raw, phase) + which * Smem::kLostInts;
+                if (__builtin_expect(lost[0], 0)) {
+                    const Place at = place();
+#pragma unroll 1
+                    for (int i = 0; i < kSlab; ++i) {
+                        if (lost[4 + i] > row) continue;
+                        if (valid == kChunk)
+                            store_smem2(swizzled(myX, row, i / 8) + 2 * (i % 8), 0x7fff);
+                        else if (at.keeps && row < valid)
+                            p.out[(tok + row) * p.out_b + at.h * p.out_h + at.slab * kSlab + i] =
+                                __ushort_as_bfloat16(0x7fff);
                     }
                 }
                 if (valid == kChunk) {

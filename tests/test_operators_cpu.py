@@ -77,7 +77,7 @@ def test_null_handles_are_refused(ssu):
         assert status == ssu.SSU_ERR_INVALID_ARG
 
 
-# unit -> kernel -> (most registers, most spilled bytes).  Prompts: 320 threads, one CTA per SM, a
+# unit -> kernel -> (most registers, most spilled bytes).  Prompts: 352 threads, one CTA per SM, a
 # row of 64 fp32 state values per thread; attention: one CTA of 8 warps per SM; rotation: 32 warps
 # per SM.
 BUDGETS = {

@@ -401,6 +401,27 @@ def test_more_prompts_than_the_device_holds(op, H, P, N, state, idx):
     assert torch.equal(pool.view(torch.int16), again[1].view(torch.int16))
 
 
+@pytest.mark.parametrize("lens,N,H", [([300], 128, 2), ([70], 64, 4), ([128, 257], 128, 3),
+                                      ([5003], 128, 2)], ids=str)
+def test_no_token_reaches_back(op, lens, N, H):
+    """An infinity or NaN in one element of x: what came before it, and every other row of the
+    state, is as it would be without it; its own row is lost from that token on."""
+    d = make(lens, H=H, N=N, seed=31)
+    clean = call(op, d)
+    lo, hi = d["cu"][-2].item(), d["cu"][-1].item()
+    for k, (t, h, p) in enumerate([(lo + 3, 0, 5), (hi - 1, H - 1, 63), ((lo + hi) // 2, 1, 0)]):
+        x = d["x"][t, h, p].clone()
+        d["x"][t, h, p] = (float("nan"), float("inf"), -float("inf"))[k]
+        out, pool = call(op, d)
+        keep = torch.ones_like(out, dtype=torch.bool)
+        keep[t:hi, h, p] = False
+        assert torch.equal(out[keep], clean[0][keep]) and not out[~keep].isfinite().any()
+        state = torch.ones_like(pool, dtype=torch.bool)
+        state[d["slots"][-1].item(), h, p] = False
+        assert torch.equal(pool[state], clean[1][state]) and not pool[~state].isfinite().any()
+        d["x"][t, h, p] = x
+
+
 @pytest.mark.parametrize("N", [64, 128])
 @pytest.mark.parametrize("slow", [False, True])
 def test_an_fp32_state_is_carried_in_fp32(op, N, slow):
