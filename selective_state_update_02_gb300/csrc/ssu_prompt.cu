@@ -76,15 +76,15 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     // One CTA per SM: as many chunks per stretch as spread the call's over them.  Where the prompts
     // alone come to more than half the SMs, a prompt of up to twice the mean length stays whole, as
     // what a cut would gain it costs in the first pass (6 prompts of 5 to 10 chunks, 16 CTAs each:
-    // 57 us cut in two, 44.7 whole; 24 of 1 to 25, 8 CTAs each: 54.5 us in stretches of 3,
-    // 49.8 of 5, 62.3 of 8; one of 16 chunks, 8 CTAs: 29.2 in stretches of 1, 38.4 of 5).
+    // 45 us whole, 1.28 of that cut in two; 24 of 1 to 25, 8 CTAs each: 50 us in stretches of 5,
+    // 1.09 of that in 3, 1.25 in 8; one of 16 chunks, 8 CTAs: 29 us in stretches of 1, 1.31 in 5).
     const long long chunks = tokens / kChunk + s.batch;
     w.seg = (chunks * w.ctas + sm_count - 1) / sm_count;
     // Where the prompts alone are more than the SMs, whole ones take the time of `rounds` of them
     // and the line (ssu_prompt_mma.cuh) that of their share, and some 4 chunks more for the parts
-    // that it adds.  16 heads, line / whole, us: 24 prompts of 4 chunks 52 / 50 (saves 3.3 chunks),
-    // 60 of 4 98 / 96 (3.8), 24 of 8 74 / 84 (6.3), 20 of 8 64 / 83 (8), 24 of 16 117 / 149 (12);
-    // lengths that differ by factors move these by 10 % either way.
+    // that it adds.  The line's time over that of whole ones, 16 heads: 24 prompts of 4 chunks 1.03
+    // (it saves 3.3 chunks), 60 of 4 1.02 (3.8), 24 of 8 0.86 (6.3), 20 of 8 0.76 (8), 24 of 16
+    // 0.77 (12); lengths that differ by factors move these by 10 % either way.
     const long long units = s.batch * w.ctas, rounds = (units + sm_count - 1) / sm_count;
     const double mean = 0.5 + static_cast<double>(tokens) / kChunk / s.batch;
     w.line = rounds > 1 && mean * (rounds - static_cast<double>(units) / sm_count) > 4.5;

@@ -399,8 +399,8 @@ __device__ __forceinline__ int stretch_chunks(const PromptMmaParams &m, unsigned
 
 // The line: every stretch `ctas` times (once per pair of columns), two places per chunk and one
 // for what a part costs before its first chunk and after its last; cut evenly, wherever that
-// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 262 us, whole
-// stretches in two rounds 290).  A CTA goes through its share backwards: a stretch cut by its end
+// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 262 us, 0.9 of
+// the time of whole stretches in two rounds).  A CTA goes through its share backwards: a stretch cut by its end
 // first, whose state goes to the next CTA, and the one that the CTA before began last, when that
 // one has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those
 // alone that run already.
