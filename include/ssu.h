@@ -441,9 +441,9 @@ typedef struct {
  * slots[t] / page_size.  A token with slots[t] = -1 has its queries written and its key and
  * value left out of the cache.  A token whose position lies outside the table, or whose slot is
  * neither -1 nor inside the cache, is skipped (nothing of it is written) and counted
- * (ssu_get_error).  Slots must be distinct.  Head strides are at most 2^31 - 1.
- * q, k, v, q_out, k_pages, v_pages, q_weight,
- * k_weight [headdim] fp32 and table are 16-byte aligned.  q_out may be q itself (same strides).
+ * (ssu_get_error).  Slots must be distinct.  Head strides are at most 2^31 - 1.  q, k, v, q_out,
+ * k_pages, v_pages, q_weight, k_weight [headdim] fp32 and table are 16-byte aligned.  q_out may be
+ * q itself (same strides).
  * Enqueued on `stream`; allocates and synchronises nothing.
  */
 ssu_status_t ssu_rotate_qk(ssu_handle_t handle, const uint16_t *q, const uint16_t *k,
