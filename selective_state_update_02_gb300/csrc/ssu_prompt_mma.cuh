@@ -316,7 +316,8 @@ struct Stretch {
 
 // The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's
 // last; all threads get the answer.  With `all`, every prompt is looked at and the bad ones
-// counted.
+// counted.  The workspace has room for the stretches of prompts that do not overlap, so one that
+// shares tokens with a good one before it is a bad one too.
 template <bool kIdx64, bool kFirst>
 __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long long at, bool all,
                                                 long long *scan) {
@@ -324,13 +325,20 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned per = static_cast<unsigned>(m.seg) * kChunk;  // at most 2^30
     long long before = 0;  // stretches of the prompts before: all << 32 | those not the last
+    bool backwards = false;  // offsets that run backwards, up to these prompts
     if (tid == 0) scan[kWarps] = -1;
     auto pick = [](long long v) { return kFirst ? v & 0xffffffffll : v >> 32; };
 #pragma unroll 1
     for (long long b0 = 0; b0 < m.q.p.batch && (all || at >= pick(before)); b0 += kPromptThreads) {
         const long long b = b0 + tid;
-        long long n = 0, slot, lo, hi;
-        if (b < m.q.p.batch && load_prompt<kIdx64>(m.q, b, all, slot, lo, hi)) {
+        long long n = 0, slot, lo = 0, hi = 0;
+        bool good = b < m.q.p.batch && load_prompt<kIdx64>(m.q, b, all, slot, lo, hi);
+        backwards = __syncthreads_or(backwards || lo > hi);
+        if (backwards && good && overlaps<kIdx64>(m.q, b, lo, hi)) {
+            good = false;
+            if (all) record_skip(m.q.p, b);
+        }
+        if (good) {
             n = (static_cast<unsigned>(hi - lo) + per - 1) / per;  // tokens fit 31 bits
             if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
         }
@@ -341,7 +349,6 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
             const long long o = __shfl_up_sync(0xffffffffu, incl, x);
             if (lane >= x) incl += o;
         }
-        __syncthreads();
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
         long long start = before + incl - mine;
@@ -377,14 +384,26 @@ struct Part {
     // where the part's stretch begins in the line, and the CTA's share of the line
     long long at, begin, end;
     int chunks;        // of the stretch
+    int mixed;         // some prompt's offsets run backwards
 };
 
-// Chunks and stretches of prompt b (of chunks `per`), packed as chunks << 32 | stretches.
+// Chunks and stretches of prompt b, packed as chunks << 32 | stretches; none for a bad one.  Where
+// offsets run backwards somewhere (`mixed`) those are bad too that overlap with a good one before
+// them.  With `counts`, the bad ones are counted: without `mixed` those that are bad by
+// themselves, with it the others.
 template <bool kIdx64>
 __device__ __forceinline__ unsigned long long prompt_extent(const PromptMmaParams &m, long long b,
-                                                            bool counts) {
+                                                            bool mixed, bool counts,
+                                                            bool &backwards) {
     long long slot, lo, hi;
-    if (b >= m.q.p.batch || !load_prompt<kIdx64>(m.q, b, counts, slot, lo, hi)) return 0;
+    if (b >= m.q.p.batch) return 0;
+    const bool good = load_prompt<kIdx64>(m.q, b, counts && !mixed, slot, lo, hi);
+    backwards |= lo > hi;
+    if (!good) return 0;
+    if (mixed && overlaps<kIdx64>(m.q, b, lo, hi)) {
+        if (counts) record_skip(m.q.p, b);
+        return 0;
+    }
     const unsigned chunks = static_cast<unsigned>((hi - lo + kChunk - 1) / kChunk);
     unsigned n = (chunks + m.seg - 1) / m.seg;
     if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
@@ -420,14 +439,15 @@ __device__ __forceinline__ void step_back(const PromptMmaParams &m, Part &w, int
             w.cta = ctas - 1;
             --w.g;
             unsigned long long extent;
+            bool backwards = false;
             if (--w.index < 0) {
                 do
-                    extent = prompt_extent<kIdx64>(m, --w.b, false);
+                    extent = prompt_extent<kIdx64>(m, --w.b, w.mixed, false, backwards);
                 while (static_cast<unsigned>(extent) == 0);
                 w.count = static_cast<int>(extent);
                 w.index = w.count - 1;
             } else {
-                extent = prompt_extent<kIdx64>(m, w.b, false);
+                extent = prompt_extent<kIdx64>(m, w.b, w.mixed, false, backwards);
             }
             w.chunks = stretch_chunks(m, extent, w.index);
         }
@@ -449,14 +469,20 @@ __device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Pa
         w.more = 0;
         w.turn = static_cast<int>(atomicAdd(m.turn, 1u));
     }
-    unsigned long long all = 0;
+    unsigned long long all;
+    bool mixed = false;
+    while (true) {
+        bool backwards = false;
+        all = 0;
 #pragma unroll 1
-    for (long long b = tid; b < m.q.p.batch; b += kPromptThreads)
-        all += prompt_extent<kIdx64>(m, b, blockIdx.x == 0);
+        for (long long b = tid; b < m.q.p.batch; b += kPromptThreads)
+            all += prompt_extent<kIdx64>(m, b, mixed, blockIdx.x == 0, backwards);
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
-    if (lane == 0) scan[warp] = static_cast<long long>(all);
-    __syncthreads();
+        for (int x = 16; x >= 1; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+        if (lane == 0) scan[warp] = static_cast<long long>(all);
+        if (!__syncthreads_or(backwards && !mixed)) break;
+        mixed = true;  // again, without those that overlap
+    }
     all = 0;
 #pragma unroll 1
     for (int k = 0; k < kWarps; ++k) all += static_cast<unsigned long long>(scan[k]);
@@ -468,7 +494,9 @@ __device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Pa
     unsigned long long before = 0;
 #pragma unroll 1
     for (long long b0 = 0; end > places(before); b0 += kPromptThreads) {
-        const unsigned long long mine = prompt_extent<kIdx64>(m, b0 + tid, false);
+        bool backwards = false;
+        const unsigned long long mine =
+            prompt_extent<kIdx64>(m, b0 + tid, mixed, false, backwards);
         unsigned long long incl = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -496,6 +524,7 @@ __device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Pa
             w.cta = static_cast<int>(o / (2 * w.chunks + 1));
             w.at = end - 1 - (o - static_cast<long long>(w.cta) * (2 * w.chunks + 1));
             w.begin = begin, w.end = end;
+            w.mixed = mixed;
             w.more = 1;
             set_chunks(w);
             if (w.chunks && (w.c1 < 0 ? w.chunks : w.c1) <= w.c0) step_back<kIdx64>(m, w, ctas);
