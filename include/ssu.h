@@ -388,7 +388,8 @@ ssu_status_t ssu_copy_set_launch(ssu_handle_t handle, const ssu_copy_launch_t *l
  * `fresh` is a device array of batch bytes, or NULL (every prompt continues from its slot).
  * `workspace` is a caller-owned device buffer, 256-byte aligned, of at least
  * ssu_prompts_workspace_bytes bytes (which may be 0: NULL is then accepted); it must not be in
- * use by other work until the stream has passed the call, and needs no initial contents.
+ * use by other work until the stream has passed the call, and needs no initial contents.  The
+ * query refuses the sizes that the call refuses.
  * Enqueued on `stream`; allocates and synchronises nothing.
  */
 ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,

@@ -34,13 +34,7 @@ bool aligned(const void *ptr, unsigned bytes) {
     return (reinterpret_cast<unsigned long long>(ptr) % bytes) == 0;
 }
 
-ssu_status_t validate_impl(const void *state_pool, const void *idx, const uint16_t *x,
-                           const uint16_t *dt, const float *dt_bias, const float *A,
-                           const uint16_t *B, const uint16_t *C, const float *D,
-                           const uint16_t *out, const ssu_shape_t *shape,
-                           const ssu_strides_t *st) {
-    if (!shape || !st) return fail(SSU_ERR_INVALID_ARG, "shape and strides must not be NULL");
-    const ssu_shape_t &s = *shape;
+ssu_status_t validate_shape(const ssu_shape_t &s) {
     if (s.batch < 0) return fail(SSU_ERR_INVALID_ARG, "batch %lld < 0", (long long)s.batch);
     if (s.nheads < 1 || s.headdim < 1 || s.dstate < 1 || s.ngroups < 1)
         return fail(SSU_ERR_INVALID_ARG, "nheads, headdim, dstate and ngroups must be >= 1");
@@ -57,6 +51,24 @@ ssu_status_t validate_impl(const void *state_pool, const void *idx, const uint16
                     (long long)s.dstate);
     if (s.headdim > (1 << 20) || s.nheads > 65535)
         return fail(SSU_ERR_UNSUPPORTED, "headdim is limited to 2^20 and nheads to 65535");
+    return ok();
+}
+
+ssu_status_t validate_batch(const ssu_shape_t &s) {
+    if (s.batch > INT_MAX / s.nheads)
+        return fail(SSU_ERR_UNSUPPORTED, "batch * nheads exceeds 2^31");
+    return ok();
+}
+
+ssu_status_t validate_impl(const void *state_pool, const void *idx, const uint16_t *x,
+                           const uint16_t *dt, const float *dt_bias, const float *A,
+                           const uint16_t *B, const uint16_t *C, const float *D,
+                           const uint16_t *out, const ssu_shape_t *shape,
+                           const ssu_strides_t *st) {
+    if (!shape || !st) return fail(SSU_ERR_INVALID_ARG, "shape and strides must not be NULL");
+    const ssu_shape_t &s = *shape;
+    const ssu_status_t sizes = validate_shape(s);
+    if (sizes != SSU_OK) return sizes;
     if (s.batch == 0) return ok();  // nothing is read or written: strides are irrelevant
 
     const int64_t *all[] = {st->state, st->x, st->out, st->dt, st->B, st->C,
@@ -93,9 +105,7 @@ ssu_status_t validate_impl(const void *state_pool, const void *idx, const uint16
         return fail(SSU_ERR_MISALIGNED, "a bf16 operand is not 2-byte aligned");
     if (!aligned(dt_bias, 4) || !aligned(A, 4) || !aligned(D, 4))
         return fail(SSU_ERR_MISALIGNED, "an fp32 operand is not 4-byte aligned");
-    if (s.batch > INT_MAX / s.nheads)
-        return fail(SSU_ERR_UNSUPPORTED, "batch * nheads exceeds 2^31");
-    return ok();
+    return validate_batch(s);
 }
 
 int rows_per_instruction(int64_t dstate, int32_t state_dtype) {

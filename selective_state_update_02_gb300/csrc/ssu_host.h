@@ -18,6 +18,9 @@ ssu_status_t fail(ssu_status_t status, const char *fmt, ...);
 // Clears the message and returns SSU_OK.
 ssu_status_t ok();
 bool aligned(const void *ptr, unsigned bytes);
+// The sizes and types of a call; whether its (request, head) pairs fit 31 bits.
+ssu_status_t validate_shape(const ssu_shape_t &s);
+ssu_status_t validate_batch(const ssu_shape_t &s);
 // The full host-side validation of one ssu_update / ssu_update_static call.
 ssu_status_t validate_impl(const void *state_pool, const void *idx, const uint16_t *x,
                            const uint16_t *dt, const float *dt_bias, const float *A,

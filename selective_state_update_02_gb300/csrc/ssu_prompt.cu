@@ -16,7 +16,9 @@ using ssu_host::aligned;
 using ssu_host::DeviceGuard;
 using ssu_host::fail;
 using ssu_host::ok;
+using ssu_host::validate_batch;
 using ssu_host::validate_impl;
+using ssu_host::validate_shape;
 
 namespace {
 
@@ -53,6 +55,12 @@ cudaError_t launch_seq(const PromptParams &q, int dstate, bool bf16, bool i64, b
                     : launch_seq<128, float>(q, i64, pdl, st);
     return bf16 ? launch_seq<256, __nv_bfloat16>(q, i64, pdl, st)
                 : launch_seq<256, float>(q, i64, pdl, st);
+}
+
+ssu_status_t validate_tokens(int64_t tokens) {
+    if (tokens < 0 || tokens > INT_MAX)
+        return fail(SSU_ERR_INVALID_ARG, "tokens %lld outside 0..2^31 - 1", (long long)tokens);
+    return ok();
 }
 
 // ---- the chunked form ----------------------------------------------------------------
@@ -205,9 +213,10 @@ extern "C" {
 ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
                                          int64_t tokens, int64_t *bytes) {
     if (!handle || !shape || !bytes) return fail(SSU_ERR_INVALID_ARG, "NULL argument");
-    if (shape->batch < 0 || shape->nheads < 1 || shape->headdim < 1 || shape->dstate < 1)
-        return fail(SSU_ERR_INVALID_ARG, "batch must be >= 0 and every dimension >= 1");
-    if (tokens < 0) return fail(SSU_ERR_INVALID_ARG, "tokens %lld < 0", (long long)tokens);
+    ssu_status_t st = validate_shape(*shape);
+    if (st == SSU_OK) st = validate_batch(*shape);
+    if (st == SSU_OK) st = validate_tokens(tokens);
+    if (st != SSU_OK) return st;
     *bytes = mma_sizes(*shape) ? prompt_plan(*shape, tokens, handle->sm_count).total : 0;
     return ok();
 }
@@ -221,15 +230,15 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
                                 int64_t tokens, void *workspace, int64_t workspace_bytes,
                                 ssu_stream_t stream) {
     if (!handle) return fail(SSU_ERR_INVALID_ARG, "NULL handle");
-    if (tokens < 0 || tokens > INT_MAX)
-        return fail(SSU_ERR_INVALID_ARG, "tokens %lld outside 0..2^31 - 1", (long long)tokens);
+    ssu_status_t st = validate_tokens(tokens);
+    if (st != SSU_OK) return st;
     if (tokens == 0) {  // no token row is read: the operands may be empty arrays
         static const uint16_t none[2] = {};
         x = dt = B = C = none;
         out = const_cast<uint16_t *>(none);
     }
-    ssu_status_t st = validate_impl(state_pool, state_batch_indices, x, dt, dt_bias, A, B, C, D,
-                                    out, shape, strides);
+    st = validate_impl(state_pool, state_batch_indices, x, dt, dt_bias, A, B, C, D,
+                       out, shape, strides);
     if (st != SSU_OK || shape->batch == 0) return st;
     const ssu_shape_t &s = *shape;
     if (!cu_tokens) return fail(SSU_ERR_INVALID_ARG, "cu_tokens is NULL");
