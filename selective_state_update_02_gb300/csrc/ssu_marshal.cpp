@@ -157,14 +157,17 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F body) {
     return nullptr;
 }
 
-template <typename F>
-long call(F entry) {
+// The C call, without the interpreter's lock.  Its arguments are worked out before, with the lock
+// held: asking a tensor without storage for its address throws.
+template <typename F, typename... Args>
+long call(F entry, Args... args) {
+    struct Unlocked {
+        PyThreadState *const thread = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(thread); }
+    };
     if (PyErr_Occurred()) throw Failed{};
-    long status;
-    Py_BEGIN_ALLOW_THREADS
-    status = entry();
-    Py_END_ALLOW_THREADS
-    return status;
+    const Unlocked unlocked;
+    return entry(args...);
 }
 
 // handle, state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D, out, workspace,
@@ -220,12 +223,10 @@ PyObject *update_prompts(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Workspace w = workspace(a[12], device);
         auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
         auto *stream = static_cast<ssu_stream_t>(pointer(a[14]));
-        return call([&] {
-            return update_prompts_fn(
-                handle, at_device(pool), at_device(slots), at_device(cu), fresh, bits(x), bits(dt),
-                at_device<float>(dt_bias), at_device<float>(A), bits(B), bits(C),
-                at_device<float>(D), bits(out), &shape, &st, T, w.at, w.bytes, stream);
-        });
+        return call(update_prompts_fn, handle, at_device(pool), at_device(slots), at_device(cu),
+                    fresh, bits(x), bits(dt), at_device<float>(dt_bias), at_device<float>(A),
+                    bits(B), bits(C), at_device<float>(D), bits(out), &shape, &st, T, w.at, w.bytes,
+                    stream);
     });
 }
 
@@ -275,12 +276,10 @@ PyObject *rotate_qk(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float eps = static_cast<float>(PyFloat_AsDouble(a[12]));
         auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
         auto *stream = static_cast<ssu_stream_t>(pointer(a[14]));
-        return call([&] {
-            return rotate_qk_fn(handle, bits(q), bits(k), bits(v), at_device<float>(q_weight),
-                                at_device<float>(k_weight), at_device<float>(table),
-                                at_device(positions), bits(q_out), bits(k_pages), bits(v_pages),
-                                at_device(slots), &shape, &st, eps, stream);
-        });
+        return call(rotate_qk_fn, handle, bits(q), bits(k), bits(v), at_device<float>(q_weight),
+                    at_device<float>(k_weight), at_device<float>(table), at_device(positions),
+                    bits(q_out), bits(k_pages), bits(v_pages), at_device(slots), &shape, &st, eps,
+                    stream);
     });
 }
 
@@ -317,11 +316,9 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t window = PyLong_AsLongLong(a[9]), sinks = PyLong_AsLongLong(a[10]);
         auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
         auto *stream = static_cast<ssu_stream_t>(pointer(a[11]));
-        return call([&] {
-            return attend_fn(handle, bits(q), bits(k_pages), bits(v_pages), at_device(page_table),
-                             at_device(lengths), bits(out), &shape, &st,
-                             static_cast<float>(scale), window, sinks, w.at, w.bytes, stream);
-        });
+        return call(attend_fn, handle, bits(q), bits(k_pages), bits(v_pages), at_device(page_table),
+                    at_device(lengths), bits(out), &shape, &st, static_cast<float>(scale), window,
+                    sinks, w.at, w.bytes, stream);
     });
 }
 
