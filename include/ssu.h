@@ -375,13 +375,13 @@ ssu_status_t ssu_copy_set_launch(ssu_handle_t handle, const ssu_copy_launch_t *l
  * prompts overlap, only rows and slots of the call's own prompts are written, and the chunked form
  * below skips and counts each that shares tokens with a good one before it.
  *
- * Two forms.  Where headdim is a multiple of 64, dstate 64 or 128, and x, B, C and out are 16-byte
- * aligned with strides that are multiples of 8, chunks of 128 tokens run as matrix products: states
- * in fp32, while the readout's weights and the state it reads are rounded to bf16 once per chunk
- * (about 2^-9 of the readout in the mean square, as much as its own rounding).  Any other call runs
- * token by token in fp32.  An infinity or NaN in a token's operands reaches its prompt's readouts
- * from that token on, and its state, as in the recurrence (in chunks an infinity comes out as
- * NaN).
+ * Two forms.  Where headdim is a multiple of 64, dstate 64 or 128, tokens below 2^31 - 512, and x,
+ * B, C and out are 16-byte aligned with strides that are multiples of 8, chunks of 128 tokens run
+ * as matrix products: states in fp32, while the readout's weights and the state it reads are
+ * rounded to bf16 once per chunk (about 2^-9 of the readout in the mean square, as much as its own
+ * rounding).  Any other call runs token by token in fp32.  An infinity or NaN in a token's
+ * operands reaches its prompt's readouts from that token on, and its state, as in the recurrence
+ * (in chunks an infinity comes out as NaN).
  *
  * shape->batch is the number of prompts; strides->x[0], out[0], dt[0], B[0] and C[0] are the
  * strides of the token index; `tokens` (up to 2^31 - 1) is the number of token rows.

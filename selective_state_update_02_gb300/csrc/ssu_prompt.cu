@@ -73,8 +73,10 @@ struct PromptPlan {
     bool line;               // the second pass runs along the line
 };
 
-bool mma_sizes(const ssu_shape_t &s) {
-    return (s.dstate == 64 || s.dstate == 128) && s.headdim % kSlab == 0;
+// The kernels' token numbers are 32 bits wide and run up to two chunks past a prompt's end.
+bool mma_sizes(const ssu_shape_t &s, int64_t tokens) {
+    return (s.dstate == 64 || s.dstate == 128) && s.headdim % kSlab == 0 &&
+           tokens <= INT_MAX - 4 * kChunk;
 }
 
 PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
@@ -217,7 +219,7 @@ ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t 
     if (st == SSU_OK) st = validate_batch(*shape);
     if (st == SSU_OK) st = validate_tokens(tokens);
     if (st != SSU_OK) return st;
-    *bytes = mma_sizes(*shape) ? prompt_plan(*shape, tokens, handle->sm_count).total : 0;
+    *bytes = mma_sizes(*shape, tokens) ? prompt_plan(*shape, tokens, handle->sm_count).total : 0;
     return ok();
 }
 
@@ -302,7 +304,7 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
     cudaError_t e = cudaErrorNotSupported;
-    if (tokens > 0 && mma_sizes(s) && mma_operands(q)) {
+    if (tokens > 0 && mma_sizes(s, tokens) && mma_operands(q)) {
         const PromptPlan w = prompt_plan(s, tokens, handle->sm_count);
         PromptMmaParams m{};
         m.q = q;

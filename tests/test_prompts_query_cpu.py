@@ -49,3 +49,12 @@ def test_sizes_that_are_accepted():
     status, n = query()
     assert status == 0 and n > 0 and n % 256 == 0
     assert query(dstate=256) == (0, 0) and query(headdim=24) == (0, 0) and query(batch=0)[0] == 0
+
+
+@pytest.mark.parametrize("chunked,sizes", [
+    (True, dict(batch=1, tokens=2 ** 31 - 1 - 512)),
+    # token numbers past a chunk's end would not fit 32 bits: token by token
+    (False, dict(batch=1, tokens=2 ** 31 - 512)), (False, dict(batch=1, tokens=2 ** 31 - 1))], ids=str)
+def test_calls_too_large_for_chunks_ask_for_no_workspace(chunked, sizes):
+    status, n = query(**sizes)
+    assert status == 0 and (n > 0) == chunked
