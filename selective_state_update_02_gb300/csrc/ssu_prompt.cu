@@ -79,6 +79,11 @@ bool mma_sizes(const ssu_shape_t &s, int64_t tokens) {
            tokens <= INT_MAX - 4 * kChunk;
 }
 
+// Grids that the device can launch (the line's is one CTA per SM).
+bool mma_grids(const PromptPlan &w) {
+    return w.earlier * w.ctas <= INT_MAX && (w.line || w.stretches * w.ctas <= INT_MAX);
+}
+
 PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     PromptPlan w{};
     w.columns = s.nheads * (s.headdim / kSlab);
@@ -219,7 +224,11 @@ ssu_status_t ssu_prompts_workspace_bytes(ssu_handle_t handle, const ssu_shape_t 
     if (st == SSU_OK) st = validate_batch(*shape);
     if (st == SSU_OK) st = validate_tokens(tokens);
     if (st != SSU_OK) return st;
-    *bytes = mma_sizes(*shape, tokens) ? prompt_plan(*shape, tokens, handle->sm_count).total : 0;
+    *bytes = 0;
+    if (mma_sizes(*shape, tokens)) {
+        const PromptPlan w = prompt_plan(*shape, tokens, handle->sm_count);
+        if (mma_grids(w)) *bytes = w.total;
+    }
     return ok();
 }
 
@@ -317,7 +326,7 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         m.hand = reinterpret_cast<float *>(room + w.hand);
         m.turn = reinterpret_cast<unsigned *>(room + w.turn);
         CUtensorMap maps[4];
-        if (w.earlier * w.ctas <= INT_MAX &&
+        if (mma_grids(w) &&
             encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b) &&
             encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b) &&
             encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b) &&

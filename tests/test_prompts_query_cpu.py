@@ -54,7 +54,10 @@ def test_sizes_that_are_accepted():
 @pytest.mark.parametrize("chunked,sizes", [
     (True, dict(batch=1, tokens=2 ** 31 - 1 - 512)),
     # token numbers past a chunk's end would not fit 32 bits: token by token
-    (False, dict(batch=1, tokens=2 ** 31 - 512)), (False, dict(batch=1, tokens=2 ** 31 - 1))], ids=str)
+    (False, dict(batch=1, tokens=2 ** 31 - 512)), (False, dict(batch=1, tokens=2 ** 31 - 1)),
+    # stretches times CTAs, where those are not shared: 4097 * 4864 and 32769 * 243200
+    (True, dict(batch=4096, heads=1216, headdim=512, tokens=2 ** 31 - 600)),
+    (False, dict(batch=32768, heads=60800, headdim=512, tokens=2 ** 31 - 600))], ids=str)
 def test_calls_too_large_for_chunks_ask_for_no_workspace(chunked, sizes):
     status, n = query(**sizes)
     assert status == 0 and (n > 0) == chunked
