@@ -572,6 +572,7 @@ __device__ __forceinline__ bool handed_on(const unsigned *flag, int lane) {
             __nanosleep(200);
         }
     }
+    __syncwarp();  // what lane 0 has acquired is there for all lanes (a shuffle orders no memory)
     return __shfl_sync(0xffffffffu, done, 0);
 }
 
