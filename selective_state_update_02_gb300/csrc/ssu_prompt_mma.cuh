@@ -539,7 +539,8 @@ __device__ __forceinline__ void chunk_decays(float *vec, bool live, float dt, fl
     float dtv = 0.0f, a = 0.0f;
     if (live) {
         dtv = softplus_f32(dt + bias);
-        a = fminf(fmaxf(dtv * A2, -256.0f), 256.0f);
+        a = dtv * A2;
+        a = a < -256.0f ? -256.0f : a > 256.0f ? 256.0f : a;  // NaN stays: fminf would drop it
     }
     float up = a, down = a;  // inclusive prefix and suffix
 #pragma unroll
