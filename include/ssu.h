@@ -199,8 +199,10 @@ ssu_status_t ssu_update_from_host(ssu_handle_t handle, void *state_pool,
 
 /*
  * Synchronise `stream`, then read and clear the handle's device counters.
- * *skipped receives the number of requests skipped since the last read (may be NULL);
- * *first_bad receives the smallest skipped request index b, or -1 (may be NULL).
+ * *skipped receives what was skipped since the last read (may be NULL): requests, prompts of
+ * ssu_update_prompts, tokens of ssu_rotate_qk, requests and single pages of ssu_attend.
+ * *first_bad receives the smallest index of these in their calls, of whatever call (for a page that
+ * of its request), or -1 (may be NULL): read after each call to tell one call from another.
  * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_ERR_CUDA when a prompt kernel gave up a wait
  * for its own copies or products (after ten seconds; its results are then not valid), SSU_OK
  * otherwise.

@@ -330,8 +330,11 @@ ssu_status_t ssu_get_error(ssu_handle_t handle, ssu_stream_t stream, uint32_t *s
     if (host[2])
         return fail(SSU_ERR_CUDA, "a kernel gave up waiting for its own copies or products; "
                                   "the results of the calls since the last check are not valid");
-    if (host[0]) return fail(SSU_ERR_INDEX_OOB, "%u request(s) named a slot outside the pool",
-                             host[0]);
+    if (host[0])
+        return fail(SSU_ERR_INDEX_OOB,
+                    "%u request(s), prompts, tokens or pages with an index, offset, position or "
+                    "length out of range were skipped; the smallest is number %u of its call",
+                    host[0], host[1]);
     return ok();
 }
 
