@@ -23,6 +23,7 @@ import torch
 
 _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "libssu.so"
+MARSHAL_PATH = _PKG / "_marshal.so"
 
 SSU_OK = 0
 SSU_ERR_INVALID_ARG = 1
@@ -489,6 +490,9 @@ def _calls():
     built."""
     global _bound
     if _bound is None:
+        if not MARSHAL_PATH.exists():
+            raise RuntimeError(f"{MARSHAL_PATH} is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
         module = importlib.import_module(f"{__name__}._marshal")
         module.bind(*(ctypes.cast(getattr(lib(), name), _vp).value
                       for name in ("ssu_update_prompts", "ssu_rotate_qk", "ssu_attend")))

@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -59,25 +60,57 @@ def _older(built: Path, sources: list[Path]) -> bool:
     return not built.exists() or any(p.stat().st_mtime > built.stat().st_mtime for p in sources)
 
 
+def _library_stale() -> bool:
+    return _older(LIB, SOURCES + HEADERS)
+
+
+def _marshal_stale() -> bool:
+    return _older(MARSHAL, [MARSHAL_SOURCE, HEADERS[0]])
+
+
 def stale() -> bool:
-    return _older(LIB, SOURCES + HEADERS) or _older(MARSHAL, [MARSHAL_SOURCE, HEADERS[0]])
+    return _library_stale() or _marshal_stale()
 
 
-def build(force: bool = False, extra: list[str] | None = None) -> Path:
-    """Compile libssu.so and _marshal.so next to this file unless they are up to date."""
-    if not (force or stale()):
-        return LIB
+def _build_library(extra: list[str] | None) -> None:
     OBJDIR.mkdir(exist_ok=True)
     objs = [OBJDIR / (src.name + ".o") for src in SOURCES]
     procs = [subprocess.Popen(compile_command(src, obj, extra))
              for src, obj in zip(SOURCES, objs)]
-    marshal = MARSHAL.with_name(f"_marshal.so.tmp{os.getpid()}")
-    procs.append(subprocess.Popen(marshal_command(marshal)))
     codes = [p.wait() for p in procs]
     if any(codes):
-        raise subprocess.CalledProcessError(max(codes), "nvcc, g++ (libssu sources)")
-    os.replace(marshal, MARSHAL)
+        raise subprocess.CalledProcessError(max(codes), "nvcc (libssu sources)")
     tmp = LIB.with_name(f"libssu.so.tmp{os.getpid()}")
     subprocess.run(link_command(objs, tmp), check=True)
     os.replace(tmp, LIB)
+
+
+def _start_marshal(out: Path) -> subprocess.Popen | None:
+    try:
+        return subprocess.Popen(marshal_command(out))
+    except (ImportError, OSError):  # no torch, no g++
+        return None
+
+
+def build(force: bool = False, extra: list[str] | None = None) -> Path:
+    """Compile libssu.so and _marshal.so next to this file unless they are up to date.  nvcc alone is
+    enough for libssu.so, which the C ABI and every call but the prompt, rotation and attention
+    calls of the Python binding are content with: where _marshal.so cannot be built (it needs
+    g++ and the headers of Python and torch), that is a warning."""
+    library, binding = force or _library_stale(), force or _marshal_stale()
+    tmp = MARSHAL.with_name(f"_marshal.so.tmp{os.getpid()}")
+    marshal = _start_marshal(tmp) if binding else None
+    try:
+        if library:
+            _build_library(extra)
+    finally:
+        built = marshal is not None and marshal.wait() == 0
+        if built:
+            os.replace(tmp, MARSHAL)
+        elif binding:
+            tmp.unlink(missing_ok=True)
+            MARSHAL.unlink(missing_ok=True)  # what is there is of other sources
+    if binding and not built:
+        warnings.warn("_marshal.so could not be built: the prompt, rotation and attention calls are "
+                      "not available from Python", stacklevel=2)
     return LIB
