@@ -493,6 +493,11 @@ def _calls():
         if not MARSHAL_PATH.exists():
             raise RuntimeError(f"{MARSHAL_PATH} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import _build
+        if _build.marshal_built_for() != _build.marshal_wants():
+            raise RuntimeError(f"{MARSHAL_PATH} was built for "
+                               f"{_build.marshal_built_for() or 'something unknown'}, this is "
+                               f"{_build.marshal_wants()}: build it again")
         module = importlib.import_module(f"{__name__}._marshal")
         module.bind(*(ctypes.cast(getattr(lib(), name), _vp).value
                       for name in ("ssu_update_prompts", "ssu_rotate_qk", "ssu_attend")))

@@ -64,8 +64,31 @@ def _library_stale() -> bool:
     return _older(LIB, SOURCES + HEADERS)
 
 
+def _marshal_note() -> Path:
+    return MARSHAL.with_name("_marshal.built_for")
+
+
+def marshal_wants() -> str:
+    """What _marshal.so must have been built for: it uses torch's C++ classes and Python's ABI, so
+    that one of another version may crash instead of failing."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def marshal_built_for() -> str:
+    """What _marshal.so was built for; "" if that is not known."""
+    try:
+        return _marshal_note().read_text()
+    except OSError:
+        return ""
+
+
 def _marshal_stale() -> bool:
-    return _older(MARSHAL, [MARSHAL_SOURCE, HEADERS[0]])
+    try:
+        wanted = marshal_wants()
+    except ImportError:
+        return True
+    return _older(MARSHAL, [MARSHAL_SOURCE, HEADERS[0]]) or marshal_built_for() != wanted
 
 
 def stale() -> bool:
@@ -106,7 +129,9 @@ def build(force: bool = False, extra: list[str] | None = None) -> Path:
     finally:
         built = marshal is not None and marshal.wait() == 0
         if built:
+            _marshal_note().unlink(missing_ok=True)
             os.replace(tmp, MARSHAL)
+            _marshal_note().write_text(marshal_wants())
         elif binding:
             tmp.unlink(missing_ok=True)
             MARSHAL.unlink(missing_ok=True)  # what is there is of other sources

@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
 from selective_state_update_02_gb300 import _build
 import selective_state_update_02_gb300 as ssu
@@ -58,3 +59,18 @@ def test_a_library_that_does_not_compile_is_an_error(elsewhere, monkeypatch):
     with pytest.raises(Exception, match="nvcc"):
         _build.build(force=True)
     assert not (elsewhere / "libssu.so").exists()
+
+
+def test_the_binding_is_built_again_for_another_torch(elsewhere, monkeypatch):
+    monkeypatch.setattr(_build, "marshal_command", lambda out: ["touch", str(out)])
+    _build.build()
+    assert not _build.stale()
+    monkeypatch.setattr(torch, "__version__", "0.1")
+    assert _build.stale()
+    monkeypatch.setattr(ssu, "_bound", None)
+    monkeypatch.setattr(ssu, "MARSHAL_PATH", elsewhere / "_marshal.so")
+    with pytest.raises(RuntimeError, match="was built for torch .* build it again"):
+        ssu.ssu_attend(0, None, None, None, None, None, None, stream=0)
+    before = (elsewhere / "libssu.so").stat().st_mtime_ns
+    _build.build()
+    assert not _build.stale() and (elsewhere / "libssu.so").stat().st_mtime_ns == before
