@@ -107,6 +107,13 @@ __device__ __forceinline__ Visible visible_of(const AttendParams &p, long long b
 // ones (128 ragged requests: 28.5 us, 0.89 of the time without).
 constexpr int kUnitCost = 1;
 
+// Whether request b has no places and is for CTA `cta` of `ctas` to see to in the end; threads also
+// ask past the last request.
+__host__ __device__ inline bool sees_to(long long b, long long requests, unsigned places,
+                                        unsigned cta, unsigned ctas) {
+    return b < requests && places == 0 && static_cast<unsigned>(b) % ctas == cta;
+}
+
 struct Cursor {
     long long at;   // place of the tile in the line
     long long b;    // request
@@ -630,13 +637,13 @@ __global__ void __launch_bounds__(32 * AttendGeo<D>::kWarps, 1)
         return n;
     };
     const unsigned n0 = places_of(tid), incl0 = warp_scan(n0);
-    bool empty = n0 == 0 && tid % gridDim.x == blockIdx.x;  // a request this CTA sees to in the end
+    bool empty = sees_to(tid, p.requests, n0, blockIdx.x, gridDim.x);
     long long rest = 0;
 #pragma unroll 1
     for (long long b0 = kThreads; b0 < p.requests; b0 += kThreads) {
         const unsigned n = places_of(b0 + tid);
         rest += n;
-        empty |= n == 0 && static_cast<unsigned>(b0 + tid) % gridDim.x == blockIdx.x;
+        empty |= sees_to(b0 + tid, p.requests, n, blockIdx.x, gridDim.x);
     }
     if (p.requests > kThreads) {
 #pragma unroll
