@@ -485,12 +485,13 @@ typedef struct {
  *
  *     out[b,h] = bf16_rne( sum_j p_j v_j ),   p = softmax over visible j of scale * q[b,h] . k_j
  *
- * Positions 0 .. lengths[b] - 1 are visible; with window > 0 only those with
- * j >= lengths[b] - window or j < sinks.  A request of length 0 gets zeros.  A request whose
- * length is negative or above max_pages * page_size is skipped (its out rows are not touched)
- * and counted (ssu_get_error).  A visible page whose id lies outside [0, num_pages) is left out
- * of the sums and its request counted, once for each such page.  Scores, softmax statistics and
- * sums are fp32; the weights p are rounded to bf16 for the product with v.
+ * Positions 0 .. lengths[b] - 1 are visible; with window > 0 only those with j >= lengths[b] -
+ * window or j < sinks.  A request of length 0 gets zeros, as does a query head whose visible
+ * scores are all minus infinity.  A request whose length is negative or above max_pages *
+ * page_size is skipped (its out rows are not touched) and counted (ssu_get_error).  A visible
+ * page whose id lies outside [0, num_pages) is left out of the sums and its request counted,
+ * once for each such page.  Scores, softmax statistics and sums are fp32; the weights p are
+ * rounded to bf16 for the product with v.
  *
  * q, k_pages, v_pages and out are 16-byte aligned.  `workspace` is a caller-owned device buffer,
  * 256-byte aligned, of at least ssu_attend_workspace_bytes bytes, filled with zeros before its

@@ -59,7 +59,7 @@ constexpr int kAttendRows = 16;     // query heads per unit: the MMA's M
 
 // Keys per warp and step: the second product's K, twice for the shortest rows, whose steps would
 // otherwise be as long as those of twice the bytes (40 requests through a window of 1000, 8 heads
-// of 64: 27.3 us, 0.92 of the time with 16).
+// of 64: 28.0 us, 0.92 of the time with 16).
 template <int D>
 struct AttendGeo {
     static constexpr int kKeys = D == 64 ? 32 : 16;

@@ -147,3 +147,15 @@ def test_tokens_without_dependent_launch(op, D):
         ssu.ssu_set_pdl(op.handle, True)
     assert same(*results) and results[0].isfinite().all()
     assert op.get_error() == (0, -1)
+
+
+def test_a_head_without_a_finite_score(op):
+    """Scores of minus infinity alone: zeros, as for an empty cache; the other heads are as they are."""
+    d = test_attend_gpu.make([40, 300], Hq=4, Hk=2, D=64, seed=57)
+    op.attend(**d, workspace=test_attend_gpu.workspace(op, d))
+    want = d["out"].clone()
+    d["q"][:, :2] = 1.0
+    d["k_pages"][:, :, 0] = float("-inf")
+    op.attend(**d, workspace=test_attend_gpu.workspace(op, d))
+    torch.cuda.synchronize()
+    assert (d["out"][:, :2] == 0).all() and torch.equal(d["out"][:, 2:], want[:, 2:])
