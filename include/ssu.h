@@ -375,7 +375,7 @@ ssu_status_t ssu_copy_set_launch(ssu_handle_t handle, const ssu_copy_launch_t *l
  * is out of range or if its offsets are not 0 <= cu_tokens[b] <= cu_tokens[b + 1] <= tokens.
  * Slots must be distinct and prompts must not overlap.  Where offsets that run backwards make
  * prompts overlap, only rows and slots of the call's own prompts are written, and the chunked form
- * below skips and counts each that shares tokens with a good one before it.
+ * below skips and counts each that begins before the end of a good one before it.
  *
  * Two forms.  Where headdim is a multiple of 64, dstate 64 or 128, tokens below 2^31 - 512, and x,
  * B, C and out are 16-byte aligned with strides that are multiples of 8, chunks of 128 tokens run

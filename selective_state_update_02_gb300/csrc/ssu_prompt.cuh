@@ -44,20 +44,6 @@ __device__ __forceinline__ bool load_prompt(const PromptParams &q, long long b, 
     return good;
 }
 
-// Whether prompt b, good by itself, shares tokens with a good one before it.  That takes offsets
-// that run backwards between the two, so it is asked only where some do.
-template <bool kIdx64>
-__device__ __forceinline__ bool overlaps(const PromptParams &q, long long b, long long begin,
-                                         long long end) {
-    long long slot, lo, hi;
-#pragma unroll 1
-    for (long long j = 0; j < b; ++j)
-        if (load_prompt<kIdx64>(q, j, false, slot, lo, hi) && lo < end && begin < hi && lo < hi &&
-            begin < end)
-            return true;
-    return false;
-}
-
 template <int SLOTS, int N, typename ST, bool kIdx64>
 __global__ void __launch_bounds__(128) ssu_prompt_seq_kernel(PromptParams q) {
     pdl_wait();

@@ -314,10 +314,49 @@ struct Stretch {
     int index, count;  // of the prompt's stretches
 };
 
+// Prompts that overlap.  The workspace has room for the stretches of prompts that do not, so a
+// prompt that begins before the end of a good one before it is a bad one too.  That takes offsets
+// that run backwards somewhere, and is looked for only where some do.
+
+// The largest of the ends of the thread's earlier prompts (`seen`, of all threads) and of those of
+// the threads before it (`end`; 0: none); all threads call it, and `scan` is free afterwards.
+__device__ __forceinline__ int end_before(int end, int seen, long long *scan) {
+    constexpr int kWarps = kPromptThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = end;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl = max(incl, o);
+    }
+    const int earlier = __reduce_max_sync(0xffffffffu, seen);
+    __syncthreads();
+    if (lane == 31) scan[warp] = static_cast<long long>(earlier) << 32 | incl;
+    __syncthreads();
+    int most = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) most = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+        most = max(most, static_cast<int>(scan[w] >> 32));
+        if (w < warp) most = max(most, static_cast<int>(scan[w]));
+    }
+    __syncthreads();
+    return most;
+}
+
+// The same question about one prompt that begins at `begin`, by one thread.
+template <bool kIdx64>
+__device__ __forceinline__ bool begins_early(const PromptParams &q, long long b, long long begin) {
+    long long slot, lo, hi;
+#pragma unroll 1
+    for (long long j = 0; j < b; ++j)
+        if (load_prompt<kIdx64>(q, j, false, slot, lo, hi) && lo < hi && begin < hi) return true;
+    return false;
+}
+
 // The stretch that is the `at`-th of the call, or (kFirst) of those that are not their prompt's
 // last; all threads get the answer.  With `all`, every prompt is looked at and the bad ones
-// counted.  The workspace has room for the stretches of prompts that do not overlap, so one that
-// shares tokens with a good one before it is a bad one too.
+// counted.
 template <bool kIdx64, bool kFirst>
 __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long long at, bool all,
                                                 long long *scan) {
@@ -326,6 +365,7 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
     const unsigned per = static_cast<unsigned>(m.seg) * kChunk;  // at most 2^30
     long long before = 0;  // stretches of the prompts before: all << 32 | those not the last
     bool backwards = false;  // offsets that run backwards, up to these prompts
+    int seen = 0;            // the largest end of the thread's earlier prompts
     if (tid == 0) scan[kWarps] = -1;
     auto pick = [](long long v) { return kFirst ? v & 0xffffffffll : v >> 32; };
 #pragma unroll 1
@@ -334,10 +374,12 @@ __device__ __forceinline__ Stretch find_stretch(const PromptMmaParams &m, long l
         long long n = 0, slot, lo = 0, hi = 0;
         bool good = b < m.q.p.batch && load_prompt<kIdx64>(m.q, b, all, slot, lo, hi);
         backwards = __syncthreads_or(backwards || lo > hi);
-        if (backwards && good && overlaps<kIdx64>(m.q, b, lo, hi)) {
+        const int ends = good && lo < hi ? static_cast<int>(hi) : 0;
+        if (backwards && end_before(ends, seen, scan) > lo && ends) {
             good = false;
             if (all) record_skip(m.q.p, b);
         }
+        seen = max(seen, ends);
         if (good) {
             n = (static_cast<unsigned>(hi - lo) + per - 1) / per;  // tokens fit 31 bits
             if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
@@ -387,23 +429,15 @@ struct Part {
     int mixed;         // some prompt's offsets run backwards
 };
 
-// Chunks and stretches of prompt b, packed as chunks << 32 | stretches; none for a bad one.  Where
-// offsets run backwards somewhere (`mixed`) those are bad too that overlap with a good one before
-// them.  With `counts`, the bad ones are counted: without `mixed` those that are bad by
-// themselves, with it the others.
+// Chunks and stretches of prompt b (tokens lo .. hi - 1), packed as chunks << 32 | stretches; none
+// for one that is bad by itself.
 template <bool kIdx64>
 __device__ __forceinline__ unsigned long long prompt_extent(const PromptMmaParams &m, long long b,
-                                                            bool mixed, bool counts,
-                                                            bool &backwards) {
-    long long slot, lo, hi;
-    if (b >= m.q.p.batch) return 0;
-    const bool good = load_prompt<kIdx64>(m.q, b, counts && !mixed, slot, lo, hi);
-    backwards |= lo > hi;
-    if (!good) return 0;
-    if (mixed && overlaps<kIdx64>(m.q, b, lo, hi)) {
-        if (counts) record_skip(m.q.p, b);
-        return 0;
-    }
+                                                            bool counts, long long &lo,
+                                                            long long &hi) {
+    long long slot;
+    lo = hi = 0;
+    if (b >= m.q.p.batch || !load_prompt<kIdx64>(m.q, b, counts, slot, lo, hi)) return 0;
     const unsigned chunks = static_cast<unsigned>((hi - lo + kChunk - 1) / kChunk);
     unsigned n = (chunks + m.seg - 1) / m.seg;
     if (n == 0 && m.q.fresh && m.q.fresh[b]) n = 1;  // only clears the slot
@@ -438,18 +472,20 @@ __device__ __forceinline__ void step_back(const PromptMmaParams &m, Part &w, int
         if (--w.cta < 0) {
             w.cta = ctas - 1;
             --w.g;
-            unsigned long long extent;
-            bool backwards = false;
             if (--w.index < 0) {
-                do
-                    extent = prompt_extent<kIdx64>(m, --w.b, w.mixed, false, backwards);
-                while (static_cast<unsigned>(extent) == 0);
+                unsigned long long extent;
+                do {
+                    long long lo, hi;
+                    extent = prompt_extent<kIdx64>(m, --w.b, false, lo, hi);
+                    if (w.mixed && lo < hi && extent && begins_early<kIdx64>(m.q, w.b, lo))
+                        extent = 0;
+                } while (static_cast<unsigned>(extent) == 0);
                 w.count = static_cast<int>(extent);
                 w.index = w.count - 1;
+                w.chunks = stretch_chunks(m, extent, w.index);
             } else {
-                extent = prompt_extent<kIdx64>(m, w.b, w.mixed, false, backwards);
+                w.chunks = m.seg;  // not its prompt's last
             }
-            w.chunks = stretch_chunks(m, extent, w.index);
         }
         w.at -= 2 * w.chunks + 1;
         set_chunks(w);
@@ -469,14 +505,34 @@ __device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Pa
         w.more = 0;
         w.turn = static_cast<int>(atomicAdd(m.turn, 1u));
     }
+    // the extent of a prompt that does not overlap with one before it, all threads side by side
+    auto apart = [&](long long b, int &seen, bool counts) {
+        long long lo, hi;
+        unsigned long long extent = prompt_extent<kIdx64>(m, b, false, lo, hi);
+        const int ends = extent && lo < hi ? static_cast<int>(hi) : 0;
+        if (end_before(ends, seen, scan) > lo && ends) {
+            extent = 0;
+            if (counts) record_skip(m.q.p, b);
+        }
+        seen = max(seen, ends);
+        return extent;
+    };
     unsigned long long all;
     bool mixed = false;
     while (true) {
         bool backwards = false;
+        int seen = 0;
         all = 0;
 #pragma unroll 1
-        for (long long b = tid; b < m.q.p.batch; b += kPromptThreads)
-            all += prompt_extent<kIdx64>(m, b, mixed, blockIdx.x == 0, backwards);
+        for (long long b0 = 0; b0 < m.q.p.batch; b0 += kPromptThreads) {
+            if (mixed) {
+                all += apart(b0 + tid, seen, blockIdx.x == 0);
+            } else {
+                long long lo, hi;
+                all += prompt_extent<kIdx64>(m, b0 + tid, blockIdx.x == 0, lo, hi);
+                backwards |= lo > hi;
+            }
+        }
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
         if (lane == 0) scan[warp] = static_cast<long long>(all);
@@ -492,11 +548,12 @@ __device__ __forceinline__ void find_line(const PromptMmaParams &m, int ctas, Pa
     const long long begin = w.turn * each, end = min(begin + each, total);
     if (begin >= end) return;
     unsigned long long before = 0;
+    int seen = 0;
 #pragma unroll 1
     for (long long b0 = 0; end > places(before); b0 += kPromptThreads) {
-        bool backwards = false;
-        const unsigned long long mine =
-            prompt_extent<kIdx64>(m, b0 + tid, mixed, false, backwards);
+        long long lo, hi;
+        const unsigned long long mine = mixed ? apart(b0 + tid, seen, false)
+                                              : prompt_extent<kIdx64>(m, b0 + tid, false, lo, hi);
         unsigned long long incl = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {

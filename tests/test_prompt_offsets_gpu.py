@@ -87,3 +87,32 @@ def test_overlaps_among_prompts_that_share_ctas(op):
     assert n > 0
     check(d, out, pool, ref)
     assert op.get_error() == (2, 30)
+
+
+def clean_call(op, d, skip):
+    """The same prompts at offsets that do not run backwards, those of ``skip`` without a slot."""
+    slots = d["slots"].clone()
+    slots[list(skip)] = -1
+    out, pool, _ = guarded_call(op, {**d, "slots": slots})
+    assert op.get_error() == (len(skip), min(skip))
+    return out, pool
+
+
+@pytest.mark.parametrize("lens,H", [
+    ([3 + i % 5 for i in range(800)], 2),                  # whole prompts
+    ([3 + i % 5 for i in range(799)] + [3000], 2),         # the last one cut
+    ([800 + 13 * (i % 9) if i != 10 else 5000 for i in range(360)], 2)],  # shared, and one cut
+    ids=["whole", "cut", "shared"])
+def test_more_prompts_than_a_scan_takes_at_once(op, lens, H):
+    d = make(lens, H=H, seed=5)
+    n = len(lens)
+    bad = [(n // 7, 0), (n * 5 // 8, n // 3), (n * 7 // 8, n * 3 // 8)]
+    skip = {p - 1 for p, _ in bad} | {p for p, _ in bad}
+    op.get_error()
+    want = clean_call(op, d, sorted(skip))
+    cu = d["cu"].clone()
+    for p, to in bad:  # prompt p - 1 runs back to the start of another, prompt p from there on
+        d["cu"][p] = cu[to]
+    out, pool, _ = guarded_call(op, d)
+    assert op.get_error() == (len(skip), min(skip))
+    assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
