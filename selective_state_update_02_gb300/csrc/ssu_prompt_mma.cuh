@@ -34,7 +34,7 @@
 // there are more stretches than SMs, CTAs share their chunks along a line (below).
 //
 // What bounds it: the chain of a chunk's steps.  Of some 8,300 cycles per pair of columns and chunk
-// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 263 us, 2.2 TB/s, 0.3 of
+// (measured inside the kernel; 8 prompts of 4096 tokens through 64 heads: 264 us, 2.2 TB/s, 0.3 of
 // the tensor pipe) M takes 2,000, W 2,000, Y and U 2,600 with the decays and the readout under
 // them, I 500 and the state 650; the tensor pipe is busy for 3,300 of them, issue slots for a
 // third.
@@ -452,7 +452,7 @@ __device__ __forceinline__ int stretch_chunks(const PromptMmaParams &m, unsigned
 
 // The line: every stretch `ctas` times (once per pair of columns), two places per chunk and one
 // for what a part costs before its first chunk and after its last; cut evenly, wherever that
-// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 263 us, 0.9 of
+// falls, so that CTAs end together (8 prompts of 32 chunks, 32 pairs, 152 CTAs: 264 us, 0.9 of
 // the time of whole stretches in two rounds).  A CTA goes through its share backwards: a stretch cut by its end
 // first, whose state goes to the next CTA, and the one that the CTA before began last, when that
 // one has long handed its state on.  Turns are given out as CTAs begin, so a CTA waits for those
