@@ -507,6 +507,104 @@ ssu_status_t ssu_attend(ssu_handle_t handle, const uint16_t *q, const uint16_t *
                         int64_t sinks, void *workspace, int64_t workspace_bytes,
                         ssu_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The gated delta rule: a linear token mixer whose state forgets by a decay and is corrected
+ * towards each new value along its key.  Per request or prompt and head h (key head g = h / (H / G)),
+ *
+ *     a    = exp(softplus(dt[t,h] + dt_bias[h]) * A[h]);    beta = 1 / (1 + exp(-b[t,h]))
+ *     kn   = k[t,g] / sqrt(sum_n k[t,g,n]^2 + qk_eps)
+ *     qn   = scale * q[t,g] / sqrt(sum_n q[t,g,n]^2 + qk_eps)
+ *     e[p] = beta * (v[t,h,p] - a * sum_n S[p,n] * kn[n])
+ *     S[p,n] = a * S[p,n] + e[p] * kn[n]
+ *     out[t,h,p] = bf16_rne( sum_n S[p,n] * qn[n] )
+ *
+ * with S = state_pool[s,h], slot s = state_batch_indices[request]; a negative qk_eps leaves q and
+ * k as they are (qn = scale * q).  The pool, its types, sizes and limits are those of ssu_update:
+ * ssu_shape_t with headdim P (rows of a value), dstate N (a key's elements), nheads H (value
+ * heads) and ngroups G (key heads).  q, k, v, dt, b and out are bfloat16; dt_bias and A fp32.
+ */
+
+/* Element strides, outermost dimension first; those of P and N are 1. */
+typedef struct {
+    int64_t state[3];              /* slot, head, row: multiples of 16 bytes */
+    int64_t q[2], k[2];            /* token (or request), key head */
+    int64_t v[2], out[2];          /* token, head */
+    int64_t dt[2], b[2];           /* token, head */
+    int64_t dt_bias, A;            /* head */
+    int64_t idx;                   /* state_batch_indices */
+} ssu_delta_strides_t;
+
+/*
+ * One new token per request: q, k [bs, G, N], v and out [bs, H, P], dt and b [bs, H].  A request
+ * whose slot is out of range is skipped and counted (ssu_get_error).  Slots must be distinct.
+ * qk_eps and scale must not be NaN, scale finite.  Enqueued on `stream`; allocates and synchronises
+ * nothing.
+ */
+ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
+                              const void *state_batch_indices, const uint16_t *q,
+                              const uint16_t *k, const uint16_t *v, const uint16_t *dt,
+                              const float *dt_bias, const float *A, const uint16_t *b,
+                              uint16_t *out, const ssu_shape_t *shape,
+                              const ssu_delta_strides_t *strides, float scale, float qk_eps,
+                              ssu_stream_t stream);
+
+/*
+ * Whole prompts, packed as for ssu_update_prompts: prompt b is tokens cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 of q, k, v, dt, b and out, continues its slot (or starts from zero where
+ * fresh[b] != 0: the slot is then not read) and leaves its last state there.  cu_tokens, fresh,
+ * tokens, workspace, the skipping and counting of bad prompts and what is asked of slots and
+ * offsets are as there; shape->batch is the number of prompts.
+ */
+ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
+                                       int64_t tokens, int64_t *bytes);
+ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
+                               const void *state_batch_indices, const void *cu_tokens,
+                               const uint8_t *fresh, const uint16_t *q, const uint16_t *k,
+                               const uint16_t *v, const uint16_t *dt, const float *dt_bias,
+                               const float *A, const uint16_t *b, uint16_t *out,
+                               const ssu_shape_t *shape, const ssu_delta_strides_t *strides,
+                               int64_t tokens, float scale, float qk_eps, void *workspace,
+                               int64_t workspace_bytes, ssu_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * What stands before every mixer: the residual's addition and RMS norm, into bf16 or into e4m3
+ * with scales for an 8-bit product.
+ */
+
+/* Element types of a residual and of a norm's output. */
+typedef enum { SSU_RESIDUAL_BF16 = 0, SSU_RESIDUAL_F32 = 1 } ssu_residual_dtype_t;
+typedef enum { SSU_NORM_BF16 = 0, SSU_NORM_E4M3 = 1 } ssu_norm_dtype_t;
+
+/* Sizes, types and element strides of one ssu_add_norm call. */
+typedef struct {
+    int64_t tokens;          /* 0 is valid and enqueues nothing; at most 2^31 - 1 */
+    int64_t width;           /* columns: a multiple of 8, 8 .. 32768 */
+    int64_t group;           /* columns per scale: 32, 64, 128 or 256, or width; width must be a
+                                multiple of it.  Not looked at for a bf16 output */
+    int32_t residual_dtype;  /* ssu_residual_dtype_t; not looked at without a residual */
+    int32_t out_dtype;       /* ssu_norm_dtype_t */
+    int64_t x, residual, out; /* token strides: multiples of 8 (residual and out: >= width) */
+    int64_t scales[2];       /* token, group; distinct places */
+} ssu_norm_args_t;
+
+/*
+ * For every token t, in fp32 and rounded once,
+ *
+ *     r[i] = x[t,i] + residual[t,i];   residual[t,i] = r[i]
+ *     y[i] = r[i] / sqrt(mean_j r[j]^2 + eps) * weight[i]
+ *     out[t,i] = bf16_rne(y[i])        or, for e4m3 and every group of columns,
+ *     scales[t,c] = max(max_i |y[i]| / 448, 2^-126);   out[t,i] = e4m3_rne(y[i] / scales[t,c])
+ *
+ * The norm is that of the sum in fp32, not of what a bf16 residual keeps of it.  residual may be
+ * NULL (r = x).  x, residual, out and weight [width] fp32 are 16-byte aligned (an e4m3 out 8-byte).
+ * out may be x itself (bf16, same strides); nothing else may overlap.  A NaN or infinity in a
+ * token makes that token's scales and outputs NaN or what the formula gives, and no other's.
+ * Enqueued on `stream`; allocates and synchronises nothing.
+ */
+ssu_status_t ssu_add_norm(ssu_handle_t handle, const uint16_t *x, void *residual,
+                          const float *weight, void *out, float *scales,
+                          const ssu_norm_args_t *args, float eps, ssu_stream_t stream);
+
 /*
  * Allocation-free variant of ssu_update.  No counterpart exists in the paper: it serves
  * callers that cannot call cudaMalloc, such as code running under an allocator that must not

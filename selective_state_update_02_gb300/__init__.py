@@ -38,6 +38,12 @@ SSU_INDEX_I64 = 1
 SSU_STATE_F32 = 0
 SSU_STATE_BF16 = 1
 
+SSU_RESIDUAL_BF16 = 0
+SSU_RESIDUAL_F32 = 1
+
+SSU_NORM_BF16 = 0
+SSU_NORM_E4M3 = 1
+
 SSU_MODE_AUTO = 0
 SSU_MODE_VEC = 1
 
@@ -108,6 +114,18 @@ class ssu_attend_strides_t(ctypes.Structure):
                 ("v_pages", _i64 * 3), ("page_table", _i64 * 2), ("lengths", _i64)]
 
 
+class ssu_delta_strides_t(ctypes.Structure):
+    _fields_ = [("state", _i64 * 3), ("q", _i64 * 2), ("k", _i64 * 2), ("v", _i64 * 2),
+                ("out", _i64 * 2), ("dt", _i64 * 2), ("b", _i64 * 2), ("dt_bias", _i64),
+                ("A", _i64), ("idx", _i64)]
+
+
+class ssu_norm_args_t(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("width", _i64), ("group", _i64),
+                ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("x", _i64),
+                ("residual", _i64), ("out", _i64), ("scales", _i64 * 2)]
+
+
 class SsuError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status
@@ -144,6 +162,11 @@ _EXPORTS = {
     "ssu_rotate_qk": (ctypes.c_int, [_vp] * 14 + [ctypes.c_float, _vp]),
     "ssu_attend_workspace_bytes": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_i64)]),
     "ssu_attend": (ctypes.c_int, [_vp] * 9 + [ctypes.c_float, _i64, _i64, _vp, _i64, _vp]),
+    "ssu_delta_update": (ctypes.c_int, [_vp] * 13 + [ctypes.c_float, ctypes.c_float, _vp]),
+    "ssu_delta_workspace_bytes": (ctypes.c_int, [_vp, _vp, _i64, ctypes.POINTER(_i64)]),
+    "ssu_delta_prompts": (ctypes.c_int, [_vp] * 15 + [_i64, ctypes.c_float, ctypes.c_float, _vp,
+                                                      _i64, _vp]),
+    "ssu_add_norm": (ctypes.c_int, [_vp] * 7 + [ctypes.c_float, _vp]),
     "ssu_copy_blocks": (ctypes.c_int, [_vp, ctypes.POINTER(ssu_block_tensor_t), ctypes.c_int32,
                                        _vp, _vp, ctypes.c_int64, ctypes.c_int32, _vp]),
     "ssu_copy_set_launch": (ctypes.c_int, [_vp, ctypes.POINTER(ssu_copy_launch_t)]),
@@ -473,7 +496,7 @@ def ssu_update_tokens(handle: int, state_pool, state_batch_indices, x, dt, dt_bi
                                    ctypes.byref(ts), _stream_ptr(stream)), "ssu_update_tokens")
 
 
-# ---- prompts and attention ---------------------------------------------------------------
+# ---- prompts, attention, the delta rule and norms ------------------------------------------
 #
 # These calls are often shorter on the device than their marshalling from Python would be, so
 # _marshal.so (csrc/ssu_marshal.cpp) looks at the tensors, checks them and calls the C entry points.
@@ -500,7 +523,8 @@ def _calls():
                                f"{_build.marshal_wants()}: build it again")
         module = importlib.import_module(f"{__name__}._marshal")
         module.bind(*(ctypes.cast(getattr(lib(), name), _vp).value
-                      for name in ("ssu_update_prompts", "ssu_rotate_qk", "ssu_attend")))
+                      for name in ("ssu_update_prompts", "ssu_rotate_qk", "ssu_attend",
+                                   "ssu_delta_update", "ssu_delta_prompts", "ssu_add_norm")))
         _bound = module
     return _bound
 
@@ -514,12 +538,16 @@ def _stream_on(t, stream) -> int:
 
 def ssu_prompts_workspace_bytes(handle: int, state_pool, x, B, state_batch_indices) -> int:
     """Device workspace bytes ``ssu_update_prompts`` needs for these operands' sizes."""
+    return _prompt_workspace("ssu_prompts_workspace_bytes", handle, state_pool, x, B,
+                             state_batch_indices)
+
+
+def _prompt_workspace(query: str, handle: int, state_pool, x, B, state_batch_indices) -> int:
     pool, H, P, N = state_pool.shape
     shape = ssu_shape_t(state_batch_indices.shape[0], H, P, N, B.shape[1], pool, SSU_INDEX_I32,
                         _STATE_TYPE.get(state_pool.dtype, SSU_STATE_F32))
     n = _i64()
-    _check(lib().ssu_prompts_workspace_bytes(handle, ctypes.byref(shape), x.shape[0],
-                                             ctypes.byref(n)), "ssu_prompts_workspace_bytes")
+    _check(getattr(lib(), query)(handle, ctypes.byref(shape), x.shape[0], ctypes.byref(n)), query)
     return int(n.value)
 
 
@@ -572,6 +600,53 @@ def ssu_attend(handle: int, q, k_pages, v_pages, page_table, lengths, out, works
                          window, sinks, _stream_on(q, stream))
     if st:
         _check(st, "ssu_attend")
+
+
+def ssu_delta_update(handle: int, state_pool, state_batch_indices, q, k, v, dt, dt_bias, A, b,
+                     out, scale: float | None = None, qk_eps: float | None = 1e-6,
+                     stream=None) -> None:
+    """The gated delta rule for one new token per request: ``q`` and ``k`` ``[bs, G, N]``, ``v``
+    and ``out`` ``[bs, H, P]``, ``dt`` and ``b`` (the gate before its sigmoid) ``[bs, H]`` bf16,
+    ``dt_bias`` and ``A`` ``[H]`` fp32, the state in slots of ``state_pool`` ``[pool, H, P, N]``.
+    ``q`` and ``k`` are brought to length one, with ``qk_eps`` added to their sums of squares
+    (None: left as they are), and ``q`` scaled by ``scale`` (default ``N ** -0.5``)."""
+    st = _calls().delta_update(handle, state_pool, state_batch_indices, q, k, v, dt, dt_bias, A, b,
+                               out, scale, qk_eps, _stream_on(v, stream))
+    if st:
+        _check(st, "ssu_delta_update")
+
+
+def ssu_delta_workspace_bytes(handle: int, state_pool, v, k, state_batch_indices) -> int:
+    """Device workspace bytes ``ssu_delta_prompts`` needs for these operands' sizes."""
+    return _prompt_workspace("ssu_delta_workspace_bytes", handle, state_pool, v, k,
+                             state_batch_indices)
+
+
+def ssu_delta_prompts(handle: int, state_pool, state_batch_indices, cu_tokens, q, k, v, dt,
+                      dt_bias, A, b, out, workspace=None, fresh=None, scale: float | None = None,
+                      qk_eps: float | None = 1e-6, stream=None) -> None:
+    """The gated delta rule over packed prompts: prompt ``i`` is rows
+    ``cu_tokens[i]:cu_tokens[i + 1]`` of ``q`` and ``k`` ``[tokens, G, N]``, ``v`` and ``out``
+    ``[tokens, H, P]``, ``dt`` and ``b`` ``[tokens, H]``; it continues its slot, or starts from
+    zero where ``fresh[i]`` (uint8 or bool) is set, and leaves its last state there.  The other
+    operands as for ``ssu_delta_update``; ``workspace`` is a device uint8 tensor of
+    ``ssu_delta_workspace_bytes``."""
+    st = _calls().delta_prompts(handle, state_pool, state_batch_indices, cu_tokens, q, k, v, dt,
+                                dt_bias, A, b, out, workspace, fresh, scale, qk_eps,
+                                _stream_on(v, stream))
+    if st:
+        _check(st, "ssu_delta_prompts")
+
+
+def ssu_add_norm(handle: int, x, weight, out, residual=None, scales=None, eps: float = 1e-6,
+                 stream=None) -> None:
+    """RMS norm of ``x + residual`` times ``weight`` (fp32 ``[width]``), the sum back into
+    ``residual`` (bf16 or fp32 ``[tokens, width]``; None: of ``x`` alone).  ``out`` is bf16, or
+    float8_e4m3fn with fp32 ``scales`` ``[tokens, width / group]``: groups of 32, 64, 128 or 256
+    columns, or (one column of scales) the whole row."""
+    st = _calls().add_norm(handle, x, residual, weight, out, scales, eps, _stream_on(x, stream))
+    if st:
+        _check(st, "ssu_add_norm")
 
 
 def describe_blocks(tensors) -> tuple[ctypes.Array, int]:
@@ -654,6 +729,25 @@ class SelectiveStateUpdate:
                window=0, sinks=0, stream=None):
         ssu_attend(self.handle, q, k_pages, v_pages, page_table, lengths, out, workspace, scale,
                    window, sinks, stream)
+        return out
+
+    def delta(self, state_pool, state_batch_indices, q, k, v, dt, dt_bias, A, b, out, scale=None,
+              qk_eps=1e-6, stream=None):
+        ssu_delta_update(self.handle, state_pool, state_batch_indices, q, k, v, dt, dt_bias, A, b,
+                         out, scale, qk_eps, stream)
+        return out
+
+    def delta_workspace_bytes(self, state_pool, v, k, state_batch_indices) -> int:
+        return ssu_delta_workspace_bytes(self.handle, state_pool, v, k, state_batch_indices)
+
+    def delta_prompts(self, state_pool, state_batch_indices, cu_tokens, q, k, v, dt, dt_bias, A, b,
+                      out, workspace=None, fresh=None, scale=None, qk_eps=1e-6, stream=None):
+        ssu_delta_prompts(self.handle, state_pool, state_batch_indices, cu_tokens, q, k, v, dt,
+                          dt_bias, A, b, out, workspace, fresh, scale, qk_eps, stream)
+        return out
+
+    def add_norm(self, x, weight, out, residual=None, scales=None, eps=1e-6, stream=None):
+        ssu_add_norm(self.handle, x, weight, out, residual, scales, eps, stream)
         return out
 
     def copy_blocks(self, tensors, src_idx, dst_idx, stream=None):

@@ -16,12 +16,12 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 SOURCES = [CSRC / "ssu.cu", CSRC / "ssu_tokens.cu", CSRC / "ssu_copy.cu",
            CSRC / "ssu_prompt.cu", CSRC / "ssu_rotate.cu", CSRC / "ssu_attend.cu",
-           CSRC / "ssu_host.cpp"]
+           CSRC / "ssu_delta.cu", CSRC / "ssu_norm.cu", CSRC / "ssu_host.cpp"]
 HEADERS = [ROOT / "include" / "ssu.h", CSRC / "ssu_device.cuh", CSRC / "ssu_host.h",
            CSRC / "ssu_vec.cuh", CSRC / "ssu_stage.cuh",
            CSRC / "ssu_tokens.cuh", CSRC / "ssu_tokens_mma.cuh",
            CSRC / "ssu_prompt.cuh", CSRC / "ssu_prompt_mma.cuh",
-           CSRC / "ssu_attend.cuh"]
+           CSRC / "ssu_attend.cuh", CSRC / "ssu_delta.cuh"]
 OBJDIR = PKG / "_build"
 LIB = PKG / "libssu.so"
 MARSHAL_SOURCE = CSRC / "ssu_marshal.cpp"
@@ -117,8 +117,8 @@ def _start_marshal(out: Path) -> subprocess.Popen | None:
 
 def build(force: bool = False, extra: list[str] | None = None) -> Path:
     """Compile libssu.so and _marshal.so next to this file unless they are up to date.  nvcc alone is
-    enough for libssu.so, which the C ABI and every call but the prompt, rotation and attention
-    calls of the Python binding are content with: where _marshal.so cannot be built (it needs
+    enough for libssu.so, which the C ABI and every call but the prompt, rotation, attention,
+    delta-rule and norm calls of the Python binding are content with: where _marshal.so cannot be built (it needs
     g++ and the headers of Python and torch), that is a warning."""
     library, binding = force or _library_stale(), force or _marshal_stale()
     tmp = MARSHAL.with_name(f"_marshal.so.tmp{os.getpid()}")
@@ -136,6 +136,6 @@ def build(force: bool = False, extra: list[str] | None = None) -> Path:
             tmp.unlink(missing_ok=True)
             MARSHAL.unlink(missing_ok=True)  # what is there is of other sources
     if binding and not built:
-        warnings.warn("_marshal.so could not be built: the prompt, rotation and attention calls are "
-                      "not available from Python", stacklevel=2)
+        warnings.warn("_marshal.so could not be built: the prompt, rotation, attention, delta-rule "
+                      "and norm calls are not available from Python", stacklevel=2)
     return LIB

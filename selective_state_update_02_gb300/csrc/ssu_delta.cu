@@ -1,0 +1,236 @@
+// The gated delta rule: the C entry points ssu_delta_update, ssu_delta_workspace_bytes and
+// ssu_delta_prompts (validation, choice of form) and the kernels' instantiations.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "ssu.h"
+#include "ssu_delta.cuh"
+#include "ssu_host.h"
+
+using ssu_host::aligned;
+using ssu_host::DeviceGuard;
+using ssu_host::fail;
+using ssu_host::ok;
+using ssu_host::validate_batch;
+using ssu_host::validate_shape;
+
+namespace {
+
+struct DeltaOperands {
+    void *state_pool;
+    const void *idx;
+    const uint16_t *q, *k, *v, *dt, *b;
+    const float *dt_bias, *A;
+    uint16_t *out;
+};
+
+ssu_status_t validate_delta(const DeltaOperands &o, const ssu_shape_t *shape,
+                            const ssu_delta_strides_t *strides, float scale, float eps) {
+    if (!shape || !strides)
+        return fail(SSU_ERR_INVALID_ARG, "shape and strides must not be NULL");
+    const ssu_shape_t &s = *shape;
+    const ssu_delta_strides_t &u = *strides;
+    const ssu_status_t sizes = validate_shape(s);
+    if (sizes != SSU_OK) return sizes;
+    if (!(scale == scale) || scale - scale != 0.0f)
+        return fail(SSU_ERR_INVALID_ARG, "scale must be finite");
+    if (!(eps == eps)) return fail(SSU_ERR_INVALID_ARG, "qk_eps must not be NaN");
+    if (s.batch == 0) return ok();
+    const int64_t all[] = {u.state[0], u.state[1], u.state[2], u.q[0], u.q[1], u.k[0], u.k[1],
+                           u.v[0], u.v[1], u.out[0], u.out[1], u.dt[0], u.dt[1], u.b[0], u.b[1],
+                           u.dt_bias, u.A, u.idx};
+    for (int64_t x : all)
+        if (x < 0) return fail(SSU_ERR_INVALID_ARG, "negative stride");
+    const int per16 = s.state_dtype == SSU_STATE_BF16 ? 8 : 4;
+    for (int j = 0; j < 3; ++j)
+        if (u.state[j] % per16)
+            return fail(SSU_ERR_MISALIGNED,
+                        "state stride %d (%lld elements) is not a multiple of 16 bytes", j,
+                        (long long)u.state[j]);
+    if (!o.state_pool || !o.idx || !o.q || !o.k || !o.v || !o.dt || !o.b || !o.dt_bias || !o.A ||
+        !o.out)
+        return fail(SSU_ERR_INVALID_ARG, "a data pointer is NULL");
+    if (!aligned(o.state_pool, 16))
+        return fail(SSU_ERR_MISALIGNED, "state_pool is not 16-byte aligned");
+    if (!aligned(o.idx, s.index_dtype == SSU_INDEX_I64 ? 8 : 4))
+        return fail(SSU_ERR_MISALIGNED, "state_batch_indices is not aligned to its type");
+    for (const void *ptr : {o.q, o.k, o.v, o.dt, o.b, static_cast<const uint16_t *>(o.out)})
+        if (!aligned(ptr, 2))
+            return fail(SSU_ERR_MISALIGNED, "a bf16 operand is not 2-byte aligned");
+    if (!aligned(o.dt_bias, 4) || !aligned(o.A, 4))
+        return fail(SSU_ERR_MISALIGNED, "an fp32 operand is not 4-byte aligned");
+    return validate_batch(s);
+}
+
+DeltaParams delta_params(const ssu_handle_s &handle, const DeltaOperands &o, const ssu_shape_t &s,
+                         const ssu_delta_strides_t &u, float scale, float eps) {
+    DeltaParams d{};
+    SsuParams &p = d.m.p;
+    auto bf = [](const uint16_t *t) { return reinterpret_cast<const __nv_bfloat16 *>(t); };
+    p.state = o.state_pool, p.idx = o.idx;
+    p.x = bf(o.v), p.B = bf(o.k), p.C = bf(o.q), p.dt = bf(o.dt), d.beta = bf(o.b);
+    p.dt_bias = o.dt_bias, p.A = o.A;
+    p.out = reinterpret_cast<__nv_bfloat16 *>(o.out);
+    p.st_pool = u.state[0], p.st_head = u.state[1], p.st_row = u.state[2];
+    p.x_b = u.v[0], p.x_h = u.v[1], p.out_b = u.out[0], p.out_h = u.out[1];
+    p.dt_b = u.dt[0], p.dt_h = u.dt[1], d.beta_t = u.b[0], d.beta_h = u.b[1];
+    p.B_b = u.k[0], p.B_g = u.k[1], p.C_b = u.q[0], p.C_g = u.q[1];
+    p.bias_h = u.dt_bias, p.A_h = u.A, p.idx_s = u.idx;
+    p.pool_size = s.pool_size, p.batch = s.batch;
+    p.nheads = static_cast<int>(s.nheads), p.headdim = static_cast<int>(s.headdim);
+    p.heads_per_group = static_cast<int>(s.nheads / s.ngroups);
+    p.group_magic = group_magic(static_cast<unsigned>(p.heads_per_group));
+    p.err = handle.err;
+    const int epv = s.state_dtype == SSU_STATE_BF16 ? 8 : 4;
+    d.m.bc_vec = aligned(o.k, 2 * epv) && p.B_b % epv == 0 && p.B_g % epv == 0 &&
+                 aligned(o.q, 2 * epv) && p.C_b % epv == 0 && p.C_g % epv == 0;
+    d.scale = scale, d.eps = eps;
+    return d;
+}
+
+// Launches `kernel` with a warp per kRows rows of a head, up to four warps to a CTA.
+template <int kRows, typename Kernel>
+cudaError_t launch_rows(Kernel *kernel, DeltaParams d, bool pdl, cudaStream_t st) {
+    SsuParams &p = d.m.p;
+    int warps = 4;
+    while (warps > 1 && kRows * (warps / 2) >= p.headdim) warps >>= 1;
+    p.rows_per_cta = kRows * warps;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.headdim + p.rows_per_cta - 1) / p.rows_per_cta),
+                       static_cast<unsigned>(p.nheads),
+                       static_cast<unsigned>(p.batch < 65535 ? p.batch : 65535));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, d);
+}
+
+template <int N, typename ST, bool kIdx64>
+cudaError_t launch_step(const DeltaParams &d, bool pdl, cudaStream_t st) {
+    constexpr int kSlots = RowGeo<N, ST>::L / 4;
+    return launch_rows<kSlots * RowGeo<N, ST>::RPI>(ssu_delta_step_kernel<kSlots, N, ST, kIdx64>, d,
+                                                    pdl, st);
+}
+
+constexpr int kSeqSlots = 4;
+
+template <int N, typename ST, bool kIdx64>
+cudaError_t launch_seq(const DeltaParams &d, bool pdl, cudaStream_t st) {
+    return launch_rows<kSeqSlots * RowGeo<N, ST>::RPI>(
+        ssu_delta_seq_kernel<kSeqSlots, N, ST, kIdx64>, d, pdl, st);
+}
+
+// `launch` (a generic functor of dstate, state and index type) at the call's types.
+template <typename F>
+cudaError_t dispatch(const ssu_shape_t &s, F launch) {
+    const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
+    auto typed = [&](auto n) {
+        if (bf16)
+            return i64 ? launch(n, __nv_bfloat16(), std::true_type())
+                       : launch(n, __nv_bfloat16(), std::false_type());
+        return i64 ? launch(n, float(), std::true_type()) : launch(n, float(), std::false_type());
+    };
+    if (s.dstate == 64) return typed(std::integral_constant<int, 64>());
+    if (s.dstate == 128) return typed(std::integral_constant<int, 128>());
+    return typed(std::integral_constant<int, 256>());
+}
+
+ssu_status_t validate_tokens(int64_t tokens) {
+    if (tokens < 0 || tokens > INT_MAX)
+        return fail(SSU_ERR_INVALID_ARG, "tokens %lld outside 0..2^31 - 1", (long long)tokens);
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
+                              const void *state_batch_indices, const uint16_t *q,
+                              const uint16_t *k, const uint16_t *v, const uint16_t *dt,
+                              const float *dt_bias, const float *A, const uint16_t *b,
+                              uint16_t *out, const ssu_shape_t *shape,
+                              const ssu_delta_strides_t *strides, float scale, float qk_eps,
+                              ssu_stream_t stream) {
+    if (!handle) return fail(SSU_ERR_INVALID_ARG, "NULL handle");
+    const DeltaOperands o = {state_pool, state_batch_indices, q, k, v, dt, b, dt_bias, A, out};
+    const ssu_status_t st = validate_delta(o, shape, strides, scale, qk_eps);
+    if (st != SSU_OK || shape->batch == 0) return st;
+    const DeltaParams d = delta_params(*handle, o, *shape, *strides, scale, qk_eps);
+    DeviceGuard guard(handle->device);
+    if (guard.err != cudaSuccess)
+        return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dispatch(*shape, [&](auto n, auto st, auto i64) {
+        return launch_step<decltype(n)::value, decltype(st), decltype(i64)::value>(d, handle->pdl,
+                                                                                 cs);
+    });
+    if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
+                                       int64_t tokens, int64_t *bytes) {
+    if (!handle || !shape || !bytes) return fail(SSU_ERR_INVALID_ARG, "NULL argument");
+    ssu_status_t st = validate_shape(*shape);
+    if (st == SSU_OK) st = validate_batch(*shape);
+    if (st == SSU_OK) st = validate_tokens(tokens);
+    if (st != SSU_OK) return st;
+    *bytes = 0;
+    return ok();
+}
+
+ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
+                               const void *state_batch_indices, const void *cu_tokens,
+                               const uint8_t *fresh, const uint16_t *q, const uint16_t *k,
+                               const uint16_t *v, const uint16_t *dt, const float *dt_bias,
+                               const float *A, const uint16_t *b, uint16_t *out,
+                               const ssu_shape_t *shape, const ssu_delta_strides_t *strides,
+                               int64_t tokens, float scale, float qk_eps, void *workspace,
+                               int64_t workspace_bytes, ssu_stream_t stream) {
+    if (!handle) return fail(SSU_ERR_INVALID_ARG, "NULL handle");
+    ssu_status_t st = validate_tokens(tokens);
+    if (st != SSU_OK) return st;
+    if (tokens == 0) {  // no token row is read: the operands may be empty arrays
+        static const uint16_t none[2] = {};
+        q = k = v = dt = b = none;
+        out = const_cast<uint16_t *>(none);
+    }
+    const DeltaOperands o = {state_pool, state_batch_indices, q, k, v, dt, b, dt_bias, A, out};
+    st = validate_delta(o, shape, strides, scale, qk_eps);
+    if (st != SSU_OK || shape->batch == 0) return st;
+    const ssu_shape_t &s = *shape;
+    if (!cu_tokens) return fail(SSU_ERR_INVALID_ARG, "cu_tokens is NULL");
+    if (!aligned(cu_tokens, s.index_dtype == SSU_INDEX_I64 ? 8 : 4))
+        return fail(SSU_ERR_MISALIGNED, "cu_tokens is not aligned to its type");
+    int64_t need = 0;
+    st = ssu_delta_workspace_bytes(handle, shape, tokens, &need);
+    if (st != SSU_OK) return st;
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(SSU_ERR_INVALID_ARG, "workspace holds %lld bytes; this shape needs %lld",
+                    (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    if (need && !aligned(workspace, 256))
+        return fail(SSU_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+    DeltaParams d = delta_params(*handle, o, s, *strides, scale, qk_eps);
+    d.m.cu = cu_tokens, d.m.fresh = fresh, d.m.tokens = tokens;
+    DeviceGuard guard(handle->device);
+    if (guard.err != cudaSuccess)
+        return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dispatch(s, [&](auto n, auto st, auto i64) {
+        return launch_seq<decltype(n)::value, decltype(st), decltype(i64)::value>(d, handle->pdl,
+                                                                                cs);
+    });
+    if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
-// Marshalling of the prompt, rotation and attention calls from Python: one look at every tensor,
-// the ABI's structs, and the C entry points by the addresses that bind() was given.
+// Marshalling of the prompt, rotation, attention, delta-rule and norm calls from Python: one look at
+// every tensor, the ABI's structs, and the C entry points by the addresses that bind() was given.
 //
 // These calls sit in a serving loop beside the decode step and are often shorter on the device than
 // their marshalling: attribute by attribute from Python it took 7.3 us of a rotation's call (a
@@ -27,6 +27,9 @@ using at::Tensor;
 decltype(&ssu_update_prompts) update_prompts_fn;
 decltype(&ssu_rotate_qk) rotate_qk_fn;
 decltype(&ssu_attend) attend_fn;
+decltype(&ssu_delta_update) delta_update_fn;
+decltype(&ssu_delta_prompts) delta_prompts_fn;
+decltype(&ssu_add_norm) add_norm_fn;
 
 struct Refusal {
     PyObject *type;
@@ -170,6 +173,22 @@ long call(F entry, Args... args) {
     return entry(args...);
 }
 
+void check_offsets(const Tensor &cu, const Tensor &slots) {
+    if (cu.size(0) != slots.size(0) + 1 || !cu.is_contiguous())
+        refuse("cu_tokens must be contiguous with " + std::to_string(slots.size(0) + 1) +
+               " entries");
+}
+
+const uint8_t *fresh_of(PyObject *o, const Tensor &slots, int device) {
+    if (o == Py_None) return nullptr;
+    const Tensor &f = tensor(o, "fresh");
+    if ((f.scalar_type() != at::kByte && f.scalar_type() != at::kBool) ||
+        f.sizes() != slots.sizes() || !f.is_contiguous() || !f.is_cuda() ||
+        f.get_device() != device)
+        refuse("fresh must be a contiguous uint8 or bool CUDA tensor with one entry per prompt");
+    return at_device<uint8_t>(f);
+}
+
 // handle, state_pool, state_batch_indices, cu_tokens, x, dt, dt_bias, A, B, C, D, out, workspace,
 // fresh, stream
 PyObject *update_prompts(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -192,20 +211,10 @@ PyObject *update_prompts(PyObject *, PyObject *const *a, Py_ssize_t n) {
             shaped(dt, "dt", {T, H});
         else
             shaped(dt, "dt", {T, H, P});
-        if (cu.size(0) != bs + 1 || !cu.is_contiguous())
-            refuse("cu_tokens must be contiguous with " + std::to_string(bs + 1) + " entries");
+        check_offsets(cu, slots);
         const int device = device_of(
             {&pool, &slots, &cu, &x, &dt, &dt_bias, &A, &B, &C, &D, &out});
-        const uint8_t *fresh = nullptr;
-        if (a[13] != Py_None) {
-            const Tensor &f = tensor(a[13], "fresh");
-            if ((f.scalar_type() != at::kByte && f.scalar_type() != at::kBool) ||
-                f.sizes() != slots.sizes() || !f.is_contiguous() || !f.is_cuda() ||
-                f.get_device() != device)
-                refuse("fresh must be a contiguous uint8 or bool CUDA tensor with one entry per "
-                       "prompt");
-            fresh = at_device<uint8_t>(f);
-        }
+        const uint8_t *fresh = fresh_of(a[13], slots, device);
         const ssu_shape_t shape = {bs, H, P, N, G, pool.size(0), index_dtype(cu),
                                    pool.scalar_type() == at::kFloat ? SSU_STATE_F32
                                                                     : SSU_STATE_BF16};
@@ -322,12 +331,148 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// Addresses of ssu_update_prompts, ssu_rotate_qk and ssu_attend.
+// The operands that both delta-rule calls have, and their structs.
+struct Delta {
+    const Tensor &pool, &slots, &q, &k, &v, &dt, &dt_bias, &A, &b, &out;
+    ssu_shape_t shape;
+    ssu_delta_strides_t st;
+    int64_t tokens;
+    int device;
+    float scale, eps;
+};
+
+// `a` holds q, k, v, dt, dt_bias, A, b, out; requests: the tokens where each is one.
+Delta delta_operands(const Tensor &pool, const Tensor &slots, PyObject *const *a, PyObject *scale,
+                     PyObject *eps, bool one_each) {
+    Delta d{pool, slots, bf16(a[0], "q", 3), bf16(a[1], "k", 3), bf16(a[2], "v", 3),
+            bf16(a[3], "dt", 2), fp32(a[4], "dt_bias", 1, 1), fp32(a[5], "A", 1, 1),
+            bf16(a[6], "b", 2), bf16(a[7], "out", 3), {}, {}, 0, 0, 0.0f, 0.0f};
+    const int64_t H = pool.size(1), P = pool.size(2), N = pool.size(3), G = d.q.size(1);
+    d.tokens = one_each ? slots.size(0) : d.q.size(0);
+    shaped(d.q, "q", {d.tokens, G, N});
+    shaped(d.k, "k", {d.tokens, G, N});
+    shaped(d.v, "v", {d.tokens, H, P});
+    shaped(d.out, "out", {d.tokens, H, P});
+    shaped(d.dt, "dt", {d.tokens, H});
+    shaped(d.b, "b", {d.tokens, H});
+    shaped(d.dt_bias, "dt_bias", {H});
+    shaped(d.A, "A", {H});
+    if (pool.stride(3) != 1 || d.q.stride(2) != 1 || d.k.stride(2) != 1 || d.v.stride(2) != 1 ||
+        d.out.stride(2) != 1)
+        refuse("the last dimension of state_pool, q, k, v and out must have stride 1");
+    d.device = device_of({&pool, &slots, &d.q, &d.k, &d.v, &d.dt, &d.dt_bias, &d.A, &d.b, &d.out});
+    d.shape = {slots.size(0), H, P, N, G, pool.size(0), index_dtype(slots),
+               pool.scalar_type() == at::kFloat ? SSU_STATE_F32 : SSU_STATE_BF16};
+    strides_of(pool, 3, d.st.state);
+    strides_of(d.q, 2, d.st.q);
+    strides_of(d.k, 2, d.st.k);
+    strides_of(d.v, 2, d.st.v);
+    strides_of(d.out, 2, d.st.out);
+    strides_of(d.dt, 2, d.st.dt);
+    strides_of(d.b, 2, d.st.b);
+    d.st.dt_bias = d.dt_bias.stride(0);
+    d.st.A = d.A.stride(0);
+    d.st.idx = slots.stride(0);
+    d.scale = static_cast<float>(scale == Py_None ? 1.0 / std::sqrt(static_cast<double>(N))
+                                                  : PyFloat_AsDouble(scale));
+    d.eps = eps == Py_None ? -1.0f : static_cast<float>(PyFloat_AsDouble(eps));
+    return d;
+}
+
+// handle, state_pool, state_batch_indices, q, k, v, dt, dt_bias, A, b, out, scale, qk_eps, stream
+PyObject *delta_update(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const Tensor &pool = operand(a[1], "state_pool", at::kFloat, at::kBFloat16, 4, 4);
+        const Delta d =
+            delta_operands(pool, index(a[2], "state_batch_indices", 1), a + 3, a[11], a[12], true);
+        auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
+        auto *stream = static_cast<ssu_stream_t>(pointer(a[13]));
+        return call(delta_update_fn, handle, at_device(pool), at_device(d.slots), bits(d.q),
+                    bits(d.k), bits(d.v), bits(d.dt), at_device<float>(d.dt_bias),
+                    at_device<float>(d.A), bits(d.b), bits(d.out), &d.shape, &d.st, d.scale, d.eps,
+                    stream);
+    });
+}
+
+// handle, state_pool, state_batch_indices, cu_tokens, q, k, v, dt, dt_bias, A, b, out, workspace,
+// fresh, scale, qk_eps, stream
+PyObject *delta_prompts(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 17, [&] {
+        const Tensor &pool = operand(a[1], "state_pool", at::kFloat, at::kBFloat16, 4, 4);
+        const Tensor &cu = index(a[3], "cu_tokens", 1);
+        const Delta d = delta_operands(pool, index_like(a[2], "state_batch_indices", 1, cu), a + 4,
+                                       a[14], a[15], false);
+        check_offsets(cu, d.slots);
+        device_of({&d.slots, &cu});
+        const uint8_t *fresh = fresh_of(a[13], d.slots, d.device);
+        const Workspace w = workspace(a[12], d.device);
+        auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
+        auto *stream = static_cast<ssu_stream_t>(pointer(a[16]));
+        return call(delta_prompts_fn, handle, at_device(pool), at_device(d.slots), at_device(cu),
+                    fresh, bits(d.q), bits(d.k), bits(d.v), bits(d.dt),
+                    at_device<float>(d.dt_bias), at_device<float>(d.A), bits(d.b), bits(d.out),
+                    &d.shape, &d.st, d.tokens, d.scale, d.eps, w.at, w.bytes, stream);
+    });
+}
+
+// handle, x, residual, weight, out, scales, eps, stream
+PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const Tensor &x = bf16(a[1], "x", 2), &weight = fp32(a[3], "weight", 1, 1);
+        const Tensor &out = operand(a[4], "out", at::kBFloat16, at::kFloat8_e4m3fn, 2, 2);
+        const bool e4m3 = out.scalar_type() == at::kFloat8_e4m3fn;
+        const int64_t T = x.size(0), W = x.size(1);
+        shaped(out, "out", {T, W});
+        shaped(weight, "weight", {W});
+        if (x.stride(1) != 1 || out.stride(1) != 1 || weight.stride(0) != 1)
+            refuse("the last dimension of x, weight and out must have stride 1");
+        device_of({&x, &weight, &out});
+        ssu_norm_args_t args{};
+        args.tokens = T, args.width = W;
+        args.out_dtype = e4m3 ? SSU_NORM_E4M3 : SSU_NORM_BF16;
+        args.x = x.stride(0), args.out = out.stride(0);
+        void *residual = nullptr;
+        if (a[2] != Py_None) {
+            const Tensor &r = operand(a[2], "residual", at::kBFloat16, at::kFloat, 2, 2);
+            shaped(r, "residual", {T, W});
+            if (r.stride(1) != 1) refuse("the last dimension of residual must have stride 1");
+            device_of({&x, &r});
+            args.residual = r.stride(0);
+            args.residual_dtype =
+                r.scalar_type() == at::kFloat ? SSU_RESIDUAL_F32 : SSU_RESIDUAL_BF16;
+            residual = at_device(r);
+        }
+        float *scales = nullptr;
+        if (e4m3 != (a[5] != Py_None))
+            refuse("an e4m3 out needs scales, and a bf16 out has none");
+        if (e4m3) {
+            const Tensor &s = fp32(a[5], "scales", 2, 2);
+            if (s.size(1) < 1 || W % s.size(1))
+                refuse("scales must have one column for every equal group of x's columns, got " +
+                       listed(s.sizes()));
+            shaped(s, "scales", {T, s.size(1)});
+            device_of({&x, &s});
+            args.group = W / s.size(1);
+            strides_of(s, 2, args.scales);
+            scales = at_device<float>(s);
+        }
+        const float eps = static_cast<float>(PyFloat_AsDouble(a[6]));
+        auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
+        auto *stream = static_cast<ssu_stream_t>(pointer(a[7]));
+        return call(add_norm_fn, handle, bits(x), residual, at_device<float>(weight),
+                    at_device(out), scales, &args, eps, stream);
+    });
+}
+
+// Addresses of the entry points, in the order below.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 3, [&] {
+    return guarded(n, 6, [&] {
         update_prompts_fn = reinterpret_cast<decltype(update_prompts_fn)>(pointer(a[0]));
         rotate_qk_fn = reinterpret_cast<decltype(rotate_qk_fn)>(pointer(a[1]));
         attend_fn = reinterpret_cast<decltype(attend_fn)>(pointer(a[2]));
+        delta_update_fn = reinterpret_cast<decltype(delta_update_fn)>(pointer(a[3]));
+        delta_prompts_fn = reinterpret_cast<decltype(delta_prompts_fn)>(pointer(a[4]));
+        add_norm_fn = reinterpret_cast<decltype(add_norm_fn)>(pointer(a[5]));
         if (PyErr_Occurred()) throw Failed{};
         return 0L;
     });
@@ -340,7 +485,9 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {method<update_prompts>("update_prompts"), method<rotate_qk>("rotate_qk"),
-                         method<attend>("attend"), method<bind>("bind"),
+                         method<attend>("attend"), method<delta_update>("delta_update"),
+                         method<delta_prompts>("delta_prompts"), method<add_norm>("add_norm"),
+                         method<bind>("bind"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
