@@ -21,7 +21,8 @@ HEADERS = [ROOT / "include" / "ssu.h", CSRC / "ssu_device.cuh", CSRC / "ssu_host
            CSRC / "ssu_vec.cuh", CSRC / "ssu_stage.cuh",
            CSRC / "ssu_tokens.cuh", CSRC / "ssu_tokens_mma.cuh",
            CSRC / "ssu_prompt.cuh", CSRC / "ssu_prompt_mma.cuh",
-           CSRC / "ssu_attend.cuh", CSRC / "ssu_delta.cuh"]
+           CSRC / "ssu_attend.cuh", CSRC / "ssu_delta.cuh", CSRC / "ssu_delta_mma.cuh",
+           CSRC / "ssu_tc.cuh", CSRC / "ssu_tma.h"]
 OBJDIR = PKG / "_build"
 LIB = PKG / "libssu.so"
 MARSHAL_SOURCE = CSRC / "ssu_marshal.cpp"

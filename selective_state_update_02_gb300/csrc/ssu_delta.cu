@@ -9,7 +9,9 @@
 
 #include "ssu.h"
 #include "ssu_delta.cuh"
+#include "ssu_delta_mma.cuh"
 #include "ssu_host.h"
+#include "ssu_tma.h"
 
 using ssu_host::aligned;
 using ssu_host::DeviceGuard;
@@ -149,6 +151,97 @@ ssu_status_t validate_tokens(int64_t tokens) {
     return ok();
 }
 
+// ---- the chunked form ----------------------------------------------------------------
+
+// Where its arrays lie in the workspace.
+struct DeltaPlan {
+    long long chunks;  // the most that good prompts can have
+    long long order, prompts, list, records, total;
+};
+
+// Records past this (1.2 million tokens of 32 heads) leave a call to the token-by-token form.
+constexpr double kMostRecords = 3.2e10;
+
+bool mma_sizes(const ssu_shape_t &s, int64_t tokens) {
+    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 &&
+           (tokens / kDeltaChunk + static_cast<double>(s.batch)) * s.nheads *
+                   DeltaRecord::kBytes <= kMostRecords &&
+           s.batch * static_cast<double>(s.nheads) * ((s.headdim + kDeltaRows - 1) / kDeltaRows) <=
+               INT_MAX;
+}
+
+DeltaPlan delta_plan(const ssu_shape_t &s, int64_t tokens) {
+    auto up = [](long long bytes) { return (bytes + 255) / 256 * 256; };
+    DeltaPlan w;
+    w.chunks = tokens / kDeltaChunk + s.batch;
+    w.order = 256;
+    w.prompts = w.order + up(4ll * s.batch);
+    w.list = w.prompts + up(16ll * s.batch);
+    w.records = w.list + up(8ll * w.chunks);
+    w.total = w.records + w.chunks * s.nheads * DeltaRecord::kBytes;
+    return w;
+}
+
+// Operands that the chunked form can read: 16-byte rows for the tensor maps.
+bool mma_operands(const DeltaParams &d) {
+    const SsuParams &p = d.m.p;
+    if (!aligned(p.x, 16) || !aligned(p.B, 16) || !aligned(p.C, 16)) return false;
+    const long long strides[] = {p.x_b, p.x_h, p.B_b, p.B_g, p.C_b, p.C_g};
+    for (long long v : strides)
+        if (v % 8 != 0 || v >= (1ll << 38)) return false;
+    return true;
+}
+
+template <int N, typename ST, bool kIdx64>
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[3],
+                       ssu_handle_s &handle, cudaStream_t st) {
+    auto *prep = ssu_delta_prep_kernel<N>;
+    auto *main = ssu_delta_mma_kernel<N, ST, kIdx64>;
+    constexpr int kPrepBytes = PrepSmem<N>::kTotal, kBytes = DeltaSmem<N>::kTotal + 1024;
+    cudaError_t e =
+        ssu_host::allow_smem(handle, reinterpret_cast<const void *>(prep), kPrepBytes);
+    if (e == cudaSuccess)
+        e = ssu_host::allow_smem(handle, reinterpret_cast<const void *>(main), kBytes);
+    if (e != cudaSuccess) return e;
+    const SsuParams &p = m.d.m.p;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = handle.pdl ? 1 : 0;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    e = cudaLaunchKernelEx(&cfg, ssu_delta_plan_kernel<kIdx64>, m);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(w.chunks),
+                       static_cast<unsigned>(p.nheads / m.per_cta));
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.dynamicSmemBytes = kPrepBytes;
+    e = cudaLaunchKernelEx(&cfg, prep, m);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.nheads * m.slabs));
+    cfg.blockDim = dim3(kDeltaThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    return cudaLaunchKernelEx(&cfg, main, m, maps[0], maps[1], maps[2]);
+}
+
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[3],
+                       const ssu_shape_t &s, ssu_handle_s &handle, cudaStream_t st) {
+    const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
+#define SSU_MMA(N_, ST_)                                              \
+    return i64 ? launch_mma<N_, ST_, true>(m, w, maps, handle, st)    \
+               : launch_mma<N_, ST_, false>(m, w, maps, handle, st)
+    if (s.dstate == 64) {
+        if (bf16) SSU_MMA(64, __nv_bfloat16);
+        SSU_MMA(64, float);
+    }
+    if (bf16) SSU_MMA(128, __nv_bfloat16);
+    SSU_MMA(128, float);
+#undef SSU_MMA
+}
+
 }  // namespace
 
 extern "C" {
@@ -184,7 +277,7 @@ ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *s
     if (st == SSU_OK) st = validate_batch(*shape);
     if (st == SSU_OK) st = validate_tokens(tokens);
     if (st != SSU_OK) return st;
-    *bytes = 0;
+    *bytes = mma_sizes(*shape, tokens) ? delta_plan(*shape, tokens).total : 0;
     return ok();
 }
 
@@ -225,7 +318,32 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
     if (guard.err != cudaSuccess)
         return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dispatch(s, [&](auto n, auto st, auto i64) {
+    cudaError_t e = cudaErrorNotSupported;
+    if (tokens > 0 && mma_sizes(s, tokens) && mma_operands(d)) {
+        const SsuParams &p = d.m.p;
+        const DeltaPlan w = delta_plan(s, tokens);
+        DeltaMmaParams m{};
+        m.d = d;
+        m.slabs = static_cast<int>((s.headdim + kDeltaRows - 1) / kDeltaRows);
+        // Heads of one key head share its products in the first pass where that leaves two CTAs
+        // per SM and more.
+        m.per_cta = 1;
+        while (m.per_cta < kPrepHeads && p.heads_per_group % (2 * m.per_cta) == 0 &&
+               w.chunks * (s.nheads / (2 * m.per_cta)) >= 2 * handle->sm_count)
+            m.per_cta *= 2;
+        char *const room = static_cast<char *>(workspace);
+        m.total = reinterpret_cast<int *>(room);
+        m.order = reinterpret_cast<int *>(room + w.order);
+        m.prompts = reinterpret_cast<int4 *>(room + w.prompts);
+        m.chunks = reinterpret_cast<int2 *>(room + w.list);
+        m.records = reinterpret_cast<unsigned char *>(room + w.records);
+        CUtensorMap maps[3];
+        if (encode_map(&maps[0], k, s.dstate, s.ngroups, tokens, p.B_g, p.B_b, kDeltaChunk) &&
+            encode_map(&maps[1], q, s.dstate, s.ngroups, tokens, p.C_g, p.C_b, kDeltaChunk) &&
+            encode_map(&maps[2], v, s.headdim, s.nheads, tokens, p.x_h, p.x_b, kDeltaChunk))
+            e = launch_mma(m, w, maps, s, *handle, cs);
+    }
+    if (e == cudaErrorNotSupported) e = dispatch(s, [&](auto n, auto st, auto i64) {
         return launch_seq<decltype(n)::value, decltype(st), decltype(i64)::value>(d, handle->pdl,
                                                                                 cs);
     });

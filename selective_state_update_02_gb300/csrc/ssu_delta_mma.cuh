@@ -1,0 +1,1017 @@
+// The gated delta rule over prompts in chunks, on the tcgen05 tensor cores (sm_103a), instantiated by
+// ssu_delta.cu beside the token-by-token kernel of ssu_delta.cuh.
+//
+// Mathematics.  Over a chunk of C = 64 tokens, with s_i the sum of the log decays up to token i, kn and
+// qn the keys and queries at length one, and S the state [P, N] that the chunk begins with:
+//
+//   L_ij = beta_i e^{s_i - s_j} (kn_i . kn_j)  for j < i;      T = (I + L)^-1
+//   U    = T R,  R_i = beta_i (v_i - e^{s_i} S kn_i)           (the corrections e_i of all tokens)
+//   y_i  = e^{s_i} S qn_i + sum_{j <= i} (kn_j . qn_i) e^{s_i - s_j} U_j
+//   S'   = e^{s_C} S + sum_j e^{s_C - s_j} U_j kn_j^T
+//
+// Three kernels.  A plan (one CTA) lists the chunks of all prompts.  A first pass, parallel over chunks
+// and heads, makes of keys and gates alone what a chunk needs beside its state: T, the masked M_ij =
+// (k_j . qn_i) e^{s_i - s_j} and the tokens' factors.  A second pass takes a head's state (128 of its
+// rows) through a prompt, chunk after chunk.
+//
+// The second pass holds everything transposed, with the state's 128 rows p as the MMA's M: then S, R
+// and U are first operands, which come from TMEM, where the thread that made a row puts it, and
+// the tiles of K, Q, T and M in shared memory, as they were copied, are the second ones:
+//
+//   S K^T [128 x 64],  S Q^T [128 x 64],  R T^T [128 x 64],  U M^T [128 x 64],  U K [128 x N]
+//
+// Two warpgroups share the rows' elementwise work, a thread holding half a row of S in registers.
+//
+// Precision.  States, statistics and sums are fp32.  K and Q are bf16 and exact (their lengths are
+// factors of tokens).  What decides the state enters as sums of bf16 parts: S, R and U three (24
+// bits; two for a state kept in bf16), T two (1 on its diagonal is exact, and its other elements to
+// 2^-17 are below the fp32 sums' own error).  The readout alone sees U and M rounded to bf16, once
+// each, and S to two parts.  T is worked out in fp32 by inverting blocks of 16 along the diagonal row by
+// row and joining them, T21 = -T22 L21 T11 (powers of L, as a product formula would have, grow
+// like binomials where keys are alike).
+//
+// A chunk with an infinity, a NaN or growing decays (a zero weight times such an element is NaN) is
+// taken token by token by the second pass, from the state in registers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ssu_delta.cuh"
+#include "ssu_tc.cuh"
+
+namespace {
+
+constexpr int kDeltaChunk = 64;  // tokens per chunk
+constexpr int kDeltaRows = 128;  // state rows per CTA: the MMA's M
+constexpr int kDeltaTile = kDeltaChunk * 128;  // 64 rows of 64 bf16
+
+// What the first pass leaves of a chunk for one head: T's two parts and M, as the tiles of an
+// operand, and the tokens' factors.
+struct DeltaRecord {
+    enum : int {
+        kT1 = 0,
+        kT2 = kDeltaTile,
+        kM = 2 * kDeltaTile,
+        kVec = 3 * kDeltaTile,
+        kBytes = kVec + 2048
+    };
+    enum : int {  // floats of kVec, 64 each
+        kBeta = 0,     // beta
+        kPast = 64,    // beta e^{s} / |k|: of S k in R
+        kLeft = 128,   // e^{s_C - s} / |k|: of U in the next state
+        kRead = 192,   // scale / |q|: of U M^T
+        kReadS = 256,  // scale / |q| e^{s}: of S q
+        kDecay = 320,  // the token's own decay
+        kKey = 384,    // 1 / |k|
+        kWhole = 448,  // e^{s_C}; then whether the chunk is to be taken token by token
+        kSlow = 449
+    };
+};
+
+struct DeltaMmaParams {
+    DeltaParams d;
+    int slabs;              // of 128 rows
+    int per_cta;            // heads per CTA of the first pass
+    int *total;             // chunks of the call
+    int *order;             // prompts, the longest first
+    int4 *prompts;          // good, first token, end, first chunk
+    int2 *chunks;           // first token, tokens
+    unsigned char *records;  // [chunk][head]
+};
+
+// ---- the plan ----------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanSorted = 1024;  // prompts up to which the longest come first
+
+// A prompt that begins before the end of a good one before it is a bad one too (offsets ran
+// backwards): chunks never outnumber tokens / 64 + batch, which the workspace has room for.
+template <bool kIdx64>
+__global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
+    const __grid_constant__ DeltaMmaParams m) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kWarps = kPlanThreads / 32;
+    __shared__ int warp_end[kWarps], warp_chunks[kWarps], firsts[kPlanThreads];
+    __shared__ int2 spans[kPlanThreads];
+    __shared__ int lengths[kPlanSorted];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const SsuParams &p = m.d.m.p;
+    int seen = 0, total = 0;  // the largest end and the chunks of the prompts before
+    for (long long b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+        const long long b = b0 + tid;
+        long long slot, lo = 0, hi = 0;
+        bool good = b < p.batch && load_prompt<kIdx64>(m.d.m, b, true, slot, lo, hi);
+        int end = good && lo < hi ? static_cast<int>(hi) : 0, most = end;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, most, x);
+            if (lane >= x) most = max(most, o);
+        }
+        if (lane == 31) warp_end[warp] = most;
+        __syncthreads();
+        int before = __shfl_up_sync(0xffffffffu, most, 1);
+        if (lane == 0) before = 0;
+        before = max(before, seen);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before = max(before, warp_end[w]);
+            seen = max(seen, warp_end[w]);
+        }
+        if (end && before > lo) {
+            good = false;
+            record_skip(p, b);
+        }
+        const int n = good ? static_cast<int>((hi - lo + kDeltaChunk - 1) / kDeltaChunk) : 0;
+        int incl = n;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += o;
+        }
+        if (lane == 31) warp_chunks[warp] = incl;
+        __syncthreads();
+        int first = total + incl - n;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) first += warp_chunks[w];
+            total += warp_chunks[w];
+        }
+        if (b < p.batch) {
+            m.prompts[b] = make_int4(good, static_cast<int>(lo), static_cast<int>(hi), first);
+            if (b < kPlanSorted) lengths[b] = good ? static_cast<int>(hi - lo) : -1;
+        }
+        firsts[tid] = first;
+        spans[tid] = n ? make_int2(static_cast<int>(lo), static_cast<int>(hi)) : make_int2(0, 0);
+        __syncthreads();
+        const int these = static_cast<int>(min(p.batch - b0, static_cast<long long>(kPlanThreads)));
+        for (int k = warp; k < these; k += kWarps) {
+            const int2 span = spans[k];
+            for (int i = lane; i < (span.y - span.x + kDeltaChunk - 1) / kDeltaChunk; i += 32) {
+                const int at = span.x + i * kDeltaChunk;
+                m.chunks[firsts[k] + i] = make_int2(at, min(kDeltaChunk, span.y - at));
+            }
+        }
+        __syncthreads();
+    }
+    if (tid == 0) *m.total = total;
+    for (long long b = tid; b < p.batch; b += kPlanThreads) {
+        int rank = static_cast<int>(b);
+        if (p.batch <= kPlanSorted) {
+            const int mine = lengths[b];
+            rank = 0;
+            for (int o = 0; o < static_cast<int>(p.batch); ++o)
+                rank += lengths[o] > mine || (lengths[o] == mine && o < b);
+        }
+        m.order[rank] = static_cast<int>(b);
+    }
+}
+
+// ---- the first pass ------------------------------------------------------------------------
+
+constexpr int kPrepThreads = 128;
+constexpr int kPrepHeads = 4;   // the most heads per CTA
+constexpr int kPrepPitch = 68;  // floats per row of L and T
+
+template <int N>
+struct PrepSmem {
+    static constexpr int kPitch = N * 2 + 16;  // bytes per row of K and Q
+    static constexpr int kL = 0;               // over K and Q, when those are in registers
+    static constexpr int kT = kL + kDeltaChunk * kPrepPitch * 4;
+    static constexpr int kTilesEnd = 2 * kDeltaChunk * kPitch;
+    static constexpr int kMatEnd = kT + kDeltaChunk * kPrepPitch * 4;
+    static constexpr int kM = kTilesEnd > kMatEnd ? kTilesEnd : kMatEnd;
+    static constexpr int kLengths = kM + kDeltaTile;  // 1 / |k|, 1 / |q|
+    static constexpr int kSums = kLengths + 2 * kDeltaChunk * 4;  // s in two floats, per head
+    static constexpr int kVec = kSums + kPrepHeads * 2 * kDeltaChunk * 4;  // per head
+    static constexpr int kTotal = kVec + kPrepHeads * 2048;
+};
+
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4], unsigned b0,
+                                          unsigned b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One head's factors of the chunk's tokens, two per lane of one warp.
+__device__ __forceinline__ void delta_factors(const DeltaParams &d, int h, int tok, int valid,
+                                              const float *lengths, bool bad, float *sums,
+                                              float *vec, int lane) {
+    using R = DeltaRecord;
+    const SsuParams &p = d.m.p;
+    const float bias = __ldg(p.dt_bias + h * p.bias_h), A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+    float a[2], beta[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = 2 * lane + k;
+        const long long t = static_cast<long long>(tok) + i;
+        a[k] = beta[k] = 0.0f;
+        if (i >= valid) continue;
+        a[k] = softplus_f32(__bfloat162float(p.dt[t * p.dt_b + h * p.dt_h]) + bias) * A2;
+        if (a[k] < -300.0f) a[k] = -300.0f;  // 2^-300 is 0; NaN stays
+        beta[k] = 1.0f / (1.0f + expf(-__bfloat162float(d.beta[t * d.beta_t + h * d.beta_h])));
+        bad |= !(a[k] < 60.0f) || !(beta[k] <= 1.0f);
+    }
+    // sums in double, kept as two floats: differences of neighbours stay exact behind long decays
+    double upto = static_cast<double>(a[0]) + a[1];
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += o;
+    }
+    const double s[2] = {upto - a[1], upto};
+    const double whole = __shfl_sync(0xffffffffu, upto, 31);
+    bad |= !(s[0] < 60.0) || !(s[1] < 60.0);
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = 2 * lane + k;
+        const float hi = static_cast<float>(s[k]);
+        sums[i] = hi;
+        sums[kDeltaChunk + i] = static_cast<float>(s[k] - hi);
+        const float rk = lengths[i], rq = lengths[kDeltaChunk + i], e = exp2f(hi);
+        vec[R::kBeta + i] = beta[k];
+        vec[R::kPast + i] = beta[k] * e * rk;
+        vec[R::kLeft + i] = exp2f(static_cast<float>(whole - s[k])) * rk;
+        vec[R::kRead + i] = rq;
+        vec[R::kReadS + i] = rq * e;
+        vec[R::kDecay + i] = exp2f(a[k]);
+        vec[R::kKey + i] = rk;
+    }
+    if (lane == 0) {
+        vec[R::kWhole] = exp2f(static_cast<float>(whole));
+        vec[R::kSlow] = bad ? 1.0f : 0.0f;
+    }
+}
+
+// Grid: chunks, heads / per_cta (the heads of a CTA are of one key head).
+template <int N>
+__global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
+    const __grid_constant__ DeltaMmaParams m) {
+    pdl_wait();
+    pdl_trigger();
+    using Smem = PrepSmem<N>;
+    using R = DeltaRecord;
+    extern __shared__ __align__(128) unsigned char raw[];
+    if (static_cast<int>(blockIdx.x) >= *m.total) return;
+    const SsuParams &p = m.d.m.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int2 chunk = m.chunks[blockIdx.x];
+    const int tok = chunk.x, valid = chunk.y;
+    const int h0 = blockIdx.y * m.per_cta, grp = group_of(h0, p.group_magic);
+    {
+        constexpr int kPieces = N / 8;
+#pragma unroll 4
+        for (int k = tid; k < kDeltaChunk * kPieces; k += kPrepThreads) {
+            const int row = k / kPieces, piece = k % kPieces;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (row < valid) {
+                const long long t = static_cast<long long>(tok) + row;
+                a = __ldg(reinterpret_cast<const uint4 *>(p.B + t * p.B_b + grp * p.B_g) + piece);
+                b = __ldg(reinterpret_cast<const uint4 *>(p.C + t * p.C_b + grp * p.C_g) + piece);
+            }
+            *reinterpret_cast<uint4 *>(raw + row * Smem::kPitch + piece * 16) = a;
+            *reinterpret_cast<uint4 *>(raw + (kDeltaChunk + row) * Smem::kPitch + piece * 16) = b;
+        }
+    }
+    __syncthreads();
+    float *const lengths = reinterpret_cast<float *>(raw + Smem::kLengths);
+    bool bad = false;
+    {  // lengths: two threads per row
+        const int row = tid >> 1;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint4 *const at = reinterpret_cast<const uint4 *>(
+                raw + (which * kDeltaChunk + row) * Smem::kPitch + (tid & 1) * N);
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+                float f[8];
+                widen16(at[k], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[which] = fmaf(f[i], f[i], sum[which]);
+            }
+            sum[which] += __shfl_xor_sync(0xffffffffu, sum[which], 1);
+        }
+        bad = !(sum[0] < INFINITY) || !(sum[1] < INFINITY);
+        if ((tid & 1) == 0) {
+            const bool unit = m.d.eps >= 0.0f, live = row < valid;
+            lengths[row] = !live ? 0.0f : unit ? 1.0f / sqrtf(sum[0] + m.d.eps) : 1.0f;
+            lengths[kDeltaChunk + row] =
+                !live ? 0.0f : unit ? m.d.scale / sqrtf(sum[1] + m.d.eps) : m.d.scale;
+            bad |= !(lengths[row] < INFINITY) || !(fabsf(lengths[kDeltaChunk + row]) < INFINITY);
+        }
+    }
+    // K K^T and Q K^T: 16 rows per warp, the columns up to its own 16
+    float kk[8][4] = {}, qk[8][4] = {};
+    {
+        const unsigned tiles = smem_u32(raw);
+        const int mi = lane >> 3, r = lane & 7;
+        const unsigned a_at = tiles + (16 * warp + (mi & 1) * 8 + r) * Smem::kPitch + (mi >> 1) * 16;
+        const unsigned b_at = tiles + ((mi >> 1) * 8 + r) * Smem::kPitch + (mi & 1) * 16;
+#pragma unroll
+        for (int ks = 0; ks < N / 16; ++ks) {
+            unsigned ka[4], qa[4];
+            ldsm4(ka, a_at + ks * 32);
+            ldsm4(qa, a_at + kDeltaChunk * Smem::kPitch + ks * 32);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                if (nb > warp) continue;
+                unsigned b[4];
+                ldsm4(b, b_at + nb * 16 * Smem::kPitch + ks * 32);
+                mma_16816(kk[2 * nb], ka, b[0], b[1]);
+                mma_16816(kk[2 * nb + 1], ka, b[2], b[3]);
+                mma_16816(qk[2 * nb], qa, b[0], b[1]);
+                mma_16816(qk[2 * nb + 1], qa, b[2], b[3]);
+            }
+        }
+    }
+    bad = __syncthreads_or(bad);
+    for (int k = warp; k < m.per_cta; k += kPrepThreads / 32)
+        delta_factors(m.d, h0 + k, tok, valid, lengths, bad,
+                      reinterpret_cast<float *>(raw + Smem::kSums) + k * 2 * kDeltaChunk,
+                      reinterpret_cast<float *>(raw + Smem::kVec) + k * 512, lane);
+    float *const L = reinterpret_cast<float *>(raw + Smem::kL);
+    float *const T = reinterpret_cast<float *>(raw + Smem::kT);
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int k = 0; k < m.per_cta; ++k) {
+        __syncthreads();  // the factors; the head before has left
+        const float *const sums = reinterpret_cast<float *>(raw + Smem::kSums) + k * 2 * kDeltaChunk;
+        const float *const vec = reinterpret_cast<float *>(raw + Smem::kVec) + k * 512;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = 16 * warp + g + 8 * half;
+            const float hi = sums[i], lo = sums[kDeltaChunk + i], f = vec[R::kBeta + i] * lengths[i];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int j = 8 * n + 2 * t;
+                float l[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
+                if (n <= 2 * warp + 1) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float gap = (hi - sums[j + c]) + (lo - sums[kDeltaChunk + j + c]);
+                        const float e = j + c <= i ? exp2f(gap) * lengths[j + c] : 0.0f;
+                        w[c] = j + c <= i ? qk[n][2 * half + c] * e : 0.0f;
+                        l[c] = j + c < i ? kk[n][2 * half + c] * (e * f) : 0.0f;
+                    }
+                    *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) = make_float2(l[0], l[1]);
+                }
+                *reinterpret_cast<float2 *>(T + i * kPrepPitch + j) = make_float2(0.0f, 0.0f);
+                *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 + ((n ^ (i & 7)) << 4) +
+                                              4 * t) = f2_to_bf2(w[0], w[1]);
+            }
+        }
+        __syncthreads();
+        // the blocks of 16 on the diagonal: a column of the inverse per thread
+        if (tid < kDeltaChunk) {
+            const int block = tid & ~15, c = tid & 15;
+            float x[16];
+            x[0] = c == 0 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < i; j += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(
+                        L + (block + i) * kPrepPitch + block + j);
+                    sum = fmaf(l.x, x[j], sum);
+                    if (j + 1 < i) sum = fmaf(l.y, x[j + 1], sum);
+                    if (j + 2 < i) sum = fmaf(l.z, x[j + 2], sum);
+                    if (j + 3 < i) sum = fmaf(l.w, x[j + 3], sum);
+                }
+                x[i] = i == c ? 1.0f : i < c ? 0.0f : -sum;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) T[(block + i) * kPrepPitch + block + c] = x[i];
+        }
+        __syncthreads();
+        // joined to blocks of 32, then of 64: L21 <- L21 T11, T21 = -T22 L21
+        auto join = [&](auto size_of, int row0, int r, int c) {
+            constexpr int kSize = decltype(size_of)::value, kCols = kSize / 4;
+            float acc[kCols];
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) acc[x] = 0.0f;
+#pragma unroll 8
+            for (int j = 0; j < kSize; ++j) {
+                const float l = L[(row0 + kSize + r) * kPrepPitch + row0 + j];
+#pragma unroll
+                for (int x = 0; x < kCols; x += 4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(
+                        T + (row0 + j) * kPrepPitch + row0 + c + x);
+                    acc[x] = fmaf(l, b.x, acc[x]), acc[x + 1] = fmaf(l, b.y, acc[x + 1]);
+                    acc[x + 2] = fmaf(l, b.z, acc[x + 2]), acc[x + 3] = fmaf(l, b.w, acc[x + 3]);
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kCols; ++x) {
+                L[(row0 + kSize + r) * kPrepPitch + row0 + c + x] = acc[x];
+                acc[x] = 0.0f;
+            }
+            __syncthreads();
+#pragma unroll 8
+            for (int j = 0; j < kSize; ++j) {
+                const float a = T[(row0 + kSize + r) * kPrepPitch + row0 + kSize + j];
+#pragma unroll
+                for (int x = 0; x < kCols; x += 4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(
+                        L + (row0 + kSize + j) * kPrepPitch + row0 + c + x);
+                    acc[x] = fmaf(a, b.x, acc[x]), acc[x + 1] = fmaf(a, b.y, acc[x + 1]);
+                    acc[x + 2] = fmaf(a, b.z, acc[x + 2]), acc[x + 3] = fmaf(a, b.w, acc[x + 3]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kCols; ++x)
+                T[(row0 + kSize + r) * kPrepPitch + row0 + c + x] = -acc[x];
+            __syncthreads();
+        };
+        join(std::integral_constant<int, 16>(), tid / 64 * 32, tid % 64 / 4, tid % 4 * 4);
+        join(std::integral_constant<int, 32>(), 0, tid / 4, tid % 4 * 8);
+        unsigned char *const to =
+            m.records + (static_cast<long long>(blockIdx.x) * p.nheads + h0 + k) * R::kBytes;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int row = (tid + x * kPrepThreads) / 8, piece = tid % 8;
+            const float4 *const f =
+                reinterpret_cast<const float4 *>(T + row * kPrepPitch + piece * 8);
+            const float4 a = f[0], b = f[1];
+            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            unsigned one[4], two[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                one[i] = f2_to_bf2(v[2 * i], v[2 * i + 1]);
+                two[i] = f2_to_bf2(v[2 * i] - __uint_as_float(one[i] << 16),
+                                   v[2 * i + 1] - __uint_as_float(one[i] & 0xffff0000u));
+            }
+            const int at = row * 128 + ((piece ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(to + R::kT1 + at) = make_uint4(one[0], one[1], one[2], one[3]);
+            *reinterpret_cast<uint4 *>(to + R::kT2 + at) = make_uint4(two[0], two[1], two[2], two[3]);
+            const int m_at = (tid + x * kPrepThreads) * 16;
+            *reinterpret_cast<uint4 *>(to + R::kM + m_at) =
+                *reinterpret_cast<const uint4 *>(raw + Smem::kM + m_at);
+        }
+        *reinterpret_cast<uint4 *>(to + R::kVec + tid * 16) =
+            *reinterpret_cast<const uint4 *>(raw + Smem::kVec + k * 2048 + tid * 16);
+    }
+}
+
+// ---- the second pass -----------------------------------------------------------------------
+
+constexpr int kDeltaCompute = 256;
+// warps after the compute warps: one issues the products, one the copies, one looks values over
+constexpr int kDeltaIssuer = kDeltaCompute / 32, kDeltaLoader = kDeltaIssuer + 1,
+              kDeltaLooker = kDeltaIssuer + 2;
+constexpr int kDeltaThreads = kDeltaCompute + 96;
+constexpr int kDeltaStages = 3;
+
+template <int N>
+struct DeltaSmem {
+    static constexpr int kBlocks = N / 64;
+    static constexpr int kK = 0;
+    static constexpr int kQ = kK + kBlocks * kDeltaTile;
+    static constexpr int kV = kQ + kBlocks * kDeltaTile;
+    static constexpr int kRecord = kV + 2 * kDeltaTile;
+    static constexpr int kStage = kRecord + DeltaRecord::kBytes;
+    static constexpr int kSwap = kDeltaStages * kStage;  // two floats per compute thread
+    static constexpr int kFlags = kSwap + 2 * kDeltaCompute * 4;
+    static constexpr int kBars = kFlags + 16;
+    static constexpr int kTotal = kBars + 8 * (3 * kDeltaStages + 8);
+    static_assert(kStage % 1024 == 0, "tiles start at 1024 bytes");
+};
+
+__device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigned bytes,
+                                          unsigned bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// Two values as bf16 parts; each part is what the ones before leave.
+template <int kParts>
+__device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+        bits[k] = f2_to_bf2(f.x, f.y);
+        if (k + 1 < kParts)
+            f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k] << 16),
+                                          -__uint_as_float(bits[k] & 0xffff0000u)));
+    }
+}
+
+// Roles.  Per chunk, with the barrier of each hand-over ([s] and [o] once per chunk, the others once
+// per chunk that is not taken token by token):
+//
+//   loader:  [empty] tiles and record -> full
+//   looker:  [full] values looked over -> look
+//   issuer:  [look, s] S K^T -> p; [o] S Q^T; [r] R T^T -> u; [w] U K -> d; U M^T -> m, empty
+//   compute: [full, look, p] R -> r; [u] U -> w; [d] S -> s; [m] readout -> o, empty
+template <int N, typename ST, bool kIdx64>
+__global__ void __launch_bounds__(kDeltaThreads, 1)
+    ssu_delta_mma_kernel(const __grid_constant__ DeltaMmaParams m,
+                         const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_v) {
+    using Smem = DeltaSmem<N>;
+    using R = DeltaRecord;
+    constexpr int kParts = sizeof(ST) == 4 ? 3 : 2, kBlocks = Smem::kBlocks;
+    extern __shared__ unsigned char raw[];
+    __shared__ unsigned tmem_slot;
+    const SsuParams &p = m.d.m.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char *const smem = raw + (base - smem_u32(raw));
+    const unsigned bars = base + Smem::kBars;
+    const unsigned full = bars, empty = bars + 8 * kDeltaStages, look = empty + 8 * kDeltaStages;
+    const unsigned bar_s = look + 8 * kDeltaStages, bar_o = bar_s + 8, bar_p = bar_s + 16,
+                   bar_r = bar_s + 24, bar_u = bar_s + 32, bar_w = bar_s + 40, bar_d = bar_s + 48,
+                   bar_m = bar_s + 56;
+    if (tid == 0) {
+        for (int i = 0; i < kDeltaStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kDeltaCompute / 32 + 1);
+            mbar_init(look + 8 * i, 1);
+        }
+        for (unsigned bar : {bar_s, bar_o, bar_r, bar_w}) mbar_init(bar, kDeltaCompute / 32);
+        for (unsigned bar : {bar_p, bar_u, bar_d, bar_m}) mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kDeltaIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = tmem_slot;
+    // TMEM columns: S's parts (then U's, for the next state); the next state's sum (before it, R's
+    // parts); S K^T, then U, then U in bf16; S Q^T; U M^T
+    const unsigned tS = tmem, tD = tmem + 192, tP = tmem + 320, tQ = tmem + 384, tM = tmem + 448;
+
+    pdl_wait();
+    const int columns = p.nheads * m.slabs;
+    const int column = blockIdx.x % columns, h = column / m.slabs;
+    const int row0 = (column - h * m.slabs) * kDeltaRows;
+    const long long b = m.order[blockIdx.x / columns];
+    const int4 prompt = m.prompts[b];
+    const bool fresh = m.d.m.fresh && m.d.m.fresh[b] != 0;
+    const int begin = prompt.y, end = prompt.z;
+    const int chunks = prompt.x ? (end - begin + kDeltaChunk - 1) / kDeltaChunk : 0;
+    const int grp = group_of(h, p.group_magic);
+    const int v_blocks = min(2, (p.headdim - row0 + 63) / 64);
+    bool alive = true;
+
+    if (warp == kDeltaLoader) {
+        if (lane == 0) {
+            const unsigned bytes = (2 * kBlocks + v_blocks) * kDeltaTile + R::kBytes;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+                const unsigned to = base + stage * Smem::kStage, bar = full + 8 * stage;
+                if (turn > 0 && alive) alive = mbar_wait(empty + 8 * stage, (turn - 1) & 1);
+                if (!alive) break;
+                mbar_expect(bar, bytes);
+                const int tok = begin + c * kDeltaChunk;
+                for (int k = 0; k < kBlocks; ++k) {
+                    tma_load(to + Smem::kK + k * kDeltaTile, &map_k, bar, k * 64, grp, tok);
+                    tma_load(to + Smem::kQ + k * kDeltaTile, &map_q, bar, k * 64, grp, tok);
+                }
+                for (int k = 0; k < v_blocks; ++k)
+                    tma_load(to + Smem::kV + k * kDeltaTile, &map_v, bar, row0 + k * 64, h, tok);
+                bulk_load(to + Smem::kRecord,
+                          m.records + (static_cast<long long>(prompt.w + c) * p.nheads + h) *
+                                          R::kBytes,
+                          R::kBytes, bar);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kDeltaLooker) {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+            if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
+            const unsigned at = base + stage * Smem::kStage + Smem::kV;
+            const int valid = min(kDeltaChunk, end - begin - c * kDeltaChunk);
+            const __nv_bfloat162 zero{};
+            __nv_bfloat162 sum[4] = {};
+#pragma unroll 8
+            for (int k = 0; k < v_blocks * kDeltaTile / 512; ++k) {  // 4 rows of a tile each
+                const uint4 v = load_smem16(at + k * 512 + lane * 16);
+                if ((4 * k + lane / 8) % kDeltaChunk >= valid) continue;
+                sum[0] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.x), zero, sum[0]);
+                sum[1] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.y), zero, sum[1]);
+                sum[2] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.z), zero, sum[2]);
+                sum[3] = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(v.w), zero, sum[3]);
+            }
+            sum[0] = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+            const bool any = __any_sync(
+                0xffffffffu, (reinterpret_cast<const unsigned &>(sum[0]) & 0x7fff7fffu) != 0);
+            if (lane == 0) {
+                const float *const vec = reinterpret_cast<const float *>(
+                    smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
+                reinterpret_cast<int *>(smem + Smem::kFlags)[stage] =
+                    any || vec[R::kSlow] != 0.0f;
+                mbar_arrive(look + 8 * stage);
+            }
+            __syncwarp();
+        }
+    } else if (warp == kDeltaIssuer) {
+        if (lane == 0) {
+            unsigned fast = 0;  // parity of the chunks not taken token by token
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+                const unsigned at = base + stage * Smem::kStage;
+                if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
+                if (alive) alive = mbar_wait(look + 8 * stage, turn & 1);
+                if (alive) alive = mbar_wait(bar_s, c & 1);
+                if (!alive) break;
+                if (reinterpret_cast<const volatile int *>(smem + Smem::kFlags)[stage]) {
+                    if (c > 0) alive = mbar_wait(bar_o, (c - 1) & 1);
+                    mbar_arrive(empty + 8 * stage);
+                    continue;
+                }
+                tc_fence_after();
+                // small parts first: sums lose less
+#pragma unroll
+                for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < N / 16; ++k)
+                        mma_ts(tP, tS + part * (N / 2) + 8 * k,
+                               operand(at + Smem::kK + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
+                               instruction(kDeltaChunk, false, false), part < kParts - 1 || k > 0);
+                tc_commit(bar_p);
+                if (c > 0) alive = mbar_wait(bar_o, (c - 1) & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < N / 16; ++k)
+                        mma_ts(tQ, tS + part * (N / 2) + 8 * k,
+                               operand(at + Smem::kQ + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
+                               instruction(kDeltaChunk, false, false), part < 1 || k > 0);
+                if (alive) alive = mbar_wait(bar_r, fast);
+                if (!alive) break;
+                tc_fence_after();
+                const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
+                auto correct = [&](int part, unsigned t, bool add) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0),
+                               instruction(kDeltaChunk, false, false), add || k > 0);
+                };
+                if constexpr (kParts == 3) {
+                    correct(2, t1, false);
+                    correct(1, t2, true);
+                    correct(0, t2, true);
+                } else {
+                    correct(0, t2, false);
+                }
+                correct(1, t1, true);
+                correct(0, t1, true);
+                tc_commit(bar_u);
+                if (alive) alive = mbar_wait(bar_w, fast);
+                if (!alive) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tD, tS + part * 32 + 8 * k,
+                               operand(at + Smem::kK + k * 2048, N == 128 ? kDeltaTile : 0),
+                               instruction(N, false, true), part < kParts - 1 || k > 0);
+                tc_commit(bar_d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ts(tM, tP + 32 * (k / 2) + 8 * (k % 2),
+                           operand(at + Smem::kRecord + R::kM + k * 32, 0),
+                           instruction(kDeltaChunk, false, false), k > 0);
+                tc_commit(empty + 8 * stage);
+                tc_commit(bar_m);
+                fast ^= 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = 32 * quarter + lane;  // TMEM lane; state row row0 + row
+        const bool own = row0 + row < p.headdim;
+        const unsigned lanes = static_cast<unsigned>(quarter) << 21;
+        constexpr int kCols = N / 2;  // of the thread's half row
+        float S[kCols];
+        long long slot = 0;
+        if (prompt.x) slot = load_slot<kIdx64>(p, b);
+        ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
+                          (row0 + row) * p.st_row + half * kCols;
+        constexpr int kPer = 16 / static_cast<int>(sizeof(ST));
+        if (prompt.x && own && !fresh && chunks) {
+#pragma unroll
+            for (int i = 0; i < kCols / kPer; ++i) {
+                const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(state) + i);
+                if constexpr (sizeof(ST) == 4) {
+                    S[4 * i] = __uint_as_float(w.x), S[4 * i + 1] = __uint_as_float(w.y);
+                    S[4 * i + 2] = __uint_as_float(w.z), S[4 * i + 3] = __uint_as_float(w.w);
+                } else {
+                    float f[8];
+                    widen16(w, f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) S[8 * i + k] = f[k];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) S[i] = 0.0f;
+        }
+        auto publish = [&](int k) {  // 16 columns of S as the next products' operand
+            unsigned bits[kParts][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                unsigned w[kParts];
+                split2<kParts>(make_float2(S[16 * k + 2 * i], S[16 * k + 2 * i + 1]), w);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+            }
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+                tc_store8(tS + lanes + part * (N / 2) + half * (N / 4) + 8 * k, bits[part]);
+        };
+        auto published = [&]() {
+            tc_wait_st();
+            tc_fence_before();
+            warp_arrive(bar_s, lane);
+        };
+        if (chunks) {
+#pragma unroll
+            for (int k = 0; k < kCols / 16; ++k) publish(k);
+            published();
+        }
+        unsigned fast = 0;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+            const unsigned at = base + stage * Smem::kStage;
+            const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
+            const float *const vec = reinterpret_cast<const float *>(
+                smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
+            // the thread's column of V
+            const unsigned v_at = at + Smem::kV + (row >> 6) * kDeltaTile + 2 * (row & 7);
+            const int v_piece = (row & 63) >> 3;
+            auto value = [&](int j) {
+                unsigned short u;
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(u)
+                             : "r"(v_at + j * 128 + ((v_piece ^ (j & 7)) << 4))
+                             : "memory");
+                return __uint_as_float(static_cast<unsigned>(u) << 16);
+            };
+            __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
+                                       h * p.out_h + row0 + row;
+            if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
+            if (alive) alive = mbar_wait(look + 8 * stage, turn & 1);
+            const bool slow =
+                reinterpret_cast<const volatile int *>(smem + Smem::kFlags)[stage] != 0;
+            if (__builtin_expect(slow, 0)) {
+                float *const swap = reinterpret_cast<float *>(smem + Smem::kSwap);
+                auto both = [&](float mine, float *room) {  // the sum over both halves of the row
+                    room[tid] = mine;
+                    asm volatile("bar.sync 1, %0;" ::"n"(kDeltaCompute) : "memory");
+                    return room[row] + room[kDeltaRows + row];
+                };
+                // four of the thread's columns of token t's key or query
+                auto row_of = [&](int tile, int t, int i) {
+                    const int col = half * kCols + i;
+                    uint2 w;
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(w.x), "=r"(w.y)
+                                 : "r"(swizzled(at + tile + (col / 64) * kDeltaTile, t,
+                                                col % 64 / 8) + 2 * (col % 8))
+                                 : "memory");
+                    return make_float4(__uint_as_float(w.x << 16),
+                                       __uint_as_float(w.x & 0xffff0000u),
+                                       __uint_as_float(w.y << 16),
+                                       __uint_as_float(w.y & 0xffff0000u));
+                };
+#pragma unroll 1
+                for (int t = 0; t < valid; ++t) {
+                    const float a = vec[R::kDecay + t], rk = vec[R::kKey + t];
+                    float part = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 k = row_of(Smem::kK, t, i);
+                        part = fmaf(S[i], k.x, part), part = fmaf(S[i + 1], k.y, part);
+                        part = fmaf(S[i + 2], k.z, part), part = fmaf(S[i + 3], k.w, part);
+                    }
+                    const float sk = both(part, swap) * rk;
+                    const float e = vec[R::kBeta + t] * (value(t) - a * sk) * rk;
+                    part = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 4) {
+                        const float4 k = row_of(Smem::kK, t, i), q = row_of(Smem::kQ, t, i);
+                        S[i] = fmaf(S[i], a, e * k.x);
+                        S[i + 1] = fmaf(S[i + 1], a, e * k.y);
+                        S[i + 2] = fmaf(S[i + 2], a, e * k.z);
+                        S[i + 3] = fmaf(S[i + 3], a, e * k.w);
+                        part = fmaf(S[i], q.x, part), part = fmaf(S[i + 1], q.y, part);
+                        part = fmaf(S[i + 2], q.z, part), part = fmaf(S[i + 3], q.w, part);
+                    }
+                    const float y = both(part, swap + kDeltaCompute) * vec[R::kRead + t];
+                    if (half == 0 && own) out[t * p.out_b] = __float2bfloat16(y);
+                }
+                if (c + 1 < chunks) {
+#pragma unroll
+                    for (int k = 0; k < kCols / 16; ++k) publish(k);
+                    published();
+                }
+                warp_arrive(bar_o, lane);
+                warp_arrive(empty + 8 * stage, lane);
+                continue;
+            }
+            // R = beta v - (beta e^s / |k|) S k
+            if (alive) alive = mbar_wait(bar_p, fast);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j0 = 32 * half + 16 * k;
+                unsigned sk[16], bits[kParts][8];
+                tc_load16(tP + lanes + j0, sk);
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = value(j0 + i);
+                tc_wait_ld();
+                const float4 *const beta = reinterpret_cast<const float4 *>(vec + R::kBeta + j0);
+                const float4 *const past = reinterpret_cast<const float4 *>(vec + R::kPast + j0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 bt = beta[i], ps = past[i];
+                    float2 lo = __ffma2_rn(make_float2(-ps.x, -ps.y),
+                                           make_float2(__uint_as_float(sk[4 * i]),
+                                                       __uint_as_float(sk[4 * i + 1])),
+                                           __fmul2_rn(make_float2(bt.x, bt.y),
+                                                      make_float2(v[4 * i], v[4 * i + 1])));
+                    float2 hi = __ffma2_rn(make_float2(-ps.z, -ps.w),
+                                           make_float2(__uint_as_float(sk[4 * i + 2]),
+                                                       __uint_as_float(sk[4 * i + 3])),
+                                           __fmul2_rn(make_float2(bt.z, bt.w),
+                                                      make_float2(v[4 * i + 2], v[4 * i + 3])));
+                    if (valid < kDeltaChunk) {  // tokens of the next prompt
+                        const int j = j0 + 4 * i;
+                        if (j >= valid) lo.x = 0.0f;
+                        if (j + 1 >= valid) lo.y = 0.0f;
+                        if (j + 2 >= valid) hi.x = 0.0f;
+                        if (j + 3 >= valid) hi.y = 0.0f;
+                    }
+                    if (!own) lo = hi = make_float2(0.0f, 0.0f);
+                    unsigned w[kParts];
+                    split2<kParts>(lo, w);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) bits[part][2 * i] = w[part];
+                    split2<kParts>(hi, w);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) bits[part][2 * i + 1] = w[part];
+                }
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+                    tc_store8(tD + lanes + part * 32 + j0 / 2, bits[part]);
+            }
+            if (valid < kDeltaChunk) {  // what the next state's product must not meet
+                for (int k = tid; k < (kDeltaChunk - valid) * 8 * kBlocks; k += kDeltaCompute)
+                    store_smem16(at + Smem::kK + k / 8 % kBlocks * kDeltaTile +
+                                     (valid + k / 8 / kBlocks) * 128 + k % 8 * 16,
+                                 make_uint4(0, 0, 0, 0));
+                fence_async_smem();
+            }
+            tc_wait_st();
+            tc_fence_before();
+            warp_arrive(bar_r, lane);
+            // U for the readout, and with its weights for the next state
+            if (alive) alive = mbar_wait(bar_u, fast);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j0 = 32 * half + 16 * k;
+                unsigned u[16], plain[8], bits[kParts][8];
+                tc_load16(tP + lanes + j0, u);
+                tc_wait_ld();
+                const float4 *const left = reinterpret_cast<const float4 *>(vec + R::kLeft + j0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 l = left[i / 2];
+                    const float2 f =
+                        make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                    plain[i] = f2_to_bf2(f.x, f.y);
+                    unsigned w[kParts];
+                    split2<kParts>(__fmul2_rn(f, i % 2 ? make_float2(l.z, l.w)
+                                                       : make_float2(l.x, l.y)),
+                                   w);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+                }
+                // (over columns that this thread alone has read)
+                tc_store8(tP + lanes + 32 * half + 8 * k, plain);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+                    tc_store8(tS + lanes + part * 32 + j0 / 2, bits[part]);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            warp_arrive(bar_w, lane);
+            const float whole = vec[R::kWhole];
+            if (alive) alive = mbar_wait(bar_d, fast);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kCols / 16; ++k) {
+                unsigned d[16];
+                tc_load16(tD + lanes + half * kCols + 16 * k, d);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 s = __ffma2_rn(
+                        make_float2(S[16 * k + i], S[16 * k + i + 1]), make_float2(whole, whole),
+                        make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+                    S[16 * k + i] = s.x;
+                    S[16 * k + i + 1] = s.y;
+                }
+                if (c + 1 < chunks) publish(k);
+            }
+            if (c + 1 < chunks) published();
+            if (alive) alive = mbar_wait(bar_m, fast);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j0 = 32 * half + 16 * k;
+                unsigned sq[16], um[16];
+                tc_load16(tQ + lanes + j0, sq);
+                tc_load16(tM + lanes + j0, um);
+                tc_wait_ld();
+                const float4 *const read = reinterpret_cast<const float4 *>(vec + R::kRead + j0);
+                const float4 *const past = reinterpret_cast<const float4 *>(vec + R::kReadS + j0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 r = read[i], s = past[i];
+                    const float f[4] = {r.x, r.y, r.z, r.w}, e[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int j = j0 + 4 * i + x;
+                        const float y = fmaf(e[x], __uint_as_float(sq[4 * i + x]),
+                                             f[x] * __uint_as_float(um[4 * i + x]));
+                        if (j < valid && own) out[j * p.out_b] = __float2bfloat16(y);
+                    }
+                }
+            }
+            tc_fence_before();
+            warp_arrive(bar_o, lane);
+            warp_arrive(empty + 8 * stage, lane);
+            fast ^= 1;
+        }
+        if (prompt.x && own && (chunks || fresh)) {
+#pragma unroll
+            for (int i = 0; i < kCols / kPer; ++i) {
+                uint4 w;
+                if constexpr (sizeof(ST) == 4)
+                    w = make_uint4(__float_as_uint(S[4 * i]), __float_as_uint(S[4 * i + 1]),
+                                   __float_as_uint(S[4 * i + 2]), __float_as_uint(S[4 * i + 3]));
+                else
+                    w = make_uint4(f2_to_bf2(S[8 * i], S[8 * i + 1]),
+                                   f2_to_bf2(S[8 * i + 2], S[8 * i + 3]),
+                                   f2_to_bf2(S[8 * i + 4], S[8 * i + 5]),
+                                   f2_to_bf2(S[8 * i + 6], S[8 * i + 7]));
+                __stcs(reinterpret_cast<uint4 *>(state) + i, w);
+            }
+        }
+    }
+    tc_fence_before();
+    if (__syncthreads_or(!alive)) {  // what is in flight lands long before this is over
+        if (tid == 0) atomicOr(&p.err[2], 1u);
+        __nanosleep(1000000);
+    }
+    __syncthreads();
+    if (warp == kDeltaIssuer) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+    }
+}
+
+}  // namespace

@@ -11,6 +11,7 @@
 #include "ssu_host.h"
 #include "ssu_prompt.cuh"
 #include "ssu_prompt_mma.cuh"
+#include "ssu_tma.h"
 
 using ssu_host::aligned;
 using ssu_host::DeviceGuard;
@@ -123,33 +124,6 @@ PromptPlan prompt_plan(const ssu_shape_t &s, int64_t tokens, int sm_count) {
         w.total = w.turn + (4ll * (sm_count + 1) + 255) / 256 * 256;
     }
     return w;
-}
-
-// x, B and C as 3-D tensors of [tokens, heads or groups, columns] in boxes of 128 tokens by 64
-// columns; false where the driver cannot describe them.
-bool encode_map(CUtensorMap *map, const void *base, int64_t columns, int64_t heads, int64_t tokens,
-                int64_t head_stride, int64_t token_stride) {
-    static const auto encode = [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                             cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn);
-    }();
-    if (!encode) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(heads),
-                                static_cast<cuuint64_t>(tokens)};
-    // a dimension of one element has no stride of its own
-    const cuuint64_t strides[2] = {
-        static_cast<cuuint64_t>(heads > 1 ? head_stride * 2 : columns * 2),
-        static_cast<cuuint64_t>(tokens > 1 ? token_stride * 2 : columns * heads * 2)};
-    const cuuint32_t box[3] = {64, 1, kChunk}, steps[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
-                  strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Operands that the chunked form can read: 16-byte rows for the tensor maps (x, B, C) and for
@@ -327,10 +301,14 @@ ssu_status_t ssu_update_prompts(ssu_handle_t handle, void *state_pool,
         m.turn = reinterpret_cast<unsigned *>(room + w.turn);
         CUtensorMap maps[4];
         if (mma_grids(w) &&
-            encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b) &&
-            encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b) &&
-            encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b) &&
-            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b))
+            encode_map(&maps[0], x, s.headdim, s.nheads, tokens, p.x_h, p.x_b,
+                       kChunk) &&
+            encode_map(&maps[1], B, s.dstate, s.ngroups, tokens, p.B_g, p.B_b,
+                       kChunk) &&
+            encode_map(&maps[2], C, s.dstate, s.ngroups, tokens, p.C_g, p.C_b,
+                       kChunk) &&
+            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b,
+                       kChunk))
             e = launch_mma(m, w, maps, static_cast<int>(s.dstate), bf16, i64, *handle, cs);
     }
     if (e == cudaErrorNotSupported)

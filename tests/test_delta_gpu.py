@@ -489,3 +489,18 @@ def test_the_same_bits_again_and_without_dependent_launch(op):
         ssu.ssu_set_pdl(op.handle, True)
     for other in (b, c):
         assert all(torch.equal(x, y) for x, y in zip(a, other))
+
+
+@pytest.mark.parametrize("cu,skip", [([0, 80, 60, 200], [1, 2]), ([0, 200, 100, 150], [1, 2]),
+                                     ([0, 64, 0, 200], [1, 2]), ([10, 10, 5, 5], [1])], ids=str)
+def test_prompts_that_overlap(op, cu, skip):
+    """Where offsets run backwards, a chunked prompt that begins before the end of a good one
+    before it is left out like a bad one."""
+    d = make([100, 50, 50], seed=39)
+    d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    op.get_error()
+    out, pool = call(op, d)
+    assert op.get_error() == (len(skip), skip[0])
+    ref = reference(d, skip=skip)
+    d["slots"] = d["slots"][[b for b in range(3) if b not in skip]]
+    check(d, out, pool, ref)
