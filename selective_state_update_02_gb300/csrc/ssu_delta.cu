@@ -185,15 +185,16 @@ DeltaPlan delta_plan(const ssu_shape_t &s, int64_t tokens) {
 // Operands that the chunked form can read: 16-byte rows for the tensor maps.
 bool mma_operands(const DeltaParams &d) {
     const SsuParams &p = d.m.p;
-    if (!aligned(p.x, 16) || !aligned(p.B, 16) || !aligned(p.C, 16)) return false;
-    const long long strides[] = {p.x_b, p.x_h, p.B_b, p.B_g, p.C_b, p.C_g};
+    if (!aligned(p.x, 16) || !aligned(p.B, 16) || !aligned(p.C, 16) || !aligned(p.out, 16))
+        return false;
+    const long long strides[] = {p.x_b, p.x_h, p.B_b, p.B_g, p.C_b, p.C_g, p.out_b, p.out_h};
     for (long long v : strides)
         if (v % 8 != 0 || v >= (1ll << 38)) return false;
     return true;
 }
 
 template <int N, typename ST, bool kIdx64>
-cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[3],
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[4],
                        ssu_handle_s &handle, cudaStream_t st) {
     auto *prep = ssu_delta_prep_kernel<N>;
     auto *main = ssu_delta_mma_kernel<N, ST, kIdx64>;
@@ -224,10 +225,10 @@ cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtens
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.nheads * m.slabs));
     cfg.blockDim = dim3(kDeltaThreads);
     cfg.dynamicSmemBytes = kBytes;
-    return cudaLaunchKernelEx(&cfg, main, m, maps[0], maps[1], maps[2]);
+    return cudaLaunchKernelEx(&cfg, main, m, maps[0], maps[1], maps[2], maps[3]);
 }
 
-cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[3],
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[4],
                        const ssu_shape_t &s, ssu_handle_s &handle, cudaStream_t st) {
     const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
 #define SSU_MMA(N_, ST_)                                              \
@@ -337,10 +338,11 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
         m.prompts = reinterpret_cast<int4 *>(room + w.prompts);
         m.chunks = reinterpret_cast<int2 *>(room + w.list);
         m.records = reinterpret_cast<unsigned char *>(room + w.records);
-        CUtensorMap maps[3];
+        CUtensorMap maps[4];
         if (encode_map(&maps[0], k, s.dstate, s.ngroups, tokens, p.B_g, p.B_b, kDeltaChunk) &&
             encode_map(&maps[1], q, s.dstate, s.ngroups, tokens, p.C_g, p.C_b, kDeltaChunk) &&
-            encode_map(&maps[2], v, s.headdim, s.nheads, tokens, p.x_h, p.x_b, kDeltaChunk))
+            encode_map(&maps[2], v, s.headdim, s.nheads, tokens, p.x_h, p.x_b, kDeltaChunk) &&
+            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b, kDeltaChunk))
             e = launch_mma(m, w, maps, s, *handle, cs);
     }
     if (e == cudaErrorNotSupported) e = dispatch(s, [&](auto n, auto st, auto i64) {

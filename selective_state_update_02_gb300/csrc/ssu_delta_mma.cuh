@@ -172,9 +172,13 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
 }
 
 // ---- the first pass ------------------------------------------------------------------------
+//
+// What bounds it: shared memory's bandwidth and the chain of its steps, so products of blocks are
+// MMAs (K K^T and Q K^T of bf16 operands; blocks of T of fp32 ones in two tf32 parts, 2^-20) and
+// everything else is done by the thread that holds an element.
 
 constexpr int kPrepThreads = 128;
-constexpr int kPrepHeads = 4;   // the most heads per CTA
+constexpr int kPrepHeads = 4;   // the most heads per CTA: one per warp makes its factors
 constexpr int kPrepPitch = 68;  // floats per row of L and T
 
 template <int N>
@@ -185,7 +189,7 @@ struct PrepSmem {
     static constexpr int kTilesEnd = 2 * kDeltaChunk * kPitch;
     static constexpr int kMatEnd = kT + kDeltaChunk * kPrepPitch * 4;
     static constexpr int kM = kTilesEnd > kMatEnd ? kTilesEnd : kMatEnd;
-    static constexpr int kLengths = kM + kDeltaTile;  // 1 / |k|, 1 / |q|
+    static constexpr int kLengths = kM + kDeltaTile;  // 1 / |k|, scale / |q|
     static constexpr int kSums = kLengths + 2 * kDeltaChunk * 4;  // s in two floats, per head
     static constexpr int kVec = kSums + kPrepHeads * 2 * kDeltaChunk * 4;  // per head
     static constexpr int kTotal = kVec + kPrepHeads * 2048;
@@ -206,23 +210,73 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One head's factors of the chunk's tokens, two per lane of one warp.
-__device__ __forceinline__ void delta_factors(const DeltaParams &d, int h, int tok, int valid,
-                                              const float *lengths, bool bad, float *sums,
-                                              float *vec, int lane) {
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const unsigned (&a)[4],
+                                         const unsigned (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// An fp32 value as two tf32 parts.
+__device__ __forceinline__ void split_tf32(float x, unsigned &hi, unsigned &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+// d += A B over K columns of A and rows of B, both in rows of kPrepPitch floats: 16 rows from `a`,
+// kTiles times 8 columns from `b`.
+template <int K, int kTiles>
+__device__ __forceinline__ void block_product(float (&d)[kTiles][4], const float *a,
+                                              const float *b, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const float *const arow = a + g * kPrepPitch + t, *const brow = b + t * kPrepPitch + g;
+#pragma unroll
+    for (int k = 0; k < K; k += 8) {
+        unsigned ah[4], al[4];
+        split_tf32(arow[k], ah[0], al[0]);
+        split_tf32(arow[8 * kPrepPitch + k], ah[1], al[1]);
+        split_tf32(arow[k + 4], ah[2], al[2]);
+        split_tf32(arow[8 * kPrepPitch + k + 4], ah[3], al[3]);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            unsigned bh[2], bl[2];
+            split_tf32(brow[k * kPrepPitch + 8 * n], bh[0], bl[0]);
+            split_tf32(brow[(k + 4) * kPrepPitch + 8 * n], bh[1], bl[1]);
+            mma_tf32(d[n], al, bh);
+            mma_tf32(d[n], ah, bl);
+            mma_tf32(d[n], ah, bh);
+        }
+    }
+}
+
+// The product's 16 x 8 kTiles values, times `sign`, to rows of kPrepPitch floats from `to`.
+template <int kTiles>
+__device__ __forceinline__ void put_product(const float (&d)[kTiles][4], float *to, float sign,
+                                            int lane) {
+    float *const row = to + (lane >> 2) * kPrepPitch + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+        *reinterpret_cast<float2 *>(row + 8 * n) = make_float2(sign * d[n][0], sign * d[n][1]);
+        *reinterpret_cast<float2 *>(row + 8 * kPrepPitch + 8 * n) =
+            make_float2(sign * d[n][2], sign * d[n][3]);
+    }
+}
+
+// One head's factors of the chunk's tokens, two per lane of one warp; dt and gate as loaded.
+__device__ __forceinline__ void delta_factors(const DeltaParams &d, const unsigned (&dt)[2],
+                                              const unsigned (&gate)[2], float bias, float A2,
+                                              int valid, const float *lengths, bool bad,
+                                              float *sums, float *vec, int lane) {
     using R = DeltaRecord;
-    const SsuParams &p = d.m.p;
-    const float bias = __ldg(p.dt_bias + h * p.bias_h), A2 = __ldg(p.A + h * p.A_h) * kLog2e;
     float a[2], beta[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int i = 2 * lane + k;
-        const long long t = static_cast<long long>(tok) + i;
         a[k] = beta[k] = 0.0f;
-        if (i >= valid) continue;
-        a[k] = softplus_f32(__bfloat162float(p.dt[t * p.dt_b + h * p.dt_h]) + bias) * A2;
+        if (2 * lane + k >= valid) continue;
+        a[k] = softplus_f32(__uint_as_float(dt[k] << 16) + bias) * A2;
         if (a[k] < -300.0f) a[k] = -300.0f;  // 2^-300 is 0; NaN stays
-        beta[k] = 1.0f / (1.0f + expf(-__bfloat162float(d.beta[t * d.beta_t + h * d.beta_h])));
+        beta[k] = 1.0f / (1.0f + expf(-__uint_as_float(gate[k] << 16)));
         bad |= !(a[k] < 60.0f) || !(beta[k] <= 1.0f);
     }
     // sums in double, kept as two floats: differences of neighbours stay exact behind long decays
@@ -266,71 +320,69 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
     using Smem = PrepSmem<N>;
     using R = DeltaRecord;
     extern __shared__ __align__(128) unsigned char raw[];
+    const int2 chunk = m.chunks[blockIdx.x];  // (past the last one: of no use, and not used)
     if (static_cast<int>(blockIdx.x) >= *m.total) return;
     const SsuParams &p = m.d.m.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int2 chunk = m.chunks[blockIdx.x];
     const int tok = chunk.x, valid = chunk.y;
     const int h0 = blockIdx.y * m.per_cta, grp = group_of(h0, p.group_magic);
     {
         constexpr int kPieces = N / 8;
-#pragma unroll 4
-        for (int k = tid; k < kDeltaChunk * kPieces; k += kPrepThreads) {
-            const int row = k / kPieces, piece = k % kPieces;
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (row < valid) {
-                const long long t = static_cast<long long>(tok) + row;
-                a = __ldg(reinterpret_cast<const uint4 *>(p.B + t * p.B_b + grp * p.B_g) + piece);
-                b = __ldg(reinterpret_cast<const uint4 *>(p.C + t * p.C_b + grp * p.C_g) + piece);
-            }
-            *reinterpret_cast<uint4 *>(raw + row * Smem::kPitch + piece * 16) = a;
-            *reinterpret_cast<uint4 *>(raw + (kDeltaChunk + row) * Smem::kPitch + piece * 16) = b;
+        const unsigned tiles = smem_u32(raw);
+#pragma unroll
+        for (int x = 0; x < kDeltaChunk * kPieces / kPrepThreads; ++x) {
+            const int k = tid + x * kPrepThreads, row = k / kPieces, piece = k % kPieces;
+            const long long t = static_cast<long long>(tok) + (row < valid ? row : 0);
+            const int bytes = row < valid ? 16 : 0;  // the others become zeros
+            const unsigned to = tiles + row * Smem::kPitch + piece * 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                         "l"(p.B + t * p.B_b + grp * p.B_g + piece * 8), "r"(bytes)
+                         : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             to + kDeltaChunk * Smem::kPitch),
+                         "l"(p.C + t * p.C_b + grp * p.C_g + piece * 8), "r"(bytes)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the rates of the warp's own head
+    unsigned dt[2] = {}, gate[2] = {};
+    float bias = 0.0f, A2 = 0.0f;
+    if (warp < m.per_cta) {
+        const int h = h0 + warp;
+        bias = __ldg(p.dt_bias + h * p.bias_h), A2 = __ldg(p.A + h * p.A_h) * kLog2e;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (2 * lane + k >= valid) continue;
+            const long long t = static_cast<long long>(tok) + 2 * lane + k;
+            dt[k] = reinterpret_cast<const unsigned short *>(p.dt)[t * p.dt_b + h * p.dt_h];
+            gate[k] =
+                reinterpret_cast<const unsigned short *>(m.d.beta)[t * m.d.beta_t + h * m.d.beta_h];
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     float *const lengths = reinterpret_cast<float *>(raw + Smem::kLengths);
-    bool bad = false;
-    {  // lengths: two threads per row
-        const int row = tid >> 1;
-        float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const uint4 *const at = reinterpret_cast<const uint4 *>(
-                raw + (which * kDeltaChunk + row) * Smem::kPitch + (tid & 1) * N);
-#pragma unroll
-            for (int k = 0; k < N / 16; ++k) {
-                float f[8];
-                widen16(at[k], f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[which] = fmaf(f[i], f[i], sum[which]);
-            }
-            sum[which] += __shfl_xor_sync(0xffffffffu, sum[which], 1);
-        }
-        bad = !(sum[0] < INFINITY) || !(sum[1] < INFINITY);
-        if ((tid & 1) == 0) {
-            const bool unit = m.d.eps >= 0.0f, live = row < valid;
-            lengths[row] = !live ? 0.0f : unit ? 1.0f / sqrtf(sum[0] + m.d.eps) : 1.0f;
-            lengths[kDeltaChunk + row] =
-                !live ? 0.0f : unit ? m.d.scale / sqrtf(sum[1] + m.d.eps) : m.d.scale;
-            bad |= !(lengths[row] < INFINITY) || !(fabsf(lengths[kDeltaChunk + row]) < INFINITY);
-        }
-    }
-    // K K^T and Q K^T: 16 rows per warp, the columns up to its own 16
-    float kk[8][4] = {}, qk[8][4] = {};
+    const int g = lane >> 2, t = lane & 3;
+    // K K^T and Q K^T: 16 rows per warp, the columns up to its own 16; of Q Q^T the diagonal
+    float kk[8][4] = {}, qk[8][4] = {}, own[2][4] = {}, qq[2][4] = {};
     {
         const unsigned tiles = smem_u32(raw);
         const int mi = lane >> 3, r = lane & 7;
         const unsigned a_at = tiles + (16 * warp + (mi & 1) * 8 + r) * Smem::kPitch + (mi >> 1) * 16;
         const unsigned b_at = tiles + ((mi >> 1) * 8 + r) * Smem::kPitch + (mi & 1) * 16;
+        constexpr int kQ = kDeltaChunk * Smem::kPitch;
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks) {
-            unsigned ka[4], qa[4];
+            unsigned ka[4], qa[4], b[4];
             ldsm4(ka, a_at + ks * 32);
-            ldsm4(qa, a_at + kDeltaChunk * Smem::kPitch + ks * 32);
+            ldsm4(qa, a_at + kQ + ks * 32);
+            ldsm4(b, b_at + kQ + warp * 16 * Smem::kPitch + ks * 32);
+            mma_16816(qq[0], qa, b[0], b[1]);
+            mma_16816(qq[1], qa, b[2], b[3]);
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) {
                 if (nb > warp) continue;
-                unsigned b[4];
                 ldsm4(b, b_at + nb * 16 * Smem::kPitch + ks * 32);
                 mma_16816(kk[2 * nb], ka, b[0], b[1]);
                 mma_16816(kk[2 * nb + 1], ka, b[2], b[3]);
@@ -338,109 +390,129 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
                 mma_16816(qk[2 * nb + 1], qa, b[2], b[3]);
             }
         }
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+            if (nb == warp)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own[0][i] = kk[2 * nb][i], own[1][i] = kk[2 * nb + 1][i];
+    }
+    bool bad = false;
+    if (t == g >> 1) {  // the thread with rows g and g + 8 of the diagonals
+        const bool unit = m.d.eps >= 0.0f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = 16 * warp + g + 8 * half;
+            const float k2 = g & 1 ? own[half][2 * half + 1] : own[half][2 * half];
+            const float q2 = g & 1 ? qq[half][2 * half + 1] : qq[half][2 * half];
+            const bool live = row < valid;
+            const float rk = !live ? 0.0f : unit ? 1.0f / sqrtf(k2 + m.d.eps) : 1.0f;
+            const float rq = !live ? 0.0f : unit ? m.d.scale / sqrtf(q2 + m.d.eps) : m.d.scale;
+            lengths[row] = rk;
+            lengths[kDeltaChunk + row] = rq;
+            bad |= !(k2 < INFINITY) || !(q2 < INFINITY) || !(rk < INFINITY) ||
+                   !(fabsf(rq) < INFINITY);
+        }
     }
     bad = __syncthreads_or(bad);
-    for (int k = warp; k < m.per_cta; k += kPrepThreads / 32)
-        delta_factors(m.d, h0 + k, tok, valid, lengths, bad,
-                      reinterpret_cast<float *>(raw + Smem::kSums) + k * 2 * kDeltaChunk,
-                      reinterpret_cast<float *>(raw + Smem::kVec) + k * 512, lane);
+    if (warp < m.per_cta)
+        delta_factors(m.d, dt, gate, bias, A2, valid, lengths, bad,
+                      reinterpret_cast<float *>(raw + Smem::kSums) + warp * 2 * kDeltaChunk,
+                      reinterpret_cast<float *>(raw + Smem::kVec) + warp * 512, lane);
     float *const L = reinterpret_cast<float *>(raw + Smem::kL);
     float *const T = reinterpret_cast<float *>(raw + Smem::kT);
-    const int g = lane >> 2, t = lane & 3;
+    // what stays zero for every head: T and M above the blocks of 16 on the diagonal
+    for (int n = 2 * warp + 2; n < 8; ++n)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = 16 * warp + g + 8 * half;
+            *reinterpret_cast<float2 *>(T + i * kPrepPitch + 8 * n + 2 * t) =
+                make_float2(0.0f, 0.0f);
+            *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 + ((n ^ (i & 7)) << 4) + 4 * t) =
+                0u;
+        }
 #pragma unroll 1
     for (int k = 0; k < m.per_cta; ++k) {
         __syncthreads();  // the factors; the head before has left
         const float *const sums = reinterpret_cast<float *>(raw + Smem::kSums) + k * 2 * kDeltaChunk;
         const float *const vec = reinterpret_cast<float *>(raw + Smem::kVec) + k * 512;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = 16 * warp + g + 8 * half;
-            const float hi = sums[i], lo = sums[kDeltaChunk + i], f = vec[R::kBeta + i] * lengths[i];
+        {
+            const int i0 = 16 * warp + g;
+            const float hi[2] = {sums[i0], sums[i0 + 8]};
+            const float lo[2] = {sums[kDeltaChunk + i0], sums[kDeltaChunk + i0 + 8]};
+            const float f[2] = {vec[R::kBeta + i0] * lengths[i0],
+                                vec[R::kBeta + i0 + 8] * lengths[i0 + 8]};
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
+                if (n > 2 * warp + 1) continue;
                 const int j = 8 * n + 2 * t;
-                float l[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
-                if (n <= 2 * warp + 1) {
+                const float2 sh = *reinterpret_cast<const float2 *>(sums + j);
+                const float2 sl = *reinterpret_cast<const float2 *>(sums + kDeltaChunk + j);
+                const float2 rk = *reinterpret_cast<const float2 *>(lengths + j);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float gap = (hi - sums[j + c]) + (lo - sums[kDeltaChunk + j + c]);
-                        const float e = j + c <= i ? exp2f(gap) * lengths[j + c] : 0.0f;
-                        w[c] = j + c <= i ? qk[n][2 * half + c] * e : 0.0f;
-                        l[c] = j + c < i ? kk[n][2 * half + c] * (e * f) : 0.0f;
-                    }
-                    *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) = make_float2(l[0], l[1]);
+                for (int half = 0; half < 2; ++half) {
+                    const int i = i0 + 8 * half;
+                    const float e0 = exp2_ftz((hi[half] - sh.x) + (lo[half] - sl.x)) * rk.x;
+                    const float e1 = exp2_ftz((hi[half] - sh.y) + (lo[half] - sl.y)) * rk.y;
+                    *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) =
+                        make_float2(kk[n][2 * half] * (e0 * f[half]),
+                                    kk[n][2 * half + 1] * (e1 * f[half]));
+                    *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 +
+                                                  ((n ^ (i & 7)) << 4) + 4 * t) =
+                        f2_to_bf2(j <= i ? qk[n][2 * half] * e0 : 0.0f,
+                                  j + 1 <= i ? qk[n][2 * half + 1] * e1 : 0.0f);
                 }
-                *reinterpret_cast<float2 *>(T + i * kPrepPitch + j) = make_float2(0.0f, 0.0f);
-                *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 + ((n ^ (i & 7)) << 4) +
-                                              4 * t) = f2_to_bf2(w[0], w[1]);
             }
         }
-        __syncthreads();
-        // the blocks of 16 on the diagonal: a column of the inverse per thread
-        if (tid < kDeltaChunk) {
-            const int block = tid & ~15, c = tid & 15;
+        __syncwarp();
+        // the warp's block of 16 on the diagonal: a column of the inverse per lane (L's elements on
+        // and above the diagonal are not looked at)
+        if (lane < 16) {
+            const float *const block = L + 16 * warp * (kPrepPitch + 1);
             float x[16];
-            x[0] = c == 0 ? 1.0f : 0.0f;
+            x[0] = lane == 0 ? 1.0f : 0.0f;
 #pragma unroll
             for (int i = 1; i < 16; ++i) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < i; j += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(
-                        L + (block + i) * kPrepPitch + block + j);
+                    const float4 l = *reinterpret_cast<const float4 *>(block + i * kPrepPitch + j);
                     sum = fmaf(l.x, x[j], sum);
                     if (j + 1 < i) sum = fmaf(l.y, x[j + 1], sum);
                     if (j + 2 < i) sum = fmaf(l.z, x[j + 2], sum);
                     if (j + 3 < i) sum = fmaf(l.w, x[j + 3], sum);
                 }
-                x[i] = i == c ? 1.0f : i < c ? 0.0f : -sum;
+                x[i] = i == lane ? 1.0f : i < lane ? 0.0f : -sum;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) T[(block + i) * kPrepPitch + block + c] = x[i];
+            for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kPrepPitch + 16 * warp + lane] = x[i];
         }
         __syncthreads();
-        // joined to blocks of 32, then of 64: L21 <- L21 T11, T21 = -T22 L21
-        auto join = [&](auto size_of, int row0, int r, int c) {
-            constexpr int kSize = decltype(size_of)::value, kCols = kSize / 4;
-            float acc[kCols];
-#pragma unroll
-            for (int x = 0; x < kCols; ++x) acc[x] = 0.0f;
-#pragma unroll 8
-            for (int j = 0; j < kSize; ++j) {
-                const float l = L[(row0 + kSize + r) * kPrepPitch + row0 + j];
-#pragma unroll
-                for (int x = 0; x < kCols; x += 4) {
-                    const float4 b = *reinterpret_cast<const float4 *>(
-                        T + (row0 + j) * kPrepPitch + row0 + c + x);
-                    acc[x] = fmaf(l, b.x, acc[x]), acc[x + 1] = fmaf(l, b.y, acc[x + 1]);
-                    acc[x + 2] = fmaf(l, b.z, acc[x + 2]), acc[x + 3] = fmaf(l, b.w, acc[x + 3]);
-                }
-            }
+        // joined to blocks of 32, then of 64: T21 = -T22 (L21 T11), the product in brackets in
+        // L's free upper half
+        {
+            const int row0 = warp / 2 * 32, c = warp % 2 * 8;
+            float y[1][4] = {};
+            block_product<16, 1>(y, L + (row0 + 16) * kPrepPitch + row0,
+                                 T + row0 * kPrepPitch + row0 + c, lane);
+            put_product<1>(y, L + row0 * kPrepPitch + row0 + 16 + c, 1.0f, lane);
             __syncthreads();
-#pragma unroll
-            for (int x = 0; x < kCols; ++x) {
-                L[(row0 + kSize + r) * kPrepPitch + row0 + c + x] = acc[x];
-                acc[x] = 0.0f;
-            }
+            float z[1][4] = {};
+            block_product<16, 1>(z, T + (row0 + 16) * kPrepPitch + row0 + 16,
+                                 L + row0 * kPrepPitch + row0 + 16 + c, lane);
+            put_product<1>(z, T + (row0 + 16) * kPrepPitch + row0 + c, -1.0f, lane);
+        }
+        __syncthreads();
+        {
+            const int r = warp % 2 * 16, c = warp / 2 * 16;
+            float y[2][4] = {};
+            block_product<32, 2>(y, L + (32 + r) * kPrepPitch, T + c, lane);
+            put_product<2>(y, L + r * kPrepPitch + 32 + c, 1.0f, lane);
             __syncthreads();
-#pragma unroll 8
-            for (int j = 0; j < kSize; ++j) {
-                const float a = T[(row0 + kSize + r) * kPrepPitch + row0 + kSize + j];
-#pragma unroll
-                for (int x = 0; x < kCols; x += 4) {
-                    const float4 b = *reinterpret_cast<const float4 *>(
-                        L + (row0 + kSize + j) * kPrepPitch + row0 + c + x);
-                    acc[x] = fmaf(a, b.x, acc[x]), acc[x + 1] = fmaf(a, b.y, acc[x + 1]);
-                    acc[x + 2] = fmaf(a, b.z, acc[x + 2]), acc[x + 3] = fmaf(a, b.w, acc[x + 3]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < kCols; ++x)
-                T[(row0 + kSize + r) * kPrepPitch + row0 + c + x] = -acc[x];
-            __syncthreads();
-        };
-        join(std::integral_constant<int, 16>(), tid / 64 * 32, tid % 64 / 4, tid % 4 * 4);
-        join(std::integral_constant<int, 32>(), 0, tid / 4, tid % 4 * 8);
+            float z[2][4] = {};
+            block_product<32, 2>(z, T + (32 + r) * kPrepPitch + 32, L + 32 + c, lane);
+            put_product<2>(z, T + (32 + r) * kPrepPitch + c, -1.0f, lane);
+        }
+        __syncthreads();
         unsigned char *const to =
             m.records + (static_cast<long long>(blockIdx.x) * p.nheads + h0 + k) * R::kBytes;
 #pragma unroll
@@ -472,10 +544,11 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
 // ---- the second pass -----------------------------------------------------------------------
 
 constexpr int kDeltaCompute = 256;
-// warps after the compute warps: one issues the products, one the copies, one looks values over
+// warps after the compute warps: one issues the products, one the copies, one looks values over,
+// one stores
 constexpr int kDeltaIssuer = kDeltaCompute / 32, kDeltaLoader = kDeltaIssuer + 1,
-              kDeltaLooker = kDeltaIssuer + 2;
-constexpr int kDeltaThreads = kDeltaCompute + 96;
+              kDeltaLooker = kDeltaIssuer + 2, kDeltaStorer = kDeltaIssuer + 3;
+constexpr int kDeltaThreads = kDeltaCompute + 128;
 constexpr int kDeltaStages = 3;
 
 template <int N>
@@ -483,13 +556,13 @@ struct DeltaSmem {
     static constexpr int kBlocks = N / 64;
     static constexpr int kK = 0;
     static constexpr int kQ = kK + kBlocks * kDeltaTile;
-    static constexpr int kV = kQ + kBlocks * kDeltaTile;
+    static constexpr int kV = kQ + kBlocks * kDeltaTile;  // the readout leaves from here
     static constexpr int kRecord = kV + 2 * kDeltaTile;
     static constexpr int kStage = kRecord + DeltaRecord::kBytes;
     static constexpr int kSwap = kDeltaStages * kStage;  // two floats per compute thread
     static constexpr int kFlags = kSwap + 2 * kDeltaCompute * 4;
     static constexpr int kBars = kFlags + 16;
-    static constexpr int kTotal = kBars + 8 * (3 * kDeltaStages + 8);
+    static constexpr int kTotal = kBars + 8 * (4 * kDeltaStages + 13);
     static_assert(kStage % 1024 == 0, "tiles start at 1024 bytes");
 };
 
@@ -514,22 +587,32 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
     }
 }
 
-// Roles.  Per chunk, with the barrier of each hand-over ([s] and [o] once per chunk, the others once
-// per chunk that is not taken token by token):
+// Roles.  Per chunk, with the barrier of each hand-over ([r], [u], [w], [d] and [m] only where the
+// chunk is not taken token by token):
 //
 //   loader:  [empty] tiles and record -> full
 //   looker:  [full] values looked over -> look
-//   issuer:  [look, s] S K^T -> p; [o] S Q^T; [r] R T^T -> u; [w] U K -> d; U M^T -> m, empty
-//   compute: [full, look, p] R -> r; [u] U -> w; [d] S -> s; [m] readout -> o, empty
+//   issuer:  [look, s] S K^T -> p; [o] S Q^T, first part; [r] R T^T -> u; S Q^T, second part;
+//            [w] U K -> d; U M^T -> m, empty
+//   compute: [full, look, p] R -> r; [u] U -> w; [d] S -> s; [m] readout into V's place -> o, t,
+//            empty
+//   storer:  [look, t] the readout's tile out -> empty
+//
+// S, R and U are handed over 16 columns of each warpgroup at a time, so that products of the first
+// run while the next are made: of a product's 4 to 24 MMAs only the last piece's are waited for.
+// S Q^T, which nothing waits for before the readout, runs in two parts under R and U.
 template <int N, typename ST, bool kIdx64>
 __global__ void __launch_bounds__(kDeltaThreads, 1)
     ssu_delta_mma_kernel(const __grid_constant__ DeltaMmaParams m,
                          const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_q,
-                         const __grid_constant__ CUtensorMap map_v) {
+                         const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_out) {
     using Smem = DeltaSmem<N>;
     using R = DeltaRecord;
     constexpr int kParts = sizeof(ST) == 4 ? 3 : 2, kBlocks = Smem::kBlocks;
+    constexpr int kCols = N / 2;           // of a row of S, per thread
+    constexpr int kPieces = kCols / 16;    // of S; R and U have two
     extern __shared__ unsigned char raw[];
     __shared__ unsigned tmem_slot;
     const SsuParams &p = m.d.m.p;
@@ -538,16 +621,17 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     unsigned char *const smem = raw + (base - smem_u32(raw));
     const unsigned bars = base + Smem::kBars;
     const unsigned full = bars, empty = bars + 8 * kDeltaStages, look = empty + 8 * kDeltaStages;
-    const unsigned bar_s = look + 8 * kDeltaStages, bar_o = bar_s + 8, bar_p = bar_s + 16,
-                   bar_r = bar_s + 24, bar_u = bar_s + 32, bar_w = bar_s + 40, bar_d = bar_s + 48,
-                   bar_m = bar_s + 56;
+    const unsigned bar_t = look + 8 * kDeltaStages, bar_s = bar_t + 8 * kDeltaStages,
+                   bar_r = bar_s + 32, bar_w = bar_r + 16, bar_o = bar_w + 16, bar_p = bar_o + 8,
+                   bar_u = bar_p + 8, bar_d = bar_u + 8, bar_m = bar_d + 8;
     if (tid == 0) {
         for (int i = 0; i < kDeltaStages; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kDeltaCompute / 32 + 1);
+            mbar_init(empty + 8 * i, kDeltaCompute / 32 + 2);
             mbar_init(look + 8 * i, 1);
+            mbar_init(bar_t + 8 * i, kDeltaCompute / 32);
         }
-        for (unsigned bar : {bar_s, bar_o, bar_r, bar_w}) mbar_init(bar, kDeltaCompute / 32);
+        for (int i = 0; i < 9; ++i) mbar_init(bar_s + 8 * i, kDeltaCompute / 32);
         for (unsigned bar : {bar_p, bar_u, bar_d, bar_m}) mbar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -562,9 +646,16 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = tmem_slot;
-    // TMEM columns: S's parts (then U's, for the next state); the next state's sum (before it, R's
-    // parts); S K^T, then U, then U in bf16; S Q^T; U M^T
-    const unsigned tS = tmem, tD = tmem + 192, tP = tmem + 320, tQ = tmem + 384, tM = tmem + 448;
+    // TMEM columns: S's parts, the third of which makes room for U's first two; the next state's sum
+    // (before it, R's parts); S K^T, then U, then in its place U in bf16 and U's third part; S Q^T;
+    // U M^T
+    const unsigned tS = tmem, tW = tmem + 128, tD = tmem + 192, tP = tmem + 320, tQ = tmem + 384,
+                   tM = tmem + 448;
+    // U's weighted parts, k-step by k-step (16 tokens): two parts of 32 columns; the third in pieces
+    auto weighted = [&](int part, int step) {
+        return part < 2 ? tW + part * 32 + 8 * step
+                        : tP + 32 * (step / 2) + 16 + 8 * (step % 2);
+    };
 
     pdl_wait();
     const int columns = p.nheads * m.slabs;
@@ -578,15 +669,23 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const int grp = group_of(h, p.group_magic);
     const int v_blocks = min(2, (p.headdim - row0 + 63) / 64);
     bool alive = true;
+    // the chunk's stage and the parity of its barriers
+    int stage = 0;
+    unsigned turn = 0;
+    auto next_stage = [&]() {
+        if (++stage == kDeltaStages) stage = 0, turn ^= 1;
+    };
+    auto flag = [&]() {
+        return reinterpret_cast<const volatile int *>(smem + Smem::kFlags)[stage] != 0;
+    };
 
     if (warp == kDeltaLoader) {
         if (lane == 0) {
             const unsigned bytes = (2 * kBlocks + v_blocks) * kDeltaTile + R::kBytes;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+            for (int c = 0; c < chunks; ++c, next_stage()) {
                 const unsigned to = base + stage * Smem::kStage, bar = full + 8 * stage;
-                if (turn > 0 && alive) alive = mbar_wait(empty + 8 * stage, (turn - 1) & 1);
+                if (c >= kDeltaStages && alive) alive = mbar_wait(empty + 8 * stage, turn ^ 1);
                 if (!alive) break;
                 mbar_expect(bar, bytes);
                 const int tok = begin + c * kDeltaChunk;
@@ -605,9 +704,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         __syncwarp();
     } else if (warp == kDeltaLooker) {
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int stage = c % kDeltaStages, turn = c / kDeltaStages;
-            if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
+        for (int c = 0; c < chunks; ++c, next_stage()) {
+            if (alive) alive = mbar_wait(full + 8 * stage, turn);
             const unsigned at = base + stage * Smem::kStage + Smem::kV;
             const int valid = min(kDeltaChunk, end - begin - c * kDeltaChunk);
             const __nv_bfloat162 zero{};
@@ -633,77 +731,120 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             }
             __syncwarp();
         }
+    } else if (warp == kDeltaStorer) {
+        if (lane == 0) {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, next_stage()) {
+                const int tok = begin + c * kDeltaChunk;
+                if (alive) alive = mbar_wait(look + 8 * stage, turn);
+                if (alive) alive = mbar_wait(bar_t + 8 * stage, turn);
+                if (!alive) break;
+                if (!flag() && tok + kDeltaChunk <= end) {
+                    for (int k = 0; k < v_blocks; ++k)
+                        tma_store(&map_out, base + stage * Smem::kStage + Smem::kV + k * kDeltaTile,
+                                  row0 + k * 64, h, tok);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                mbar_arrive(empty + 8 * stage);
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
     } else if (warp == kDeltaIssuer) {
         if (lane == 0) {
             unsigned fast = 0;  // parity of the chunks not taken token by token
+            bool any = false;
+            constexpr unsigned kTokens = instruction(kDeltaChunk, false, false);
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+            for (int c = 0; c < chunks; ++c, next_stage()) {
                 const unsigned at = base + stage * Smem::kStage;
-                if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
-                if (alive) alive = mbar_wait(look + 8 * stage, turn & 1);
-                if (alive) alive = mbar_wait(bar_s, c & 1);
+                if (alive) alive = mbar_wait(full + 8 * stage, turn);
+                if (alive) alive = mbar_wait(look + 8 * stage, turn);
                 if (!alive) break;
-                if (reinterpret_cast<const volatile int *>(smem + Smem::kFlags)[stage]) {
-                    if (c > 0) alive = mbar_wait(bar_o, (c - 1) & 1);
+                if (flag()) {
+                    for (int x = 0; x < kPieces && alive; ++x)
+                        alive = mbar_wait(bar_s + 8 * x, c & 1);
+                    if (c > 0 && alive) alive = mbar_wait(bar_o, (c - 1) & 1);
+                    mbar_arrive(bar_p);
                     mbar_arrive(empty + 8 * stage);
                     continue;
                 }
-                tc_fence_after();
-                // small parts first: sums lose less
+                // U of the last such chunk has been read before its place is written
+                if (any && alive) alive = mbar_wait(bar_m, fast ^ 1);
+                any = true;
 #pragma unroll
-                for (int part = kParts - 1; part >= 0; --part)
+                for (int x = 0; x < kPieces; ++x) {
+                    if (alive) alive = mbar_wait(bar_s + 8 * x, c & 1);
+                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        mma_ts(tP, tS + part * (N / 2) + 8 * k,
-                               operand(at + Smem::kK + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
-                               instruction(kDeltaChunk, false, false), part < kParts - 1 || k > 0);
+                    for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int k = x + half * kPieces;
+                            mma_ts(tP, tS + part * (N / 2) + 8 * k,
+                                   operand(at + Smem::kK + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
+                                   kTokens, x > 0 || part < kParts - 1 || half > 0);
+                        }
+                }
                 tc_commit(bar_p);
-                if (c > 0) alive = mbar_wait(bar_o, (c - 1) & 1);
+                if (c > 0 && alive) alive = mbar_wait(bar_o, (c - 1) & 1);
+                if (!alive) break;
                 tc_fence_after();
-#pragma unroll
-                for (int part = 1; part >= 0; --part)
+                auto read = [&](int part, bool add) {
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k)
                         mma_ts(tQ, tS + part * (N / 2) + 8 * k,
                                operand(at + Smem::kQ + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
-                               instruction(kDeltaChunk, false, false), part < 1 || k > 0);
-                if (alive) alive = mbar_wait(bar_r, fast);
-                if (!alive) break;
-                tc_fence_after();
-                const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
-                auto correct = [&](int part, unsigned t, bool add) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts(tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0),
-                               instruction(kDeltaChunk, false, false), add || k > 0);
+                               kTokens, add || k > 0);
                 };
-                if constexpr (kParts == 3) {
-                    correct(2, t1, false);
-                    correct(1, t2, true);
-                    correct(0, t2, true);
-                } else {
-                    correct(0, t2, false);
+                read(1, false);
+                const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (alive) alive = mbar_wait(bar_r + 8 * x, fast);
+                    tc_fence_after();
+                    auto correct = [&](int part, unsigned t, bool add) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int k = x + 2 * half;
+                            mma_ts(tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0), kTokens,
+                                   add || half > 0);
+                        }
+                    };
+                    if constexpr (kParts == 3) {  // small parts first: sums lose less
+                        correct(2, t1, x > 0);
+                        correct(1, t2, true);
+                        correct(0, t2, true);
+                    } else {
+                        correct(0, t2, x > 0);
+                    }
+                    correct(1, t1, true);
+                    correct(0, t1, true);
                 }
-                correct(1, t1, true);
-                correct(0, t1, true);
                 tc_commit(bar_u);
-                if (alive) alive = mbar_wait(bar_w, fast);
-                if (!alive) break;
-                tc_fence_after();
+                read(0, true);
 #pragma unroll
-                for (int part = kParts - 1; part >= 0; --part)
+                for (int x = 0; x < 2; ++x) {
+                    if (alive) alive = mbar_wait(bar_w + 8 * x, fast);
+                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts(tD, tS + part * 32 + 8 * k,
-                               operand(at + Smem::kK + k * 2048, N == 128 ? kDeltaTile : 0),
-                               instruction(N, false, true), part < kParts - 1 || k > 0);
+                    for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int k = x + 2 * half;
+                            mma_ts(tD, weighted(part, k),
+                                   operand(at + Smem::kK + k * 2048, N == 128 ? kDeltaTile : 0),
+                                   instruction(N, false, true),
+                                   x > 0 || part < kParts - 1 || half > 0);
+                        }
+                }
                 tc_commit(bar_d);
+                if (!alive) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_ts(tM, tP + 32 * (k / 2) + 8 * (k % 2),
-                           operand(at + Smem::kRecord + R::kM + k * 32, 0),
-                           instruction(kDeltaChunk, false, false), k > 0);
+                           operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, k > 0);
                 tc_commit(empty + 8 * stage);
                 tc_commit(bar_m);
                 fast ^= 1;
@@ -715,7 +856,6 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         const int row = 32 * quarter + lane;  // TMEM lane; state row row0 + row
         const bool own = row0 + row < p.headdim;
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;
-        constexpr int kCols = N / 2;  // of the thread's half row
         float S[kCols];
         long long slot = 0;
         if (prompt.x) slot = load_slot<kIdx64>(p, b);
@@ -740,55 +880,49 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
             for (int i = 0; i < kCols; ++i) S[i] = 0.0f;
         }
-        auto publish = [&](int k) {  // 16 columns of S as the next products' operand
+        auto hand_over = [&](unsigned bar) {
+            tc_wait_st();
+            tc_fence_before();
+            warp_arrive(bar, lane);
+        };
+        auto publish = [&](int x) {  // 16 columns of S as the next products' operand
             unsigned bits[kParts][8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 unsigned w[kParts];
-                split2<kParts>(make_float2(S[16 * k + 2 * i], S[16 * k + 2 * i + 1]), w);
+                split2<kParts>(make_float2(S[16 * x + 2 * i], S[16 * x + 2 * i + 1]), w);
 #pragma unroll
                 for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
             }
 #pragma unroll
             for (int part = 0; part < kParts; ++part)
-                tc_store8(tS + lanes + part * (N / 2) + half * (N / 4) + 8 * k, bits[part]);
+                tc_store8(tS + lanes + part * (N / 2) + half * (N / 4) + 8 * x, bits[part]);
+            hand_over(bar_s + 8 * x);
         };
-        auto published = [&]() {
-            tc_wait_st();
-            tc_fence_before();
-            warp_arrive(bar_s, lane);
-        };
-        if (chunks) {
+        if (chunks)
 #pragma unroll
-            for (int k = 0; k < kCols / 16; ++k) publish(k);
-            published();
-        }
+            for (int x = 0; x < kPieces; ++x) publish(x);
         unsigned fast = 0;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const int stage = c % kDeltaStages, turn = c / kDeltaStages;
+        for (int c = 0; c < chunks; ++c, next_stage()) {
             const unsigned at = base + stage * Smem::kStage;
             const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
             const float *const vec = reinterpret_cast<const float *>(
                 smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
-            // the thread's column of V
+            // the thread's column of V, and later of the readout
             const unsigned v_at = at + Smem::kV + (row >> 6) * kDeltaTile + 2 * (row & 7);
             const int v_piece = (row & 63) >> 3;
+            auto v_of = [&](int j) { return v_at + j * 128 + ((v_piece ^ (j & 7)) << 4); };
             auto value = [&](int j) {
                 unsigned short u;
-                asm volatile("ld.shared.u16 %0, [%1];"
-                             : "=h"(u)
-                             : "r"(v_at + j * 128 + ((v_piece ^ (j & 7)) << 4))
-                             : "memory");
-                return __uint_as_float(static_cast<unsigned>(u) << 16);
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(v_of(j)) : "memory");
+                return static_cast<unsigned>(u) << 16;
             };
             __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
                                        h * p.out_h + row0 + row;
-            if (alive) alive = mbar_wait(full + 8 * stage, turn & 1);
-            if (alive) alive = mbar_wait(look + 8 * stage, turn & 1);
-            const bool slow =
-                reinterpret_cast<const volatile int *>(smem + Smem::kFlags)[stage] != 0;
-            if (__builtin_expect(slow, 0)) {
+            if (alive) alive = mbar_wait(full + 8 * stage, turn);
+            if (alive) alive = mbar_wait(look + 8 * stage, turn);
+            if (__builtin_expect(flag(), 0)) {
                 float *const swap = reinterpret_cast<float *>(smem + Smem::kSwap);
                 auto both = [&](float mine, float *room) {  // the sum over both halves of the row
                     room[tid] = mine;
@@ -820,7 +954,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         part = fmaf(S[i + 2], k.z, part), part = fmaf(S[i + 3], k.w, part);
                     }
                     const float sk = both(part, swap) * rk;
-                    const float e = vec[R::kBeta + t] * (value(t) - a * sk) * rk;
+                    const float e =
+                        vec[R::kBeta + t] * (__uint_as_float(value(t)) - a * sk) * rk;
                     part = 0.0f;
 #pragma unroll
                     for (int i = 0; i < kCols; i += 4) {
@@ -835,153 +970,175 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     const float y = both(part, swap + kDeltaCompute) * vec[R::kRead + t];
                     if (half == 0 && own) out[t * p.out_b] = __float2bfloat16(y);
                 }
-                if (c + 1 < chunks) {
+                if (alive) alive = mbar_wait(bar_p, c & 1);  // the issuer has come this far
+                __syncwarp();
+                if (c + 1 < chunks)
 #pragma unroll
-                    for (int k = 0; k < kCols / 16; ++k) publish(k);
-                    published();
-                }
+                    for (int x = 0; x < kPieces; ++x) publish(x);
+                warp_arrive(bar_t + 8 * stage, lane);
                 warp_arrive(bar_o, lane);
                 warp_arrive(empty + 8 * stage, lane);
                 continue;
             }
             // R = beta v - (beta e^s / |k|) S k
-            if (alive) alive = mbar_wait(bar_p, fast);
+            unsigned v[16];  // two tokens each
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = __byte_perm(value(32 * half + 2 * i), value(32 * half + 2 * i + 1), 0x7632);
+            if (alive) alive = mbar_wait(bar_p, c & 1);
             __syncwarp();
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int j0 = 32 * half + 16 * k;
-                unsigned sk[16], bits[kParts][8];
-                tc_load16(tP + lanes + j0, sk);
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = value(j0 + i);
+            {
+                unsigned sk[2][16];
+                tc_load16(tP + lanes + 32 * half, sk[0]);
+                tc_load16(tP + lanes + 32 * half + 16, sk[1]);
                 tc_wait_ld();
-                const float4 *const beta = reinterpret_cast<const float4 *>(vec + R::kBeta + j0);
-                const float4 *const past = reinterpret_cast<const float4 *>(vec + R::kPast + j0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 bt = beta[i], ps = past[i];
-                    float2 lo = __ffma2_rn(make_float2(-ps.x, -ps.y),
-                                           make_float2(__uint_as_float(sk[4 * i]),
-                                                       __uint_as_float(sk[4 * i + 1])),
-                                           __fmul2_rn(make_float2(bt.x, bt.y),
-                                                      make_float2(v[4 * i], v[4 * i + 1])));
-                    float2 hi = __ffma2_rn(make_float2(-ps.z, -ps.w),
-                                           make_float2(__uint_as_float(sk[4 * i + 2]),
-                                                       __uint_as_float(sk[4 * i + 3])),
-                                           __fmul2_rn(make_float2(bt.z, bt.w),
-                                                      make_float2(v[4 * i + 2], v[4 * i + 3])));
-                    if (valid < kDeltaChunk) {  // tokens of the next prompt
-                        const int j = j0 + 4 * i;
-                        if (j >= valid) lo.x = 0.0f;
-                        if (j + 1 >= valid) lo.y = 0.0f;
-                        if (j + 2 >= valid) hi.x = 0.0f;
-                        if (j + 3 >= valid) hi.y = 0.0f;
+                for (int x = 0; x < 2; ++x) {
+                    const int j0 = 32 * half + 16 * x;
+                    unsigned bits[kParts][8];
+                    const float4 *const beta =
+                        reinterpret_cast<const float4 *>(vec + R::kBeta + j0);
+                    const float4 *const past =
+                        reinterpret_cast<const float4 *>(vec + R::kPast + j0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 bt = beta[i / 2], ps = past[i / 2];
+                        const unsigned u = v[8 * x + i];
+                        float2 r = __ffma2_rn(
+                            i % 2 ? make_float2(-ps.z, -ps.w) : make_float2(-ps.x, -ps.y),
+                            make_float2(__uint_as_float(sk[x][2 * i]),
+                                        __uint_as_float(sk[x][2 * i + 1])),
+                            __fmul2_rn(i % 2 ? make_float2(bt.z, bt.w) : make_float2(bt.x, bt.y),
+                                       make_float2(__uint_as_float(u << 16),
+                                                   __uint_as_float(u & 0xffff0000u))));
+                        if (valid < kDeltaChunk) {  // tokens of the next prompt
+                            if (j0 + 2 * i >= valid) r.x = 0.0f;
+                            if (j0 + 2 * i + 1 >= valid) r.y = 0.0f;
+                        }
+                        if (!own) r = make_float2(0.0f, 0.0f);
+                        unsigned w[kParts];
+                        split2<kParts>(r, w);
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
                     }
-                    if (!own) lo = hi = make_float2(0.0f, 0.0f);
-                    unsigned w[kParts];
-                    split2<kParts>(lo, w);
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part) bits[part][2 * i] = w[part];
-                    split2<kParts>(hi, w);
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part) bits[part][2 * i + 1] = w[part];
+                    for (int part = 0; part < kParts; ++part)
+                        tc_store8(tD + lanes + part * 32 + j0 / 2, bits[part]);
+                    if (x == 0 && valid < kDeltaChunk) {
+                        // what the next state's product must not meet
+                        for (int k = tid; k < (kDeltaChunk - valid) * 8 * kBlocks;
+                             k += kDeltaCompute)
+                            store_smem16(at + Smem::kK + k / 8 % kBlocks * kDeltaTile +
+                                             (valid + k / 8 / kBlocks) * 128 + k % 8 * 16,
+                                         make_uint4(0, 0, 0, 0));
+                        fence_async_smem();
+                    }
+                    hand_over(bar_r + 8 * x);
                 }
-#pragma unroll
-                for (int part = 0; part < kParts; ++part)
-                    tc_store8(tD + lanes + part * 32 + j0 / 2, bits[part]);
             }
-            if (valid < kDeltaChunk) {  // what the next state's product must not meet
-                for (int k = tid; k < (kDeltaChunk - valid) * 8 * kBlocks; k += kDeltaCompute)
-                    store_smem16(at + Smem::kK + k / 8 % kBlocks * kDeltaTile +
-                                     (valid + k / 8 / kBlocks) * 128 + k % 8 * 16,
-                                 make_uint4(0, 0, 0, 0));
-                fence_async_smem();
-            }
-            tc_wait_st();
-            tc_fence_before();
-            warp_arrive(bar_r, lane);
             // U for the readout, and with its weights for the next state
             if (alive) alive = mbar_wait(bar_u, fast);
             __syncwarp();
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int j0 = 32 * half + 16 * k;
-                unsigned u[16], plain[8], bits[kParts][8];
-                tc_load16(tP + lanes + j0, u);
+            {
+                unsigned u[2][16];
+                tc_load16(tP + lanes + 32 * half, u[0]);
+                tc_load16(tP + lanes + 32 * half + 16, u[1]);
                 tc_wait_ld();
-                const float4 *const left = reinterpret_cast<const float4 *>(vec + R::kLeft + j0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 l = left[i / 2];
-                    const float2 f =
-                        make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-                    plain[i] = f2_to_bf2(f.x, f.y);
-                    unsigned w[kParts];
-                    split2<kParts>(__fmul2_rn(f, i % 2 ? make_float2(l.z, l.w)
-                                                       : make_float2(l.x, l.y)),
-                                   w);
+                for (int x = 0; x < 2; ++x) {
+                    unsigned plain[8], bits[kParts][8];
+                    const float4 *const left =
+                        reinterpret_cast<const float4 *>(vec + R::kLeft + 32 * half + 16 * x);
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 l = left[i / 2];
+                        const float2 f = make_float2(__uint_as_float(u[x][2 * i]),
+                                                     __uint_as_float(u[x][2 * i + 1]));
+                        plain[i] = f2_to_bf2(f.x, f.y);
+                        unsigned w[kParts];
+                        split2<kParts>(__fmul2_rn(f, i % 2 ? make_float2(l.z, l.w)
+                                                           : make_float2(l.x, l.y)),
+                                       w);
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+                    }
+                    // (in tP over columns that this thread alone has read)
+                    tc_store8(tP + lanes + 32 * half + 8 * x, plain);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+                        tc_store8(weighted(part, 2 * half + x) + lanes, bits[part]);
+                    hand_over(bar_w + 8 * x);
                 }
-                // (over columns that this thread alone has read)
-                tc_store8(tP + lanes + 32 * half + 8 * k, plain);
-#pragma unroll
-                for (int part = 0; part < kParts; ++part)
-                    tc_store8(tS + lanes + part * 32 + j0 / 2, bits[part]);
             }
-            tc_wait_st();
-            tc_fence_before();
-            warp_arrive(bar_w, lane);
             const float whole = vec[R::kWhole];
             if (alive) alive = mbar_wait(bar_d, fast);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kCols / 16; ++k) {
-                unsigned d[16];
-                tc_load16(tD + lanes + half * kCols + 16 * k, d);
+            for (int y = 0; y < kPieces / 2; ++y) {
+                unsigned d[2][16];
+                tc_load16(tD + lanes + half * kCols + 32 * y, d[0]);
+                tc_load16(tD + lanes + half * kCols + 32 * y + 16, d[1]);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float2 s = __ffma2_rn(
-                        make_float2(S[16 * k + i], S[16 * k + i + 1]), make_float2(whole, whole),
-                        make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
-                    S[16 * k + i] = s.x;
-                    S[16 * k + i + 1] = s.y;
+                for (int x = 0; x < 2; ++x) {
+                    float *const at_s = S + 32 * y + 16 * x;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 f = __ffma2_rn(
+                            make_float2(at_s[i], at_s[i + 1]), make_float2(whole, whole),
+                            make_float2(__uint_as_float(d[x][i]), __uint_as_float(d[x][i + 1])));
+                        at_s[i] = f.x;
+                        at_s[i + 1] = f.y;
+                    }
+                    if (c + 1 < chunks) publish(2 * y + x);
                 }
-                if (c + 1 < chunks) publish(k);
             }
-            if (c + 1 < chunks) published();
             if (alive) alive = mbar_wait(bar_m, fast);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int j0 = 32 * half + 16 * k;
+            for (int x = 0; x < 2; ++x) {
+                const int j0 = 32 * half + 16 * x;
                 unsigned sq[16], um[16];
                 tc_load16(tQ + lanes + j0, sq);
                 tc_load16(tM + lanes + j0, um);
-                tc_wait_ld();
                 const float4 *const read = reinterpret_cast<const float4 *>(vec + R::kRead + j0);
                 const float4 *const past = reinterpret_cast<const float4 *>(vec + R::kReadS + j0);
+                tc_wait_ld();
+                if (x == 1) {
+                    tc_fence_before();
+                    warp_arrive(bar_o, lane);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 r = read[i], s = past[i];
-                    const float f[4] = {r.x, r.y, r.z, r.w}, e[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int j = j0 + 4 * i + x;
-                        const float y = fmaf(e[x], __uint_as_float(sq[4 * i + x]),
-                                             f[x] * __uint_as_float(um[4 * i + x]));
-                        if (j < valid && own) out[j * p.out_b] = __float2bfloat16(y);
+                for (int i = 0; i < 8; ++i) {
+                    const float4 r = read[i / 2], e = past[i / 2];
+                    const float2 y = __ffma2_rn(
+                        i % 2 ? make_float2(e.z, e.w) : make_float2(e.x, e.y),
+                        make_float2(__uint_as_float(sq[2 * i]), __uint_as_float(sq[2 * i + 1])),
+                        __fmul2_rn(i % 2 ? make_float2(r.z, r.w) : make_float2(r.x, r.y),
+                                   make_float2(__uint_as_float(um[2 * i]),
+                                               __uint_as_float(um[2 * i + 1]))));
+                    const unsigned two = f2_to_bf2(y.x, y.y);
+                    const int j = j0 + 2 * i;
+                    if (valid == kDeltaChunk) {
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_of(j)),
+                                     "h"(static_cast<unsigned short>(two))
+                                     : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_of(j + 1)),
+                                     "h"(static_cast<unsigned short>(two >> 16))
+                                     : "memory");
+                    } else if (own) {
+                        if (j < valid) out[j * p.out_b] = __ushort_as_bfloat16(two & 0xffff);
+                        if (j + 1 < valid)
+                            out[(j + 1) * p.out_b] = __ushort_as_bfloat16(two >> 16);
                     }
                 }
             }
-            tc_fence_before();
-            warp_arrive(bar_o, lane);
+            fence_async_smem();
+            warp_arrive(bar_t + 8 * stage, lane);
             warp_arrive(empty + 8 * stage, lane);
             fast ^= 1;
         }
