@@ -575,6 +575,49 @@ __device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigne
         : "memory");
 }
 
+// TMEM in the fragments of an 8 x 8 matrix: of 16 lanes and 8 columns a thread holds columns 2 t and
+// 2 t + 1 (t = lane % 4) of lanes g and g + 8 (g = lane / 4), and of packed pairs column t of 4.
+// So V comes by ldmatrix and the readout goes by stmatrix, both transposed, with a pair of tokens
+// per register (an element per load and store kept shared memory busy for 2,000 cycles per chunk).
+__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[16]) {  // 32 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[8]) {  // 16 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[4]) {  // 8 columns
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void load_trans4(unsigned (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_trans4(unsigned addr, const unsigned (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // Two values as bf16 parts; each part is what the ones before leave.
 template <int kParts>
 __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
@@ -591,7 +634,7 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 // chunk is not taken token by token):
 //
 //   loader:  [empty] tiles and record -> full
-//   looker:  [full] values looked over -> look
+//   looker:  [full] values looked over, a prompt's last chunk cut -> look
 //   issuer:  [look, s] S K^T -> p; [o] S Q^T, first part; [r] R T^T -> u; S Q^T, second part;
 //            [w] U K -> d; U M^T -> m, empty
 //   compute: [full, look, p] R -> r; [u] U -> w; [d] S -> s; [m] readout into V's place -> o, t,
@@ -722,6 +765,18 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             sum[0] = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
             const bool any = __any_sync(
                 0xffffffffu, (reinterpret_cast<const unsigned &>(sum[0]) & 0x7fff7fffu) != 0);
+            if (valid < kDeltaChunk) {  // tokens of the next prompt, which products would meet
+                for (int k = lane; k < (kDeltaChunk - valid) * 8; k += 32) {
+                    const unsigned to =
+                        base + stage * Smem::kStage + (valid + k / 8) * 128 + k % 8 * 16;
+                    for (int t = 0; t < kBlocks; ++t)
+                        store_smem16(to + Smem::kK + t * kDeltaTile, make_uint4(0, 0, 0, 0));
+                    for (int t = 0; t < v_blocks; ++t)
+                        store_smem16(to + Smem::kV + t * kDeltaTile, make_uint4(0, 0, 0, 0));
+                }
+                fence_async_smem();
+                __syncwarp();
+            }
             if (lane == 0) {
                 const float *const vec = reinterpret_cast<const float *>(
                     smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
@@ -852,51 +907,70 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         }
         __syncwarp();
     } else {
+        // A warp has 32 of the state's rows (TMEM lanes) and half of its columns, or half the tokens.
+        // A thread has rows g + 8 e of its 16 lanes `hh`, columns 8 i + 2 t, + 1 of every block i.
         const int quarter = warp & 3, half = warp >> 2;
-        const int row = 32 * quarter + lane;  // TMEM lane; state row row0 + row
-        const bool own = row0 + row < p.headdim;
+        const int g = lane >> 2, t = lane & 3;
         const unsigned lanes = static_cast<unsigned>(quarter) << 21;
-        float S[kCols];
+        constexpr unsigned kLanes16 = 16u << 16;
+        constexpr int kCol8 = kCols / 8;
+        float2 S[kCol8][2][2];  // [block][hh][e]
         long long slot = 0;
         if (prompt.x) slot = load_slot<kIdx64>(p, b);
         ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
-                          (row0 + row) * p.st_row + half * kCols;
-        constexpr int kPer = 16 / static_cast<int>(sizeof(ST));
-        if (prompt.x && own && !fresh && chunks) {
+                          half * kCols + 2 * t;
+        auto row_at = [&](int hh, int e) { return 32 * quarter + 16 * hh + 8 * e + g; };
+        const bool reads = prompt.x && !fresh && chunks;
 #pragma unroll
-            for (int i = 0; i < kCols / kPer; ++i) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(state) + i);
-                if constexpr (sizeof(ST) == 4) {
-                    S[4 * i] = __uint_as_float(w.x), S[4 * i + 1] = __uint_as_float(w.y);
-                    S[4 * i + 2] = __uint_as_float(w.z), S[4 * i + 3] = __uint_as_float(w.w);
-                } else {
-                    float f[8];
-                    widen16(w, f);
+        for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) S[8 * i + k] = f[k];
+            for (int e = 0; e < 2; ++e) {
+                const int row = row0 + row_at(hh, e);
+                const ST *const from = state + row * p.st_row;
+#pragma unroll
+                for (int i = 0; i < kCol8; ++i) {
+                    S[i][hh][e] = make_float2(0.0f, 0.0f);
+                    if (!reads || row >= p.headdim) continue;
+                    if constexpr (sizeof(ST) == 4) {
+                        S[i][hh][e] = __ldcs(reinterpret_cast<const float2 *>(from + 8 * i));
+                    } else {
+                        const unsigned w = __ldcs(reinterpret_cast<const unsigned *>(from + 8 * i));
+                        S[i][hh][e] = make_float2(__uint_as_float(w << 16),
+                                                  __uint_as_float(w & 0xffff0000u));
+                    }
                 }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) S[i] = 0.0f;
-        }
         auto hand_over = [&](unsigned bar) {
             tc_wait_st();
             tc_fence_before();
             warp_arrive(bar, lane);
         };
-        auto publish = [&](int x) {  // 16 columns of S as the next products' operand
-            unsigned bits[kParts][8];
+        // Two blocks of pairs as bf16 parts, to the columns that `to(part)` names.
+        auto put = [&](const float2 (&f)[2][2][2], auto to) {
+            unsigned bits[kParts][2][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                unsigned w[kParts];
-                split2<kParts>(make_float2(S[16 * x + 2 * i], S[16 * x + 2 * i + 1]), w);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
-            }
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        unsigned w[kParts];
+                        split2<kParts>(f[i][hh][e], w);
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) bits[part][hh][2 * i + e] = w[part];
+                    }
 #pragma unroll
             for (int part = 0; part < kParts; ++part)
-                tc_store8(tS + lanes + part * (N / 2) + half * (N / 4) + 8 * x, bits[part]);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tc_store_frag(to(part) + lanes + hh * kLanes16, bits[part][hh]);
+        };
+        auto publish = [&](int x) {  // 16 columns of S as the next products' operand
+            const float2 f[2][2][2] = {
+                {{S[2 * x][0][0], S[2 * x][0][1]}, {S[2 * x][1][0], S[2 * x][1][1]}},
+                {{S[2 * x + 1][0][0], S[2 * x + 1][0][1]},
+                 {S[2 * x + 1][1][0], S[2 * x + 1][1][1]}}};
+            put(f, [&](int part) { return tS + part * (N / 2) + half * (N / 4) + 8 * x; });
             hand_over(bar_s + 8 * x);
         };
         if (chunks)
@@ -909,66 +983,92 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
             const float *const vec = reinterpret_cast<const float *>(
                 smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
-            // the thread's column of V, and later of the readout
-            const unsigned v_at = at + Smem::kV + (row >> 6) * kDeltaTile + 2 * (row & 7);
-            const int v_piece = (row & 63) >> 3;
-            auto v_of = [&](int j) { return v_at + j * 128 + ((v_piece ^ (j & 7)) << 4); };
-            auto value = [&](int j) {
-                unsigned short u;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(v_of(j)) : "memory");
-                return static_cast<unsigned>(u) << 16;
-            };
             __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
-                                       h * p.out_h + row0 + row;
+                                       h * p.out_h + row0;
             if (alive) alive = mbar_wait(full + 8 * stage, turn);
             if (alive) alive = mbar_wait(look + 8 * stage, turn);
+            __syncwarp();
             if (__builtin_expect(flag(), 0)) {
                 float *const swap = reinterpret_cast<float *>(smem + Smem::kSwap);
-                auto both = [&](float mine, float *room) {  // the sum over both halves of the row
-                    room[tid] = mine;
+                // the rows' sums over the quad's lanes and both warpgroups' columns
+                auto whole_rows = [&](float (&sum)[2][2], float *room) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            sum[hh][e] += __shfl_xor_sync(0xffffffffu, sum[hh][e], 1);
+                            sum[hh][e] += __shfl_xor_sync(0xffffffffu, sum[hh][e], 2);
+                            if (t == 0) room[half * kDeltaRows + row_at(hh, e)] = sum[hh][e];
+                        }
                     asm volatile("bar.sync 1, %0;" ::"n"(kDeltaCompute) : "memory");
-                    return room[row] + room[kDeltaRows + row];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            sum[hh][e] =
+                                room[row_at(hh, e)] + room[kDeltaRows + row_at(hh, e)];
                 };
-                // four of the thread's columns of token t's key or query
-                auto row_of = [&](int tile, int t, int i) {
-                    const int col = half * kCols + i;
-                    uint2 w;
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(w.x), "=r"(w.y)
-                                 : "r"(swizzled(at + tile + (col / 64) * kDeltaTile, t,
-                                                col % 64 / 8) + 2 * (col % 8))
+                // the thread's two columns of block i of token k's key or query
+                auto pair_of = [&](int tile, int k, int i) {
+                    const int col = half * kCols + 8 * i;
+                    unsigned w;
+                    asm volatile("ld.shared.u32 %0, [%1];"
+                                 : "=r"(w)
+                                 : "r"(swizzled(at + tile + (col / 64) * kDeltaTile, k,
+                                                col % 64 / 8) + 4 * t)
                                  : "memory");
-                    return make_float4(__uint_as_float(w.x << 16),
-                                       __uint_as_float(w.x & 0xffff0000u),
-                                       __uint_as_float(w.y << 16),
-                                       __uint_as_float(w.y & 0xffff0000u));
+                    return make_float2(__uint_as_float(w << 16),
+                                       __uint_as_float(w & 0xffff0000u));
                 };
 #pragma unroll 1
-                for (int t = 0; t < valid; ++t) {
-                    const float a = vec[R::kDecay + t], rk = vec[R::kKey + t];
-                    float part = 0.0f;
+                for (int k = 0; k < valid; ++k) {
+                    const float a = vec[R::kDecay + k], rk = vec[R::kKey + k];
+                    float sum[2][2] = {};
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 4) {
-                        const float4 k = row_of(Smem::kK, t, i);
-                        part = fmaf(S[i], k.x, part), part = fmaf(S[i + 1], k.y, part);
-                        part = fmaf(S[i + 2], k.z, part), part = fmaf(S[i + 3], k.w, part);
-                    }
-                    const float sk = both(part, swap) * rk;
-                    const float e =
-                        vec[R::kBeta + t] * (__uint_as_float(value(t)) - a * sk) * rk;
-                    part = 0.0f;
+                    for (int i = 0; i < kCol8; ++i) {
+                        const float2 key = pair_of(Smem::kK, k, i);
 #pragma unroll
-                    for (int i = 0; i < kCols; i += 4) {
-                        const float4 k = row_of(Smem::kK, t, i), q = row_of(Smem::kQ, t, i);
-                        S[i] = fmaf(S[i], a, e * k.x);
-                        S[i + 1] = fmaf(S[i + 1], a, e * k.y);
-                        S[i + 2] = fmaf(S[i + 2], a, e * k.z);
-                        S[i + 3] = fmaf(S[i + 3], a, e * k.w);
-                        part = fmaf(S[i], q.x, part), part = fmaf(S[i + 1], q.y, part);
-                        part = fmaf(S[i + 2], q.z, part), part = fmaf(S[i + 3], q.w, part);
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 s = S[i][x / 2][x % 2];
+                            sum[x / 2][x % 2] += s.x * key.x + s.y * key.y;
+                        }
                     }
-                    const float y = both(part, swap + kDeltaCompute) * vec[R::kRead + t];
-                    if (half == 0 && own) out[t * p.out_b] = __float2bfloat16(y);
+                    whole_rows(sum, swap);
+                    float e[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = row_at(x / 2, x % 2);
+                        unsigned short v;
+                        asm volatile("ld.shared.u16 %0, [%1];"
+                                     : "=h"(v)
+                                     : "r"(swizzled(at + Smem::kV + row / 64 * kDeltaTile, k,
+                                                    row % 64 / 8) + 2 * (row % 8))
+                                     : "memory");
+                        e[x] = vec[R::kBeta + k] * rk *
+                               (__uint_as_float(static_cast<unsigned>(v) << 16) -
+                                a * (sum[x / 2][x % 2] * rk));
+                        sum[x / 2][x % 2] = 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kCol8; ++i) {
+                        const float2 key = pair_of(Smem::kK, k, i), q = pair_of(Smem::kQ, k, i);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float2 &s = S[i][x / 2][x % 2];
+                            s.x = fmaf(s.x, a, e[x] * key.x);
+                            s.y = fmaf(s.y, a, e[x] * key.y);
+                            sum[x / 2][x % 2] += s.x * q.x + s.y * q.y;
+                        }
+                    }
+                    whole_rows(sum, swap + kDeltaCompute);
+                    if (half == 0 && t == 0)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int row = row_at(x / 2, x % 2);
+                            if (row0 + row < p.headdim)
+                                out[k * p.out_b + row] =
+                                    __float2bfloat16(sum[x / 2][x % 2] * vec[R::kRead + k]);
+                        }
                 }
                 if (alive) alive = mbar_wait(bar_p, c & 1);  // the issuer has come this far
                 __syncwarp();
@@ -980,60 +1080,54 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 warp_arrive(empty + 8 * stage, lane);
                 continue;
             }
+            // Matrix k % 4 of 16 tokens and 16 rows `hh` in V's tiles, where ldmatrix and stmatrix
+            // take their rows' addresses from lanes.
+            auto v_at = [&](int x, int hh) {
+                const int token = 32 * half + 16 * x + 8 * (lane >> 4) + (lane & 7);
+                const int row = 32 * quarter + 16 * hh + 8 * (lane >> 3 & 1);
+                return swizzled(at + Smem::kV + (row >> 6) * kDeltaTile, token, (row & 63) >> 3);
+            };
+            // the two tokens of block i (of the warpgroup's four) that the thread has
+            auto factors = [&](int kind, int i) {
+                return *reinterpret_cast<const float2 *>(vec + kind + 32 * half + 8 * i + 2 * t);
+            };
             // R = beta v - (beta e^s / |k|) S k
-            unsigned v[16];  // two tokens each
+            unsigned v[2][2][4];  // [piece][hh][block, e]
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[i] = __byte_perm(value(32 * half + 2 * i), value(32 * half + 2 * i + 1), 0x7632);
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) load_trans4(v[x][hh], v_at(x, hh));
             if (alive) alive = mbar_wait(bar_p, c & 1);
             __syncwarp();
             tc_fence_after();
             {
                 unsigned sk[2][16];
-                tc_load16(tP + lanes + 32 * half, sk[0]);
-                tc_load16(tP + lanes + 32 * half + 16, sk[1]);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half, sk[hh]);
                 tc_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int j0 = 32 * half + 16 * x;
-                    unsigned bits[kParts][8];
-                    const float4 *const beta =
-                        reinterpret_cast<const float4 *>(vec + R::kBeta + j0);
-                    const float4 *const past =
-                        reinterpret_cast<const float4 *>(vec + R::kPast + j0);
+                    float2 r[2][2][2];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 bt = beta[i / 2], ps = past[i / 2];
-                        const unsigned u = v[8 * x + i];
-                        float2 r = __ffma2_rn(
-                            i % 2 ? make_float2(-ps.z, -ps.w) : make_float2(-ps.x, -ps.y),
-                            make_float2(__uint_as_float(sk[x][2 * i]),
-                                        __uint_as_float(sk[x][2 * i + 1])),
-                            __fmul2_rn(i % 2 ? make_float2(bt.z, bt.w) : make_float2(bt.x, bt.y),
-                                       make_float2(__uint_as_float(u << 16),
-                                                   __uint_as_float(u & 0xffff0000u))));
-                        if (valid < kDeltaChunk) {  // tokens of the next prompt
-                            if (j0 + 2 * i >= valid) r.x = 0.0f;
-                            if (j0 + 2 * i + 1 >= valid) r.y = 0.0f;
-                        }
-                        if (!own) r = make_float2(0.0f, 0.0f);
-                        unsigned w[kParts];
-                        split2<kParts>(r, w);
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 beta = factors(R::kBeta, 2 * x + i);
+                        const float2 past = factors(R::kPast, 2 * x + i);
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+                        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const unsigned u = v[x][hh][2 * i + e];
+                                const int k = 8 * x + 4 * i + 2 * e;
+                                r[i][hh][e] = __ffma2_rn(
+                                    make_float2(-past.x, -past.y),
+                                    make_float2(__uint_as_float(sk[hh][k]),
+                                                __uint_as_float(sk[hh][k + 1])),
+                                    __fmul2_rn(beta, make_float2(__uint_as_float(u << 16),
+                                                                 __uint_as_float(u & 0xffff0000u))));
+                            }
                     }
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-                        tc_store8(tD + lanes + part * 32 + j0 / 2, bits[part]);
-                    if (x == 0 && valid < kDeltaChunk) {
-                        // what the next state's product must not meet
-                        for (int k = tid; k < (kDeltaChunk - valid) * 8 * kBlocks;
-                             k += kDeltaCompute)
-                            store_smem16(at + Smem::kK + k / 8 % kBlocks * kDeltaTile +
-                                             (valid + k / 8 / kBlocks) * 128 + k % 8 * 16,
-                                         make_uint4(0, 0, 0, 0));
-                        fence_async_smem();
-                    }
+                    put(r, [&](int part) { return tD + part * 32 + 16 * half + 8 * x; });
                     hand_over(bar_r + 8 * x);
                 }
             }
@@ -1043,32 +1137,33 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             tc_fence_after();
             {
                 unsigned u[2][16];
-                tc_load16(tP + lanes + 32 * half, u[0]);
-                tc_load16(tP + lanes + 32 * half + 16, u[1]);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half, u[hh]);
                 tc_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    unsigned plain[8], bits[kParts][8];
-                    const float4 *const left =
-                        reinterpret_cast<const float4 *>(vec + R::kLeft + 32 * half + 16 * x);
+                    float2 w[2][2][2];
+                    unsigned plain[2][4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 l = left[i / 2];
-                        const float2 f = make_float2(__uint_as_float(u[x][2 * i]),
-                                                     __uint_as_float(u[x][2 * i + 1]));
-                        plain[i] = f2_to_bf2(f.x, f.y);
-                        unsigned w[kParts];
-                        split2<kParts>(__fmul2_rn(f, i % 2 ? make_float2(l.z, l.w)
-                                                           : make_float2(l.x, l.y)),
-                                       w);
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 left = factors(R::kLeft, 2 * x + i);
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part) bits[part][i] = w[part];
+                        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = 8 * x + 4 * i + 2 * e;
+                                const float2 f = make_float2(__uint_as_float(u[hh][k]),
+                                                             __uint_as_float(u[hh][k + 1]));
+                                plain[hh][2 * i + e] = f2_to_bf2(f.x, f.y);
+                                w[i][hh][e] = __fmul2_rn(f, left);
+                            }
                     }
-                    // (in tP over columns that this thread alone has read)
-                    tc_store8(tP + lanes + 32 * half + 8 * x, plain);
+                    // (in tP over columns that this warp alone has read)
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-                        tc_store8(weighted(part, 2 * half + x) + lanes, bits[part]);
+                    for (int hh = 0; hh < 2; ++hh)
+                        tc_store_frag(tP + lanes + hh * kLanes16 + 32 * half + 8 * x, plain[hh]);
+                    put(w, [&](int part) { return weighted(part, 2 * half + x); });
                     hand_over(bar_w + 8 * x);
                 }
             }
@@ -1079,20 +1174,24 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
             for (int y = 0; y < kPieces / 2; ++y) {
                 unsigned d[2][16];
-                tc_load16(tD + lanes + half * kCols + 32 * y, d[0]);
-                tc_load16(tD + lanes + half * kCols + 32 * y + 16, d[1]);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tc_load_frag(tD + lanes + hh * kLanes16 + half * kCols + 32 * y, d[hh]);
                 tc_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float *const at_s = S + 32 * y + 16 * x;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 f = __ffma2_rn(
-                            make_float2(at_s[i], at_s[i + 1]), make_float2(whole, whole),
-                            make_float2(__uint_as_float(d[x][i]), __uint_as_float(d[x][i + 1])));
-                        at_s[i] = f.x;
-                        at_s[i + 1] = f.y;
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = 8 * x + 4 * i + 2 * e;
+                                float2 &s = S[4 * y + 2 * x + i][hh][e];
+                                s = __ffma2_rn(s, make_float2(whole, whole),
+                                               make_float2(__uint_as_float(d[hh][k]),
+                                                           __uint_as_float(d[hh][k + 1])));
+                            }
                     if (c + 1 < chunks) publish(2 * y + x);
                 }
             }
@@ -1101,39 +1200,48 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int j0 = 32 * half + 16 * x;
-                unsigned sq[16], um[16];
-                tc_load16(tQ + lanes + j0, sq);
-                tc_load16(tM + lanes + j0, um);
-                const float4 *const read = reinterpret_cast<const float4 *>(vec + R::kRead + j0);
-                const float4 *const past = reinterpret_cast<const float4 *>(vec + R::kReadS + j0);
+                unsigned sq[2][8], um[2][8];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    tc_load_frag(tQ + lanes + hh * kLanes16 + 32 * half + 16 * x, sq[hh]);
+                    tc_load_frag(tM + lanes + hh * kLanes16 + 32 * half + 16 * x, um[hh]);
+                }
                 tc_wait_ld();
                 if (x == 1) {
                     tc_fence_before();
                     warp_arrive(bar_o, lane);
                 }
+                unsigned y[2][4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 r = read[i / 2], e = past[i / 2];
-                    const float2 y = __ffma2_rn(
-                        i % 2 ? make_float2(e.z, e.w) : make_float2(e.x, e.y),
-                        make_float2(__uint_as_float(sq[2 * i]), __uint_as_float(sq[2 * i + 1])),
-                        __fmul2_rn(i % 2 ? make_float2(r.z, r.w) : make_float2(r.x, r.y),
-                                   make_float2(__uint_as_float(um[2 * i]),
-                                               __uint_as_float(um[2 * i + 1]))));
-                    const unsigned two = f2_to_bf2(y.x, y.y);
-                    const int j = j0 + 2 * i;
-                    if (valid == kDeltaChunk) {
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_of(j)),
-                                     "h"(static_cast<unsigned short>(two))
-                                     : "memory");
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(v_of(j + 1)),
-                                     "h"(static_cast<unsigned short>(two >> 16))
-                                     : "memory");
-                    } else if (own) {
-                        if (j < valid) out[j * p.out_b] = __ushort_as_bfloat16(two & 0xffff);
-                        if (j + 1 < valid)
-                            out[(j + 1) * p.out_b] = __ushort_as_bfloat16(two >> 16);
+                for (int i = 0; i < 2; ++i) {
+                    const float2 read = factors(R::kRead, 2 * x + i);
+                    const float2 past = factors(R::kReadS, 2 * x + i);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = 4 * i + 2 * e;
+                            const float2 f = __ffma2_rn(
+                                past,
+                                make_float2(__uint_as_float(sq[hh][k]),
+                                            __uint_as_float(sq[hh][k + 1])),
+                                __fmul2_rn(read, make_float2(__uint_as_float(um[hh][k]),
+                                                             __uint_as_float(um[hh][k + 1]))));
+                            y[hh][2 * i + e] = f2_to_bf2(f.x, f.y);
+                        }
+                }
+                if (valid == kDeltaChunk) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) store_trans4(v_at(x, hh), y[hh]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int hh = k / 8, i = k / 4 % 2, e = k / 2 % 2, odd = k % 2;
+                        const int token = 32 * half + 16 * x + 8 * i + 2 * t + odd;
+                        const int row = row_at(hh, e);
+                        if (token < valid && row0 + row < p.headdim)
+                            out[token * p.out_b + row] =
+                                __ushort_as_bfloat16(y[hh][2 * i + e] >> (16 * odd));
                     }
                 }
             }
@@ -1142,21 +1250,23 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             warp_arrive(empty + 8 * stage, lane);
             fast ^= 1;
         }
-        if (prompt.x && own && (chunks || fresh)) {
+        if (prompt.x && (chunks || fresh))
 #pragma unroll
-            for (int i = 0; i < kCols / kPer; ++i) {
-                uint4 w;
-                if constexpr (sizeof(ST) == 4)
-                    w = make_uint4(__float_as_uint(S[4 * i]), __float_as_uint(S[4 * i + 1]),
-                                   __float_as_uint(S[4 * i + 2]), __float_as_uint(S[4 * i + 3]));
-                else
-                    w = make_uint4(f2_to_bf2(S[8 * i], S[8 * i + 1]),
-                                   f2_to_bf2(S[8 * i + 2], S[8 * i + 3]),
-                                   f2_to_bf2(S[8 * i + 4], S[8 * i + 5]),
-                                   f2_to_bf2(S[8 * i + 6], S[8 * i + 7]));
-                __stcs(reinterpret_cast<uint4 *>(state) + i, w);
-            }
-        }
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = row0 + row_at(hh, e);
+                    if (row >= p.headdim) continue;
+                    ST *const to = state + row * p.st_row;
+#pragma unroll
+                    for (int i = 0; i < kCol8; ++i) {
+                        if constexpr (sizeof(ST) == 4)
+                            __stcs(reinterpret_cast<float2 *>(to + 8 * i), S[i][hh][e]);
+                        else
+                            __stcs(reinterpret_cast<unsigned *>(to + 8 * i),
+                                   f2_to_bf2(S[i][hh][e].x, S[i][hh][e].y));
+                    }
+                }
     }
     tc_fence_before();
     if (__syncthreads_or(!alive)) {  // what is in flight lands long before this is over
