@@ -64,7 +64,7 @@ struct DeltaRecord {
         kPast = 64,    // beta e^{s} / |k|: of S k in R
         kLeft = 128,   // e^{s_C - s} / |k|: of U in the next state
         kRead = 192,   // scale / |q|: of U M^T
-        kReadS = 256,  // scale / |q| e^{s}: of S q
+        kReadS = 256,  // e^{s}: of S q
         kDecay = 320,  // the token's own decay
         kKey = 384,    // 1 / |k|
         kWhole = 448,  // e^{s_C}; then whether the chunk is to be taken token by token
@@ -301,7 +301,7 @@ __device__ __forceinline__ void delta_factors(const DeltaParams &d, const unsign
         vec[R::kPast + i] = beta[k] * e * rk;
         vec[R::kLeft + i] = exp2f(static_cast<float>(whole - s[k])) * rk;
         vec[R::kRead + i] = rq;
-        vec[R::kReadS + i] = rq * e;
+        vec[R::kReadS + i] = e;
         vec[R::kDecay + i] = exp2f(a[k]);
         vec[R::kKey + i] = rk;
     }
@@ -554,9 +554,10 @@ constexpr int kDeltaStages = 3;
 template <int N>
 struct DeltaSmem {
     static constexpr int kBlocks = N / 64;
-    static constexpr int kK = 0;
-    static constexpr int kQ = kK + kBlocks * kDeltaTile;
-    static constexpr int kV = kQ + kBlocks * kDeltaTile;  // the readout leaves from here
+    static constexpr int kK = 0;           // K's and Q's blocks of 64 columns in turn: together
+    static constexpr int kQ = kDeltaTile;  // they are an operand of 128 rows
+    static constexpr int kBlock = 2 * kDeltaTile;
+    static constexpr int kV = kBlocks * kBlock;  // the readout leaves from here
     static constexpr int kRecord = kV + 2 * kDeltaTile;
     static constexpr int kStage = kRecord + DeltaRecord::kBytes;
     static constexpr int kSwap = kDeltaStages * kStage;  // two floats per compute thread
@@ -605,6 +606,16 @@ __device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)
                  : "memory");
 }
 
+__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void load_trans4(unsigned (&r)[4], unsigned addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -630,20 +641,19 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
     }
 }
 
-// Roles.  Per chunk, with the barrier of each hand-over ([r], [u], [w], [d] and [m] only where the
-// chunk is not taken token by token):
+// Roles.  Per chunk, with the barrier of each hand-over ([r], [u], [w], [d], [q] and [m] only where
+// the chunk is not taken token by token):
 //
 //   loader:  [empty] tiles and record -> full
 //   looker:  [full] values looked over, a prompt's last chunk cut -> look
-//   issuer:  [look, s] S K^T -> p; [o] S Q^T, first part; [r] R T^T -> u; S Q^T, second part;
-//            [w] U K -> d; U M^T -> m, empty
-//   compute: [full, look, p] R -> r; [u] U -> w; [d] S -> s; [m] readout into V's place -> o, t,
-//            empty
+//   issuer:  [look, s] S (K, Q)^T -> p; [r] R T^T -> u; [w] U K -> d; [q] U M^T -> m, empty
+//   compute: [full, look, p] R -> r; the last chunk's [m] readout into its V's place -> t, empty;
+//            [u] U -> w; S Q^T with its decays to where U M^T adds to it -> q; [d] S -> s
 //   storer:  [look, t] the readout's tile out -> empty
 //
 // S, R and U are handed over 16 columns of each warpgroup at a time, so that products of the first
-// run while the next are made: of a product's 4 to 24 MMAs only the last piece's are waited for.
-// S Q^T, which nothing waits for before the readout, runs in two parts under R and U.
+// run while the next are made: of a product's MMAs only the last piece's are waited for.  K and Q
+// are one operand, as an MMA of N = 128 takes little longer than one of N = 64.
 template <int N, typename ST, bool kIdx64>
 __global__ void __launch_bounds__(kDeltaThreads, 1)
     ssu_delta_mma_kernel(const __grid_constant__ DeltaMmaParams m,
@@ -665,7 +675,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const unsigned bars = base + Smem::kBars;
     const unsigned full = bars, empty = bars + 8 * kDeltaStages, look = empty + 8 * kDeltaStages;
     const unsigned bar_t = look + 8 * kDeltaStages, bar_s = bar_t + 8 * kDeltaStages,
-                   bar_r = bar_s + 32, bar_w = bar_r + 16, bar_o = bar_w + 16, bar_p = bar_o + 8,
+                   bar_r = bar_s + 32, bar_w = bar_r + 16, bar_q = bar_w + 16, bar_p = bar_q + 8,
                    bar_u = bar_p + 8, bar_d = bar_u + 8, bar_m = bar_d + 8;
     if (tid == 0) {
         for (int i = 0; i < kDeltaStages; ++i) {
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const unsigned tmem = tmem_slot;
     // TMEM columns: S's parts, the third of which makes room for U's first two; the next state's sum
     // (before it, R's parts); S K^T, then U, then in its place U in bf16 and U's third part; S Q^T;
-    // U M^T
+    // the readout's sum
     const unsigned tS = tmem, tW = tmem + 128, tD = tmem + 192, tP = tmem + 320, tQ = tmem + 384,
                    tM = tmem + 448;
     // U's weighted parts, k-step by k-step (16 tokens): two parts of 32 columns; the third in pieces
@@ -733,8 +743,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 mbar_expect(bar, bytes);
                 const int tok = begin + c * kDeltaChunk;
                 for (int k = 0; k < kBlocks; ++k) {
-                    tma_load(to + Smem::kK + k * kDeltaTile, &map_k, bar, k * 64, grp, tok);
-                    tma_load(to + Smem::kQ + k * kDeltaTile, &map_q, bar, k * 64, grp, tok);
+                    tma_load(to + Smem::kK + k * Smem::kBlock, &map_k, bar, k * 64, grp, tok);
+                    tma_load(to + Smem::kQ + k * Smem::kBlock, &map_q, bar, k * 64, grp, tok);
                 }
                 for (int k = 0; k < v_blocks; ++k)
                     tma_load(to + Smem::kV + k * kDeltaTile, &map_v, bar, row0 + k * 64, h, tok);
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     const unsigned to =
                         base + stage * Smem::kStage + (valid + k / 8) * 128 + k % 8 * 16;
                     for (int t = 0; t < kBlocks; ++t)
-                        store_smem16(to + Smem::kK + t * kDeltaTile, make_uint4(0, 0, 0, 0));
+                        store_smem16(to + Smem::kK + t * Smem::kBlock, make_uint4(0, 0, 0, 0));
                     for (int t = 0; t < v_blocks; ++t)
                         store_smem16(to + Smem::kV + t * kDeltaTile, make_uint4(0, 0, 0, 0));
                 }
@@ -820,7 +830,6 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 if (flag()) {
                     for (int x = 0; x < kPieces && alive; ++x)
                         alive = mbar_wait(bar_s + 8 * x, c & 1);
-                    if (c > 0 && alive) alive = mbar_wait(bar_o, (c - 1) & 1);
                     mbar_arrive(bar_p);
                     mbar_arrive(empty + 8 * stage);
                     continue;
@@ -838,22 +847,13 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         for (int half = 0; half < 2; ++half) {
                             const int k = x + half * kPieces;
                             mma_ts(tP, tS + part * (N / 2) + 8 * k,
-                                   operand(at + Smem::kK + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
-                                   kTokens, x > 0 || part < kParts - 1 || half > 0);
+                                   operand(at + Smem::kK + (k / 4) * Smem::kBlock + (k % 4) * 32,
+                                           0),
+                                   instruction(2 * kDeltaChunk, false, false),
+                                   x > 0 || part < kParts - 1 || half > 0);
                         }
                 }
                 tc_commit(bar_p);
-                if (c > 0 && alive) alive = mbar_wait(bar_o, (c - 1) & 1);
-                if (!alive) break;
-                tc_fence_after();
-                auto read = [&](int part, bool add) {
-#pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        mma_ts(tQ, tS + part * (N / 2) + 8 * k,
-                               operand(at + Smem::kQ + (k / 4) * kDeltaTile + (k % 4) * 32, 0),
-                               kTokens, add || k > 0);
-                };
-                read(1, false);
                 const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -867,18 +867,14 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                    add || half > 0);
                         }
                     };
-                    if constexpr (kParts == 3) {  // small parts first: sums lose less
-                        correct(2, t1, x > 0);
-                        correct(1, t2, true);
-                        correct(0, t2, true);
-                    } else {
-                        correct(0, t2, x > 0);
-                    }
+                    // small parts first: sums lose less
+                    if constexpr (kParts == 3) correct(2, t1, x > 0);
+                    correct(0, t2, kParts == 3 || x > 0);
                     correct(1, t1, true);
                     correct(0, t1, true);
                 }
                 tc_commit(bar_u);
-                read(0, true);
+                if (!alive) break;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (alive) alive = mbar_wait(bar_w + 8 * x, fast);
@@ -889,17 +885,19 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         for (int half = 0; half < 2; ++half) {
                             const int k = x + 2 * half;
                             mma_ts(tD, weighted(part, k),
-                                   operand(at + Smem::kK + k * 2048, N == 128 ? kDeltaTile : 0),
+                                   operand(at + Smem::kK + k * 2048, N == 128 ? Smem::kBlock : 0),
                                    instruction(N, false, true),
                                    x > 0 || part < kParts - 1 || half > 0);
                         }
                 }
                 tc_commit(bar_d);
+                if (alive) alive = mbar_wait(bar_q, fast);
                 if (!alive) break;
+                tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_ts(tM, tP + 32 * (k / 2) + 8 * (k % 2),
-                           operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, k > 0);
+                           operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
                 tc_commit(empty + 8 * stage);
                 tc_commit(bar_m);
                 fast ^= 1;
@@ -977,18 +975,87 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
             for (int x = 0; x < kPieces; ++x) publish(x);
         unsigned fast = 0;
+        // Matrix k % 4 of 16 tokens and 16 rows `hh` in V's tiles, where ldmatrix and stmatrix take
+        // their rows' addresses from lanes.
+        auto v_at = [&](unsigned at, int x, int hh) {
+            const int token = 32 * half + 16 * x + 8 * (lane >> 4) + (lane & 7);
+            const int row = 32 * quarter + 16 * hh + 8 * (lane >> 3 & 1);
+            return swizzled(at + Smem::kV + (row >> 6) * kDeltaTile, token, (row & 63) >> 3);
+        };
+        // the two tokens of block i (of the warpgroup's four) that the thread has
+        auto factors = [&](const float *vec, int kind, int i) {
+            return *reinterpret_cast<const float2 *>(vec + kind + 32 * half + 8 * i + 2 * t);
+        };
+        auto vec_of = [&](int stage) {
+            return reinterpret_cast<const float *>(smem + stage * Smem::kStage + Smem::kRecord +
+                                                   R::kVec);
+        };
+        // The readout of chunk c, the last one, whose products have been waited for by nobody yet.
+        bool waits = false;
+        auto read_out = [&](int c) {
+            const int last = stage == 0 ? kDeltaStages - 1 : stage - 1;
+            const unsigned at = base + last * Smem::kStage;
+            const float *const vec = vec_of(last);
+            const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
+            if (alive) alive = mbar_wait(bar_m, fast ^ 1);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                unsigned um[2][8], y[2][4];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tc_load_frag(tM + lanes + hh * kLanes16 + 32 * half + 16 * x, um[hh]);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 read = factors(vec, R::kRead, 2 * x + i);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = 4 * i + 2 * e;
+                            const float2 f = __fmul2_rn(
+                                read, make_float2(__uint_as_float(um[hh][k]),
+                                                  __uint_as_float(um[hh][k + 1])));
+                            y[hh][2 * i + e] = f2_to_bf2(f.x, f.y);
+                        }
+                }
+                if (valid == kDeltaChunk) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) store_trans4(v_at(at, x, hh), y[hh]);
+                } else {
+                    __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
+                                               h * p.out_h + row0;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int hh = k / 8, i = k / 4 % 2, e = k / 2 % 2, odd = k % 2;
+                        const int token = 32 * half + 16 * x + 8 * i + 2 * t + odd;
+                        const int row = row_at(hh, e);
+                        if (token < valid && row0 + row < p.headdim)
+                            out[token * p.out_b + row] =
+                                __ushort_as_bfloat16(y[hh][2 * i + e] >> (16 * odd));
+                    }
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            warp_arrive(bar_t + 8 * last, lane);
+            warp_arrive(empty + 8 * last, lane);
+            waits = false;
+        };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c, next_stage()) {
             const unsigned at = base + stage * Smem::kStage;
             const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
-            const float *const vec = reinterpret_cast<const float *>(
-                smem + stage * Smem::kStage + Smem::kRecord + R::kVec);
+            const float *const vec = vec_of(stage);
             __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
                                        h * p.out_h + row0;
             if (alive) alive = mbar_wait(full + 8 * stage, turn);
             if (alive) alive = mbar_wait(look + 8 * stage, turn);
             __syncwarp();
             if (__builtin_expect(flag(), 0)) {
+                if (waits) read_out(c - 1);
                 float *const swap = reinterpret_cast<float *>(smem + Smem::kSwap);
                 // the rows' sums over the quad's lanes and both warpgroups' columns
                 auto whole_rows = [&](float (&sum)[2][2], float *room) {
@@ -1014,7 +1081,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     unsigned w;
                     asm volatile("ld.shared.u32 %0, [%1];"
                                  : "=r"(w)
-                                 : "r"(swizzled(at + tile + (col / 64) * kDeltaTile, k,
+                                 : "r"(swizzled(at + tile + (col / 64) * Smem::kBlock, k,
                                                 col % 64 / 8) + 4 * t)
                                  : "memory");
                     return make_float2(__uint_as_float(w << 16),
@@ -1076,27 +1143,15 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
                     for (int x = 0; x < kPieces; ++x) publish(x);
                 warp_arrive(bar_t + 8 * stage, lane);
-                warp_arrive(bar_o, lane);
                 warp_arrive(empty + 8 * stage, lane);
                 continue;
             }
-            // Matrix k % 4 of 16 tokens and 16 rows `hh` in V's tiles, where ldmatrix and stmatrix
-            // take their rows' addresses from lanes.
-            auto v_at = [&](int x, int hh) {
-                const int token = 32 * half + 16 * x + 8 * (lane >> 4) + (lane & 7);
-                const int row = 32 * quarter + 16 * hh + 8 * (lane >> 3 & 1);
-                return swizzled(at + Smem::kV + (row >> 6) * kDeltaTile, token, (row & 63) >> 3);
-            };
-            // the two tokens of block i (of the warpgroup's four) that the thread has
-            auto factors = [&](int kind, int i) {
-                return *reinterpret_cast<const float2 *>(vec + kind + 32 * half + 8 * i + 2 * t);
-            };
             // R = beta v - (beta e^s / |k|) S k
             unsigned v[2][2][4];  // [piece][hh][block, e]
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) load_trans4(v[x][hh], v_at(x, hh));
+                for (int hh = 0; hh < 2; ++hh) load_trans4(v[x][hh], v_at(at, x, hh));
             if (alive) alive = mbar_wait(bar_p, c & 1);
             __syncwarp();
             tc_fence_after();
@@ -1111,8 +1166,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     float2 r[2][2][2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 beta = factors(R::kBeta, 2 * x + i);
-                        const float2 past = factors(R::kPast, 2 * x + i);
+                        const float2 beta = factors(vec, R::kBeta, 2 * x + i);
+                        const float2 past = factors(vec, R::kPast, 2 * x + i);
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1131,6 +1186,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     hand_over(bar_r + 8 * x);
                 }
             }
+            if (waits) read_out(c - 1);  // under R T^T
             // U for the readout, and with its weights for the next state
             if (alive) alive = mbar_wait(bar_u, fast);
             __syncwarp();
@@ -1147,7 +1203,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     unsigned plain[2][4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 left = factors(R::kLeft, 2 * x + i);
+                        const float2 left = factors(vec, R::kLeft, 2 * x + i);
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1167,6 +1223,28 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     hand_over(bar_w + 8 * x);
                 }
             }
+            // S Q^T with its decays, where U M^T will add to it (under U K)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                unsigned sq[16];
+                tc_load_frag(tQ + lanes + hh * kLanes16 + 32 * half, sq);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 past = factors(vec, R::kReadS, i);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = 4 * i + 2 * e;
+                        const float2 f =
+                            __fmul2_rn(past, make_float2(__uint_as_float(sq[k]),
+                                                         __uint_as_float(sq[k + 1])));
+                        sq[k] = __float_as_uint(f.x);
+                        sq[k + 1] = __float_as_uint(f.y);
+                    }
+                }
+                tc_store_frag(tM + lanes + hh * kLanes16 + 32 * half, sq);
+            }
+            hand_over(bar_q);
             const float whole = vec[R::kWhole];
             if (alive) alive = mbar_wait(bar_d, fast);
             __syncwarp();
@@ -1195,61 +1273,10 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                     if (c + 1 < chunks) publish(2 * y + x);
                 }
             }
-            if (alive) alive = mbar_wait(bar_m, fast);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                unsigned sq[2][8], um[2][8];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    tc_load_frag(tQ + lanes + hh * kLanes16 + 32 * half + 16 * x, sq[hh]);
-                    tc_load_frag(tM + lanes + hh * kLanes16 + 32 * half + 16 * x, um[hh]);
-                }
-                tc_wait_ld();
-                if (x == 1) {
-                    tc_fence_before();
-                    warp_arrive(bar_o, lane);
-                }
-                unsigned y[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 read = factors(R::kRead, 2 * x + i);
-                    const float2 past = factors(R::kReadS, 2 * x + i);
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int k = 4 * i + 2 * e;
-                            const float2 f = __ffma2_rn(
-                                past,
-                                make_float2(__uint_as_float(sq[hh][k]),
-                                            __uint_as_float(sq[hh][k + 1])),
-                                __fmul2_rn(read, make_float2(__uint_as_float(um[hh][k]),
-                                                             __uint_as_float(um[hh][k + 1]))));
-                            y[hh][2 * i + e] = f2_to_bf2(f.x, f.y);
-                        }
-                }
-                if (valid == kDeltaChunk) {
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) store_trans4(v_at(x, hh), y[hh]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int hh = k / 8, i = k / 4 % 2, e = k / 2 % 2, odd = k % 2;
-                        const int token = 32 * half + 16 * x + 8 * i + 2 * t + odd;
-                        const int row = row_at(hh, e);
-                        if (token < valid && row0 + row < p.headdim)
-                            out[token * p.out_b + row] =
-                                __ushort_as_bfloat16(y[hh][2 * i + e] >> (16 * odd));
-                    }
-                }
-            }
-            fence_async_smem();
-            warp_arrive(bar_t + 8 * stage, lane);
-            warp_arrive(empty + 8 * stage, lane);
+            waits = true;
             fast ^= 1;
         }
+        if (waits) read_out(chunks - 1);
         if (prompt.x && (chunks || fresh))
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
