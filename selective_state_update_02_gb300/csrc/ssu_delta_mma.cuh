@@ -647,7 +647,7 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 //   loader:  [empty] tiles and record -> full
 //   looker:  [full] values looked over, a prompt's last chunk cut -> look
 //   issuer:  [look, s] S (K, Q)^T -> p; [r] R T^T -> u; [w] U K -> d; [q] U M^T -> m, empty
-//   compute: [full, look, p] R -> r; the last chunk's [m] readout into its V's place -> t, empty;
+//   compute: [look, p] R -> r; the last chunk's [m] readout into its V's place -> t, empty;
 //            [u] U -> w; S Q^T with its decays to where U M^T adds to it -> q; [d] S -> s
 //   storer:  [look, t] the readout's tile out -> empty
 //
@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     extern __shared__ unsigned char raw[];
     __shared__ unsigned tmem_slot;
     const SsuParams &p = m.d.m.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform to the compiler)
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char *const smem = raw + (base - smem_u32(raw));
     const unsigned bars = base + Smem::kBars;
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const unsigned tmem = tmem_slot;
+    const unsigned tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     // TMEM columns: S's parts, the third of which makes room for U's first two; the next state's sum
     // (before it, R's parts); S K^T, then U, then in its place U in bf16 and U's third part; S Q^T;
     // the readout's sum
@@ -718,10 +719,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const int4 prompt = m.prompts[b];
     const bool fresh = m.d.m.fresh && m.d.m.fresh[b] != 0;
     const int begin = prompt.y, end = prompt.z;
-    const int chunks = prompt.x ? (end - begin + kDeltaChunk - 1) / kDeltaChunk : 0;
+    const int chunks = __shfl_sync(
+        0xffffffffu, prompt.x ? (end - begin + kDeltaChunk - 1) / kDeltaChunk : 0, 0);
     const int grp = group_of(h, p.group_magic);
     const int v_blocks = min(2, (p.headdim - row0 + 63) / 64);
-    bool alive = true;
+    unsigned dead = 0;  // whether a wait gave up: what comes after it is not valid, nor waited for
     // the chunk's stage and the parity of its barriers
     int stage = 0;
     unsigned turn = 0;
@@ -738,8 +740,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, next_stage()) {
                 const unsigned to = base + stage * Smem::kStage, bar = full + 8 * stage;
-                if (c >= kDeltaStages && alive) alive = mbar_wait(empty + 8 * stage, turn ^ 1);
-                if (!alive) break;
+                if (c >= kDeltaStages) mbar_pass(empty + 8 * stage, turn ^ 1, dead);
+                if (dead) break;
                 mbar_expect(bar, bytes);
                 const int tok = begin + c * kDeltaChunk;
                 for (int k = 0; k < kBlocks; ++k) {
@@ -758,7 +760,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     } else if (warp == kDeltaLooker) {
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c, next_stage()) {
-            if (alive) alive = mbar_wait(full + 8 * stage, turn);
+            mbar_pass(full + 8 * stage, turn, dead);
             const unsigned at = base + stage * Smem::kStage + Smem::kV;
             const int valid = min(kDeltaChunk, end - begin - c * kDeltaChunk);
             const __nv_bfloat162 zero{};
@@ -801,9 +803,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, next_stage()) {
                 const int tok = begin + c * kDeltaChunk;
-                if (alive) alive = mbar_wait(look + 8 * stage, turn);
-                if (alive) alive = mbar_wait(bar_t + 8 * stage, turn);
-                if (!alive) break;
+                mbar_pass(look + 8 * stage, turn, dead);
+                mbar_pass(bar_t + 8 * stage, turn, dead);
+                if (dead) break;
                 if (!flag() && tok + kDeltaChunk <= end) {
                     for (int k = 0; k < v_blocks; ++k)
                         tma_store(&map_out, base + stage * Smem::kStage + Smem::kV + k * kDeltaTile,
@@ -817,91 +819,87 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         }
         __syncwarp();
     } else if (warp == kDeltaIssuer) {
-        if (lane == 0) {
-            unsigned fast = 0;  // parity of the chunks not taken token by token
-            bool any = false;
-            constexpr unsigned kTokens = instruction(kDeltaChunk, false, false);
+        const unsigned leader = elect_one();
+        unsigned fast = 0;  // parity of the chunks not taken token by token
+        bool any = false;
+        constexpr unsigned kTokens = instruction(kDeltaChunk, false, false);
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c, next_stage()) {
-                const unsigned at = base + stage * Smem::kStage;
-                if (alive) alive = mbar_wait(full + 8 * stage, turn);
-                if (alive) alive = mbar_wait(look + 8 * stage, turn);
-                if (!alive) break;
-                if (flag()) {
-                    for (int x = 0; x < kPieces && alive; ++x)
-                        alive = mbar_wait(bar_s + 8 * x, c & 1);
+        for (int c = 0; c < chunks; ++c, next_stage()) {
+            const unsigned at = base + stage * Smem::kStage;
+            mbar_pass(look + 8 * stage, turn, dead);
+            if (__any_sync(0xffffffffu, flag())) {
+                for (int x = 0; x < kPieces; ++x) mbar_pass(bar_s + 8 * x, c & 1, dead);
+                if (leader) {
                     mbar_arrive(bar_p);
                     mbar_arrive(empty + 8 * stage);
-                    continue;
                 }
-                // U of the last such chunk has been read before its place is written
-                if (any && alive) alive = mbar_wait(bar_m, fast ^ 1);
-                any = true;
+                __syncwarp();
+                continue;
+            }
+            // U of the last such chunk has been read before its place is written
+            if (any) mbar_pass(bar_m, fast ^ 1, dead);
+            any = true;
 #pragma unroll
-                for (int x = 0; x < kPieces; ++x) {
-                    if (alive) alive = mbar_wait(bar_s + 8 * x, c & 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int part = kParts - 1; part >= 0; --part)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int k = x + half * kPieces;
-                            mma_ts(tP, tS + part * (N / 2) + 8 * k,
-                                   operand(at + Smem::kK + (k / 4) * Smem::kBlock + (k % 4) * 32,
-                                           0),
-                                   instruction(2 * kDeltaChunk, false, false),
-                                   x > 0 || part < kParts - 1 || half > 0);
-                        }
-                }
-                tc_commit(bar_p);
-                const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (alive) alive = mbar_wait(bar_r + 8 * x, fast);
-                    tc_fence_after();
-                    auto correct = [&](int part, unsigned t, bool add) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int k = x + 2 * half;
-                            mma_ts(tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0), kTokens,
-                                   add || half > 0);
-                        }
-                    };
-                    // small parts first: sums lose less
-                    if constexpr (kParts == 3) correct(2, t1, x > 0);
-                    correct(0, t2, kParts == 3 || x > 0);
-                    correct(1, t1, true);
-                    correct(0, t1, true);
-                }
-                tc_commit(bar_u);
-                if (!alive) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (alive) alive = mbar_wait(bar_w + 8 * x, fast);
-                    tc_fence_after();
-#pragma unroll
-                    for (int part = kParts - 1; part >= 0; --part)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int k = x + 2 * half;
-                            mma_ts(tD, weighted(part, k),
-                                   operand(at + Smem::kK + k * 2048, N == 128 ? Smem::kBlock : 0),
-                                   instruction(N, false, true),
-                                   x > 0 || part < kParts - 1 || half > 0);
-                        }
-                }
-                tc_commit(bar_d);
-                if (alive) alive = mbar_wait(bar_q, fast);
-                if (!alive) break;
+            for (int x = 0; x < kPieces; ++x) {
+                mbar_pass(bar_s + 8 * x, c & 1, dead);
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tM, tP + 32 * (k / 2) + 8 * (k % 2),
-                           operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
-                tc_commit(empty + 8 * stage);
-                tc_commit(bar_m);
-                fast ^= 1;
+                for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int k = x + half * kPieces;
+                        mma_ts_of(leader, tP, tS + part * (N / 2) + 8 * k,
+                                  operand(at + Smem::kK + (k / 4) * Smem::kBlock + (k % 4) * 32, 0),
+                                  instruction(2 * kDeltaChunk, false, false),
+                                  x > 0 || part < kParts - 1 || half > 0);
+                    }
             }
+            tc_commit_of(leader, bar_p);
+            const unsigned t1 = at + Smem::kRecord + R::kT1, t2 = at + Smem::kRecord + R::kT2;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                mbar_pass(bar_r + 8 * x, fast, dead);
+                tc_fence_after();
+                auto correct = [&](int part, unsigned t, bool add) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int k = x + 2 * half;
+                        mma_ts_of(leader, tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0),
+                                  kTokens, add || half > 0);
+                    }
+                };
+                // small parts first: sums lose less
+                if constexpr (kParts == 3) correct(2, t1, x > 0);
+                correct(0, t2, kParts == 3 || x > 0);
+                correct(1, t1, true);
+                correct(0, t1, true);
+            }
+            tc_commit_of(leader, bar_u);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                mbar_pass(bar_w + 8 * x, fast, dead);
+                tc_fence_after();
+#pragma unroll
+                for (int part = kParts - 1; part >= 0; --part)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int k = x + 2 * half;
+                        mma_ts_of(leader, tD, weighted(part, k),
+                                  operand(at + Smem::kK + k * 2048, N == 128 ? Smem::kBlock : 0),
+                                  instruction(N, false, true),
+                                  x > 0 || part < kParts - 1 || half > 0);
+                    }
+            }
+            tc_commit_of(leader, bar_d);
+            mbar_pass(bar_q, fast, dead);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_ts_of(leader, tM, tP + 32 * (k / 2) + 8 * (k % 2),
+                          operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
+            tc_commit_of(leader, empty + 8 * stage);
+            tc_commit_of(leader, bar_m);
+            fast ^= 1;
         }
         __syncwarp();
     } else {
@@ -997,7 +995,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             const unsigned at = base + last * Smem::kStage;
             const float *const vec = vec_of(last);
             const int tok = begin + c * kDeltaChunk, valid = min(kDeltaChunk, end - tok);
-            if (alive) alive = mbar_wait(bar_m, fast ^ 1);
+            mbar_pass(bar_m, fast ^ 1, dead);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
@@ -1051,8 +1049,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             const float *const vec = vec_of(stage);
             __nv_bfloat16 *const out = p.out + static_cast<long long>(tok) * p.out_b +
                                        h * p.out_h + row0;
-            if (alive) alive = mbar_wait(full + 8 * stage, turn);
-            if (alive) alive = mbar_wait(look + 8 * stage, turn);
+            mbar_pass(look + 8 * stage, turn, dead);
             __syncwarp();
             if (__builtin_expect(flag(), 0)) {
                 if (waits) read_out(c - 1);
@@ -1137,7 +1134,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                     __float2bfloat16(sum[x / 2][x % 2] * vec[R::kRead + k]);
                         }
                 }
-                if (alive) alive = mbar_wait(bar_p, c & 1);  // the issuer has come this far
+                mbar_pass(bar_p, c & 1, dead);  // the issuer has come this far
                 __syncwarp();
                 if (c + 1 < chunks)
 #pragma unroll
@@ -1152,7 +1149,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) load_trans4(v[x][hh], v_at(at, x, hh));
-            if (alive) alive = mbar_wait(bar_p, c & 1);
+            mbar_pass(bar_p, c & 1, dead);
             __syncwarp();
             tc_fence_after();
             {
@@ -1188,7 +1185,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             }
             if (waits) read_out(c - 1);  // under R T^T
             // U for the readout, and with its weights for the next state
-            if (alive) alive = mbar_wait(bar_u, fast);
+            mbar_pass(bar_u, fast, dead);
             __syncwarp();
             tc_fence_after();
             {
@@ -1246,7 +1243,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             }
             hand_over(bar_q);
             const float whole = vec[R::kWhole];
-            if (alive) alive = mbar_wait(bar_d, fast);
+            mbar_pass(bar_d, fast, dead);
             __syncwarp();
             tc_fence_after();
 #pragma unroll
@@ -1296,7 +1293,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 }
     }
     tc_fence_before();
-    if (__syncthreads_or(!alive)) {  // what is in flight lands long before this is over
+    if (__syncthreads_or(dead)) {  // what is in flight lands long before this is over
         if (tid == 0) atomicOr(&p.err[2], 1u);
         __nanosleep(1000000);
     }

@@ -62,6 +62,37 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
     }
 }
 
+// The same as straight-line code, which leaves a warp's control flow uniform as the compiler sees it:
+// `dead` becomes nonzero where the wait gave up (after 4 million tries, each suspended for at most 2
+// us or so), and waits no more where it was.  For waits on the CTA's own work alone.
+__device__ __forceinline__ void mbar_pass(unsigned bar, unsigned parity, unsigned &dead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "@p bra OUT;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+        "@p bra OUT;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 4000000;\n\t"
+        "@q bra AGAIN;\n\t"
+        "mov.u32 %0, 1;\n\t"
+        "OUT:\n\t}"
+        : "+r"(dead)
+        : "r"(bar), "r"(parity)
+        : "memory");
+}
+
+// One lane of a whole warp: nonzero there.
+__device__ __forceinline__ unsigned elect_one() {
+    unsigned leader;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(leader));
+    return leader;
+}
+
 __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, unsigned bar, int x,
                                          int y, int z) {
     asm volatile(
@@ -152,6 +183,27 @@ __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long lon
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// The same, and the commit, by the one lane that elect_one() named, in code that the whole warp runs:
+// operands are then uniform to the compiler, and a product takes a third of the cycles to issue
+// (52 from one lane's own branch, where an MMA of N = 64 runs for 32).
+__device__ __forceinline__ void mma_ts_of(unsigned leader, unsigned d, unsigned a,
+                                          unsigned long long b, unsigned idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_of(unsigned leader, unsigned bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar),
+        "r"(leader)
         : "memory");
 }
 
