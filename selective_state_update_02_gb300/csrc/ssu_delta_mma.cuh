@@ -25,8 +25,8 @@
 // Precision.  States, statistics and sums are fp32.  K and Q are bf16 and exact (their lengths are
 // factors of tokens).  What decides the state enters as sums of bf16 parts: S, R and U three (24
 // bits; two for a state kept in bf16), T two (1 on its diagonal is exact, and its other elements to
-// 2^-17 are below the fp32 sums' own error).  The readout alone sees U and M rounded to bf16, once
-// each, and S to two parts.  T is worked out in fp32 by inverting blocks of 16 along the diagonal row by
+// 2^-17 are below the fp32 sums' own error).  The readout alone sees M rounded to bf16 once, and U to
+// two parts.  T is worked out in fp32 by inverting blocks of 16 along the diagonal row by
 // row and joining them, T21 = -T22 L21 T11 (powers of L, as a product formula would have, grow
 // like binomials where keys are alike).
 //
@@ -263,21 +263,28 @@ __device__ __forceinline__ void put_product(const float (&d)[kTiles][4], float *
     }
 }
 
-// One head's factors of the chunk's tokens, two per lane of one warp; dt and gate as loaded.
-__device__ __forceinline__ void delta_factors(const DeltaParams &d, const unsigned (&dt)[2],
-                                              const unsigned (&gate)[2], float bias, float A2,
-                                              int valid, const float *lengths, bool bad,
-                                              float *sums, float *vec, int lane) {
+// One head's rates of the chunk's tokens, two per lane of one warp, before their keys' lengths are
+// known; dt and gate as loaded.
+struct DeltaRates {
+    float beta[2], past[2], left[2];  // beta, e^s, e^{s_C - s}
+    bool bad;
+};
+
+__device__ __forceinline__ DeltaRates delta_rates(const unsigned (&dt)[2], const unsigned (&gate)[2],
+                                                  float bias, float A2, int valid, float *sums,
+                                                  float *vec, int lane) {
     using R = DeltaRecord;
-    float a[2], beta[2];
+    DeltaRates r;
+    r.bad = false;
+    float a[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        a[k] = beta[k] = 0.0f;
+        a[k] = r.beta[k] = 0.0f;
         if (2 * lane + k >= valid) continue;
         a[k] = softplus_f32(__uint_as_float(dt[k] << 16) + bias) * A2;
         if (a[k] < -300.0f) a[k] = -300.0f;  // 2^-300 is 0; NaN stays
-        beta[k] = 1.0f / (1.0f + expf(-__uint_as_float(gate[k] << 16)));
-        bad |= !(a[k] < 60.0f) || !(beta[k] <= 1.0f);
+        r.beta[k] = 1.0f / (1.0f + expf(-__uint_as_float(gate[k] << 16)));
+        r.bad |= !(a[k] < 60.0f) || !(r.beta[k] <= 1.0f);
     }
     // sums in double, kept as two floats: differences of neighbours stay exact behind long decays
     double upto = static_cast<double>(a[0]) + a[1];
@@ -288,27 +295,21 @@ __device__ __forceinline__ void delta_factors(const DeltaParams &d, const unsign
     }
     const double s[2] = {upto - a[1], upto};
     const double whole = __shfl_sync(0xffffffffu, upto, 31);
-    bad |= !(s[0] < 60.0) || !(s[1] < 60.0);
-    bad = __any_sync(0xffffffffu, bad);
+    r.bad |= !(s[0] < 60.0) || !(s[1] < 60.0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int i = 2 * lane + k;
         const float hi = static_cast<float>(s[k]);
         sums[i] = hi;
         sums[kDeltaChunk + i] = static_cast<float>(s[k] - hi);
-        const float rk = lengths[i], rq = lengths[kDeltaChunk + i], e = exp2f(hi);
-        vec[R::kBeta + i] = beta[k];
-        vec[R::kPast + i] = beta[k] * e * rk;
-        vec[R::kLeft + i] = exp2f(static_cast<float>(whole - s[k])) * rk;
-        vec[R::kRead + i] = rq;
-        vec[R::kReadS + i] = e;
+        r.past[k] = exp2f(hi);
+        r.left[k] = exp2f(static_cast<float>(whole - s[k]));
+        vec[R::kBeta + i] = r.beta[k];
+        vec[R::kReadS + i] = r.past[k];
         vec[R::kDecay + i] = exp2f(a[k]);
-        vec[R::kKey + i] = rk;
     }
-    if (lane == 0) {
-        vec[R::kWhole] = exp2f(static_cast<float>(whole));
-        vec[R::kSlow] = bad ? 1.0f : 0.0f;
-    }
+    if (lane == 0) vec[R::kWhole] = exp2f(static_cast<float>(whole));
+    return r;
 }
 
 // Grid: chunks, heads / per_cta (the heads of a CTA are of one key head).
@@ -360,8 +361,18 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
                 reinterpret_cast<const unsigned short *>(m.d.beta)[t * m.d.beta_t + h * m.d.beta_h];
         }
     }
+    // (under the copies)
+    float *const my_vec = reinterpret_cast<float *>(raw + Smem::kVec) + warp * 512;
+    DeltaRates rates{};
+    if (warp < m.per_cta)
+        rates = delta_rates(dt, gate, bias, A2, valid,
+                            reinterpret_cast<float *>(raw + Smem::kSums) + warp * 2 * kDeltaChunk,
+                            my_vec, lane);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
+    // the warp's 16 rows: the last rows' work is four times the first's, and warps of one number
+    // share a scheduler
+    const int block = (warp + blockIdx.x + blockIdx.y) & 3;
     float *const lengths = reinterpret_cast<float *>(raw + Smem::kLengths);
     const int g = lane >> 2, t = lane & 3;
     // K K^T and Q K^T: 16 rows per warp, the columns up to its own 16; of Q Q^T the diagonal
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
     {
         const unsigned tiles = smem_u32(raw);
         const int mi = lane >> 3, r = lane & 7;
-        const unsigned a_at = tiles + (16 * warp + (mi & 1) * 8 + r) * Smem::kPitch + (mi >> 1) * 16;
+        const unsigned a_at = tiles + (16 * block + (mi & 1) * 8 + r) * Smem::kPitch + (mi >> 1) * 16;
         const unsigned b_at = tiles + ((mi >> 1) * 8 + r) * Smem::kPitch + (mi & 1) * 16;
         constexpr int kQ = kDeltaChunk * Smem::kPitch;
 #pragma unroll
@@ -377,12 +388,12 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
             unsigned ka[4], qa[4], b[4];
             ldsm4(ka, a_at + ks * 32);
             ldsm4(qa, a_at + kQ + ks * 32);
-            ldsm4(b, b_at + kQ + warp * 16 * Smem::kPitch + ks * 32);
+            ldsm4(b, b_at + kQ + block * 16 * Smem::kPitch + ks * 32);
             mma_16816(qq[0], qa, b[0], b[1]);
             mma_16816(qq[1], qa, b[2], b[3]);
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) {
-                if (nb > warp) continue;
+                if (nb > block) continue;
                 ldsm4(b, b_at + nb * 16 * Smem::kPitch + ks * 32);
                 mma_16816(kk[2 * nb], ka, b[0], b[1]);
                 mma_16816(kk[2 * nb + 1], ka, b[2], b[3]);
@@ -392,7 +403,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         }
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
-            if (nb == warp)
+            if (nb == block)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) own[0][i] = kk[2 * nb][i], own[1][i] = kk[2 * nb + 1][i];
     }
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         const bool unit = m.d.eps >= 0.0f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int row = 16 * warp + g + 8 * half;
+            const int row = 16 * block + g + 8 * half;
             const float k2 = g & 1 ? own[half][2 * half + 1] : own[half][2 * half];
             const float q2 = g & 1 ? qq[half][2 * half + 1] : qq[half][2 * half];
             const bool live = row < valid;
@@ -414,17 +425,26 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         }
     }
     bad = __syncthreads_or(bad);
-    if (warp < m.per_cta)
-        delta_factors(m.d, dt, gate, bias, A2, valid, lengths, bad,
-                      reinterpret_cast<float *>(raw + Smem::kSums) + warp * 2 * kDeltaChunk,
-                      reinterpret_cast<float *>(raw + Smem::kVec) + warp * 512, lane);
+    if (warp < m.per_cta) {
+        const bool slow = bad || __any_sync(0xffffffffu, rates.bad);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = 2 * lane + k;
+            const float rk = lengths[i];
+            my_vec[R::kPast + i] = rates.beta[k] * rates.past[k] * rk;
+            my_vec[R::kLeft + i] = rates.left[k] * rk;
+            my_vec[R::kRead + i] = lengths[kDeltaChunk + i];
+            my_vec[R::kKey + i] = rk;
+        }
+        if (lane == 0) my_vec[R::kSlow] = slow ? 1.0f : 0.0f;
+    }
     float *const L = reinterpret_cast<float *>(raw + Smem::kL);
     float *const T = reinterpret_cast<float *>(raw + Smem::kT);
     // what stays zero for every head: T and M above the blocks of 16 on the diagonal
-    for (int n = 2 * warp + 2; n < 8; ++n)
+    for (int n = 2 * block + 2; n < 8; ++n)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int i = 16 * warp + g + 8 * half;
+            const int i = 16 * block + g + 8 * half;
             *reinterpret_cast<float2 *>(T + i * kPrepPitch + 8 * n + 2 * t) =
                 make_float2(0.0f, 0.0f);
             *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 + ((n ^ (i & 7)) << 4) + 4 * t) =
@@ -436,14 +456,14 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         const float *const sums = reinterpret_cast<float *>(raw + Smem::kSums) + k * 2 * kDeltaChunk;
         const float *const vec = reinterpret_cast<float *>(raw + Smem::kVec) + k * 512;
         {
-            const int i0 = 16 * warp + g;
+            const int i0 = 16 * block + g;
             const float hi[2] = {sums[i0], sums[i0 + 8]};
             const float lo[2] = {sums[kDeltaChunk + i0], sums[kDeltaChunk + i0 + 8]};
             const float f[2] = {vec[R::kBeta + i0] * lengths[i0],
                                 vec[R::kBeta + i0 + 8] * lengths[i0 + 8]};
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                if (n > 2 * warp + 1) continue;
+                if (n > 2 * block + 1) continue;
                 const int j = 8 * n + 2 * t;
                 const float2 sh = *reinterpret_cast<const float2 *>(sums + j);
                 const float2 sl = *reinterpret_cast<const float2 *>(sums + kDeltaChunk + j);
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         // the warp's block of 16 on the diagonal: a column of the inverse per lane (L's elements on
         // and above the diagonal are not looked at)
         if (lane < 16) {
-            const float *const block = L + 16 * warp * (kPrepPitch + 1);
+            const float *const rows = L + 16 * block * (kPrepPitch + 1);
             float x[16];
             x[0] = lane == 0 ? 1.0f : 0.0f;
 #pragma unroll
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < i; j += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(block + i * kPrepPitch + j);
+                    const float4 l = *reinterpret_cast<const float4 *>(rows + i * kPrepPitch + j);
                     sum = fmaf(l.x, x[j], sum);
                     if (j + 1 < i) sum = fmaf(l.y, x[j + 1], sum);
                     if (j + 2 < i) sum = fmaf(l.z, x[j + 2], sum);
@@ -484,7 +504,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
                 x[i] = i == lane ? 1.0f : i < lane ? 0.0f : -sum;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kPrepPitch + 16 * warp + lane] = x[i];
+            for (int i = 0; i < 16; ++i) T[(16 * block + i) * kPrepPitch + 16 * block + lane] = x[i];
         }
         __syncthreads();
         // joined to blocks of 32, then of 64: T21 = -T22 (L21 T11), the product in brackets in
@@ -647,8 +667,8 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 //   loader:  [empty] tiles and record -> full
 //   looker:  [full] values looked over, a prompt's last chunk cut -> look
 //   issuer:  [look, s] S (K, Q)^T -> p; [r] R T^T -> u; [w] U K -> d; [q] U M^T -> m, empty
-//   compute: [look, p] R -> r; the last chunk's [m] readout into its V's place -> t, empty;
-//            [u] U -> w; S Q^T with its decays to where U M^T adds to it -> q; [d] S -> s
+//   compute: [look, p] R -> r; the last chunk's [m] readout into its V's place -> t, empty; [u] U ->
+//            w; S Q^T with its decays to where U M^T adds to it, U for that -> q; [d] S -> s
 //   storer:  [look, t] the readout's tile out -> empty
 //
 // S, R and U are handed over 16 columns of each warpgroup at a time, so that products of the first
@@ -700,9 +720,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-    // TMEM columns: S's parts, the third of which makes room for U's first two; the next state's sum
-    // (before it, R's parts); S K^T, then U, then in its place U in bf16 and U's third part; S Q^T;
-    // the readout's sum
+    // TMEM columns: S's parts, the third of which makes room for two of weighted U; the next state's
+    // sum (before it, R's parts); S K^T, then U, then in its place weighted U's third part; S Q^T,
+    // then U's parts for the readout; the readout's sum
     const unsigned tS = tmem, tW = tmem + 128, tD = tmem + 192, tP = tmem + 320, tQ = tmem + 384,
                    tM = tmem + 448;
     // U's weighted parts, k-step by k-step (16 tokens): two parts of 32 columns; the third in pieces
@@ -836,7 +856,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 __syncwarp();
                 continue;
             }
-            // U of the last such chunk has been read before its place is written
+            // U of the last such chunk has been read before its places are written
             if (any) mbar_pass(bar_m, fast ^ 1, dead);
             any = true;
 #pragma unroll
@@ -894,9 +914,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             mbar_pass(bar_q, fast, dead);
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_ts_of(leader, tM, tP + 32 * (k / 2) + 8 * (k % 2),
-                          operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ts_of(leader, tM, tQ + 32 * (k / 2) + 16 * part + 8 * (k % 2),
+                              operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
             tc_commit_of(leader, empty + 8 * stage);
             tc_commit_of(leader, bar_m);
             fast ^= 1;
@@ -942,21 +964,22 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             warp_arrive(bar, lane);
         };
         // Two blocks of pairs as bf16 parts, to the columns that `to(part)` names.
-        auto put = [&](const float2 (&f)[2][2][2], auto to) {
-            unsigned bits[kParts][2][4];
+        auto put_parts = [&](auto parts, const float2 (&f)[2][2][2], auto to) {
+            constexpr int kN = decltype(parts)::value;
+            unsigned bits[kN][2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        unsigned w[kParts];
-                        split2<kParts>(f[i][hh][e], w);
+                        unsigned w[kN];
+                        split2<kN>(f[i][hh][e], w);
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part) bits[part][hh][2 * i + e] = w[part];
+                        for (int part = 0; part < kN; ++part) bits[part][hh][2 * i + e] = w[part];
                     }
 #pragma unroll
-            for (int part = 0; part < kParts; ++part)
+            for (int part = 0; part < kN; ++part)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
                     tc_store_frag(to(part) + lanes + hh * kLanes16, bits[part][hh]);
@@ -966,7 +989,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 {{S[2 * x][0][0], S[2 * x][0][1]}, {S[2 * x][1][0], S[2 * x][1][1]}},
                 {{S[2 * x + 1][0][0], S[2 * x + 1][0][1]},
                  {S[2 * x + 1][1][0], S[2 * x + 1][1][1]}}};
-            put(f, [&](int part) { return tS + part * (N / 2) + half * (N / 4) + 8 * x; });
+            put_parts(std::integral_constant<int, kParts>(), f, [&](int part) { return tS + part * (N / 2) + half * (N / 4) + 8 * x; });
             hand_over(bar_s + 8 * x);
         };
         if (chunks)
@@ -1153,14 +1176,18 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             __syncwarp();
             tc_fence_after();
             {
-                unsigned sk[2][16];
+                unsigned sk[2][2][8];
+                auto fetch = [&](int x) {  // the next piece on its way under this one's work
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half, sk[hh]);
-                tc_wait_ld();
+                    for (int hh = 0; hh < 2; ++hh)
+                        tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half + 16 * x, sk[x][hh]);
+                };
+                fetch(0);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float2 r[2][2][2];
+                    tc_wait_ld();
+                    if (x == 0) fetch(1);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float2 beta = factors(vec, R::kBeta, 2 * x + i);
@@ -1170,104 +1197,118 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const unsigned u = v[x][hh][2 * i + e];
-                                const int k = 8 * x + 4 * i + 2 * e;
+                                const int k = 4 * i + 2 * e;
                                 r[i][hh][e] = __ffma2_rn(
                                     make_float2(-past.x, -past.y),
-                                    make_float2(__uint_as_float(sk[hh][k]),
-                                                __uint_as_float(sk[hh][k + 1])),
+                                    make_float2(__uint_as_float(sk[x][hh][k]),
+                                                __uint_as_float(sk[x][hh][k + 1])),
                                     __fmul2_rn(beta, make_float2(__uint_as_float(u << 16),
                                                                  __uint_as_float(u & 0xffff0000u))));
                             }
                     }
-                    put(r, [&](int part) { return tD + part * 32 + 16 * half + 8 * x; });
+                    put_parts(std::integral_constant<int, kParts>(), r, [&](int part) { return tD + part * 32 + 16 * half + 8 * x; });
                     hand_over(bar_r + 8 * x);
                 }
             }
             if (waits) read_out(c - 1);  // under R T^T
-            // U for the readout, and with its weights for the next state
+            // U with its weights for the next state; then (under U K) S Q^T with its decays to where U M^T
+            // will add to it, and U for the readout
             mbar_pass(bar_u, fast, dead);
             __syncwarp();
             tc_fence_after();
             {
-                unsigned u[2][16];
+                unsigned u[2][2][8];
+                auto fetch = [&](int x) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half, u[hh]);
-                tc_wait_ld();
+                    for (int hh = 0; hh < 2; ++hh)
+                        tc_load_frag(tP + lanes + hh * kLanes16 + 32 * half + 16 * x, u[x][hh]);
+                };
+                auto of_u = [&](int x, int i, int hh, int e) {
+                    const int k = 4 * i + 2 * e;
+                    return make_float2(__uint_as_float(u[x][hh][k]),
+                                       __uint_as_float(u[x][hh][k + 1]));
+                };
+                fetch(0);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float2 w[2][2][2];
-                    unsigned plain[2][4];
+                    tc_wait_ld();
+                    if (x == 0) fetch(1);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float2 left = factors(vec, R::kLeft, 2 * x + i);
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int k = 8 * x + 4 * i + 2 * e;
-                                const float2 f = make_float2(__uint_as_float(u[hh][k]),
-                                                             __uint_as_float(u[hh][k + 1]));
-                                plain[hh][2 * i + e] = f2_to_bf2(f.x, f.y);
-                                w[i][hh][e] = __fmul2_rn(f, left);
-                            }
+                            for (int e = 0; e < 2; ++e)
+                                w[i][hh][e] = __fmul2_rn(of_u(x, i, hh, e), left);
                     }
-                    // (in tP over columns that this warp alone has read)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh)
-                        tc_store_frag(tP + lanes + hh * kLanes16 + 32 * half + 8 * x, plain[hh]);
-                    put(w, [&](int part) { return weighted(part, 2 * half + x); });
+                    if (x == 0) tc_wait_ld();  // (the third part goes over what has been read)
+                    put_parts(std::integral_constant<int, kParts>(), w, [&](int part) { return weighted(part, 2 * half + x); });
                     hand_over(bar_w + 8 * x);
                 }
-            }
-            // S Q^T with its decays, where U M^T will add to it (under U K)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                unsigned sq[16];
-                tc_load_frag(tQ + lanes + hh * kLanes16 + 32 * half, sq);
-                tc_wait_ld();
+                for (int hh = 0; hh < 2; ++hh) {
+                    unsigned sq[16];
+                    tc_load_frag(tQ + lanes + hh * kLanes16 + 32 * half, sq);
+                    tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 past = factors(vec, R::kReadS, i);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 past = factors(vec, R::kReadS, i);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = 4 * i + 2 * e;
-                        const float2 f =
-                            __fmul2_rn(past, make_float2(__uint_as_float(sq[k]),
-                                                         __uint_as_float(sq[k + 1])));
-                        sq[k] = __float_as_uint(f.x);
-                        sq[k + 1] = __float_as_uint(f.y);
+                        for (int k = 4 * i; k < 4 * i + 4; k += 2) {
+                            const float2 f =
+                                __fmul2_rn(past, make_float2(__uint_as_float(sq[k]),
+                                                             __uint_as_float(sq[k + 1])));
+                            sq[k] = __float_as_uint(f.x);
+                            sq[k + 1] = __float_as_uint(f.y);
+                        }
                     }
+                    tc_store_frag(tM + lanes + hh * kLanes16 + 32 * half, sq);
                 }
-                tc_store_frag(tM + lanes + hh * kLanes16 + 32 * half, sq);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float2 f[2][2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) f[i][hh][e] = of_u(x, i, hh, e);
+                    put_parts(std::integral_constant<int, 2>(), f, [&](int part) { return tQ + 32 * half + 16 * part + 8 * x; });
+                }
+                hand_over(bar_q);
             }
-            hand_over(bar_q);
             const float whole = vec[R::kWhole];
             mbar_pass(bar_d, fast, dead);
             __syncwarp();
             tc_fence_after();
+            {
+                unsigned d[2][2][8];
+                auto fetch = [&](int x) {
 #pragma unroll
-            for (int y = 0; y < kPieces / 2; ++y) {
-                unsigned d[2][16];
+                    for (int hh = 0; hh < 2; ++hh)
+                        tc_load_frag(tD + lanes + hh * kLanes16 + half * kCols + 16 * x,
+                                     d[x % 2][hh]);
+                };
+                fetch(0);
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    tc_load_frag(tD + lanes + hh * kLanes16 + half * kCols + 32 * y, d[hh]);
-                tc_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < kPieces; ++x) {
+                    tc_wait_ld();
+                    if (x + 1 < kPieces) fetch(x + 1);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int k = 8 * x + 4 * i + 2 * e;
-                                float2 &s = S[4 * y + 2 * x + i][hh][e];
+                                const int k = 4 * i + 2 * e;
+                                float2 &s = S[2 * x + i][hh][e];
                                 s = __ffma2_rn(s, make_float2(whole, whole),
-                                               make_float2(__uint_as_float(d[hh][k]),
-                                                           __uint_as_float(d[hh][k + 1])));
+                                               make_float2(__uint_as_float(d[x % 2][hh][k]),
+                                                           __uint_as_float(d[x % 2][hh][k + 1])));
                             }
-                    if (c + 1 < chunks) publish(2 * y + x);
+                    if (c + 1 < chunks) publish(x);
                 }
             }
             waits = true;
