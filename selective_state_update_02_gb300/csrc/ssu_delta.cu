@@ -194,11 +194,11 @@ bool mma_operands(const DeltaParams &d) {
 }
 
 template <int N, typename ST, bool kIdx64>
-cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[4],
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[6],
                        ssu_handle_s &handle, cudaStream_t st) {
     auto *prep = ssu_delta_prep_kernel<N>;
     auto *main = ssu_delta_mma_kernel<N, ST, kIdx64>;
-    constexpr int kPrepBytes = PrepSmem<N>::kTotal, kBytes = DeltaSmem<N>::kTotal + 1024;
+    constexpr int kPrepBytes = PrepSmem<N>::kTotal + 1024, kBytes = DeltaSmem<N>::kTotal + 1024;
     cudaError_t e =
         ssu_host::allow_smem(handle, reinterpret_cast<const void *>(prep), kPrepBytes);
     if (e == cudaSuccess)
@@ -220,7 +220,7 @@ cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtens
                        static_cast<unsigned>(p.nheads / m.per_cta));
     cfg.blockDim = dim3(kPrepThreads);
     cfg.dynamicSmemBytes = kPrepBytes;
-    e = cudaLaunchKernelEx(&cfg, prep, m);
+    e = cudaLaunchKernelEx(&cfg, prep, m, maps[4], maps[5]);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.nheads * m.slabs));
     cfg.blockDim = dim3(kDeltaThreads);
@@ -228,7 +228,7 @@ cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtens
     return cudaLaunchKernelEx(&cfg, main, m, maps[0], maps[1], maps[2], maps[3]);
 }
 
-cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[4],
+cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[6],
                        const ssu_shape_t &s, ssu_handle_s &handle, cudaStream_t st) {
     const bool bf16 = s.state_dtype == SSU_STATE_BF16, i64 = s.index_dtype == SSU_INDEX_I64;
 #define SSU_MMA(N_, ST_)                                              \
@@ -338,11 +338,13 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
         m.prompts = reinterpret_cast<int4 *>(room + w.prompts);
         m.chunks = reinterpret_cast<int2 *>(room + w.list);
         m.records = reinterpret_cast<unsigned char *>(room + w.records);
-        CUtensorMap maps[4];
+        CUtensorMap maps[6];
         if (encode_map(&maps[0], k, s.dstate, s.ngroups, tokens, p.B_g, p.B_b, kDeltaChunk) &&
             encode_map(&maps[1], q, s.dstate, s.ngroups, tokens, p.C_g, p.C_b, kDeltaChunk) &&
             encode_map(&maps[2], v, s.headdim, s.nheads, tokens, p.x_h, p.x_b, kDeltaChunk) &&
-            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b, kDeltaChunk))
+            encode_map(&maps[3], out, s.headdim, s.nheads, tokens, p.out_h, p.out_b, kDeltaChunk) &&
+            encode_map(&maps[4], k, s.dstate, s.ngroups, tokens, p.B_g, p.B_b, kDeltaChunk / 4) &&
+            encode_map(&maps[5], q, s.dstate, s.ngroups, tokens, p.C_g, p.C_b, kDeltaChunk / 4))
             e = launch_mma(m, w, maps, s, *handle, cs);
     }
     if (e == cudaErrorNotSupported) e = dispatch(s, [&](auto n, auto st, auto i64) {

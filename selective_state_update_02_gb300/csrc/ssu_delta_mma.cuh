@@ -83,6 +83,61 @@ struct DeltaMmaParams {
     unsigned char *records;  // [chunk][head]
 };
 
+// ---- pieces of both passes ----------------------------------------------------------------
+
+// TMEM in the fragments of an 8 x 8 matrix: of 16 lanes and 8 columns a thread holds columns 2 t and
+// 2 t + 1 (t = lane % 4) of lanes g and g + 8 (g = lane / 4), and of packed pairs column t of 4.
+// So V comes by ldmatrix and the readout goes by stmatrix, both transposed, with a pair of tokens
+// per register (an element per load and store kept shared memory busy for 2,000 cycles per chunk).
+__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[16]) {  // 32 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[8]) {  // 16 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[4]) {  // 8 columns
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void load_trans4(unsigned (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_trans4(unsigned addr, const unsigned (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // ---- the plan ----------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 256;
@@ -173,79 +228,75 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
 
 // ---- the first pass ------------------------------------------------------------------------
 //
-// What bounds it: shared memory's bandwidth and the chain of its steps, so products of blocks are
-// MMAs (K K^T and Q K^T of bf16 operands; blocks of T of fp32 ones in two tf32 parts, 2^-20) and
-// everything else is done by the thread that holds an element.
+// K K^T and Q K^T are one tcgen05 product of K and Q, 16 rows of each in turn, with themselves: then
+// the four warps of a TMEM quarter each have 16 rows of both, and Q's lengths are on the diagonal.
+// The blocks of T are joined by mma.sync of operands in two bf16 parts (three products, 2^-17).
+//
+// What bounds it: the chain of its steps, with 16 warps to an SM, and mma.sync, of which an SM starts
+// one per 8 cycles (with those for K K^T and Q K^T too, and tf32 parts for the joins, it bounded the
+// pass at 1.9 times its time).
 
 constexpr int kPrepThreads = 128;
 constexpr int kPrepHeads = 4;   // the most heads per CTA: one per warp makes its factors
 constexpr int kPrepPitch = 68;  // floats per row of L and T
+constexpr int kPrepColumns = 128;  // of TMEM
 
 template <int N>
 struct PrepSmem {
-    static constexpr int kPitch = N * 2 + 16;  // bytes per row of K and Q
-    static constexpr int kL = 0;               // over K and Q, when those are in registers
+    static constexpr int kBlock = 128 * 128;  // 64 columns of K's and Q's rows
+    static constexpr int kL = 0;              // over K and Q, when their products are done
     static constexpr int kT = kL + kDeltaChunk * kPrepPitch * 4;
-    static constexpr int kTilesEnd = 2 * kDeltaChunk * kPitch;
+    static constexpr int kTilesEnd = N / 64 * kBlock;
     static constexpr int kMatEnd = kT + kDeltaChunk * kPrepPitch * 4;
     static constexpr int kM = kTilesEnd > kMatEnd ? kTilesEnd : kMatEnd;
     static constexpr int kLengths = kM + kDeltaTile;  // 1 / |k|, scale / |q|
     static constexpr int kSums = kLengths + 2 * kDeltaChunk * 4;  // s in two floats, per head
     static constexpr int kVec = kSums + kPrepHeads * 2 * kDeltaChunk * 4;  // per head
-    static constexpr int kTotal = kVec + kPrepHeads * 2048;
+    static constexpr int kBars = kVec + kPrepHeads * 2048;
+    static constexpr int kTotal = kBars + 16;
 };
 
-__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4], unsigned b0,
-                                          unsigned b1) {
+__device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4],
+                                          const unsigned (&b)[2]) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const unsigned (&a)[4],
-                                         const unsigned (&b)[2]) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// An fp32 value as two tf32 parts.
-__device__ __forceinline__ void split_tf32(float x, unsigned &hi, unsigned &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
+// A pair of fp32 values as two bf16 parts.
+__device__ __forceinline__ void split_pair(float2 f, unsigned &hi, unsigned &lo) {
+    hi = f2_to_bf2(f.x, f.y);
+    lo = f2_to_bf2(f.x - __uint_as_float(hi << 16), f.y - __uint_as_float(hi & 0xffff0000u));
 }
 
-// d += A B over K columns of A and rows of B, both in rows of kPrepPitch floats: 16 rows from `a`,
-// kTiles times 8 columns from `b`.
-template <int K, int kTiles>
+// d += A B over columns k0 .. k1 - 1 of A and those rows of B, both in rows of kPrepPitch floats: 16
+// rows from `a`, kTiles times 8 columns from `b`.
+template <int kMost, int kTiles>
 __device__ __forceinline__ void block_product(float (&d)[kTiles][4], const float *a,
-                                              const float *b, int lane) {
+                                              const float *b, int k0, int k1, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const float *const arow = a + g * kPrepPitch + t, *const brow = b + t * kPrepPitch + g;
+    const float *const arow = a + g * kPrepPitch + 2 * t, *const brow = b + 2 * t * kPrepPitch + g;
 #pragma unroll
-    for (int k = 0; k < K; k += 8) {
+    for (int k = 0; k < kMost; k += 16) {
+        if (k < k0 || k >= k1) continue;
         unsigned ah[4], al[4];
-        split_tf32(arow[k], ah[0], al[0]);
-        split_tf32(arow[8 * kPrepPitch + k], ah[1], al[1]);
-        split_tf32(arow[k + 4], ah[2], al[2]);
-        split_tf32(arow[8 * kPrepPitch + k + 4], ah[3], al[3]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            split_pair(*reinterpret_cast<const float2 *>(arow + x % 2 * 8 * kPrepPitch + k +
+                                                         x / 2 * 8),
+                       ah[x], al[x]);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
             unsigned bh[2], bl[2];
-            split_tf32(brow[k * kPrepPitch + 8 * n], bh[0], bl[0]);
-            split_tf32(brow[(k + 4) * kPrepPitch + 8 * n], bh[1], bl[1]);
-            mma_tf32(d[n], al, bh);
-            mma_tf32(d[n], ah, bl);
-            mma_tf32(d[n], ah, bh);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float *const at = brow + (k + 8 * x) * kPrepPitch + 8 * n;
+                split_pair(make_float2(at[0], at[kPrepPitch]), bh[x], bl[x]);
+            }
+            mma_16816(d[n], al, bh);
+            mma_16816(d[n], ah, bl);
+            mma_16816(d[n], ah, bh);
         }
     }
 }
@@ -261,6 +312,16 @@ __device__ __forceinline__ void put_product(const float (&d)[kTiles][4], float *
         *reinterpret_cast<float2 *>(row + 8 * kPrepPitch + 8 * n) =
             make_float2(sign * d[n][2], sign * d[n][3]);
     }
+}
+
+// Sums of log decays are pairs of floats, the second what rounding the first has lost: differences of
+// neighbours stay exact behind long decays.  (In double, which this GPU has few units for, the sums of
+// a chunk took 6,000 cycles.)
+__device__ __forceinline__ float2 add_pairs(float2 a, float2 b) {
+    const float sum = a.x + b.x, of_b = sum - a.x;
+    const float lost = (a.x - (sum - of_b)) + (b.x - of_b) + (a.y + b.y);
+    const float x = sum + lost;
+    return make_float2(x, lost - (x - sum));
 }
 
 // One head's rates of the chunk's tokens, two per lane of one warp, before their keys' lengths are
@@ -286,65 +347,93 @@ __device__ __forceinline__ DeltaRates delta_rates(const unsigned (&dt)[2], const
         r.beta[k] = 1.0f / (1.0f + expf(-__uint_as_float(gate[k] << 16)));
         r.bad |= !(a[k] < 60.0f) || !(r.beta[k] <= 1.0f);
     }
-    // sums in double, kept as two floats: differences of neighbours stay exact behind long decays
-    double upto = static_cast<double>(a[0]) + a[1];
+    float2 upto = add_pairs(make_float2(a[0], 0.0f), make_float2(a[1], 0.0f));
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, upto, x);
-        if (lane >= x) upto += o;
+        const float2 o = make_float2(__shfl_up_sync(0xffffffffu, upto.x, x),
+                                     __shfl_up_sync(0xffffffffu, upto.y, x));
+        if (lane >= x) upto = add_pairs(o, upto);
     }
-    const double s[2] = {upto - a[1], upto};
-    const double whole = __shfl_sync(0xffffffffu, upto, 31);
-    r.bad |= !(s[0] < 60.0) || !(s[1] < 60.0);
+    float2 before = make_float2(__shfl_up_sync(0xffffffffu, upto.x, 1),
+                                __shfl_up_sync(0xffffffffu, upto.y, 1));
+    if (lane == 0) before = make_float2(0.0f, 0.0f);
+    const float2 s[2] = {add_pairs(before, make_float2(a[0], 0.0f)), upto};
+    const float2 whole = make_float2(__shfl_sync(0xffffffffu, upto.x, 31),
+                                     __shfl_sync(0xffffffffu, upto.y, 31));
+    r.bad |= !(s[0].x < 60.0f) || !(s[1].x < 60.0f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int i = 2 * lane + k;
-        const float hi = static_cast<float>(s[k]);
-        sums[i] = hi;
-        sums[kDeltaChunk + i] = static_cast<float>(s[k] - hi);
-        r.past[k] = exp2f(hi);
-        r.left[k] = exp2f(static_cast<float>(whole - s[k]));
+        sums[i] = s[k].x;
+        sums[kDeltaChunk + i] = s[k].y;
+        r.past[k] = exp2f(s[k].x);
+        r.left[k] = exp2f((whole.x - s[k].x) + (whole.y - s[k].y));
         vec[R::kBeta + i] = r.beta[k];
         vec[R::kReadS + i] = r.past[k];
         vec[R::kDecay + i] = exp2f(a[k]);
     }
-    if (lane == 0) vec[R::kWhole] = exp2f(static_cast<float>(whole));
+    if (lane == 0) vec[R::kWhole] = exp2f(whole.x);
     return r;
 }
 
 // Grid: chunks, heads / per_cta (the heads of a CTA are of one key head).
 template <int N>
-__global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
-    const __grid_constant__ DeltaMmaParams m) {
-    pdl_wait();
-    pdl_trigger();
+__global__ void __launch_bounds__(kPrepThreads)
+    ssu_delta_prep_kernel(const __grid_constant__ DeltaMmaParams m,
+                          const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_q) {
     using Smem = PrepSmem<N>;
     using R = DeltaRecord;
-    extern __shared__ __align__(128) unsigned char raw[];
+    extern __shared__ unsigned char unaligned[];
+    __shared__ unsigned tmem_slot;
+    const unsigned tiles = (smem_u32(unaligned) + 1023u) & ~1023u;
+    unsigned char *const raw = unaligned + (tiles - smem_u32(unaligned));
+    const unsigned bar_tiles = tiles + Smem::kBars, bar_product = bar_tiles + 8;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        mbar_init(bar_tiles, 1);
+        mbar_init(bar_product, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_slot)),
+                     "r"(kPrepColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    auto free_tmem = [&]() {
+        if (warp == 0)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(kPrepColumns)
+                         : "memory");
+    };
+    pdl_wait();
+    pdl_trigger();
     const int2 chunk = m.chunks[blockIdx.x];  // (past the last one: of no use, and not used)
-    if (static_cast<int>(blockIdx.x) >= *m.total) return;
+    if (static_cast<int>(blockIdx.x) >= *m.total) {
+        free_tmem();
+        return;
+    }
     const SsuParams &p = m.d.m.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tok = chunk.x, valid = chunk.y;
     const int h0 = blockIdx.y * m.per_cta, grp = group_of(h0, p.group_magic);
-    {
-        constexpr int kPieces = N / 8;
-        const unsigned tiles = smem_u32(raw);
+    unsigned dead = 0;
+    if (tid == 96) {
+        mbar_expect(bar_tiles, N / 64 * Smem::kBlock);
 #pragma unroll
-        for (int x = 0; x < kDeltaChunk * kPieces / kPrepThreads; ++x) {
-            const int k = tid + x * kPrepThreads, row = k / kPieces, piece = k % kPieces;
-            const long long t = static_cast<long long>(tok) + (row < valid ? row : 0);
-            const int bytes = row < valid ? 16 : 0;  // the others become zeros
-            const unsigned to = tiles + row * Smem::kPitch + piece * 16;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                         "l"(p.B + t * p.B_b + grp * p.B_g + piece * 8), "r"(bytes)
-                         : "memory");
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             to + kDeltaChunk * Smem::kPitch),
-                         "l"(p.C + t * p.C_b + grp * p.C_g + piece * 8), "r"(bytes)
-                         : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int k = 0; k < N / 64; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const unsigned to = tiles + k * Smem::kBlock + w * 4096;
+                tma_load(to, &map_k, bar_tiles, k * 64, grp, tok + 16 * w);
+                tma_load(to + 2048, &map_q, bar_tiles, k * 64, grp, tok + 16 * w);
+            }
     }
     // the rates of the warp's own head
     unsigned dt[2] = {}, gate[2] = {};
@@ -368,45 +457,51 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
         rates = delta_rates(dt, gate, bias, A2, valid,
                             reinterpret_cast<float *>(raw + Smem::kSums) + warp * 2 * kDeltaChunk,
                             my_vec, lane);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    // the warp's 16 rows: the last rows' work is four times the first's, and warps of one number
-    // share a scheduler
-    const int block = (warp + blockIdx.x + blockIdx.y) & 3;
+    if (warp == 3) {
+        const unsigned leader = elect_one();
+        mbar_pass(bar_tiles, 0, dead);
+        if (leader)
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+                const unsigned long long at =
+                    operand(tiles + (k / 4) * Smem::kBlock + (k % 4) * 32, 0);
+                mma_ss(tmem, at, at, instruction(128, false, false), k > 0);
+            }
+        tc_commit_of(leader, bar_product);
+        __syncwarp();
+    }
+    // The warp's 16 rows are its TMEM quarter's: lanes 0 .. 15 have K's, the others Q's.
+    const int block = warp;
     float *const lengths = reinterpret_cast<float *>(raw + Smem::kLengths);
     const int g = lane >> 2, t = lane & 3;
-    // K K^T and Q K^T: 16 rows per warp, the columns up to its own 16; of Q Q^T the diagonal
     float kk[8][4] = {}, qk[8][4] = {}, own[2][4] = {}, qq[2][4] = {};
+    mbar_pass(bar_product, 0, dead);
+    __syncwarp();
+    tc_fence_after();
     {
-        const unsigned tiles = smem_u32(raw);
-        const int mi = lane >> 3, r = lane & 7;
-        const unsigned a_at = tiles + (16 * block + (mi & 1) * 8 + r) * Smem::kPitch + (mi >> 1) * 16;
-        const unsigned b_at = tiles + ((mi >> 1) * 8 + r) * Smem::kPitch + (mi & 1) * 16;
-        constexpr int kQ = kDeltaChunk * Smem::kPitch;
+        const unsigned k_rows = tmem + (static_cast<unsigned>(block) << 21);
+        const unsigned q_rows = k_rows + (16u << 16);
+        unsigned r[8];
+        auto take = [&](float (&a)[4], float (&b)[4]) {
 #pragma unroll
-        for (int ks = 0; ks < N / 16; ++ks) {
-            unsigned ka[4], qa[4], b[4];
-            ldsm4(ka, a_at + ks * 32);
-            ldsm4(qa, a_at + kQ + ks * 32);
-            ldsm4(b, b_at + kQ + block * 16 * Smem::kPitch + ks * 32);
-            mma_16816(qq[0], qa, b[0], b[1]);
-            mma_16816(qq[1], qa, b[2], b[3]);
+            for (int i = 0; i < 4; ++i) a[i] = __uint_as_float(r[i]), b[i] = __uint_as_float(r[4 + i]);
+        };
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                if (nb > block) continue;
-                ldsm4(b, b_at + nb * 16 * Smem::kPitch + ks * 32);
-                mma_16816(kk[2 * nb], ka, b[0], b[1]);
-                mma_16816(kk[2 * nb + 1], ka, b[2], b[3]);
-                mma_16816(qk[2 * nb], qa, b[0], b[1]);
-                mma_16816(qk[2 * nb + 1], qa, b[2], b[3]);
-            }
+        for (int nb = 0; nb < 4; ++nb) {
+            if (nb > block) continue;
+            tc_load_frag(k_rows + 32 * nb, r);
+            tc_wait_ld();
+            take(kk[2 * nb], kk[2 * nb + 1]);
+            if (nb == block) take(own[0], own[1]);
+            tc_load_frag(q_rows + 32 * nb, r);
+            tc_wait_ld();
+            take(qk[2 * nb], qk[2 * nb + 1]);
         }
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-            if (nb == block)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) own[0][i] = kk[2 * nb][i], own[1][i] = kk[2 * nb + 1][i];
+        tc_load_frag(q_rows + 32 * block + 16, r);
+        tc_wait_ld();
+        take(qq[0], qq[1]);
     }
+    tc_fence_before();
     bool bad = false;
     if (t == g >> 1) {  // the thread with rows g and g + 8 of the diagonals
         const bool unit = m.d.eps >= 0.0f;
@@ -420,11 +515,17 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
             const float rq = !live ? 0.0f : unit ? m.d.scale / sqrtf(q2 + m.d.eps) : m.d.scale;
             lengths[row] = rk;
             lengths[kDeltaChunk + row] = rq;
-            bad |= !(k2 < INFINITY) || !(q2 < INFINITY) || !(rk < INFINITY) ||
-                   !(fabsf(rq) < INFINITY);
+            bad |= live && (!(k2 < INFINITY) || !(q2 < INFINITY) || !(rk < INFINITY) ||
+                            !(fabsf(rq) < INFINITY));
         }
     }
     bad = __syncthreads_or(bad);
+    free_tmem();
+    if (__syncthreads_or(dead)) {  // what is in flight lands long before this is over
+        if (tid == 0) atomicOr(&p.err[2], 1u);
+        __nanosleep(1000000);
+        return;
+    }
     if (warp < m.per_cta) {
         const bool slow = bad || __any_sync(0xffffffffu, rates.bad);
 #pragma unroll
@@ -473,9 +574,11 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
                     const int i = i0 + 8 * half;
                     const float e0 = exp2_ftz((hi[half] - sh.x) + (lo[half] - sl.x)) * rk.x;
                     const float e1 = exp2_ftz((hi[half] - sh.y) + (lo[half] - sl.y)) * rk.y;
+                    // (rows past the prompt's end hold anything)
                     *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) =
-                        make_float2(kk[n][2 * half] * (e0 * f[half]),
-                                    kk[n][2 * half + 1] * (e1 * f[half]));
+                        i < valid ? make_float2(kk[n][2 * half] * (e0 * f[half]),
+                                                kk[n][2 * half + 1] * (e1 * f[half]))
+                                  : make_float2(0.0f, 0.0f);
                     *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 +
                                                   ((n ^ (i & 7)) << 4) + 4 * t) =
                         f2_to_bf2(j <= i ? qk[n][2 * half] * e0 : 0.0f,
@@ -513,23 +616,24 @@ __global__ void __launch_bounds__(kPrepThreads) ssu_delta_prep_kernel(
             const int row0 = warp / 2 * 32, c = warp % 2 * 8;
             float y[1][4] = {};
             block_product<16, 1>(y, L + (row0 + 16) * kPrepPitch + row0,
-                                 T + row0 * kPrepPitch + row0 + c, lane);
+                                 T + row0 * kPrepPitch + row0 + c, 0, 16, lane);
             put_product<1>(y, L + row0 * kPrepPitch + row0 + 16 + c, 1.0f, lane);
             __syncthreads();
             float z[1][4] = {};
             block_product<16, 1>(z, T + (row0 + 16) * kPrepPitch + row0 + 16,
-                                 L + row0 * kPrepPitch + row0 + 16 + c, lane);
+                                 L + row0 * kPrepPitch + row0 + 16 + c, 0, 16, lane);
             put_product<1>(z, T + (row0 + 16) * kPrepPitch + row0 + c, -1.0f, lane);
         }
         __syncthreads();
         {
             const int r = warp % 2 * 16, c = warp / 2 * 16;
             float y[2][4] = {};
-            block_product<32, 2>(y, L + (32 + r) * kPrepPitch, T + c, lane);
+            // (T11 and T22 are zero above their diagonals)
+            block_product<32, 2>(y, L + (32 + r) * kPrepPitch, T + c, c, 32, lane);
             put_product<2>(y, L + r * kPrepPitch + 32 + c, 1.0f, lane);
             __syncthreads();
             float z[2][4] = {};
-            block_product<32, 2>(z, T + (32 + r) * kPrepPitch + 32, L + 32 + c, lane);
+            block_product<32, 2>(z, T + (32 + r) * kPrepPitch + 32, L + 32 + c, 0, r + 16, lane);
             put_product<2>(z, T + (32 + r) * kPrepPitch + c, -1.0f, lane);
         }
         __syncthreads();
@@ -594,59 +698,6 @@ __device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigne
             "r"(dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
-}
-
-// TMEM in the fragments of an 8 x 8 matrix: of 16 lanes and 8 columns a thread holds columns 2 t and
-// 2 t + 1 (t = lane % 4) of lanes g and g + 8 (g = lane / 4), and of packed pairs column t of 4.
-// So V comes by ldmatrix and the readout goes by stmatrix, both transposed, with a pair of tokens
-// per register (an element per load and store kept shared memory busy for 2,000 cycles per chunk).
-__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[16]) {  // 32 columns
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_load_frag(unsigned addr, unsigned (&r)[8]) {  // 16 columns
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(addr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[4]) {  // 8 columns
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_store_frag(unsigned addr, const unsigned (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void load_trans4(unsigned (&r)[4], unsigned addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void store_trans4(unsigned addr, const unsigned (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
 }
 
 // Two values as bf16 parts; each part is what the ones before leave.

@@ -63,8 +63,9 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity) {
 }
 
 // The same as straight-line code, which leaves a warp's control flow uniform as the compiler sees it:
-// `dead` becomes nonzero where the wait gave up (after 4 million tries, each suspended for at most 2
-// us or so), and waits no more where it was.  For waits on the CTA's own work alone.
+// `dead` becomes nonzero where the wait gave up (after 40 million looks: a second and more), and waits
+// no more where it was.  For waits on the CTA's own work alone.  (Looks, and not try_wait, whose
+// suspended threads come back some 30 cycles later: 3 % of the delta rule's prompts.)
 __device__ __forceinline__ void mbar_pass(unsigned bar, unsigned parity, unsigned &dead) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
@@ -72,10 +73,10 @@ __device__ __forceinline__ void mbar_pass(unsigned bar, unsigned parity, unsigne
         "setp.ne.u32 p, %0, 0;\n\t"
         "@p bra OUT;\n\t"
         "AGAIN:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra OUT;\n\t"
         "add.u32 n, n, 1;\n\t"
-        "setp.lt.u32 q, n, 4000000;\n\t"
+        "setp.lt.u32 q, n, 40000000;\n\t"
         "@q bra AGAIN;\n\t"
         "mov.u32 %0, 1;\n\t"
         "OUT:\n\t}"
@@ -187,8 +188,8 @@ __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long lon
 }
 
 // The same, and the commit, by the one lane that elect_one() named, in code that the whole warp runs:
-// operands are then uniform to the compiler, and a product takes a third of the cycles to issue
-// (52 from one lane's own branch, where an MMA of N = 64 runs for 32).
+// operands are then uniform to the compiler, and a product takes 23 cycles to issue (52 from one
+// lane's own branch: as long as an MMA of N = 64 runs).
 __device__ __forceinline__ void mma_ts_of(unsigned leader, unsigned d, unsigned a,
                                           unsigned long long b, unsigned idesc, bool add) {
     asm volatile(
