@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
 // pass at 1.9 times its time).
 
 constexpr int kPrepThreads = 128;
-constexpr int kPrepHeads = 4;   // the most heads per CTA: one per warp makes its factors
+constexpr int kPrepHeads = 2;   // the most heads per CTA: a warp each makes their factors
 constexpr int kPrepPitch = 68;  // floats per row of L and T
 constexpr int kPrepColumns = 128;  // of TMEM
 
@@ -378,7 +378,7 @@ __device__ __forceinline__ DeltaRates delta_rates(const unsigned (&dt)[2], const
 
 // Grid: chunks, heads / per_cta (the heads of a CTA are of one key head).
 template <int N>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 4)
     ssu_delta_prep_kernel(const __grid_constant__ DeltaMmaParams m,
                           const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_q) {
