@@ -156,14 +156,24 @@ ssu_status_t validate_tokens(int64_t tokens) {
 // Where its arrays lie in the workspace.
 struct DeltaPlan {
     long long chunks;  // the most that good prompts can have
-    long long order, prompts, list, records, total;
+    long long prompts, list, records, total;
 };
 
 // Records past this (1.2 million tokens of 32 heads) leave a call to the token-by-token form.
 constexpr double kMostRecords = 3.2e10;
 
-bool mma_sizes(const ssu_shape_t &s, int64_t tokens) {
-    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 &&
+// Few tokens go token by token: 3 us and 0.42 for every token of the longest prompt (of which the
+// host knows that it has no more than all), against 8 us and 10 for every round of the device's SMs
+// in chunks (32 heads of 128 x 128, one prompt of 24 tokens: 12.9 us and 17.8, of 64: 29.7 and 17.1; 8
+// prompts of 8 tokens: 24.2 and 28.8; 32 of 2: 41 and 82).
+bool few_tokens(const ssu_shape_t &s, int64_t tokens, int sm_count) {
+    const double units = static_cast<double>(s.batch) * s.nheads *
+                         ((s.headdim + kDeltaRows - 1) / kDeltaRows);
+    return tokens <= 12 + 24 * (units > sm_count ? units / sm_count : 1.0);
+}
+
+bool mma_sizes(const ssu_shape_t &s, int64_t tokens, int sm_count) {
+    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 && !few_tokens(s, tokens, sm_count) &&
            (tokens / kDeltaChunk + static_cast<double>(s.batch)) * s.nheads *
                    DeltaRecord::kBytes <= kMostRecords &&
            s.batch * static_cast<double>(s.nheads) * ((s.headdim + kDeltaRows - 1) / kDeltaRows) <=
@@ -174,9 +184,8 @@ DeltaPlan delta_plan(const ssu_shape_t &s, int64_t tokens) {
     auto up = [](long long bytes) { return (bytes + 255) / 256 * 256; };
     DeltaPlan w;
     w.chunks = tokens / kDeltaChunk + s.batch;
-    w.order = 256;
-    w.prompts = w.order + up(4ll * s.batch);
-    w.list = w.prompts + up(16ll * s.batch);
+    w.prompts = 256;
+    w.list = w.prompts + up(s.batch * static_cast<long long>(sizeof(DeltaPrompt)));
     w.records = w.list + up(8ll * w.chunks);
     w.total = w.records + w.chunks * s.nheads * DeltaRecord::kBytes;
     return w;
@@ -197,7 +206,7 @@ template <int N, typename ST, bool kIdx64>
 cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtensorMap (&maps)[6],
                        ssu_handle_s &handle, cudaStream_t st) {
     auto *prep = ssu_delta_prep_kernel<N>;
-    auto *main = ssu_delta_mma_kernel<N, ST, kIdx64>;
+    auto *main = ssu_delta_mma_kernel<N, ST>;
     constexpr int kPrepBytes = PrepSmem<N>::kTotal + 1024, kBytes = DeltaSmem<N>::kTotal + 1024;
     cudaError_t e =
         ssu_host::allow_smem(handle, reinterpret_cast<const void *>(prep), kPrepBytes);
@@ -278,7 +287,7 @@ ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *s
     if (st == SSU_OK) st = validate_batch(*shape);
     if (st == SSU_OK) st = validate_tokens(tokens);
     if (st != SSU_OK) return st;
-    *bytes = mma_sizes(*shape, tokens) ? delta_plan(*shape, tokens).total : 0;
+    *bytes = mma_sizes(*shape, tokens, handle->sm_count) ? delta_plan(*shape, tokens).total : 0;
     return ok();
 }
 
@@ -320,7 +329,7 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
         return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorNotSupported;
-    if (tokens > 0 && mma_sizes(s, tokens) && mma_operands(d)) {
+    if (tokens > 0 && mma_sizes(s, tokens, handle->sm_count) && mma_operands(d)) {
         const SsuParams &p = d.m.p;
         const DeltaPlan w = delta_plan(s, tokens);
         DeltaMmaParams m{};
@@ -334,8 +343,7 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
             m.per_cta *= 2;
         char *const room = static_cast<char *>(workspace);
         m.total = reinterpret_cast<int *>(room);
-        m.order = reinterpret_cast<int *>(room + w.order);
-        m.prompts = reinterpret_cast<int4 *>(room + w.prompts);
+        m.prompts = reinterpret_cast<DeltaPrompt *>(room + w.prompts);
         m.chunks = reinterpret_cast<int2 *>(room + w.list);
         m.records = reinterpret_cast<unsigned char *>(room + w.records);
         CUtensorMap maps[6];

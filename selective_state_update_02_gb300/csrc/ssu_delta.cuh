@@ -88,10 +88,15 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// A head's decay and gate at a token.
+__device__ __forceinline__ float2 rates_of(float dt, float bias, float A, float b) {
+    return make_float2(expf(softplus_f32(dt + bias) * A), 1.0f / (1.0f + expf(-b)));
+}
+
+// (Without branches, so that it can run beside another token's work; rsqrtf is within 2 ulp.)
 template <class G>
 __device__ __forceinline__ void make_token(const DeltaParams &d, const RawKey<G> &k,
-                                           const RawKey<G> &q, float dt, float bias, float A,
-                                           float b, Token<G> &t) {
+                                           const RawKey<G> &q, float2 rates, Token<G> &t) {
     widen_key<G>(k, t.k);
     widen_key<G>(q, t.q);
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
@@ -102,13 +107,13 @@ __device__ __forceinline__ void make_token(const DeltaParams &d, const RawKey<G>
         kq = fmaf(t.k[i], t.q[i], kq);
     }
     kk = row_sum<G>(kk), qq = row_sum<G>(qq), kq = row_sum<G>(kq);
-    const float rk = d.eps >= 0.0f ? 1.0f / sqrtf(kk + d.eps) : 1.0f;
-    t.rq = d.eps >= 0.0f ? d.scale / sqrtf(qq + d.eps) : d.scale;
+    const float rk = d.eps >= 0.0f ? rsqrtf(kk + d.eps) : 1.0f;
+    t.rq = d.scale * (d.eps >= 0.0f ? rsqrtf(qq + d.eps) : 1.0f);
     t.kq = kq * rk * t.rq;
 #pragma unroll
     for (int i = 0; i < G::NC; ++i) t.k[i] *= rk;
-    t.a = expf(softplus_f32(dt + bias) * A);
-    t.beta = 1.0f / (1.0f + expf(-b));
+    t.a = rates.x;
+    t.beta = rates.y;
 }
 
 // The lane of its row's group that reduce_rows<R, L> leaves the total of `slot` in.
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(128) ssu_delta_step_kernel(const __grid_consta
         const float dt = __bfloat162float(p.dt[b * p.dt_b + h * p.dt_h]);
         const float gate = __bfloat162float(d.beta[b * d.beta_t + h * d.beta_h]);
         Token<G> t;
-        make_token<G>(d, rk, rq, dt, p.dt_bias[h * p.bias_h], p.A[h * p.A_h], gate, t);
+        make_token<G>(d, rk, rq, rates_of(dt, p.dt_bias[h * p.bias_h], p.A[h * p.A_h], gate), t);
         float S[SLOTS][G::NC];
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r) raw_to_f32<G, ST>(raw[r], S[r]);
@@ -257,28 +262,62 @@ __global__ void __launch_bounds__(128) ssu_delta_seq_kernel(const __grid_constan
             if (!fresh && at < p.headdim) load_raw<G>(state + at * p.st_row, raw);
             raw_to_f32<G, ST>(raw, S[r]);
         }
-        RawKey<G> rk{}, rq{};
-        unsigned short v = 0, dt = 0, gate = 0;
-        auto fetch = [&](long long t) {
-            load_key<G>(p.B + t * p.B_b + grp * p.B_g + col0, d.m.bc_vec, rk);
-            load_key<G>(p.C + t * p.C_b + grp * p.C_g + col0, d.m.bc_vec, rq);
-            if (row < p.headdim)
-                v = reinterpret_cast<const unsigned short *>(p.x)[t * p.x_b + h * p.x_h + row];
-            dt = reinterpret_cast<const unsigned short *>(p.dt)[t * p.dt_b + h * p.dt_h];
-            gate = reinterpret_cast<const unsigned short *>(d.beta)[t * d.beta_t + h * d.beta_h];
-        };
+        // A token's operands are fetched kAhead tokens ahead and made ready, its lengths, beside the
+        // chain of the token before; decays and gates are worked out for 32 tokens at a time, one
+        // per lane.
+        constexpr int kAhead = G::NC <= 4 ? 4 : 2;
+        struct {
+            RawKey<G> k, q;
+            unsigned short v;
+        } raw[kAhead] = {};
         auto wide = [](unsigned short u) {
             return __uint_as_float(static_cast<unsigned>(u) << 16);
         };
-        if (begin < end) fetch(begin);
-        for (long long t = begin; t < end; ++t) {
-            Token<G> now;
-            make_token<G>(d, rk, rq, wide(dt), bias, A, wide(gate), now);
-            const float value = wide(v);
-            if (t + 1 < end) fetch(t + 1);
-            const float y = delta_rows<G, SLOTS>(S, now, value, lane);
-            if (reads_out<G, SLOTS>(lane) && row < p.headdim)
-                p.out[t * p.out_b + h * p.out_h + row] = __float2bfloat16(y);
+        auto fetch = [&](int i, long long t) {
+            if (t >= end) return;
+            load_key<G>(p.B + t * p.B_b + grp * p.B_g + col0, d.m.bc_vec, raw[i].k);
+            load_key<G>(p.C + t * p.C_b + grp * p.C_g + col0, d.m.bc_vec, raw[i].q);
+            if (row < p.headdim)
+                raw[i].v =
+                    reinterpret_cast<const unsigned short *>(p.x)[t * p.x_b + h * p.x_h + row];
+        };
+        float2 rates = make_float2(0.0f, 0.0f);  // of the lane's token
+        auto rate = [&](long long t0) {
+            const long long t = t0 + lane;
+            if (t >= end) return;
+            const unsigned short *const dt = reinterpret_cast<const unsigned short *>(p.dt);
+            const unsigned short *const gate = reinterpret_cast<const unsigned short *>(d.beta);
+            rates = rates_of(wide(dt[t * p.dt_b + h * p.dt_h]), bias, A,
+                             wide(gate[t * d.beta_t + h * d.beta_h]));
+        };
+        Token<G> now, next;
+        float value = 0.0f, after = 0.0f;
+        auto prepare = [&](int i, int n) {  // the n-th token of those whose rates the lanes have
+            make_token<G>(d, raw[i].k, raw[i].q,
+                          make_float2(__shfl_sync(0xffffffffu, rates.x, n),
+                                      __shfl_sync(0xffffffffu, rates.y, n)),
+                          next);
+            after = wide(raw[i].v);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i, begin + i);
+        rate(begin);
+        prepare(0, 0);
+        for (long long t0 = begin; t0 < end; t0 += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const long long t = t0 + i;
+                if (t >= end) break;
+                const int n = static_cast<int>(t - begin + 1) & 31;
+                if (n == 0) rate(t + 1);
+                now = next;
+                value = after;
+                fetch(i, t + kAhead);
+                prepare((i + 1) % kAhead, n);
+                const float y = delta_rows<G, SLOTS>(S, now, value, lane);
+                if (reads_out<G, SLOTS>(lane) && row < p.headdim)
+                    p.out[t * p.out_b + h * p.out_h + row] = __float2bfloat16(y);
+            }
         }
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r) {

@@ -72,13 +72,21 @@ struct DeltaRecord {
     };
 };
 
+// What the plan says of a prompt.
+struct __align__(32) DeltaPrompt {
+    int begin, end;  // tokens
+    int first;       // chunk
+    int starts;      // kNot: a bad prompt; else whether from zeros or from its slot
+    long long slot;
+    enum : int { kNot = 0, kSlot = 1, kZeros = 2 };
+};
+
 struct DeltaMmaParams {
     DeltaParams d;
     int slabs;              // of 128 rows
     int per_cta;            // heads per CTA of the first pass
     int *total;             // chunks of the call
-    int *order;             // prompts, the longest first
-    int4 *prompts;          // good, first token, end, first chunk
+    DeltaPrompt *prompts;   // the longest first
     int2 *chunks;           // first token, tokens
     unsigned char *records;  // [chunk][head]
 };
@@ -153,10 +161,20 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
     constexpr int kWarps = kPlanThreads / 32;
     __shared__ int warp_end[kWarps], warp_chunks[kWarps], firsts[kPlanThreads];
     __shared__ int2 spans[kPlanThreads];
-    __shared__ int lengths[kPlanSorted];
+    __shared__ int lengths[kPlanSorted], chunks_of[kPlanSorted];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const SsuParams &p = m.d.m.p;
     int seen = 0, total = 0;  // the largest end and the chunks of the prompts before
+    auto put = [&](long long at, long long b, bool good, int first) {
+        DeltaPrompt d{0, 0, first, DeltaPrompt::kNot, 0};
+        if (good) {
+            long long lo, hi;
+            load_prompt<kIdx64>(m.d.m, b, false, d.slot, lo, hi);
+            d.begin = static_cast<int>(lo), d.end = static_cast<int>(hi);
+            d.starts = m.d.m.fresh && m.d.m.fresh[b] != 0 ? DeltaPrompt::kZeros : DeltaPrompt::kSlot;
+        }
+        m.prompts[at] = d;
+    };
     for (long long b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
         const long long b = b0 + tid;
         long long slot, lo = 0, hi = 0;
@@ -196,9 +214,10 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
             if (w < warp) first += warp_chunks[w];
             total += warp_chunks[w];
         }
-        if (b < p.batch) {
-            m.prompts[b] = make_int4(good, static_cast<int>(lo), static_cast<int>(hi), first);
-            if (b < kPlanSorted) lengths[b] = good ? static_cast<int>(hi - lo) : -1;
+        if (p.batch <= kPlanSorted) {
+            if (b < p.batch) lengths[b] = good ? static_cast<int>(hi - lo) : -1, chunks_of[b] = first;
+        } else if (b < p.batch) {
+            put(b, b, good, first);
         }
         firsts[tid] = first;
         spans[tid] = n ? make_int2(static_cast<int>(lo), static_cast<int>(hi)) : make_int2(0, 0);
@@ -214,15 +233,13 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
         __syncthreads();
     }
     if (tid == 0) *m.total = total;
+    if (p.batch > kPlanSorted) return;
     for (long long b = tid; b < p.batch; b += kPlanThreads) {
-        int rank = static_cast<int>(b);
-        if (p.batch <= kPlanSorted) {
-            const int mine = lengths[b];
-            rank = 0;
-            for (int o = 0; o < static_cast<int>(p.batch); ++o)
-                rank += lengths[o] > mine || (lengths[o] == mine && o < b);
-        }
-        m.order[rank] = static_cast<int>(b);
+        const int mine = lengths[b];
+        int rank = 0;
+        for (int o = 0; o < static_cast<int>(p.batch); ++o)
+            rank += lengths[o] > mine || (lengths[o] == mine && o < b);
+        put(rank, b, mine >= 0, chunks_of[b]);
     }
 }
 
@@ -725,7 +742,7 @@ __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 // S, R and U are handed over 16 columns of each warpgroup at a time, so that products of the first
 // run while the next are made: of a product's MMAs only the last piece's are waited for.  K and Q
 // are one operand, as an MMA of N = 128 takes little longer than one of N = 64.
-template <int N, typename ST, bool kIdx64>
+template <int N, typename ST>
 __global__ void __launch_bounds__(kDeltaThreads, 1)
     ssu_delta_mma_kernel(const __grid_constant__ DeltaMmaParams m,
                          const __grid_constant__ CUtensorMap map_k,
@@ -786,12 +803,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const int columns = p.nheads * m.slabs;
     const int column = blockIdx.x % columns, h = column / m.slabs;
     const int row0 = (column - h * m.slabs) * kDeltaRows;
-    const long long b = m.order[blockIdx.x / columns];
-    const int4 prompt = m.prompts[b];
-    const bool fresh = m.d.m.fresh && m.d.m.fresh[b] != 0;
-    const int begin = prompt.y, end = prompt.z;
+    const DeltaPrompt prompt = m.prompts[blockIdx.x / columns];
+    const bool good = prompt.starts != DeltaPrompt::kNot;
+    const bool fresh = prompt.starts == DeltaPrompt::kZeros;
+    const int begin = prompt.begin, end = prompt.end;
     const int chunks = __shfl_sync(
-        0xffffffffu, prompt.x ? (end - begin + kDeltaChunk - 1) / kDeltaChunk : 0, 0);
+        0xffffffffu, good ? (end - begin + kDeltaChunk - 1) / kDeltaChunk : 0, 0);
     const int grp = group_of(h, p.group_magic);
     const int v_blocks = min(2, (p.headdim - row0 + 63) / 64);
     unsigned dead = 0;  // whether a wait gave up: what comes after it is not valid, nor waited for
@@ -822,7 +839,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                 for (int k = 0; k < v_blocks; ++k)
                     tma_load(to + Smem::kV + k * kDeltaTile, &map_v, bar, row0 + k * 64, h, tok);
                 bulk_load(to + Smem::kRecord,
-                          m.records + (static_cast<long long>(prompt.w + c) * p.nheads + h) *
+                          m.records + (static_cast<long long>(prompt.first + c) * p.nheads + h) *
                                           R::kBytes,
                           R::kBytes, bar);
             }
@@ -984,12 +1001,10 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         constexpr unsigned kLanes16 = 16u << 16;
         constexpr int kCol8 = kCols / 8;
         float2 S[kCol8][2][2];  // [block][hh][e]
-        long long slot = 0;
-        if (prompt.x) slot = load_slot<kIdx64>(p, b);
-        ST *const state = static_cast<ST *>(p.state) + slot * p.st_pool + h * p.st_head +
+        ST *const state = static_cast<ST *>(p.state) + prompt.slot * p.st_pool + h * p.st_head +
                           half * kCols + 2 * t;
         auto row_at = [&](int hh, int e) { return 32 * quarter + 16 * hh + 8 * e + g; };
-        const bool reads = prompt.x && !fresh && chunks;
+        const bool reads = good && !fresh && chunks;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1366,7 +1381,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             fast ^= 1;
         }
         if (waits) read_out(chunks - 1);
-        if (prompt.x && (chunks || fresh))
+        if (good && (chunks || fresh))
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
