@@ -97,6 +97,21 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
             res[i][1] = __ldcs(r + 1);
         }
     }
+    // With few vectors per thread the weights come under the sum of squares; more would cost resident
+    // warps, of which a call of many rows has enough to hide them (8192 x 4096 into e4m3: 45 us, 54
+    // with them).
+    constexpr bool kEarly = V <= 2;
+    float4 weight[kEarly ? V : 1][2];
+    auto weigh = [&](int i, float4 (&to)[2]) {
+        const float4 *const w =
+            reinterpret_cast<const float4 *>(p.weight) + 2 * (threadIdx.x + i * blockDim.x);
+        to[0] = __ldg(w);
+        to[1] = __ldg(w + 1);
+    };
+    if constexpr (kEarly)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (holds(i)) weigh(i, weight[i]);
     float v[V][8], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -139,9 +154,8 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (!holds(i)) continue;
-        const float4 *w = reinterpret_cast<const float4 *>(p.weight) +
-                          2 * (threadIdx.x + i * blockDim.x);
-        const float4 a = __ldg(w), b = __ldg(w + 1);
+        if constexpr (!kEarly) weigh(i, weight[0]);
+        const float4 a = weight[kEarly ? i : 0][0], b = weight[kEarly ? i : 0][1];
         const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -207,12 +221,16 @@ cudaError_t launch_norm(const cudaLaunchConfig_t &cfg, const NormParams &p, Resi
                                          : launch_norm<V, Residual::kF32>(cfg, p, e4m3);
 }
 
-cudaError_t launch_norm(const NormParams &p, Residual residual, bool e4m3, bool pdl,
+cudaError_t launch_norm(const NormParams &p, Residual residual, bool e4m3, int sm_count, bool pdl,
                         cudaStream_t st) {
     // Threads per row for `v` vectors each, in whole warps.
     auto threads = [&](int v) { return (p.vectors + 32 * v - 1) / (32 * v) * 32; };
+    // Many rows: up to four vectors per thread (16384 x 8192: 154 us, 170 with two).  Rows that are all
+    // resident at once: fewer, for more loads of weights under the sums (777 x 2560 into e4m3 with a
+    // scale per row 5.8 us, 8.3 with four).
+    const int most = p.tokens <= 8ll * sm_count ? 256 : 128;
     int v = 1;
-    while (v < 4 && threads(v) > 128) v *= 2;
+    while (v < 4 && threads(v) > most) v *= 2;
     if (threads(v) > kMostThreads) v = kMostVectors;
     const int per_row = threads(v);
     const int rows = per_row >= 128 ? 1 : 128 / per_row;
@@ -291,7 +309,7 @@ extern "C" ssu_status_t ssu_add_norm(ssu_handle_t handle, const uint16_t *x, voi
         p, !residual                               ? Residual::kNone
            : s.residual_dtype == SSU_RESIDUAL_BF16 ? Residual::kBf16
                                                    : Residual::kF32,
-        e4m3, handle->pdl, reinterpret_cast<cudaStream_t>(stream));
+        e4m3, handle->sm_count, handle->pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(SSU_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
     return ok();
 }
