@@ -117,7 +117,7 @@ cudaError_t launch_rows(Kernel *kernel, DeltaParams d, bool pdl, cudaStream_t st
 
 template <int N, typename ST, bool kIdx64>
 cudaError_t launch_step(const DeltaParams &d, bool pdl, cudaStream_t st) {
-    constexpr int kSlots = RowGeo<N, ST>::L / 4;
+    constexpr int kSlots = RowGeo<N, ST>::L == 8 ? 4 : RowGeo<N, ST>::L / 4;
     return launch_rows<kSlots * RowGeo<N, ST>::RPI>(ssu_delta_step_kernel<kSlots, N, ST, kIdx64>, d,
                                                     pdl, st);
 }
@@ -223,8 +223,10 @@ cudaError_t launch_mma(const DeltaMmaParams &m, const DeltaPlan &w, const CUtens
     cfg.numAttrs = handle.pdl ? 1 : 0;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    e = cudaLaunchKernelEx(&cfg, ssu_delta_plan_kernel<kIdx64>, m);
-    if (e != cudaSuccess) return e;
+    if (!m.few) {
+        e = cudaLaunchKernelEx(&cfg, ssu_delta_plan_kernel<kIdx64>, m);
+        if (e != cudaSuccess) return e;
+    }
     cfg.gridDim = dim3(static_cast<unsigned>(w.chunks),
                        static_cast<unsigned>(p.nheads / m.per_cta));
     cfg.blockDim = dim3(kPrepThreads);
@@ -334,6 +336,8 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
         const DeltaPlan w = delta_plan(s, tokens);
         DeltaMmaParams m{};
         m.d = d;
+        m.idx64 = s.index_dtype == SSU_INDEX_I64;
+        m.few = s.batch <= 32;
         m.slabs = static_cast<int>((s.headdim + kDeltaRows - 1) / kDeltaRows);
         // Heads of one key head share its products in the first pass where that leaves two CTAs
         // per SM and more.

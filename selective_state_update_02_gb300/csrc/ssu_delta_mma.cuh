@@ -9,7 +9,7 @@
 //   y_i  = e^{s_i} S qn_i + sum_{j <= i} (kn_j . qn_i) e^{s_i - s_j} U_j
 //   S'   = e^{s_C} S + sum_j e^{s_C - s_j} U_j kn_j^T
 //
-// Three kernels.  A plan (one CTA) lists the chunks of all prompts.  A first pass, parallel over chunks
+// Three kernels.  A plan (one CTA; none for few prompts) lists the chunks of all prompts.  A first pass, parallel over chunks
 // and heads, makes of keys and gates alone what a chunk needs beside its state: T, the masked M_ij =
 // (k_j . qn_i) e^{s_i - s_j} and the tokens' factors.  A second pass takes a head's state (128 of its
 // rows) through a prompt, chunk after chunk.
@@ -83,6 +83,8 @@ struct __align__(32) DeltaPrompt {
 
 struct DeltaMmaParams {
     DeltaParams d;
+    int idx64;              // the index type is int64
+    int few;                // at most 32 prompts: without a plan
     int slabs;              // of 128 rows
     int per_cta;            // heads per CTA of the first pass
     int *total;             // chunks of the call
@@ -241,6 +243,65 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
             rank += lengths[o] > mine || (lengths[o] == mine && o < b);
         put(rank, b, mine >= 0, chunks_of[b]);
     }
+}
+
+// Of at most 32 prompts every CTA works out the same for itself, a prompt per lane of one warp (a plan
+// in front costs a call 3 us); `chunks` is the number of the lane's prompt's.
+__device__ __forceinline__ DeltaPrompt plan_lane(const DeltaMmaParams &m, bool counts, int lane,
+                                                 int &chunks) {
+    DeltaPrompt d{0, 0, 0, DeltaPrompt::kNot, 0};
+    long long lo = 0, hi = 0;
+    bool good = false;
+    if (lane < m.d.m.p.batch)
+        good = m.idx64 ? load_prompt<true>(m.d.m, lane, counts, d.slot, lo, hi)
+                       : load_prompt<false>(m.d.m, lane, counts, d.slot, lo, hi);
+    const int end = good && lo < hi ? static_cast<int>(hi) : 0;
+    int most = end;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, most, x);
+        if (lane >= x) most = max(most, o);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, most, 1);
+    if (lane > 0 && end && before > lo) {
+        good = false;
+        if (counts) record_skip(m.d.m.p, lane);
+    }
+    chunks = good ? static_cast<int>((hi - lo + kDeltaChunk - 1) / kDeltaChunk) : 0;
+    d.first = chunks;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, d.first, x);
+        if (lane >= x) d.first += o;
+    }
+    d.first -= chunks;
+    if (good) {
+        d.begin = static_cast<int>(lo), d.end = static_cast<int>(hi);
+        d.starts =
+            m.d.m.fresh && m.d.m.fresh[lane] != 0 ? DeltaPrompt::kZeros : DeltaPrompt::kSlot;
+    }
+    return d;
+}
+
+// The prompt that is the `rank`-th longest (lane 0's answer counts).
+__device__ __forceinline__ DeltaPrompt few_ranked(const DeltaMmaParams &m, int rank, int lane) {
+    int chunks;
+    DeltaPrompt d = plan_lane(m, false, lane, chunks);
+    const int mine = d.starts == DeltaPrompt::kNot ? -1 : d.end - d.begin;
+    int before = 0;
+    for (int o = 0; o < static_cast<int>(m.d.m.p.batch); ++o) {
+        const int other = __shfl_sync(0xffffffffu, mine, o);
+        before += other > mine || (other == mine && o < lane);
+    }
+    const unsigned found =
+        __ballot_sync(0xffffffffu, lane < m.d.m.p.batch && before == rank);
+    const int from = __ffs(found) - 1;
+    d.begin = __shfl_sync(0xffffffffu, d.begin, from);
+    d.end = __shfl_sync(0xffffffffu, d.end, from);
+    d.first = __shfl_sync(0xffffffffu, d.first, from);
+    d.starts = __shfl_sync(0xffffffffu, d.starts, from);
+    d.slot = __shfl_sync(0xffffffffu, d.slot, from);
+    return d;
 }
 
 // ---- the first pass ------------------------------------------------------------------------
@@ -403,6 +464,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     using R = DeltaRecord;
     extern __shared__ unsigned char unaligned[];
     __shared__ unsigned tmem_slot;
+    __shared__ int2 found;
     const unsigned tiles = (smem_u32(unaligned) + 1023u) & ~1023u;
     unsigned char *const raw = unaligned + (tiles - smem_u32(unaligned));
     const unsigned bar_tiles = tiles + Smem::kBars, bar_product = bar_tiles + 8;
@@ -432,8 +494,26 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     };
     pdl_wait();
     pdl_trigger();
-    const int2 chunk = m.chunks[blockIdx.x];  // (past the last one: of no use, and not used)
-    if (static_cast<int>(blockIdx.x) >= *m.total) {
+    int2 chunk;  // first token, tokens; of no chunk: no tokens
+    if (m.few) {
+        if (warp == 0) {
+            int chunks;
+            const DeltaPrompt d =
+                plan_lane(m, blockIdx.x == 0 && blockIdx.y == 0, lane, chunks);
+            const int at = static_cast<int>(blockIdx.x) - d.first;
+            if (lane == 0) found = make_int2(0, 0);
+            __syncwarp();
+            if (at >= 0 && at < chunks)
+                found = make_int2(d.begin + at * kDeltaChunk,
+                                  min(kDeltaChunk, d.end - d.begin - at * kDeltaChunk));
+        }
+        __syncthreads();
+        chunk = found;
+    } else {
+        chunk = m.chunks[blockIdx.x];  // (past the last one: of no use)
+        if (static_cast<int>(blockIdx.x) >= *m.total) chunk.y = 0;
+    }
+    if (chunk.y == 0) {
         free_tmem();
         return;
     }
@@ -756,6 +836,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     constexpr int kPieces = kCols / 16;    // of S; R and U have two
     extern __shared__ unsigned char raw[];
     __shared__ unsigned tmem_slot;
+    __shared__ DeltaPrompt ranked;
     const SsuParams &p = m.d.m.p;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform to the compiler)
@@ -803,7 +884,14 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const int columns = p.nheads * m.slabs;
     const int column = blockIdx.x % columns, h = column / m.slabs;
     const int row0 = (column - h * m.slabs) * kDeltaRows;
-    const DeltaPrompt prompt = m.prompts[blockIdx.x / columns];
+    if (m.few) {
+        if (warp == 0) {
+            const DeltaPrompt d = few_ranked(m, blockIdx.x / columns, lane);
+            if (lane == 0) ranked = d;
+        }
+        __syncthreads();
+    }
+    const DeltaPrompt prompt = m.few ? ranked : m.prompts[blockIdx.x / columns];
     const bool good = prompt.starts != DeltaPrompt::kNot;
     const bool fresh = prompt.starts == DeltaPrompt::kZeros;
     const int begin = prompt.begin, end = prompt.end;
