@@ -426,41 +426,38 @@ PyObject *add_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         shaped(weight, "weight", {W});
         if (x.stride(1) != 1 || out.stride(1) != 1 || weight.stride(0) != 1)
             refuse("the last dimension of x, weight and out must have stride 1");
-        device_of({&x, &weight, &out});
+        const Tensor *const residual =
+            a[2] == Py_None ? nullptr : &operand(a[2], "residual", at::kBFloat16, at::kFloat, 2, 2);
+        if (e4m3 != (a[5] != Py_None))
+            refuse("an e4m3 out needs scales, and a bf16 out has none");
+        const Tensor *const scales = e4m3 ? &fp32(a[5], "scales", 2, 2) : nullptr;
         ssu_norm_args_t args{};
         args.tokens = T, args.width = W;
         args.out_dtype = e4m3 ? SSU_NORM_E4M3 : SSU_NORM_BF16;
         args.x = x.stride(0), args.out = out.stride(0);
-        void *residual = nullptr;
-        if (a[2] != Py_None) {
-            const Tensor &r = operand(a[2], "residual", at::kBFloat16, at::kFloat, 2, 2);
-            shaped(r, "residual", {T, W});
-            if (r.stride(1) != 1) refuse("the last dimension of residual must have stride 1");
-            device_of({&x, &r});
-            args.residual = r.stride(0);
+        if (residual) {
+            shaped(*residual, "residual", {T, W});
+            if (residual->stride(1) != 1)
+                refuse("the last dimension of residual must have stride 1");
+            args.residual = residual->stride(0);
             args.residual_dtype =
-                r.scalar_type() == at::kFloat ? SSU_RESIDUAL_F32 : SSU_RESIDUAL_BF16;
-            residual = at_device(r);
+                residual->scalar_type() == at::kFloat ? SSU_RESIDUAL_F32 : SSU_RESIDUAL_BF16;
         }
-        float *scales = nullptr;
-        if (e4m3 != (a[5] != Py_None))
-            refuse("an e4m3 out needs scales, and a bf16 out has none");
-        if (e4m3) {
-            const Tensor &s = fp32(a[5], "scales", 2, 2);
-            if (s.size(1) < 1 || W % s.size(1))
+        if (scales) {
+            if (scales->size(1) < 1 || W % scales->size(1))
                 refuse("scales must have one column for every equal group of x's columns, got " +
-                       listed(s.sizes()));
-            shaped(s, "scales", {T, s.size(1)});
-            device_of({&x, &s});
-            args.group = W / s.size(1);
-            strides_of(s, 2, args.scales);
-            scales = at_device<float>(s);
+                       listed(scales->sizes()));
+            shaped(*scales, "scales", {T, scales->size(1)});
+            args.group = W / scales->size(1);
+            strides_of(*scales, 2, args.scales);
         }
+        device_of({&x, &weight, &out, residual ? residual : &x, scales ? scales : &x});
         const float eps = static_cast<float>(PyFloat_AsDouble(a[6]));
         auto *handle = static_cast<ssu_handle_t>(pointer(a[0]));
         auto *stream = static_cast<ssu_stream_t>(pointer(a[7]));
-        return call(add_norm_fn, handle, bits(x), residual, at_device<float>(weight),
-                    at_device(out), scales, &args, eps, stream);
+        return call(add_norm_fn, handle, bits(x), residual ? at_device(*residual) : nullptr,
+                    at_device<float>(weight), at_device(out),
+                    scales ? at_device<float>(*scales) : nullptr, &args, eps, stream);
     });
 }
 

@@ -292,6 +292,8 @@ extern "C" ssu_status_t ssu_add_norm(ssu_handle_t handle, const uint16_t *x, voi
     if (e4m3) {
         if (s.scales[0] < 0 || s.scales[1] < 0)
             return fail(SSU_ERR_INVALID_ARG, "negative stride");
+        if ((s.tokens > 1 && s.scales[0] == 0) || (s.group < s.width && s.scales[1] == 0))
+            return fail(SSU_ERR_INVALID_ARG, "scales overlap");
         if (!aligned(scales, 4)) return fail(SSU_ERR_MISALIGNED, "scales are not 4-byte aligned");
     }
     NormParams p{};

@@ -32,6 +32,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import selective_state_update_02_gb300 as ssu  # noqa: E402
+from test_guards_gpu import Guarded  # noqa: E402
 
 EPS = 1e-6
 
@@ -504,3 +505,160 @@ def test_prompts_that_overlap(op, cu, skip):
     ref = reference(d, skip=skip)
     d["slots"] = d["slots"][[b for b in range(3) if b not in skip]]
     check(d, out, pool, ref)
+
+
+@pytest.mark.parametrize("A", [0.02, 0.7])
+def test_growing_states(op, A):
+    """Decays above one: within a chunk's range, and past it (such chunks go token by token)."""
+    d = make([150, 70], seed=73)
+    d["A"] = torch.full_like(d["A"], A)
+    d["dt"] = torch.full_like(d["dt"], 0.5)
+    out, pool = call(op, d)
+    y, want, Y, R, most = reference(d)
+    # With 0.7 a state grows by up to 3.18 a token: 150 of them are a factor of 2^250, which fp32 does
+    # not hold.  Heads are compared up to where their magnitudes pass 2^100, and their states where
+    # they never do.
+    cu = d["cu"].tolist()
+    for i, slot in enumerate(d["slots"].tolist()):
+        rows = slice(cu[i], cu[i + 1])
+        size = Y[rows].amax(-1).cummax(0).values  # [tokens, H]
+        keep = size < 2.0 ** 100
+        err = (out[rows].double() - y[rows]).abs()
+        tol = 2.0 ** -8 * y[rows].abs() + (2.0 ** -7 + 2.0 ** -13) * Y[rows]
+        assert (err <= tol)[keep].all()
+        whole = keep.all(0) & (R[slot].amax(-1) < 2.0 ** 100)
+        rows_off = (pool[slot].double() - want[slot]).norm(dim=-1)
+        assert (rows_off <= (cu[i + 1] - cu[i]) * 2.0 ** -20 * R[slot])[whole].all()
+        assert A > 0.1 or whole.all()
+
+
+def test_many_prompts(op):
+    """More prompts than a warp has lanes and than a sort takes, bad ones and empty ones among
+    them: nothing of one in another."""
+    lens = [(37 * i) % 131 if i % 9 else 0 for i in range(70)]
+    d = make(lens, H=2, G=1, seed=79)
+    d["slots"][5] = -1
+    check_some(op, d, skip=(5,))
+    lens = [1 + (i * i) % 7 for i in range(1100)]
+    d = make(lens, H=1, P=64, N=64, G=1, seed=83)
+    check_some(op, d)
+
+
+def check_some(op, d, skip=()):
+    op.get_error()
+    out, pool = call(op, d)
+    assert op.get_error() == (len(skip), min(skip, default=-1))
+    ref = reference(d, skip=skip)
+    keep = [b for b in range(len(d["slots"])) if b not in skip]
+    d["slots"] = d["slots"][keep]
+    check(d, out, pool, ref)
+
+
+def test_slots_past_32_bits(op):
+    """A pool of more than 2^31 elements: its last slot, by prompts in both forms and one token."""
+    H, P, N = 32, 128, 128
+    slots = 2 ** 31 // (H * P * N) + 3
+    pool = torch.zeros(slots, H, P, N, device="cuda")
+    for tokens in (200, 20):
+        d = make([tokens], H, P, N, G=16, seed=tokens, extra=0)
+        d["fresh"] = None
+        pool[-1] = d["pool"][0]
+        y, want, Y, R, most = reference(d)
+        out = torch.zeros_like(d["v"])
+        at = torch.tensor([slots - 1], dtype=torch.int32, device="cuda")
+        ws = torch.empty(op.delta_workspace_bytes(pool, d["v"], d["k"], at), dtype=torch.uint8,
+                         device="cuda")
+        op.delta_prompts(pool, at, d["cu"], d["q"], d["k"], d["v"], d["dt"], d["dt_bias"], d["A"],
+                         d["b"], out, ws)
+        check(d, out, pool[-1:].clone(), (y, want, Y, R, most))
+        assert (pool[:-1] == 0).all()
+    d = make([1], H, P, N, G=16, seed=89, extra=0)
+    d["fresh"] = None
+    pool[-1] = d["pool"][0]
+    out = torch.zeros_like(d["v"])
+    step(op, dict(d, slots=at), pool, out)
+    check(d, out, pool[-1:].clone(), reference(d), chunked=False)
+    assert (pool[:-1] == 0).all()
+
+
+def test_batches_past_the_grid(op):
+    """More requests than a grid's third dimension has."""
+    bs = 66000
+    d = make([1] * bs, H=1, P=8, N=64, G=1, seed=97, extra=0)
+    pool, out = d["pool"].clone(), torch.zeros_like(d["v"])
+    step(op, d, pool, out)
+    pick = [0, 1, 65534, 65535, 65536, bs - 1]
+    part = {k: d[k][pick] for k in ("q", "k", "v", "dt", "b")}
+    part.update(slots=torch.arange(6, dtype=torch.int32, device="cuda"), dt_bias=d["dt_bias"],
+                A=d["A"], pool=d["pool"][d["slots"][pick].long()], fresh=None,
+                cu=torch.arange(7, dtype=torch.int32, device="cuda"))
+    check(part, out[pick], pool[d["slots"][pick].long()], reference(part), chunked=False)
+
+
+KINDS = {"few": dict(lens=[1, 0, 129, 64], H=4), "many": dict(lens=[65 + i for i in range(40)], H=2),
+         "bf16": dict(lens=[300, 130], H=4, P=72, N=64, state=torch.bfloat16),
+         "by token": dict(lens=[20, 150], H=3, P=24, N=256, G=3)}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_calls_stay_in_their_buffers(op, kind):
+    """Canaries on both sides of the pool, the readouts and the workspace."""
+    d = make(seed=101, extra=0, **KINDS[kind])
+    d["slots"][0] = len(d["pool"])  # one prompt is skipped
+    out, pool = call(op, d)
+    n = op.delta_workspace_bytes(d["pool"], d["v"], d["k"], d["slots"])
+    guards = [Guarded(t) for t in (d["pool"], torch.full_like(out, 7.0),
+                                   torch.zeros(n, dtype=torch.uint8, device="cuda"))]
+    room, y, ws = (g.t for g in guards)
+    op.delta_prompts(room, d["slots"], d["cu"], d["q"], d["k"], d["v"], d["dt"], d["dt_bias"],
+                     d["A"], d["b"], y, ws, fresh=d["fresh"])
+    assert op.get_error() == (2, 0)
+    assert all(g.intact() for g in guards)
+    assert torch.equal(room, pool) and torch.equal(y, out)
+    rows = d["cu"][1:].long() - 1
+    one = torch.zeros_like(d["v"][rows])
+    guard = Guarded(one)
+    step(op, d, room, guard.t, rows)
+    assert op.get_error() == (1, 0) and guard.intact() and guards[0].intact()
+
+
+def test_calls_side_by_side(op):
+    """Two handles on two streams with a workspace each; and two captured graphs that share one,
+    replayed one after the other: the bits of calls alone."""
+    ds = [make([150, 65, 200], seed=103), make([90, 300], seed=107)]
+    want = [call(op, d) for d in ds]
+    other = ssu.SelectiveStateUpdate(0)
+    for _ in range(3):
+        got = []
+        for d, o in zip(ds, (op, other)):
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                pool, out = d["pool"].clone(), torch.full_like(d["v"], 7.0)
+                ws = torch.empty(o.delta_workspace_bytes(pool, d["v"], d["k"], d["slots"]),
+                                 dtype=torch.uint8, device="cuda")
+                o.delta_prompts(pool, d["slots"], d["cu"], d["q"], d["k"], d["v"], d["dt"],
+                                d["dt_bias"], d["A"], d["b"], out, ws, fresh=d["fresh"])
+                got.append((out, pool, ws))
+        torch.cuda.synchronize()
+        for (out, pool, _), (y, state) in zip(got, want):
+            assert torch.equal(out, y) and torch.equal(pool, state)
+    n = max(op.delta_workspace_bytes(d["pool"], d["v"], d["k"], d["slots"]) for d in ds)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs, results = [], []
+    for d in ds:
+        pool, out = d["pool"].clone(), torch.full_like(d["v"], 7.0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op.delta_prompts(pool, d["slots"], d["cu"], d["q"], d["k"], d["v"], d["dt"],
+                             d["dt_bias"], d["A"], d["b"], out, ws, fresh=d["fresh"])
+        graphs.append(graph)
+        results.append((out, pool))
+    for _ in range(2):
+        for d, graph, (out, pool), (y, state) in zip(ds, graphs, results, want):
+            pool.copy_(d["pool"])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, y) and torch.equal(pool, state)
+    assert op.get_error() == (0, -1) and other.get_error() == (0, -1)
+    other.close()

@@ -20,6 +20,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import selective_state_update_02_gb300 as ssu  # noqa: E402
+from test_guards_gpu import Guarded  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -186,3 +187,37 @@ def test_zero_tokens_and_graphs(op):
         graph.replay()
         torch.cuda.synchronize()
         check(d, d["residual"], formula(dict(d, residual=start)))
+
+
+@pytest.mark.parametrize("T,W,group", [(3, 72, 72), (700, 1024, 64), (5, 20000, 32)], ids=str)
+def test_calls_stay_in_their_buffers(op, T, W, group):
+    """Canaries on both sides of what a call writes."""
+    for e4m3 in (False, True):
+        d = make(T, W, torch.bfloat16, e4m3, group)
+        r = run(op, d)
+        guards = {"residual": Guarded(d["residual"]), "out": Guarded(torch.zeros_like(d["out"].view(
+            torch.uint8) if e4m3 else d["out"]))}
+        if e4m3:
+            guards["scales"] = Guarded(torch.zeros_like(d["scales"]))
+        out = guards["out"].t.view(torch.float8_e4m3fn) if e4m3 else guards["out"].t
+        op.add_norm(d["x"], d["weight"], out, residual=guards["residual"].t,
+                    scales=guards["scales"].t if e4m3 else None)
+        torch.cuda.synchronize()
+        assert all(g.intact() for g in guards.values())
+        assert torch.equal(guards["residual"].t, r) and torch.equal(out.float(), d["out"].float())
+        if e4m3:
+            assert torch.equal(guards["scales"].t, d["scales"])
+
+
+def test_rows_past_32_bits(op):
+    """More than 2^31 elements: the last rows."""
+    T, W = 2 ** 31 // 8192 + 40, 8192
+    x = torch.zeros(T, W, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, W, device="cuda").bfloat16()
+    out = torch.empty(T, W, dtype=torch.float8_e4m3fn, device="cuda")
+    d = dict(x=x[-3:], residual=None, weight=torch.rand(W, device="cuda") + 0.5, out=out[-3:],
+             scales=torch.zeros(T, 1, device="cuda"))
+    op.add_norm(x, d["weight"], out, scales=d["scales"])
+    torch.cuda.synchronize()
+    check(dict(d, scales=d["scales"][-3:]), None, formula(d))
+    assert (out[::4096].view(torch.uint8)[:-1] == 0).all()
