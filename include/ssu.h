@@ -200,7 +200,8 @@ ssu_status_t ssu_update_from_host(ssu_handle_t handle, void *state_pool,
 /*
  * Synchronise `stream`, then read and clear the handle's device counters.
  * *skipped receives what was skipped since the last read (may be NULL): requests, prompts of
- * ssu_update_prompts, tokens of ssu_rotate_qk, requests and single pages of ssu_attend.
+ * ssu_update_prompts and ssu_delta_prompts, tokens of ssu_rotate_qk, requests and single pages of
+ * ssu_attend.
  * *first_bad receives the smallest index of these in their calls, of whatever call (for a page that
  * of its request), or -1 (may be NULL): read after each call to tell one call from another.
  * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_ERR_CUDA when a prompt kernel gave up a wait
@@ -554,6 +555,18 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * fresh[b] != 0: the slot is then not read) and leaves its last state there.  cu_tokens, fresh,
  * tokens, workspace, the skipping and counting of bad prompts and what is asked of slots and
  * offsets are as there; shape->batch is the number of prompts.
+ *
+ * Two forms.  Where dstate is 64 or 128, q, k, v and out are 16-byte aligned with strides that are
+ * multiples of 8, tokens are more than a few (12, and 24 for every round of the device's SMs that
+ * prompts times heads come to) and the workspace stays within 32 GB, chunks of 64 tokens run as
+ * matrix products: states and sums in fp32, while the readout meets its chunk's weights rounded to
+ * bf16 once (about 2^-9 of a chunk's share in the mean square, as much as its own rounding).  Any
+ * other call runs token by token in fp32.  An infinity or NaN in a token's operands reaches its
+ * prompt's readouts from that token on, and its state, as in the recurrence (a value's its own row,
+ * a query's its own token; an infinity may come out as NaN); one in a slot's state its own row.
+ * A token's sums of squares are fp32: a key of 1.8e19 and more becomes zero.
+ *
+ * The workspace is 26 KiB for every 64 tokens, and prompt, and head.
  */
 ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
                                        int64_t tokens, int64_t *bytes);
