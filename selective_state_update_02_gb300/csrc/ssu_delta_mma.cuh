@@ -571,42 +571,23 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     const int block = warp;
     float *const lengths = reinterpret_cast<float *>(raw + Smem::kLengths);
     const int g = lane >> 2, t = lane & 3;
-    float kk[8][4] = {}, qk[8][4] = {}, own[2][4] = {}, qq[2][4] = {};
     mbar_pass(bar_product, 0, dead);
     __syncwarp();
     tc_fence_after();
-    {
-        const unsigned k_rows = tmem + (static_cast<unsigned>(block) << 21);
-        const unsigned q_rows = k_rows + (16u << 16);
-        unsigned r[8];
-        auto take = [&](float (&a)[4], float (&b)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = __uint_as_float(r[i]), b[i] = __uint_as_float(r[4 + i]);
-        };
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            if (nb > block) continue;
-            tc_load_frag(k_rows + 32 * nb, r);
-            tc_wait_ld();
-            take(kk[2 * nb], kk[2 * nb + 1]);
-            if (nb == block) take(own[0], own[1]);
-            tc_load_frag(q_rows + 32 * nb, r);
-            tc_wait_ld();
-            take(qk[2 * nb], qk[2 * nb + 1]);
-        }
-        tc_load_frag(q_rows + 32 * block + 16, r);
-        tc_wait_ld();
-        take(qq[0], qq[1]);
-    }
-    tc_fence_before();
+    const unsigned k_rows = tmem + (static_cast<unsigned>(block) << 21);
+    const unsigned q_rows = k_rows + (16u << 16);
+    unsigned own[8], qq[8];  // the diagonals
+    tc_load_frag(k_rows + 32 * block, own);
+    tc_load_frag(q_rows + 32 * block + 16, qq);
+    tc_wait_ld();
     bool bad = false;
     if (t == g >> 1) {  // the thread with rows g and g + 8 of the diagonals
         const bool unit = m.d.eps >= 0.0f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int row = 16 * block + g + 8 * half;
-            const float k2 = g & 1 ? own[half][2 * half + 1] : own[half][2 * half];
-            const float q2 = g & 1 ? qq[half][2 * half + 1] : qq[half][2 * half];
+            const float k2 = __uint_as_float(g & 1 ? own[6 * half + 1] : own[6 * half]);
+            const float q2 = __uint_as_float(g & 1 ? qq[6 * half + 1] : qq[6 * half]);
             const bool live = row < valid;
             const float rk = !live ? 0.0f : unit ? 1.0f / sqrtf(k2 + m.d.eps) : 1.0f;
             const float rq = !live ? 0.0f : unit ? m.d.scale / sqrtf(q2 + m.d.eps) : m.d.scale;
@@ -617,10 +598,12 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         }
     }
     bad = __syncthreads_or(bad);
-    free_tmem();
     if (__syncthreads_or(dead)) {  // what is in flight lands long before this is over
         if (tid == 0) atomicOr(&p.err[2], 1u);
         __nanosleep(1000000);
+        tc_fence_before();
+        __syncthreads();
+        free_tmem();
         return;
     }
     if (warp < m.per_cta) {
@@ -660,26 +643,33 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             const float f[2] = {vec[R::kBeta + i0] * lengths[i0],
                                 vec[R::kBeta + i0 + 8] * lengths[i0 + 8]};
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                if (n > 2 * block + 1) continue;
-                const int j = 8 * n + 2 * t;
-                const float2 sh = *reinterpret_cast<const float2 *>(sums + j);
-                const float2 sl = *reinterpret_cast<const float2 *>(sums + kDeltaChunk + j);
-                const float2 rk = *reinterpret_cast<const float2 *>(lengths + j);
+            for (int nb = 0; nb < 4; ++nb) {
+                if (nb > block) continue;
+                unsigned kk[8], qk[8];
+                tc_load_frag(k_rows + 32 * nb, kk);
+                tc_load_frag(q_rows + 32 * nb, qk);
+                tc_wait_ld();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i = i0 + 8 * half;
-                    const float e0 = exp2_ftz((hi[half] - sh.x) + (lo[half] - sl.x)) * rk.x;
-                    const float e1 = exp2_ftz((hi[half] - sh.y) + (lo[half] - sl.y)) * rk.y;
-                    // (rows past the prompt's end hold anything)
-                    *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) =
-                        i < valid ? make_float2(kk[n][2 * half] * (e0 * f[half]),
-                                                kk[n][2 * half + 1] * (e1 * f[half]))
-                                  : make_float2(0.0f, 0.0f);
-                    *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 +
-                                                  ((n ^ (i & 7)) << 4) + 4 * t) =
-                        f2_to_bf2(j <= i ? qk[n][2 * half] * e0 : 0.0f,
-                                  j + 1 <= i ? qk[n][2 * half + 1] * e1 : 0.0f);
+                for (int x = 0; x < 2; ++x) {
+                    const int n = 2 * nb + x, j = 8 * n + 2 * t;
+                    const float2 sh = *reinterpret_cast<const float2 *>(sums + j);
+                    const float2 sl = *reinterpret_cast<const float2 *>(sums + kDeltaChunk + j);
+                    const float2 rk = *reinterpret_cast<const float2 *>(lengths + j);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int i = i0 + 8 * half, at = 4 * x + 2 * half;
+                        const float e0 = exp2_ftz((hi[half] - sh.x) + (lo[half] - sl.x)) * rk.x;
+                        const float e1 = exp2_ftz((hi[half] - sh.y) + (lo[half] - sl.y)) * rk.y;
+                        // (rows past the prompt's end hold anything)
+                        *reinterpret_cast<float2 *>(L + i * kPrepPitch + j) =
+                            i < valid ? make_float2(__uint_as_float(kk[at]) * (e0 * f[half]),
+                                                    __uint_as_float(kk[at + 1]) * (e1 * f[half]))
+                                      : make_float2(0.0f, 0.0f);
+                        *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 +
+                                                      ((n ^ (i & 7)) << 4) + 4 * t) =
+                            f2_to_bf2(j <= i ? __uint_as_float(qk[at]) * e0 : 0.0f,
+                                      j + 1 <= i ? __uint_as_float(qk[at + 1]) * e1 : 0.0f);
+                    }
                 }
             }
         }
@@ -760,6 +750,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         *reinterpret_cast<uint4 *>(to + R::kVec + tid * 16) =
             *reinterpret_cast<const uint4 *>(raw + Smem::kVec + k * 2048 + tid * 16);
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    free_tmem();
 }
 
 // ---- the second pass -----------------------------------------------------------------------
