@@ -316,7 +316,7 @@ __device__ __forceinline__ DeltaPrompt few_ranked(const DeltaMmaParams &m, int r
 
 constexpr int kPrepThreads = 128;
 constexpr int kPrepHeads = 2;   // the most heads per CTA: a warp each makes their factors
-constexpr int kPrepPitch = 68;  // floats per row of L and T
+constexpr int kPrepPitch = 72;  // floats per row of L and T: pairs of 8 rows on 32 banks
 constexpr int kPrepColumns = 128;  // of TMEM
 
 template <int N>
@@ -731,7 +731,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             const int row = (tid + x * kPrepThreads) / 8, piece = tid % 8;
             const float4 *const f =
                 reinterpret_cast<const float4 *>(T + row * kPrepPitch + piece * 8);
-            const float4 a = f[0], b = f[1];
+            // (half the lanes the other way round: 8 lanes' 16 bytes on 32 banks)
+            const int turned = piece >> 2;
+            const float4 first = f[turned], second = f[1 - turned];
+            const float4 a = turned ? second : first, b = turned ? first : second;
             const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             unsigned one[4], two[4];
 #pragma unroll
