@@ -54,6 +54,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return m;
 }
 
+__device__ __forceinline__ float largest(const float2 (&v)[4]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max_nan(m, max_nan(fabsf(v[j].x), fabsf(v[j].y)));
+    return m;
+}
+
+__device__ __forceinline__ uint4 packed(const float2 (&v)[4]) {
+    return make_uint4(f2_to_bf2(v[0].x, v[0].y), f2_to_bf2(v[1].x, v[1].y),
+                      f2_to_bf2(v[2].x, v[2].y), f2_to_bf2(v[3].x, v[3].y));
+}
+
 // The combined value of a row's threads (every thread of the CTA calls it: rows share the barrier).
 template <typename F>
 __device__ __forceinline__ float over_row(float v, F join, float *room) {
@@ -112,43 +124,43 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (holds(i)) weigh(i, weight[i]);
-    float v[V][8], sum = 0.0f;
+    float2 v[V][4], squares = make_float2(0.0f, 0.0f);  // packed fp32x2 arithmetic: issue counts
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const unsigned u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         const unsigned r[4] = {res[i][0].x, res[i][0].y, res[i][0].z, res[i][0].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[i][2 * j] = __uint_as_float(u[j] << 16);
-            v[i][2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-            if constexpr (kResidual == Residual::kBf16) {
-                v[i][2 * j] += __uint_as_float(r[j] << 16);
-                v[i][2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
-            }
+            v[i][j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+            if constexpr (kResidual == Residual::kBf16)
+                v[i][j] = __fadd2_rn(v[i][j], make_float2(__uint_as_float(r[j] << 16),
+                                                          __uint_as_float(r[j] & 0xffff0000u)));
         }
         if constexpr (kResidual == Residual::kF32) {
             const uint4 &a = res[i][0], &b = res[i][1];
             const unsigned f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] += __uint_as_float(f[j]);
+            for (int j = 0; j < 4; ++j)
+                v[i][j] = __fadd2_rn(v[i][j], make_float2(__uint_as_float(f[2 * j]),
+                                                          __uint_as_float(f[2 * j + 1])));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+        for (int j = 0; j < 4; ++j) squares = __ffma2_rn(v[i][j], v[i][j], squares);
         if (kResidual == Residual::kNone || !holds(i)) continue;
         const long long at = 8ll * (threadIdx.x + i * blockDim.x);
         if constexpr (kResidual == Residual::kBf16) {
             __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.residual) + t * p.r_t +
                                              at),
-                   make_uint4(f2_to_bf2(v[i][0], v[i][1]), f2_to_bf2(v[i][2], v[i][3]),
-                              f2_to_bf2(v[i][4], v[i][5]), f2_to_bf2(v[i][6], v[i][7])));
+                   packed(v[i]));
         } else {
             float4 *r = reinterpret_cast<float4 *>(static_cast<float *>(p.residual) + t * p.r_t +
                                                    at);
-            __stcs(r, make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
-            __stcs(r + 1, make_float4(v[i][4], v[i][5], v[i][6], v[i][7]));
+            __stcs(r, make_float4(v[i][0].x, v[i][0].y, v[i][1].x, v[i][1].y));
+            __stcs(r + 1, make_float4(v[i][2].x, v[i][2].y, v[i][3].x, v[i][3].y));
         }
     }
-    sum = over_row(sum, [](float a, float b) { return a + b; }, room[0]);
+    const float sum = over_row(squares.x + squares.y, [](float a, float b) { return a + b; },
+                               room[0]);
     const float rms = 1.0f / sqrtf(sum / p.width + p.eps);
     float most = 0.0f;  // of the thread's columns, where the row has one scale
 #pragma unroll
@@ -156,21 +168,22 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
         if (!holds(i)) continue;
         if constexpr (!kEarly) weigh(i, weight[0]);
         const float4 a = weight[kEarly ? i : 0][0], b = weight[kEarly ? i : 0][1];
-        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const float2 f[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
+                             make_float2(b.z, b.w)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[i][j] = v[i][j] * rms * f[j];
-            most = max_nan(most, fabsf(v[i][j]));
-        }
-        if constexpr (!kE4m3)
+        for (int j = 0; j < 4; ++j)
+            v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], make_float2(rms, rms)), f[j]);
+        if constexpr (kE4m3) {
+            if (p.lanes == 0) most = max_nan(most, largest(v[i]));
+        } else {
             __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + t * p.o_t +
                                              8ll * (threadIdx.x + i * blockDim.x)),
-                   make_uint4(f2_to_bf2(v[i][0], v[i][1]), f2_to_bf2(v[i][2], v[i][3]),
-                              f2_to_bf2(v[i][4], v[i][5]), f2_to_bf2(v[i][6], v[i][7])));
+                   packed(v[i]));
+        }
     }
     if constexpr (kE4m3) {
         auto scale_of = [](float m) {
-            const float s = m / kE4m3Most;
+            const float s = m * (1.0f / kE4m3Most);
             return s < 0x1p-126f ? 0x1p-126f : s;  // NaN stays
         };
         float scale = 0.0f;
@@ -182,9 +195,7 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
         for (int i = 0; i < V; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (p.lanes) {
-                float m = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
+                float m = largest(v[i]);
                 for (int x = p.lanes >> 1; x >= 1; x >>= 1)
                     m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
                 scale = scale_of(m);
@@ -192,13 +203,13 @@ __global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
                     p.scales[t * p.s_t + at / p.lanes * p.s_c] = scale;
             }
             if (!holds(i)) continue;
-            const float inverse = 1.0f / scale;
+            const float inverse = __fdividef(1.0f, scale);  // 2 ulp; scales lie in 2^-126 .. 2^120
             unsigned o[2] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o[j / 2] |= static_cast<unsigned>(__nv_cvt_float2_to_fp8x2(
-                                make_float2(v[i][2 * j] * inverse, v[i][2 * j + 1] * inverse),
-                                __NV_SATFINITE, __NV_E4M3))
+                                __fmul2_rn(v[i][j], make_float2(inverse, inverse)), __NV_SATFINITE,
+                                __NV_E4M3))
                             << (16 * (j % 2));
             __stcs(reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.out) + t * p.o_t +
                                              8ll * at),

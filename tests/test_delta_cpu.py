@@ -290,7 +290,7 @@ BUDGETS = {
     "ssu_delta.cu": {"ssu_delta_mma_kernel": (168, 64), "ssu_delta_prep_kernel": (128, 0),
                      "ssu_delta_step_kernel": (128, 0), "ssu_delta_seq_kernel": (168, 0),
                      "ssu_delta_plan_kernel": (64, 0)},
-    "ssu_norm.cu": {"ssu_add_norm_kernel": (128, 0)},
+    "ssu_norm.cu": {"ssu_add_norm_kernel": (128, 96)},
 }
 
 
