@@ -564,7 +564,9 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * other call runs token by token in fp32.  An infinity or NaN in a token's operands reaches its
  * prompt's readouts from that token on, and its state, as in the recurrence (a value's its own row,
  * a query's its own token; an infinity may come out as NaN); one in a slot's state its own row.
- * A token's sums of squares are fp32: a key of 1.8e19 and more becomes zero.
+ * A token's sums of squares are fp32: a key of 1.8e19 and more becomes zero.  With a negative qk_eps
+ * keys should be no longer than one: past that the recurrence itself grows without bound, and the
+ * chunks' triangular systems lose digits with it.
  *
  * The workspace is 26 KiB for every 64 tokens, and prompt, and head.
  */

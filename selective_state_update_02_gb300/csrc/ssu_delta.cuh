@@ -11,8 +11,9 @@
 //
 // What bounds the one-token form: HBM, reading and writing the state once.  Rows are spread over
 // lanes as in the decode step (RowGeo, ssu_device.cuh); all of a warp's state loads are in flight
-// before anything else.  What bounds prompts in this form: the chain of one token after the other
-// in a warp (two products, a tree of shuffles, e back to the lanes), some 0.2 us per token.
+// before anything else (256 requests of 32 heads of 128 x 128 fp32: 156 us, 1.02 of the measured copy
+// rate).  What bounds prompts in this form: the chain of one token after the other in a warp (two
+// products, a tree of shuffles, e back to the lanes), 0.42 us per token.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -1,37 +1,43 @@
 // The gated delta rule over prompts in chunks, on the tcgen05 tensor cores (sm_103a), instantiated by
 // ssu_delta.cu beside the token-by-token kernel of ssu_delta.cuh.
 //
-// Mathematics.  Over a chunk of C = 64 tokens, with s_i the sum of the log decays up to token i, kn and
-// qn the keys and queries at length one, and S the state [P, N] that the chunk begins with:
+// Mathematics.  Over a chunk of C = 64 tokens, with s_i the sum of the log decays up to token i, kn
+// and qn the keys and queries at length one, and S the state [P, N] that the chunk begins with:
 //
 //   L_ij = beta_i e^{s_i - s_j} (kn_i . kn_j)  for j < i;      T = (I + L)^-1
 //   U    = T R,  R_i = beta_i (v_i - e^{s_i} S kn_i)           (the corrections e_i of all tokens)
 //   y_i  = e^{s_i} S qn_i + sum_{j <= i} (kn_j . qn_i) e^{s_i - s_j} U_j
 //   S'   = e^{s_C} S + sum_j e^{s_C - s_j} U_j kn_j^T
 //
-// Three kernels.  A plan (one CTA; none for few prompts) lists the chunks of all prompts.  A first pass, parallel over chunks
-// and heads, makes of keys and gates alone what a chunk needs beside its state: T, the masked M_ij =
-// (k_j . qn_i) e^{s_i - s_j} and the tokens' factors.  A second pass takes a head's state (128 of its
-// rows) through a prompt, chunk after chunk.
+// Three kernels.  A plan (one CTA; none for few prompts) lists the chunks of all prompts.  A first
+// pass, parallel over chunks and heads, makes of keys and gates alone what a chunk needs beside its
+// state: T, the masked M_ij = (k_j . qn_i) e^{s_i - s_j} and the tokens' factors.  A second pass
+// takes a head's state (128 of its rows) through a prompt, chunk after chunk.
 //
 // The second pass holds everything transposed, with the state's 128 rows p as the MMA's M: then S, R
-// and U are first operands, which come from TMEM, where the thread that made a row puts it, and
-// the tiles of K, Q, T and M in shared memory, as they were copied, are the second ones:
+// and U are first operands, which come from TMEM, where the threads that made them put them, and the
+// tiles of K, Q, T and M in shared memory, as they were copied, are the second ones:
 //
-//   S K^T [128 x 64],  S Q^T [128 x 64],  R T^T [128 x 64],  U M^T [128 x 64],  U K [128 x N]
+//   S (K, Q)^T [128 x 128],  R T^T [128 x 64],  U M^T [128 x 64],  U K [128 x N]
 //
-// Two warpgroups share the rows' elementwise work, a thread holding half a row of S in registers.
+// Two warpgroups share the rows' elementwise work, a thread holding 4 rows' 16 columns of S.
 //
 // Precision.  States, statistics and sums are fp32.  K and Q are bf16 and exact (their lengths are
 // factors of tokens).  What decides the state enters as sums of bf16 parts: S, R and U three (24
 // bits; two for a state kept in bf16), T two (1 on its diagonal is exact, and its other elements to
-// 2^-17 are below the fp32 sums' own error).  The readout alone sees M rounded to bf16 once, and U to
-// two parts.  T is worked out in fp32 by inverting blocks of 16 along the diagonal row by
-// row and joining them, T21 = -T22 L21 T11 (powers of L, as a product formula would have, grow
-// like binomials where keys are alike).
+// 2^-17 leave fp32 states 2e-7 off or less).  The readout alone sees M rounded to bf16 once, and U
+// to two parts: 0.0022 off in the 2-norm, of which its own rounding is 0.0017.  T is worked out by
+// inverting blocks of 16 along the diagonal row by row and joining them, T21 = -T22 L21 T11 (powers
+// of L, as a product formula would have, grow like binomials where keys are alike).
 //
 // A chunk with an infinity, a NaN or growing decays (a zero weight times such an element is NaN) is
 // taken token by token by the second pass, from the state in registers.
+//
+// What bounds it (8 prompts of 4096 tokens through 32 heads of 128 x 128: 566 us): the second pass by
+// the chain of a chunk's steps, 6,000 cycles at one CTA per SM, of which products take 3,300 (24
+// MMAs of N = 128, 16 of N = 64, 12 of N = 128) and the elementwise work between a product's end and
+// the next one's first operand three times 650 to 730; the first pass (175 us of it) by shared
+// memory and the chain of its own steps.
 #pragma once
 
 #include <cuda.h>
@@ -143,7 +149,8 @@ __device__ __forceinline__ void load_trans4(unsigned (&r)[4], unsigned addr) {
 }
 
 __device__ __forceinline__ void store_trans4(unsigned addr, const unsigned (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     addr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
@@ -173,7 +180,8 @@ __global__ void __launch_bounds__(kPlanThreads) ssu_delta_plan_kernel(
             long long lo, hi;
             load_prompt<kIdx64>(m.d.m, b, false, d.slot, lo, hi);
             d.begin = static_cast<int>(lo), d.end = static_cast<int>(hi);
-            d.starts = m.d.m.fresh && m.d.m.fresh[b] != 0 ? DeltaPrompt::kZeros : DeltaPrompt::kSlot;
+            d.starts =
+                m.d.m.fresh && m.d.m.fresh[b] != 0 ? DeltaPrompt::kZeros : DeltaPrompt::kSlot;
         }
         m.prompts[at] = d;
     };
@@ -310,9 +318,9 @@ __device__ __forceinline__ DeltaPrompt few_ranked(const DeltaMmaParams &m, int r
 // the four warps of a TMEM quarter each have 16 rows of both, and Q's lengths are on the diagonal.
 // The blocks of T are joined by mma.sync of operands in two bf16 parts (three products, 2^-17).
 //
-// What bounds it: the chain of its steps, with 16 warps to an SM, and mma.sync, of which an SM starts
-// one per 8 cycles (with those for K K^T and Q K^T too, and tf32 parts for the joins, it bounded the
-// pass at 1.9 times its time).
+// What bounds it: shared memory's bandwidth (68 % of it taken in calls of many waves) and the chain of
+// its steps with 16 warps to an SM.  (Scalar joins, three shared loads for eight multiplications, took
+// 2.1 times the pass's time; K K^T and Q K^T by mma.sync and joins of tf32 parts 1.1.)
 
 constexpr int kPrepThreads = 128;
 constexpr int kPrepHeads = 2;   // the most heads per CTA: a warp each makes their factors

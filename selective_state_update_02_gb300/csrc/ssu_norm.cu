@@ -5,6 +5,8 @@
 //
 // What bounds it: HBM.  Every element of x and the residual is read once and of the residual and
 // out written once: a row's sum stays in registers between the sum of squares and the output.
+// 16384 x 8192 into bf16 154 us (1.03 of the measured copy rate); 8192 x 4096 into e4m3 with scales of
+// 128 columns 45 us (0.77), where the groups' maxima, scales and conversions add issue; 8 x 4096 2.8.
 //
 // Layout.  A row belongs to a number of whole warps with up to kMostVectors vectors of 8 columns
 // per thread, neighbours in neighbouring threads, so that a warp instruction moves 512 contiguous
