@@ -363,6 +363,7 @@ __device__ __forceinline__ void block_product(float (&d)[kTiles][4], const float
                                               const float *b, int k0, int k1, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const float *const arow = a + g * kPrepPitch + 2 * t, *const brow = b + 2 * t * kPrepPitch + g;
+    float small[2][kTiles][4] = {};  // the products side by side: a sum's MMAs are a chain
 #pragma unroll
     for (int k = 0; k < kMost; k += 16) {
         if (k < k0 || k >= k1) continue;
@@ -380,11 +381,15 @@ __device__ __forceinline__ void block_product(float (&d)[kTiles][4], const float
                 const float *const at = brow + (k + 8 * x) * kPrepPitch + 8 * n;
                 split_pair(make_float2(at[0], at[kPrepPitch]), bh[x], bl[x]);
             }
-            mma_16816(d[n], al, bh);
-            mma_16816(d[n], ah, bl);
+            mma_16816(small[0][n], al, bh);
+            mma_16816(small[1][n], ah, bl);
             mma_16816(d[n], ah, bh);
         }
     }
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n][i] += small[0][n][i] + small[1][n][i];
 }
 
 // The product's 16 x 8 kTiles values, times `sign`, to rows of kPrepPitch floats from `to`.
@@ -802,16 +807,19 @@ __device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigne
         : "memory");
 }
 
-// Two values as bf16 parts; each part is what the ones before leave.
+// Two values as bf16 parts: all but the last cut off after 8 bits (two masks and a byte permutation;
+// rounding conversions, which run at a fraction of that rate, took longer), the last rounded.
 template <int kParts>
 __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-        bits[k] = f2_to_bf2(f.x, f.y);
-        if (k + 1 < kParts)
-            f = __fadd2_rn(f, make_float2(-__uint_as_float(bits[k] << 16),
-                                          -__uint_as_float(bits[k] & 0xffff0000u)));
+    for (int k = 0; k + 1 < kParts; ++k) {
+        const unsigned x = __float_as_uint(f.x) & 0xffff0000u;
+        const unsigned y = __float_as_uint(f.y) & 0xffff0000u;
+        bits[k] = __byte_perm(x, y, 0x7632);
+        f = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)),
+                       make_float2(-1.0f, -1.0f), f);
     }
+    bits[kParts - 1] = f2_to_bf2(f.x, f.y);
 }
 
 // Roles.  Per chunk, with the barrier of each hand-over ([r], [u], [w], [d], [q] and [m] only where
