@@ -807,19 +807,28 @@ __device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigne
         : "memory");
 }
 
-// Two values as bf16 parts: all but the last cut off after 8 bits (two masks and a byte permutation;
-// rounding conversions, which run at a fraction of that rate, took longer), the last rounded.
+// f - (the bf16 halves of `bits`), exactly, in FMAs of mixed types: the same by masks and shifts is
+// bound by the integer pipe, which has half their rate.
+__device__ __forceinline__ float2 less_halves(float2 f, unsigned bits) {
+    float2 r;
+    asm("{\n\t.reg .b16 l, h, m;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "mov.b16 m, 0xbf80;\n\t"  // -1
+        "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
+        "fma.rn.f32.bf16 %1, h, m, %4;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(bits), "f"(f.x), "f"(f.y));
+    return r;
+}
+
+// Two values as bf16 parts; each part is what the ones before leave.
 template <int kParts>
 __device__ __forceinline__ void split2(float2 f, unsigned (&bits)[kParts]) {
 #pragma unroll
-    for (int k = 0; k + 1 < kParts; ++k) {
-        const unsigned x = __float_as_uint(f.x) & 0xffff0000u;
-        const unsigned y = __float_as_uint(f.y) & 0xffff0000u;
-        bits[k] = __byte_perm(x, y, 0x7632);
-        f = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)),
-                       make_float2(-1.0f, -1.0f), f);
+    for (int k = 0; k < kParts; ++k) {
+        bits[k] = f2_to_bf2(f.x, f.y);
+        if (k + 1 < kParts) f = less_halves(f, bits[k]);
     }
-    bits[kParts - 1] = f2_to_bf2(f.x, f.y);
 }
 
 // Roles.  Per chunk, with the barrier of each hand-over ([r], [u], [w], [d], [q] and [m] only where
