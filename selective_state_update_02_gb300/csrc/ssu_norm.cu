@@ -85,7 +85,7 @@ __device__ __forceinline__ float over_row(float v, F join, float *room) {
 
 // blockDim = (threads per row, rows).
 template <int V, Residual kResidual, bool kE4m3>
-__global__ void __launch_bounds__(kMostThreads) ssu_add_norm_kernel(
+__global__ void __launch_bounds__(kMostThreads, V <= 4 ? 2 : 1) ssu_add_norm_kernel(
     const __grid_constant__ NormParams p) {
     pdl_wait();
     pdl_trigger();
