@@ -6,7 +6,8 @@
 // What bounds it: HBM.  Every element of x and the residual is read once and of the residual and
 // out written once: a row's sum stays in registers between the sum of squares and the output.
 // 16384 x 8192 into bf16 154 us (1.03 of the measured copy rate); 8192 x 4096 into e4m3 with scales of
-// 128 columns 45 us (0.77), where the groups' maxima, scales and conversions add issue; 8 x 4096 2.8.
+// 128 columns 42 us (0.83; 45 with half of the warps at 78 registers), where the groups' maxima,
+// scales and conversions add issue; 8 x 4096 2.6 to 3.0.
 //
 // Layout.  A row belongs to a number of whole warps with up to kMostVectors vectors of 8 columns
 // per thread, neighbours in neighbouring threads, so that a warp instruction moves 512 contiguous
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kMostThreads, V <= 4 ? 2 : 1) ssu_add_norm_ker
     }
     // With few vectors per thread the weights come under the sum of squares; more would cost resident
     // warps, of which a call of many rows has enough to hide them (8192 x 4096 into e4m3: 45 us, 54
-    // with them).
+    // with them, before the arithmetic was packed).
     constexpr bool kEarly = V <= 2;
     float4 weight[kEarly ? V : 1][2];
     auto weigh = [&](int i, float4 (&to)[2]) {
@@ -240,7 +241,7 @@ cudaError_t launch_norm(const NormParams &p, Residual residual, bool e4m3, int s
     auto threads = [&](int v) { return (p.vectors + 32 * v - 1) / (32 * v) * 32; };
     // Many rows: up to four vectors per thread (16384 x 8192: 154 us, 170 with two).  Rows that are all
     // resident at once: fewer, for more loads of weights under the sums (777 x 2560 into e4m3 with a
-    // scale per row 5.8 us, 8.3 with four).
+    // scale per row 5.8 us, 8.3 with four, before the arithmetic was packed; 4.9 now).
     const int most = p.tokens <= 8ll * sm_count ? 256 : 128;
     int v = 1;
     while (v < 4 && threads(v) > most) v *= 2;
