@@ -662,3 +662,45 @@ def test_calls_side_by_side(op):
             assert torch.equal(out, y) and torch.equal(pool, state)
     assert op.get_error() == (0, -1) and other.get_error() == (0, -1)
     other.close()
+
+
+@pytest.mark.parametrize("P,N,state", [(72, 64, torch.bfloat16), (192, 128, torch.float32)], ids=str)
+@pytest.mark.parametrize("where", ["k", "v", "dt"])
+def test_bad_tokens_of_other_sizes(op, P, N, state, where):
+    """Chunks taken token by token where a CTA's rows are not all the head's, and in two slabs."""
+    d = make([100, 150], P=P, N=N, state=state, seed=109)
+    y, want, Y, R, most = reference(d)
+    t = 170  # token 70 of the second prompt: the rows before it are as the formula gives them
+    d[where][(t, 0, 3) if where == "v" else (t, 0)] = float("nan")
+    out, pool = call(op, d)
+    tol = 2.0 ** -8 * y.abs() + (2.0 ** -7 + 2.0 ** -13) * Y
+    assert ((out.double() - y).abs() <= tol)[:t].all()
+    assert torch.isnan(out[t:, 0, 3]).all()
+    other = torch.ones(4, dtype=torch.bool, device="cuda")
+    other[:2] = False  # the heads of key head 0; for a value and a decay more is right, below
+    assert ((out.double() - y).abs() <= tol)[t:][:, other].all()
+    if where != "k":
+        assert ((out.double() - y).abs() <= tol)[t:, 1].all()
+    if where == "v":
+        rows = [p for p in range(P) if p != 3]
+        assert ((out.double() - y).abs() <= tol)[t:, 0][:, rows].all()
+    first = d["slots"][0].item()
+    err = (pool[first].double() - want[first]).norm(dim=-1)
+    half = 2.0 ** -8 * want[first].norm(dim=-1) if state == torch.bfloat16 else 0.0
+    assert (err <= min(250, 1.0 / (1.0 - most)) * 2.0 ** -20 * R[first] + half).all()
+
+
+def test_broadcast_operands(op):
+    """One key and query for all key heads, one decay and gate for all heads, by strides of zero."""
+    d = make([100, 40], H=4, G=4, seed=113)
+    e = {k: (v.contiguous() if k in ("q", "k") else v) for k, v in d.items()}
+    for k in ("q", "k", "dt", "b"):
+        d[k] = d[k][:, :1].contiguous().expand_as(d[k])
+        e[k] = d[k].contiguous()
+    assert d["k"].stride(1) == 0
+    check(e, *call(op, d), reference(e))
+    pool, out = d["pool"].clone(), torch.zeros_like(d["v"][:2])
+    step(op, d, pool, out, slice(0, 2))
+    pool2, out2 = d["pool"].clone(), torch.zeros_like(out)
+    step(op, e, pool2, out2, slice(0, 2))
+    assert torch.equal(pool, pool2) and torch.equal(out, out2)
