@@ -1383,6 +1383,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             }
                     }
                     put_parts(std::integral_constant<int, kParts>(), r, [&](int part) { return tD + part * 32 + 16 * half + 8 * x; });
+                    // (R T^T goes over S K^T from its first piece on: no load of what the next product
+                    // overwrites is in flight where its operand is handed over)
+                    if (x == 0) tc_wait_ld();
                     hand_over(bar_r + 8 * x);
                 }
             }

@@ -704,3 +704,26 @@ def test_broadcast_operands(op):
     pool2, out2 = d["pool"].clone(), torch.zeros_like(out)
     step(op, e, pool2, out2, slice(0, 2))
     assert torch.equal(pool, pool2) and torch.equal(out, out2)
+
+
+def test_the_same_bits_beside_other_work(op):
+    """Chunks of every SM beside a stream that keeps memory busy: the bits of the call alone, many
+    times (a piece of an operand read after its place was given away would show here)."""
+    for N, state in ((128, torch.float32), (64, torch.bfloat16)):
+        d = make([700, 650, 600, 64, 1], H=32, N=N, G=8, state=state, seed=127)
+        want = call(op, d)
+        ws = torch.empty(op.delta_workspace_bytes(d["pool"], d["v"], d["k"], d["slots"]),
+                         dtype=torch.uint8, device="cuda")
+        pools, outs = [d["pool"].clone() for _ in range(20)], []
+        side, a = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                a.add_(1.0)
+        for pool in pools:
+            outs.append(torch.full(d["v"].shape, 7.0, dtype=torch.bfloat16, device="cuda"))
+            op.delta_prompts(pool, d["slots"], d["cu"], d["q"], d["k"], d["v"], d["dt"],
+                             d["dt_bias"], d["A"], d["b"], outs[-1], ws, fresh=d["fresh"])
+        torch.cuda.synchronize()
+        for out, pool in zip(outs, pools):
+            assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
