@@ -205,8 +205,8 @@ ssu_status_t ssu_update_from_host(ssu_handle_t handle, void *state_pool,
  * *first_bad receives the smallest index of these in their calls, of whatever call (for a page that
  * of its request), or -1 (may be NULL): read after each call to tell one call from another.
  * Returns SSU_ERR_INDEX_OOB when *skipped > 0, SSU_ERR_CUDA when a prompt kernel gave up a wait
- * for its own copies or products (after ten seconds; its results are then not valid), SSU_OK
- * otherwise.
+ * for its own copies or products (after ten seconds, in ssu_delta_prompts after a second and more;
+ * its results are then not valid), SSU_OK otherwise.
  */
 ssu_status_t ssu_get_error(ssu_handle_t handle, ssu_stream_t stream, uint32_t *skipped,
                            int64_t *first_bad);

@@ -794,7 +794,7 @@ struct DeltaSmem {
     static constexpr int kSwap = kDeltaStages * kStage;  // two floats per compute thread
     static constexpr int kFlags = kSwap + 2 * kDeltaCompute * 4;
     static constexpr int kBars = kFlags + 16;
-    static constexpr int kTotal = kBars + 8 * (4 * kDeltaStages + 13);
+    static constexpr int kTotal = kBars + 8 * (4 * kDeltaStages + 14);
     static_assert(kStage % 1024 == 0, "tiles start at 1024 bytes");
 };
 
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
     const unsigned full = bars, empty = bars + 8 * kDeltaStages, look = empty + 8 * kDeltaStages;
     const unsigned bar_t = look + 8 * kDeltaStages, bar_s = bar_t + 8 * kDeltaStages,
                    bar_r = bar_s + 32, bar_w = bar_r + 16, bar_q = bar_w + 16, bar_p = bar_q + 8,
-                   bar_u = bar_p + 8, bar_d = bar_u + 8, bar_m = bar_d + 8;
+                   bar_u = bar_p + 8, bar_d = bar_u + 8, bar_m = bar_d + 8, bar_x = bar_m + 8;
     if (tid == 0) {
         for (int i = 0; i < kDeltaStages; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -878,6 +878,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         }
         for (int i = 0; i < 9; ++i) mbar_init(bar_s + 8 * i, kDeltaCompute / 32);
         for (unsigned bar : {bar_p, bar_u, bar_d, bar_m}) mbar_init(bar, 1);
+        mbar_init(bar_x, kDeltaCompute / 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kDeltaIssuer) {
@@ -1250,11 +1251,12 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                        h * p.out_h + row0;
             mbar_pass(look + 8 * stage, turn, dead);
             __syncwarp();
-            if (__builtin_expect(flag(), 0)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, flag()), 0)) {
                 if (waits) read_out(c - 1);
                 float *const swap = reinterpret_cast<float *>(smem + Smem::kSwap);
-                // the rows' sums over the quad's lanes and both warpgroups' columns
-                auto whole_rows = [&](float (&sum)[2][2], float *room) {
+                // the rows' sums over the quad's lanes and both warpgroups' columns (twice a token: the
+                // first one's barrier has the parity 0)
+                auto whole_rows = [&](float (&sum)[2][2], float *room, unsigned parity) {
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1263,7 +1265,11 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             sum[hh][e] += __shfl_xor_sync(0xffffffffu, sum[hh][e], 2);
                             if (t == 0) room[half * kDeltaRows + row_at(hh, e)] = sum[hh][e];
                         }
-                    asm volatile("bar.sync 1, %0;" ::"n"(kDeltaCompute) : "memory");
+                    // (not a barrier of the CTA's: where a wait has given up, warps may have
+                    // parted, and every wait has to end)
+                    warp_arrive(bar_x, lane);
+                    mbar_pass(bar_x, parity, dead);
+                    __syncwarp();
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1296,7 +1302,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             sum[x / 2][x % 2] += s.x * key.x + s.y * key.y;
                         }
                     }
-                    whole_rows(sum, swap);
+                    whole_rows(sum, swap, 0);
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -1323,7 +1329,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             sum[x / 2][x % 2] += s.x * q.x + s.y * q.y;
                         }
                     }
-                    whole_rows(sum, swap + kDeltaCompute);
+                    whole_rows(sum, swap + kDeltaCompute, 1);
                     if (half == 0 && t == 0)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {

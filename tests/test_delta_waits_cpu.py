@@ -40,3 +40,22 @@ def test_no_load_is_in_flight_when_its_accumulator_is_handed_over():
                     handed += 1
                     break
         assert handed == 2
+
+
+def test_every_wait_of_the_passes_is_bounded():
+    """After a wait has given up, warps may see different flags and take different ways through a
+    chunk: no barrier but the CTA's own, which every warp comes to, may count on the others."""
+    assert "bar.sync" not in SOURCE and "barrier.sync" not in SOURCE
+    assert "mbar_wait(" not in SOURCE and "try_wait" not in SOURCE
+    second = SOURCE[SOURCE.index("// ---- the second pass"):]
+    # the CTA's barriers: before the roles part and after they meet again
+    roles, end = second.index("if (warp == kDeltaLoader)"), second.index("tc_fence_before();\n    if (__syncthreads_or")
+    assert "__syncthreads" not in second[roles:end]
+
+
+def test_warps_take_one_way_through_a_chunk():
+    """A warp's lanes agree on whether a chunk goes token by token: what follows are instructions of
+    the whole warp."""
+    for use in re.findall(r"[^\n]*flag\(\)[^\n]*", SOURCE):
+        assert ("__any_sync" in use or "auto flag" in use or "!flag() && tok" in use  # one lane
+                ), use
