@@ -159,23 +159,34 @@ struct DeltaPlan {
     long long prompts, list, records, total;
 };
 
-// Records past this (1.2 million tokens of 32 heads) leave a call to the token-by-token form.
+// Records past this (2.4 million tokens of 32 heads) leave a call to the token-by-token form.
 constexpr double kMostRecords = 3.2e10;
 
 // Few tokens go token by token: 3 us and 0.42 for every token of the longest prompt (of which the
 // host knows that it has no more than all), against 8 us and 10 for every round of the device's SMs
 // in chunks (32 heads of 128 x 128, one prompt of 24 tokens: 12.9 us and 17.8, of 64: 29.7 and 17.1; 8
 // prompts of 8 tokens: 24.2 and 28.8; 32 of 2: 41 and 82).
+constexpr int kFewTokens = 12, kFewPerRound = 24;
+
 bool few_tokens(const ssu_shape_t &s, int64_t tokens, int sm_count) {
     const double units = static_cast<double>(s.batch) * s.nheads *
                          ((s.headdim + kDeltaRows - 1) / kDeltaRows);
-    return tokens <= 12 + 24 * (units > sm_count ? units / sm_count : 1.0);
+    return tokens <= kFewTokens + kFewPerRound * (units > sm_count ? units / sm_count : 1.0);
 }
 
-bool mma_sizes(const ssu_shape_t &s, int64_t tokens, int sm_count) {
-    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 && !few_tokens(s, tokens, sm_count) &&
+// Whether a call of these sizes, or one of fewer prompts with the same sizes otherwise, may go in
+// chunks: what the workspace query answers by.  Unlike a call's own choice it only grows with
+// prompts, tokens and heads up to kMostRecords, so that a buffer for the largest call serves all.
+bool chunk_sizes(const ssu_shape_t &s, int64_t tokens) {
+    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 &&
+           tokens > kFewTokens + kFewPerRound &&
            (tokens / kDeltaChunk + static_cast<double>(s.batch)) * s.nheads *
-                   DeltaRecord::kBytes <= kMostRecords &&
+                   DeltaRecord::kBytes <= kMostRecords;
+}
+
+// Whether a call goes in chunks, as far as its sizes say.
+bool mma_sizes(const ssu_shape_t &s, int64_t tokens, int sm_count) {
+    return chunk_sizes(s, tokens) && !few_tokens(s, tokens, sm_count) &&
            s.batch * static_cast<double>(s.nheads) * ((s.headdim + kDeltaRows - 1) / kDeltaRows) <=
                INT_MAX;
 }
@@ -289,7 +300,7 @@ ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *s
     if (st == SSU_OK) st = validate_batch(*shape);
     if (st == SSU_OK) st = validate_tokens(tokens);
     if (st != SSU_OK) return st;
-    *bytes = mma_sizes(*shape, tokens, handle->sm_count) ? delta_plan(*shape, tokens).total : 0;
+    *bytes = chunk_sizes(*shape, tokens) ? delta_plan(*shape, tokens).total : 0;
     return ok();
 }
 
@@ -316,9 +327,8 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
     if (!cu_tokens) return fail(SSU_ERR_INVALID_ARG, "cu_tokens is NULL");
     if (!aligned(cu_tokens, s.index_dtype == SSU_INDEX_I64 ? 8 : 4))
         return fail(SSU_ERR_MISALIGNED, "cu_tokens is not aligned to its type");
-    int64_t need = 0;
-    st = ssu_delta_workspace_bytes(handle, shape, tokens, &need);
-    if (st != SSU_OK) return st;
+    const bool chunks = mma_sizes(s, tokens, handle->sm_count);
+    const int64_t need = chunks ? delta_plan(s, tokens).total : 0;
     if (workspace_bytes < need || (need && !workspace))
         return fail(SSU_ERR_INVALID_ARG, "workspace holds %lld bytes; this shape needs %lld",
                     (long long)(workspace ? workspace_bytes : 0), (long long)need);
@@ -331,7 +341,7 @@ ssu_status_t ssu_delta_prompts(ssu_handle_t handle, void *state_pool,
         return fail(SSU_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(guard.err));
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorNotSupported;
-    if (tokens > 0 && mma_sizes(s, tokens, handle->sm_count) && mma_operands(d)) {
+    if (chunks && mma_operands(d)) {
         const SsuParams &p = d.m.p;
         const DeltaPlan w = delta_plan(s, tokens);
         DeltaMmaParams m{};

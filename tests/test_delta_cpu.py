@@ -313,3 +313,40 @@ def test_register_budgets(tmp_path, unit):
                 seen.add(kernel)
                 assert used <= most and spill <= spilled, (name, used, spill)
     assert seen == set(BUDGETS[unit])
+
+
+LARGEST = dict(batch=512, tokens=65536, nheads=32)
+
+
+@pytest.fixture()
+def nowhere():
+    """A handle on a device that no machine has: what is not refused ends there (status 4)."""
+    return ctypes.create_string_buffer(struct.pack("ii", 1 << 20, 152), 4096)
+
+
+@pytest.mark.parametrize("batch", [1, 2, 16, 33, 256, 511])
+@pytest.mark.parametrize("tokens", [1, 36, 37, 64, 400, 1000, 4097, 65535])
+@pytest.mark.parametrize("nheads", [4, 32])
+def test_a_workspace_for_the_largest_call_serves_all(ssu, nowhere, batch, tokens, nheads):
+    """The query's answer does not fall where prompts, tokens or heads grow, and no call of smaller
+    sizes is refused with a buffer of that many bytes (status 4: it went on to the device)."""
+    at = dict(batch=batch, tokens=tokens, nheads=nheads)
+    status, need = query(ssu, nowhere, **at)
+    assert status == 0
+    for k in LARGEST:
+        for more in (at[k] + 1, 2 * at[k], LARGEST[k]):
+            larger = dict(at, **{k: more * 2 if k == "nheads" and more % 2 else more})
+            assert query(ssu, nowhere, **larger)[1] >= need, larger
+    shape = dict(batch=batch, nheads=nheads, headdim=128, pool_size=1024)
+    assert delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(BASE, need)) == 4
+    most = query(ssu, nowhere, **LARGEST)[1]
+    assert delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(BASE, most)) == 4
+
+
+@pytest.mark.parametrize("batch,tokens,status", [(256, 1000, 4), (16, 64, 4), (8, 64, 1), (1, 36, 4),
+                                                 (1, 64, 1)])
+def test_calls_token_by_token_need_no_workspace(ssu, nowhere, batch, tokens, status):
+    """32 heads of 128 x 128 on 152 SMs: where the token-by-token form is taken, none is asked for."""
+    shape = dict(batch=batch, nheads=32, headdim=128, pool_size=1024)
+    got = delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(None, 0))
+    assert got == status, ssu.last_error()
