@@ -564,9 +564,10 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * other call runs token by token in fp32.  An infinity or NaN in a token's operands reaches its
  * prompt's readouts from that token on, and its state, as in the recurrence (a value's its own row,
  * a query's its own token; an infinity may come out as NaN); one in a slot's state its own row.
- * A token's sums of squares are fp32: a key of 1.8e19 and more becomes zero.  With a negative qk_eps
- * keys should be no longer than one: past that the recurrence itself grows without bound, and the
- * chunks' triangular systems lose digits with it.
+ * A token's sums of squares are fp32, here and in ssu_delta_update: a key or query of 1.8e19 and more
+ * becomes zero (token by token such a query's readout is NaN where its product with the state
+ * overflows).  With a negative qk_eps keys should be no longer than one: past that the recurrence
+ * itself grows without bound, and the chunks' triangular systems lose digits with it.
  *
  * The workspace is 26 KiB for every 64 tokens, and prompt, and head, and some 40 bytes for each of the
  * first two.  A buffer for the largest call serves all smaller ones: up to 32 GB the query's answer

@@ -1277,8 +1277,9 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                             sum[hh][e] =
                                 room[row_at(hh, e)] + room[kDeltaRows + row_at(hh, e)];
                 };
-                // the thread's two columns of block i of token k's key or query
-                auto pair_of = [&](int tile, int k, int i) {
+                // the thread's two columns of block i of token k's key or query, at its length (before
+                // any product: a length past fp32 leaves zeros)
+                auto pair_of = [&](int tile, int k, int i, float factor) {
                     const int col = half * kCols + 8 * i;
                     unsigned w;
                     asm volatile("ld.shared.u32 %0, [%1];"
@@ -1286,16 +1287,16 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                  : "r"(swizzled(at + tile + (col / 64) * Smem::kBlock, k,
                                                 col % 64 / 8) + 4 * t)
                                  : "memory");
-                    return make_float2(__uint_as_float(w << 16),
-                                       __uint_as_float(w & 0xffff0000u));
+                    return make_float2(__uint_as_float(w << 16) * factor,
+                                       __uint_as_float(w & 0xffff0000u) * factor);
                 };
 #pragma unroll 1
                 for (int k = 0; k < valid; ++k) {
-                    const float a = vec[R::kDecay + k], rk = vec[R::kKey + k];
+                    const float a = vec[R::kDecay + k], rk = vec[R::kKey + k], rq = vec[R::kRead + k];
                     float sum[2][2] = {};
 #pragma unroll
                     for (int i = 0; i < kCol8; ++i) {
-                        const float2 key = pair_of(Smem::kK, k, i);
+                        const float2 key = pair_of(Smem::kK, k, i, rk);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const float2 s = S[i][x / 2][x % 2];
@@ -1313,14 +1314,14 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                                      : "r"(swizzled(at + Smem::kV + row / 64 * kDeltaTile, k,
                                                     row % 64 / 8) + 2 * (row % 8))
                                      : "memory");
-                        e[x] = vec[R::kBeta + k] * rk *
-                               (__uint_as_float(static_cast<unsigned>(v) << 16) -
-                                a * (sum[x / 2][x % 2] * rk));
+                        e[x] = vec[R::kBeta + k] * (__uint_as_float(static_cast<unsigned>(v) << 16) -
+                                                    a * sum[x / 2][x % 2]);
                         sum[x / 2][x % 2] = 0.0f;
                     }
 #pragma unroll
                     for (int i = 0; i < kCol8; ++i) {
-                        const float2 key = pair_of(Smem::kK, k, i), q = pair_of(Smem::kQ, k, i);
+                        const float2 key = pair_of(Smem::kK, k, i, rk),
+                                     q = pair_of(Smem::kQ, k, i, rq);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             float2 &s = S[i][x / 2][x % 2];
@@ -1335,8 +1336,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
                         for (int x = 0; x < 4; ++x) {
                             const int row = row_at(x / 2, x % 2);
                             if (row0 + row < p.headdim)
-                                out[k * p.out_b + row] =
-                                    __float2bfloat16(sum[x / 2][x % 2] * vec[R::kRead + k]);
+                                out[k * p.out_b + row] = __float2bfloat16(sum[x / 2][x % 2]);
                         }
                 }
                 mbar_pass(bar_p, c & 1, dead);  // the issuer has come this far

@@ -727,3 +727,32 @@ def test_the_same_bits_beside_other_work(op):
         torch.cuda.synchronize()
         for out, pool in zip(outs, pools):
             assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
+
+
+@pytest.mark.parametrize("lens,N", [([1, 1, 1], 128), ([9, 6, 5], 64), ([100, 70], 128), ([90, 80], 64)],
+                         ids=str)
+@pytest.mark.parametrize("size", [2.0 ** 65, 2.0 ** 127])
+def test_keys_past_fp32_become_zeros(op, lens, N, size):
+    """A key whose squares' sum is past fp32, finite itself: its token decays the state and reads it,
+    and neither products with it nor with the query (of 4, so that they overflow too) leave a trace.
+    One token, few tokens, and chunks."""
+    d = make(lens, N=N, seed=131)
+    steps = max(lens) == 1
+    if steps:
+        d["fresh"] = None
+    t = d["cu"][1].item() + lens[1] // 2
+    d["k"], d["q"] = d["k"].clone(), d["q"].clone()
+    d["k"][t, 0], d["q"][t, 0] = size, 4.0
+    zeroed = dict(d, k=d["k"].clone())
+    zeroed["k"][t, 0] = 0.0
+    if steps:
+        pool, out = d["pool"].clone(), torch.zeros_like(d["v"])
+        step(op, d, pool, out)
+        torch.cuda.synchronize()
+    else:
+        out, pool = call(op, d)
+    check(d, out, pool, reference(zeroed), chunked=sum(lens) > 36)
+    if sum(lens) > 36:  # in chunks a query's does too: its readout is zero
+        d["q"][t, 0] = size
+        out, _ = call(op, d)
+        assert (out[t, :2] == 0).all() and torch.isfinite(out).all()
