@@ -557,8 +557,8 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * offsets are as there; shape->batch is the number of prompts.
  *
  * Two forms.  Where dstate is 64 or 128, q, k, v and out are 16-byte aligned with strides that are
- * multiples of 8, tokens are more than a few (12, and 24 for every round of the device's SMs that
- * prompts times heads come to) and the workspace stays within 32 GB, chunks of 64 tokens run as
+ * multiples of 8, tokens are more than a few (20 and more, by what both forms were measured to take at
+ * the call's prompts, heads and sizes) and the workspace stays within 32 GB, chunks of 64 tokens run as
  * matrix products: states and sums in fp32, while the readout meets its chunk's weights rounded to
  * bf16 once (about 2^-9 of a chunk's share in the mean square, as much as its own rounding).  Any
  * other call runs token by token in fp32.  An infinity or NaN in a token's operands reaches its

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "ssu.h"
@@ -162,16 +163,30 @@ struct DeltaPlan {
 // Records past this (2.4 million tokens of 32 heads) leave a call to the token-by-token form.
 constexpr double kMostRecords = 3.2e10;
 
-// Few tokens go token by token: 3 us and 0.42 for every token of the longest prompt (of which the
-// host knows that it has no more than all), against 8 us and 10 for every round of the device's SMs
-// in chunks (32 heads of 128 x 128, one prompt of 24 tokens: 12.9 us and 17.8, of 64: 29.7 and 17.1; 8
-// prompts of 8 tokens: 24.2 and 28.8; 32 of 2: 41 and 82).
-constexpr int kFewTokens = 12, kFewPerRound = 24;
+// Few tokens go token by token.  Both forms in us, fitted to 1 to 128 prompts of 1 to 2048 tokens, with
+// w the elements of a request's state by those of 32 heads of 128 x 128:
+//   chunks          5 and 11 (dstate 64: 8) for every round of SMs that prompts times heads' slabs come
+//                   to (32 heads, 1 prompt 15.8, 8 prompts 27, 32 83, 128 302; 16 of 64 x 64, 1 prompt
+//                   13, 128 118)
+//   token by token  3 and 0.32 + 0.16 w for each token of the longest prompt (1 prompt of 24: 12.8, of
+//                   36: 17.8; 64 heads 18.8 and 27.2), or what all of them take: w (0.8 a prompt, 0.26
+//                   a token) (128 prompts of 6 tokens: 278)
+// Of the longest prompt the host knows no more than that the others may have a token each, and takes
+// that.  Where tokens are spread evenly, token by token would pay for more than the rule leaves to it,
+// most where heads are few and small: 8 prompts of 8 tokens through 32 heads take 27.0 in chunks and
+// 24.4 token by token (33.5 where one has 57 of them), 16 of 8 through 16 of 64 x 64 21.8 and 8.0 (40.8).
+// Below kFewest every call goes token by token, whose workspace is none.
+constexpr int kFewest = 20;
 
 bool few_tokens(const ssu_shape_t &s, int64_t tokens, int sm_count) {
-    const double units = static_cast<double>(s.batch) * s.nheads *
-                         ((s.headdim + kDeltaRows - 1) / kDeltaRows);
-    return tokens <= kFewTokens + kFewPerRound * (units > sm_count ? units / sm_count : 1.0);
+    if (tokens <= kFewest) return true;
+    const double prompts = static_cast<double>(s.batch), all = static_cast<double>(tokens);
+    const double w = static_cast<double>(s.nheads) * s.headdim * s.dstate / (32 * 128 * 128);
+    const double rounds =
+        std::ceil(prompts * s.nheads * ((s.headdim + kDeltaRows - 1) / kDeltaRows) / sm_count);
+    const double chain = 3 + (0.32 + 0.16 * w) * (all - prompts + 1);
+    const double work = 1.5 + w * (0.8 * prompts + 0.26 * all);
+    return (chain > work ? chain : work) <= 5 + (s.dstate == 64 ? 8 : 11) * rounds;
 }
 
 // Whether a call of these sizes, or one of fewer prompts with the same sizes otherwise, may go in
@@ -179,7 +194,7 @@ bool few_tokens(const ssu_shape_t &s, int64_t tokens, int sm_count) {
 // prompts, tokens and heads up to kMostRecords, so that a buffer for the largest call serves all.
 bool chunk_sizes(const ssu_shape_t &s, int64_t tokens) {
     return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 &&
-           tokens > kFewTokens + kFewPerRound &&
+           tokens > kFewest &&
            (tokens / kDeltaChunk + static_cast<double>(s.batch)) * s.nheads *
                    DeltaRecord::kBytes <= kMostRecords;
 }

@@ -343,10 +343,15 @@ def test_a_workspace_for_the_largest_call_serves_all(ssu, nowhere, batch, tokens
     assert delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(BASE, most)) == 4
 
 
-@pytest.mark.parametrize("batch,tokens,status", [(256, 1000, 4), (16, 64, 4), (8, 64, 1), (1, 36, 4),
-                                                 (1, 64, 1)])
-def test_calls_token_by_token_need_no_workspace(ssu, nowhere, batch, tokens, status):
-    """32 heads of 128 x 128 on 152 SMs: where the token-by-token form is taken, none is asked for."""
-    shape = dict(batch=batch, nheads=32, headdim=128, pool_size=1024)
+@pytest.mark.parametrize("nheads,batch,tokens,status", [
+    (32, 1, 24, 4), (32, 1, 36, 1), (32, 1, 64, 1), (32, 8, 48, 4), (32, 8, 96, 1), (32, 16, 64, 4),
+    (32, 16, 192, 1), (32, 128, 512, 4), (32, 128, 1024, 1), (64, 1, 16, 4), (64, 1, 24, 1),
+    (64, 1, 36, 1), (64, 2, 28, 1), (64, 8, 48, 4), (64, 8, 96, 1), (64, 32, 96, 4),
+    (64, 32, 256, 1), (64, 128, 1024, 1)], ids=str)
+def test_calls_token_by_token_need_no_workspace(ssu, nowhere, nheads, batch, tokens, status):
+    """Heads of 128 x 128 on 152 SMs, at points where one form was measured to be the faster one however
+    a call's tokens are spread (or where all but one each are one prompt's): where that is the
+    token-by-token form (status 4: the call went on), no workspace is asked for."""
+    shape = dict(batch=batch, nheads=nheads, headdim=128, pool_size=1024)
     got = delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(None, 0))
     assert got == status, ssu.last_error()
