@@ -355,3 +355,39 @@ def test_calls_token_by_token_need_no_workspace(ssu, nowhere, nheads, batch, tok
     shape = dict(batch=batch, nheads=nheads, headdim=128, pool_size=1024)
     got = delta_call(ssu, nowhere, True, shape=shape, tokens=tokens, workspace=(None, 0))
     assert got == status, ssu.last_error()
+
+
+# unit -> pattern of a kernel's instantiations -> (most registers, most spilled bytes): what the
+# kernels' times were measured at.  Norms of up to four vectors a thread keep two CTAs of 512
+# threads to an SM, those into e4m3 with a residual at 36 spilled bytes; eight vectors (rows past
+# 16384 columns) one CTA.
+MEASURED = {
+    "ssu_delta.cu": {r"ssu_delta_mma_kernel": (164, 0), r"ssu_delta_prep_kernel": (110, 0),
+                     r"ssu_delta_step_kernelILi8ELi128Ef": (96, 0),
+                     r"ssu_delta_step_kernelILi4ELi64E": (80, 0)},
+    "ssu_norm.cu": {r"ssu_add_norm_kernelILi[124]E.*Lb0E": (64, 0),
+                    r"ssu_add_norm_kernelILi[12]E.*Lb1E": (64, 0),
+                    r"ssu_add_norm_kernelILi4E.*Lb1E": (64, 36),
+                    r"ssu_add_norm_kernelILi8E": (128, 52)},
+}
+
+
+@pytest.mark.parametrize("unit", sorted(MEASURED))
+def test_registers_as_measured(tmp_path, unit):
+    from selective_state_update_02_gb300 import _build
+    csrc = ROOT / "selective_state_update_02_gb300" / "csrc"
+    out = subprocess.run(
+        [_build.nvcc_path(), *_build.ARCH, "-O3", "-std=c++17", "-I", str(ROOT / "include"), "-I",
+         str(csrc), "-Xptxas", "-v", "-cubin", "-c", str(csrc / unit), "-o",
+         str(tmp_path / "unit.cubin")], capture_output=True, text=True, timeout=600,
+        check=True).stderr
+    seen = set()
+    for block in out.split("ptxas info    : Compiling entry function '")[1:]:
+        name = block.split("'")[0]
+        used = int(re.search(r"Used (\d+) registers", block).group(1))
+        spill = int(re.search(r"(\d+) bytes spill stores", block).group(1))
+        for kernel, (most, spilled) in MEASURED[unit].items():
+            if re.search(kernel, name):
+                seen.add(kernel)
+                assert used <= most and spill <= spilled, (name, used, spill)
+    assert seen == set(MEASURED[unit])
