@@ -559,11 +559,12 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * Two forms.  Where dstate is 64 or 128, q, k, v and out are 16-byte aligned with strides that are
  * multiples of 8, tokens are more than a few (20 and more, by what both forms were measured to take at
  * the call's prompts, heads and sizes) and the workspace stays within 32 GB, chunks of 64 tokens run as
- * matrix products: states and sums in fp32, while the readout meets its chunk's weights rounded to
- * bf16 once (about 2^-9 of a chunk's share in the mean square, as much as its own rounding).  Any
- * other call runs token by token in fp32.  An infinity or NaN in a token's operands reaches its
- * prompt's readouts from that token on, and its state, as in the recurrence (a value's its own row,
- * a query's its own token; an infinity may come out as NaN); one in a slot's state its own row.
+ * matrix products of fp32 sums, whose operands are split into bf16 parts to 2^-17 and more: readouts
+ * are as near as fp32 ones rounded once, and states as the fp32 recurrence's (but for a head whose
+ * keys are all the same: up to 2^-14 of their 2-norm).  Any other call runs token by token in fp32.
+ * An infinity or NaN in a token's operands reaches its prompt's readouts from that token on, and its
+ * state, as in the recurrence (a value's its own row, a query's its own token; an infinity may come
+ * out as NaN); one in a slot's state its own row.
  * A token's sums of squares are fp32, here and in ssu_delta_update: a key or query of 1.8e19 and more
  * becomes zero (token by token such a query's readout is NaN where its product with the state
  * overflows).  With a negative qk_eps keys should be no longer than one: past that the recurrence

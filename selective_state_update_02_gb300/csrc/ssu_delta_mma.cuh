@@ -23,12 +23,16 @@
 // Two warpgroups share the rows' elementwise work, a thread holding 4 rows' 16 columns of S.
 //
 // Precision.  States, statistics and sums are fp32.  K and Q are bf16 and exact (their lengths are
-// factors of tokens).  What decides the state enters as sums of bf16 parts: S, R and U three (24
-// bits; two for a state kept in bf16), T two (1 on its diagonal is exact, and its other elements to
-// 2^-17 leave fp32 states 2e-7 off or less).  The readout alone sees M rounded to bf16 once, and U
-// to two parts: 0.0022 off in the 2-norm, of which its own rounding is 0.0017.  T is worked out by
-// inverting blocks of 16 along the diagonal row by row and joining them, T21 = -T22 L21 T11 (powers
-// of L, as a product formula would have, grow like binomials where keys are alike).
+// factors of tokens).  The other operands enter as sums of bf16 parts: for the state S, R and U three
+// (24 bits; two for a state kept in bf16) and T two (1 on its diagonal is exact, the other elements are
+// to 2^-17); for the readout U and M two each, three of the four products.  Readouts are then as far
+// off as fp32 sums rounded once, 0.0017 in the 2-norm (with M in one part 0.0022, and 0.0102 where a
+// head's keys are all the same and its corrections cancel).  fp32 states are 2e-7 to 5e-6 off with
+// decays of up to thousands of tokens, as the fp32 recurrence's are (3e-7 to 1e-5: its decays'
+// roundings add up); where all keys are the same T's second part shows, 2^-16.7 to 2^-14.3 (of 4000
+// tokens with gates of 0.5 to 1).  T is worked out by inverting blocks of 16 along the diagonal row by
+// row and joining them, T21 = -T22 L21 T11 (powers of L, as a product formula would have, grow like
+// binomials where keys are alike).
 //
 // A chunk with an infinity, a NaN or growing decays (a zero weight times such an element is NaN) is
 // taken token by token by the second pass, from the state in registers.
@@ -55,8 +59,11 @@ constexpr int kDeltaChunk = 64;  // tokens per chunk
 constexpr int kDeltaRows = 128;  // state rows per CTA: the MMA's M
 constexpr int kDeltaTile = kDeltaChunk * 128;  // 64 rows of 64 bf16
 
-// What the first pass leaves of a chunk for one head: T's two parts and M, as the tiles of an
-// operand, and the tokens' factors.
+// What the first pass leaves of a chunk for one head: T's and M's two parts as the tiles of an operand,
+// and the tokens' factors.  All four are lower triangles, in blocks of 16 x 16, of which products take
+// no block above the diagonal (a step of 16 columns k has the rows from 16 k on).  So M's second part
+// lies where the others have those blocks: its columns k = 1 .. 3 in M's tile, from row 0 on at the
+// columns 4 - k, its first ones, rows 0 .. 47, in T's first part at the columns 3, the rest at 1.
 struct DeltaRecord {
     enum : int {
         kT1 = 0,
@@ -335,7 +342,8 @@ struct PrepSmem {
     static constexpr int kTilesEnd = N / 64 * kBlock;
     static constexpr int kMatEnd = kT + kDeltaChunk * kPrepPitch * 4;
     static constexpr int kM = kTilesEnd > kMatEnd ? kTilesEnd : kMatEnd;
-    static constexpr int kLengths = kM + kDeltaTile;  // 1 / |k|, scale / |q|
+    static constexpr int kMFirst = kM + kDeltaTile;  // the first 16 columns of M's second part
+    static constexpr int kLengths = kMFirst + kDeltaChunk * 32;  // 1 / |k|, scale / |q|
     static constexpr int kSums = kLengths + 2 * kDeltaChunk * 4;  // s in two floats, per head
     static constexpr int kVec = kSums + kPrepHeads * 2 * kDeltaChunk * 4;  // per head
     static constexpr int kBars = kVec + kPrepHeads * 2048;
@@ -634,16 +642,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     }
     float *const L = reinterpret_cast<float *>(raw + Smem::kL);
     float *const T = reinterpret_cast<float *>(raw + Smem::kT);
-    // what stays zero for every head: T and M above the blocks of 16 on the diagonal
-    for (int n = 2 * block + 2; n < 8; ++n)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = 16 * block + g + 8 * half;
-            *reinterpret_cast<float2 *>(T + i * kPrepPitch + 8 * n + 2 * t) =
-                make_float2(0.0f, 0.0f);
-            *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 + ((n ^ (i & 7)) << 4) + 4 * t) =
-                0u;
-        }
 #pragma unroll 1
     for (int k = 0; k < m.per_cta; ++k) {
         __syncthreads();  // the factors; the head before has left
@@ -678,10 +676,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                             i < valid ? make_float2(__uint_as_float(kk[at]) * (e0 * f[half]),
                                                     __uint_as_float(kk[at + 1]) * (e1 * f[half]))
                                       : make_float2(0.0f, 0.0f);
+                        unsigned one, two;
+                        split_pair(make_float2(j <= i ? __uint_as_float(qk[at]) * e0 : 0.0f,
+                                               j + 1 <= i ? __uint_as_float(qk[at + 1]) * e1 : 0.0f),
+                                   one, two);
                         *reinterpret_cast<unsigned *>(raw + Smem::kM + i * 128 +
-                                                      ((n ^ (i & 7)) << 4) + 4 * t) =
-                            f2_to_bf2(j <= i ? __uint_as_float(qk[at]) * e0 : 0.0f,
-                                      j + 1 <= i ? __uint_as_float(qk[at + 1]) * e1 : 0.0f);
+                                                      ((n ^ (i & 7)) << 4) + 4 * t) = one;
+                        const int to = nb == 0 ? Smem::kMFirst + i * 32 + x * 16
+                                               : Smem::kM + (i - 16 * nb) * 128 +
+                                                     (((2 * (4 - nb) + x) ^ (i & 7)) << 4);
+                        *reinterpret_cast<unsigned *>(raw + to + 4 * t) = two;
                     }
                 }
             }
@@ -757,7 +761,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
                                    v[2 * i + 1] - __uint_as_float(one[i] & 0xffff0000u));
             }
             const int at = row * 128 + ((piece ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(to + R::kT1 + at) = make_uint4(one[0], one[1], one[2], one[3]);
+            uint4 first_part = make_uint4(one[0], one[1], one[2], one[3]);
+            // M's second part, above T's diagonal
+            const int of_m = piece / 2 == 3 && row < 48 ? row : piece / 2 == 1 && row < 16 ? row + 48 : -1;
+            if (of_m >= 0)
+                first_part = *reinterpret_cast<const uint4 *>(raw + Smem::kMFirst + of_m * 32 +
+                                                              piece % 2 * 16);
+            *reinterpret_cast<uint4 *>(to + R::kT1 + at) = first_part;
             *reinterpret_cast<uint4 *>(to + R::kT2 + at) = make_uint4(two[0], two[1], two[2], two[3]);
             const int m_at = (tid + x * kPrepThreads) * 16;
             *reinterpret_cast<uint4 *>(to + R::kM + m_at) =
@@ -1021,7 +1031,10 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
         const unsigned leader = elect_one();
         unsigned fast = 0;  // parity of the chunks not taken token by token
         bool any = false;
-        constexpr unsigned kTokens = instruction(kDeltaChunk, false, false);
+        // d, its tokens from `first` on, += a step of 16 tokens' a by a triangle's columns at b
+        auto triangle = [&](unsigned d, unsigned a, unsigned b, int first, int tokens, bool add) {
+            mma_ts_of(leader, d + first, a, operand(b, 0), instruction(tokens, false, false), add);
+        };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c, next_stage()) {
             const unsigned at = base + stage * Smem::kStage;
@@ -1063,8 +1076,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int k = x + 2 * half;
-                        mma_ts_of(leader, tP, tD + part * 32 + 8 * k, operand(t + k * 32, 0),
-                                  kTokens, add || half > 0);
+                        triangle(tP, tD + part * 32 + 8 * k, t + k * (2048 + 32), 16 * k, 64 - 16 * k,
+                                 add || half > 0);
                     }
                 };
                 // small parts first: sums lose less
@@ -1092,12 +1105,18 @@ __global__ void __launch_bounds__(kDeltaThreads, 1)
             tc_commit_of(leader, bar_d);
             mbar_pass(bar_q, fast, dead);
             tc_fence_after();
+            const unsigned tile = at + Smem::kRecord + R::kM;
+            auto u_at = [&](int part, int k) { return tQ + 32 * (k / 2) + 16 * part + 8 * (k % 2); };
+            triangle(tM, u_at(0, 0), t1 + 3 * 32, 0, 48, true);
+            triangle(tM, u_at(0, 0), t1 + 32, 48, 16, true);
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                triangle(tM, u_at(0, k), tile + (4 - k) * 32, 16 * k, 64 - 16 * k, true);
 #pragma unroll
             for (int part = 1; part >= 0; --part)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ts_of(leader, tM, tQ + 32 * (k / 2) + 16 * part + 8 * (k % 2),
-                              operand(at + Smem::kRecord + R::kM + k * 32, 0), kTokens, true);
+                    triangle(tM, u_at(part, k), tile + k * (2048 + 32), 16 * k, 64 - 16 * k, true);
             tc_commit_of(leader, empty + 8 * stage);
             tc_commit_of(leader, bar_m);
             fast ^= 1;
