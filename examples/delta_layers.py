@@ -1,5 +1,5 @@
-"""Layers of a model whose token mixer is the gated delta rule, served with an 8-bit residual stream
-in front of every mixer.
+"""Layers of a model whose token mixer is the gated delta rule, served with a bf16 residual stream and
+a norm in front of every mixer whose output may be 8 bits wide.
 
 Each layer adds the last one's output to the residual and norms the sum in one call (``op.add_norm``:
 bf16 for the first projections, or e4m3 with a scale per 128 columns where ``eight_bits`` is set),

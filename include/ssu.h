@@ -616,6 +616,9 @@ typedef struct {
  *     out[t,i] = bf16_rne(y[i])        or, for e4m3 and every group of columns,
  *     scales[t,c] = max(max_i |y[i]| / 448, 2^-126);   out[t,i] = e4m3_rne(y[i] / scales[t,c])
  *
+ * where the two quotients are products with reciprocals: scales are within 2^-23 of the formula's, and
+ * what is rounded to e4m3 within 2^-21 of y / scales, so that a value next to the middle of two e4m3
+ * neighbours may become either.
  * The norm is that of the sum in fp32, not of what a bf16 residual keeps of it.  residual may be
  * NULL (r = x).  x, residual, out and weight [width] fp32 are 16-byte aligned (an e4m3 out 8-byte).
  * out may be x itself (bf16, same strides); nothing else may overlap.  A NaN or infinity in a

@@ -206,7 +206,10 @@ __global__ void __launch_bounds__(kMostThreads, V <= 4 ? 2 : 1) ssu_add_norm_ker
                     p.scales[t * p.s_t + at / p.lanes * p.s_c] = scale;
             }
             if (!holds(i)) continue;
-            const float inverse = __fdividef(1.0f, scale);  // 2 ulp; scales lie in 2^-126 .. 2^120
+            // 2 ulp; scales lie in 2^-126 .. 2^120.  (A product: eight divisions per vector would come
+            // to more than all the rest of this loop, for values that the rounding to 4 bits moves by
+            // 2^-4 at most and 2^-21 of this only next to the middle of two neighbours.)
+            const float inverse = __fdividef(1.0f, scale);
             unsigned o[2] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
