@@ -37,11 +37,11 @@
 // A chunk with an infinity, a NaN or growing decays (a zero weight times such an element is NaN) is
 // taken token by token by the second pass, from the state in registers.
 //
-// What bounds it (8 prompts of 4096 tokens through 32 heads of 128 x 128: 535 us): the second pass by
-// the chain of a chunk's steps, 5,500 cycles at one CTA per SM, of which products take 3,300 (24
-// MMAs of N = 128, 16 of N = 64, 12 of N = 128) and the rest is the elementwise work between a
-// product's end and the next one's first operand (of R 430 cycles, 340 of them arithmetic); the
-// first pass (some 165 us of it) by shared memory and the chain of its own steps.
+// What bounds it (8 prompts of 4096 tokens through 32 heads of 128 x 128: 541 us): the second pass (360
+// of them) by the chain of a chunk's steps, 2.8 us or 5,500 cycles at one CTA per SM, of which more
+// than half is products (24 MMAs of N = 128, 16 of N = 64 down to 16, 12 of N = 128) and the rest the
+// elementwise work between a product's end and the next one's first operand (of R 430 cycles, 340 of
+// them arithmetic); the first pass by shared memory and the chain of its own steps.
 #pragma once
 
 #include <cuda.h>

@@ -7,7 +7,9 @@
 // out written once: a row's sum stays in registers between the sum of squares and the output.
 // 16384 x 8192 into bf16 154 us (1.03 of the measured copy rate); 8192 x 4096 into e4m3 with scales of
 // 128 columns 42 us (0.83; 45 with half of the warps at 78 registers), where the groups' maxima,
-// scales and conversions add issue; 8 x 4096 2.6 to 3.0.
+// scales and conversions add issue; 8 x 4096 2.7 to 3.2 (a launch: it differs as much between boxes).
+// Rows past 16384 columns take eight vectors a thread and one CTA per SM: 4096 x 32768 into bf16 192 us
+// (0.82), into e4m3 233 (0.60, with 52 spilled bytes); 4096 x 20000 111 and 179 (0.87 and 0.48).
 //
 // Layout.  A row belongs to a number of whole warps with up to kMostVectors vectors of 8 columns
 // per thread, neighbours in neighbouring threads, so that a warp instruction moves 512 contiguous
@@ -206,9 +208,9 @@ __global__ void __launch_bounds__(kMostThreads, V <= 4 ? 2 : 1) ssu_add_norm_ker
                     p.scales[t * p.s_t + at / p.lanes * p.s_c] = scale;
             }
             if (!holds(i)) continue;
-            // 2 ulp; scales lie in 2^-126 .. 2^120.  (A product: eight divisions per vector would come
-            // to more than all the rest of this loop, for values that the rounding to 4 bits moves by
-            // 2^-4 at most and 2^-21 of this only next to the middle of two neighbours.)
+            // 2 ulp; scales lie in 2^-126 .. 2^120.  (Eight divisions per vector instead: 48.4 us for 42.3
+            // of 8192 x 4096, 6.5 for 4.9 of 777 x 2560.  The rounding to 4 bits moves a value by 2^-4 at
+            // most, and 2^-21 of it shows only next to the middle of two neighbours.)
             const float inverse = __fdividef(1.0f, scale);
             unsigned o[2] = {};
 #pragma unroll

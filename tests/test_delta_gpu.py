@@ -756,3 +756,29 @@ def test_keys_past_fp32_become_zeros(op, lens, N, size):
         d["q"][t, 0] = size
         out, _ = call(op, d)
         assert (out[t, :2] == 0).all() and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("N,H", [(128, 4), (64, 8)])
+def test_many_prompts_by_64_bit_indices(op, N, H):
+    """The plan of more than 32 prompts from int64 slots and offsets, bad and empty prompts among
+    them, rows of no prompt on both sides."""
+    lens = [(53 * i) % 150 if i % 7 else 0 for i in range(45)]
+    d = make(lens, H=H, N=N, G=2, seed=157, idx=torch.int64, lead=3, gap=5)
+    d["slots"][4], d["slots"][30] = len(d["pool"]), -(1 << 40)
+    check_some(op, d, skip=(4, 30))
+
+
+def test_a_workspace_of_a_larger_call(op):
+    """One buffer, asked for once with the most prompts and tokens, serves calls of any smaller size,
+    in chunks or not, and a call token by token takes none."""
+    big = make([20] * 60, H=8, seed=163)
+    n = op.delta_workspace_bytes(big["pool"], big["v"], big["k"], big["slots"])
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for lens in ([20] * 60, [700], [1, 2, 3], [64] * 3, [33], [1] * 50):
+        d = make(lens, H=8, seed=167)
+        pool, out = d["pool"].clone(), torch.full(d["v"].shape, 7.0, dtype=torch.bfloat16,
+                                                  device="cuda")
+        op.delta_prompts(pool, d["slots"], d["cu"], d["q"], d["k"], d["v"], d["dt"], d["dt_bias"],
+                         d["A"], d["b"], out, None if sum(lens) < 20 else ws, fresh=d["fresh"])
+        torch.cuda.synchronize()
+        check(d, out, pool, reference(d))
