@@ -573,8 +573,8 @@ ssu_status_t ssu_delta_update(ssu_handle_t handle, void *state_pool,
  * The workspace is 26 KiB for every 64 tokens, and prompt, and head, and some 40 bytes for each of the
  * first two.  A buffer for the largest call serves all smaller ones: up to 32 GB the query's answer
  * grows with prompts, tokens and heads, and no call needs more than it.  Past 32 GB the answer is 0
- * (such calls run token by token, and are no bound for smaller ones).  A call that runs token by token
- * does without a workspace.
+ * (such calls run token by token, and are no bound for smaller ones).  A call whose sizes make it run
+ * token by token does without a workspace.
  */
 ssu_status_t ssu_delta_workspace_bytes(ssu_handle_t handle, const ssu_shape_t *shape,
                                        int64_t tokens, int64_t *bytes);

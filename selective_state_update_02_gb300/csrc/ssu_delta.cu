@@ -174,7 +174,8 @@ constexpr double kMostRecords = 3.2e10;
 // Of the longest prompt the host knows no more than that the others may have a token each, and takes
 // that.  Where tokens are spread evenly, token by token would pay for more than the rule leaves to it,
 // most where heads are few and small: 8 prompts of 8 tokens through 32 heads take 27.0 in chunks and
-// 24.4 token by token (33.5 where one has 57 of them), 16 of 8 through 16 of 64 x 64 21.8 and 8.0 (40.8).
+// 24.4 token by token (33.5 where one has 57 of them), 16 of 8 through 16 of 64 x 64 21.8 and 8.0
+// (40.8).
 // Below kFewest every call goes token by token, whose workspace is none.
 constexpr int kFewest = 20;
 
@@ -193,8 +194,7 @@ bool few_tokens(const ssu_shape_t &s, int64_t tokens, int sm_count) {
 // chunks: what the workspace query answers by.  Unlike a call's own choice it only grows with
 // prompts, tokens and heads up to kMostRecords, so that a buffer for the largest call serves all.
 bool chunk_sizes(const ssu_shape_t &s, int64_t tokens) {
-    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 &&
-           tokens > kFewest &&
+    return (s.dstate == 64 || s.dstate == 128) && s.batch > 0 && tokens > kFewest &&
            (tokens / kDeltaChunk + static_cast<double>(s.batch)) * s.nheads *
                    DeltaRecord::kBytes <= kMostRecords;
 }

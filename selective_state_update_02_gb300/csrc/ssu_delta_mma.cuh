@@ -763,7 +763,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
             const int at = row * 128 + ((piece ^ (row & 7)) << 4);
             uint4 first_part = make_uint4(one[0], one[1], one[2], one[3]);
             // M's second part, above T's diagonal
-            const int of_m = piece / 2 == 3 && row < 48 ? row : piece / 2 == 1 && row < 16 ? row + 48 : -1;
+            const int of_m = piece / 2 == 3 && row < 48   ? row
+                             : piece / 2 == 1 && row < 16 ? row + 48
+                                                          : -1;
             if (of_m >= 0)
                 first_part = *reinterpret_cast<const uint4 *>(raw + Smem::kMFirst + of_m * 32 +
                                                               piece % 2 * 16);

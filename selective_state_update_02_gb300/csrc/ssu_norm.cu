@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(kMostThreads, V <= 4 ? 2 : 1) ssu_add_norm_ker
                     p.scales[t * p.s_t + at / p.lanes * p.s_c] = scale;
             }
             if (!holds(i)) continue;
-            // 2 ulp; scales lie in 2^-126 .. 2^120.  (Eight divisions per vector instead: 48.4 us for 42.3
-            // of 8192 x 4096, 6.5 for 4.9 of 777 x 2560.  The rounding to 4 bits moves a value by 2^-4 at
-            // most, and 2^-21 of it shows only next to the middle of two neighbours.)
+            // 2 ulp; scales lie in 2^-126 .. 2^120.  (Eight divisions per vector instead: 48.4 us for
+            // 42.3 of 8192 x 4096, 6.5 for 4.9 of 777 x 2560.  The rounding to 4 bits moves a value by
+            // 2^-4 at most, and 2^-21 of it shows only next to the middle of two neighbours.)
             const float inverse = __fdividef(1.0f, scale);
             unsigned o[2] = {};
 #pragma unroll

@@ -254,7 +254,7 @@ __device__ __forceinline__ void widen16(const uint4 &w, float (&v)[8]) {
 }
 
 // 2^x by the hardware's approximation (2 ulp), results below 2^-126 as 0: for weights that are
-// rounded to bf16 next.
+// rounded to bf16 next, or kept to 2^-17 in two parts.
 __device__ __forceinline__ float exp2_ftz(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -729,8 +729,8 @@ def test_the_same_bits_beside_other_work(op):
             assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
 
 
-@pytest.mark.parametrize("lens,N", [([1, 1, 1], 128), ([9, 6, 5], 64), ([100, 70], 128), ([90, 80], 64)],
-                         ids=str)
+@pytest.mark.parametrize("lens,N", [([1, 1, 1], 128), ([9, 6, 5], 64), ([100, 70], 128),
+                                    ([90, 80], 64)], ids=str)
 @pytest.mark.parametrize("size", [2.0 ** 65, 2.0 ** 127])
 def test_keys_past_fp32_become_zeros(op, lens, N, size):
     """A key whose squares' sum is past fp32, finite itself: its token decays the state and reads it,

@@ -49,7 +49,8 @@ def test_every_wait_of_the_passes_is_bounded():
     assert "mbar_wait(" not in SOURCE and "try_wait" not in SOURCE
     second = SOURCE[SOURCE.index("// ---- the second pass"):]
     # the CTA's barriers: before the roles part and after they meet again
-    roles, end = second.index("if (warp == kDeltaLoader)"), second.index("tc_fence_before();\n    if (__syncthreads_or")
+    roles = second.index("if (warp == kDeltaLoader)")
+    end = second.index("tc_fence_before();\n    if (__syncthreads_or")
     assert "__syncthreads" not in second[roles:end]
 
 
