@@ -362,7 +362,7 @@ def test_calls_token_by_token_need_no_workspace(ssu, nowhere, nheads, batch, tok
 # threads to an SM, those into e4m3 with a residual at 36 spilled bytes; eight vectors (rows past
 # 16384 columns) one CTA.
 MEASURED = {
-    "ssu_delta.cu": {r"ssu_delta_mma_kernel": (164, 0), r"ssu_delta_prep_kernel": (110, 0),
+    "ssu_delta.cu": {r"ssu_delta_mma_kernel": (164, 0), r"ssu_delta_prep_kernel": (124, 0),
                      r"ssu_delta_step_kernelILi8ELi128Ef": (96, 0),
                      r"ssu_delta_step_kernelILi4ELi64E": (80, 0)},
     "ssu_norm.cu": {r"ssu_add_norm_kernelILi[124]E.*Lb0E": (64, 0),
